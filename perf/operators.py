@@ -230,7 +230,7 @@ def prepare(case, seed):
             if t in s:
                 s["cache" + t] = _handle(dkv, s, t)
         if case["op"] in ("full", "select"):
-            n = dkv.workspace_bytes(B, Hq, Hkv, d, N, case["top_k"])
+            n = dkv.workspace_bytes(B, Hq, Hkv, d, N, case["top_k"], fp8=True)
             s["workspace"] = torch.zeros(n, dtype=torch.uint8, device="cuda")
         s["dkv"] = dkv
     return s
