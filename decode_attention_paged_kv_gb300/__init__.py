@@ -11,9 +11,11 @@ Public calls (same names as the C ABI, without the ``dkv_`` prefix):
   decode_attn_full(q, K, V)             -> out
   decode_attn_select(q, K, V, meta, k)  -> out (, selected)
   kv_quant4(x) / kv_dequant4(q4)
+  kv_append(k, v, K, V, lens)           new tokens into a cache (-> rotated q)
   workspace_bytes(...), read_device_status(workspace)
 K and V are dense tensors [B, Hkv, N, d] (bf16 / fp16; any batch / head
-strides, token stride d) or ``Q4Cache`` tuples in the 4-bit format.
+strides, token stride d), ``Q4Cache`` tuples in the 4-bit format,
+``PagedCache`` pools, or ``Fp8Cache`` / ``Fp8PagedCache`` in the 8-bit format.
 """
 
 from __future__ import annotations
@@ -29,8 +31,8 @@ import torch
 from . import build as _build_mod
 
 __all__ = [
-    "Q4Cache", "PagedCache", "Meta8", "DkvError", "lib", "kv_meta_build", "kv_meta8_build",
-    "kv_meta_append", "hot_state", "hot_stats", "decode_attn_full",
+    "Q4Cache", "PagedCache", "Fp8Cache", "Fp8PagedCache", "Meta8", "DkvError", "lib", "kv_meta_build", "kv_meta8_build",
+    "kv_append", "kv_meta_append", "rope_table", "hot_state", "hot_stats", "decode_attn_full",
     "decode_attn_select", "decode_attn_topk_tokens", "kv_quant4", "kv_dequant4",
     "workspace_bytes", "workspace_bytes_tokens", "read_device_status", "status_string",
     "PAGE_SIZE", "DKV_FLAG_GROUP_SELECT",
@@ -43,7 +45,8 @@ DKV_OK = 0
 DKV_ERR_DEVICE_TIMEOUT = 8
 DKV_ERR_DEVICE_CHECK = 9
 DKV_BF16, DKV_FP16, DKV_FP32 = 0, 1, 2
-DKV_KV_DENSE, DKV_KV_Q4G64, DKV_KV_PAGED = 0, 1, 2
+DKV_KV_DENSE, DKV_KV_Q4G64, DKV_KV_PAGED, DKV_KV_FP8, DKV_KV_FP8_PAGED = 0, 1, 2, 3, 4
+DKV_WORKSPACE_HEADER_BYTES = 256
 DKV_FLAG_FORCE_TIMEOUT = 0x1
 DKV_FLAG_GROUP_SELECT = 0x2
 
@@ -89,6 +92,31 @@ class PagedCache(NamedTuple):
     seq_len: int
 
 
+class Fp8Cache(NamedTuple):
+    """A K or V cache in the 8-bit format: a value is code * scale.
+
+    codes [B, Hkv, N, d] float8_e4m3fn (any batch / head strides, token stride
+    d); scale [B, Hkv, ceil(N / 16)] float32, one per 16 tokens and kv head;
+    dtype: the 16-bit type of q, of the tokens appended and of the metadata.
+    """
+    codes: torch.Tensor
+    scale: torch.Tensor
+    dtype: torch.dtype = torch.bfloat16
+
+
+class Fp8PagedCache(NamedTuple):
+    """A K or V cache in the 8-bit format, held as a pool of 16-token blocks.
+
+    pool [num_blocks, Hkv, 16, d] float8_e4m3fn; scale [num_blocks, Hkv]
+    float32; block_table, seq_len as for PagedCache; dtype as for Fp8Cache.
+    """
+    pool: torch.Tensor
+    scale: torch.Tensor
+    block_table: torch.Tensor
+    seq_len: int
+    dtype: torch.dtype = torch.bfloat16
+
+
 class _Params(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
@@ -105,7 +133,17 @@ class _KV(ctypes.Structure):
                 ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
                 ("gstride_b", ctypes.c_int64), ("gstride_h", ctypes.c_int64),
                 ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64),
-                ("num_blocks", ctypes.c_int32)]
+                ("num_blocks", ctypes.c_int32), ("scale", ctypes.c_void_p),
+                ("sstride_b", ctypes.c_int64), ("sstride_h", ctypes.c_int64)]
+
+
+class _Append(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in
+                 ("batch", "num_q_heads", "num_kv_heads", "head_dim", "seq_len", "new_tokens",
+                  "rotary_dim", "rope_len", "interleaved")]
+                + [(n, ctypes.c_void_p) for n in ("k", "v", "q", "q_out")]
+                + [(f"{t}_stride_{x}", ctypes.c_int64) for t in "kvqo" for x in "bth"]
+                + [(n, ctypes.c_void_p) for n in ("cos", "sin", "seq_lens", "new_lens")])
 
 
 _lib = None
@@ -127,6 +165,9 @@ def lib() -> ctypes.CDLL:
             P, KVp = ctypes.POINTER(_Params), ctypes.POINTER(_KV)
             L.dkv_workspace_bytes.argtypes = [P, i32]
             L.dkv_workspace_bytes.restype = sz
+            L.dkv_workspace_bytes_fp8.argtypes = [P, i32]
+            L.dkv_workspace_bytes_fp8.restype = sz
+            L.dkv_kv_append.argtypes = [ctypes.POINTER(_Append), KVp, KVp, vp, vp]
             L.dkv_kv_meta_build.argtypes = [P, KVp, vp, vp, vp]
             L.dkv_decode_attn_full.argtypes = [P, vp, KVp, KVp, vp, i32, vp, sz, vp]
             L.dkv_decode_attn_select.argtypes = [P, vp, KVp, KVp, vp, vp, i32, vp, i32, vp, vp,
@@ -152,7 +193,7 @@ def lib() -> ctypes.CDLL:
             for name in ("dkv_kv_meta_build", "dkv_decode_attn_full", "dkv_decode_attn_select",
                          "dkv_decode_attn_topk_tokens", "dkv_kv_meta8_build",
                          "dkv_decode_attn_select_meta8", "dkv_kv_meta_append",
-                         "dkv_decode_attn_select_hot",
+                         "dkv_decode_attn_select_hot", "dkv_kv_append",
                          "dkv_kv_quant4", "dkv_kv_dequant4", "dkv_read_device_status",
                          "dkv_attn_ctas_per_sm"):
                 getattr(L, name).restype = ctypes.c_int
@@ -173,6 +214,20 @@ def _stream(t: torch.Tensor) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
+def _call(where: str, dev: torch.device, *args) -> None:
+    """One library call on the current stream of `dev`, which is made the
+    current device for it; raises on an error status."""
+    fn = getattr(lib(), where)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != DKV_OK:
+        raise DkvError(st, where)
+
+
 def _dtype_code(dt: torch.dtype) -> int:
     if dt == torch.bfloat16:
         return DKV_BF16
@@ -184,10 +239,34 @@ def _dtype_code(dt: torch.dtype) -> int:
 
 
 def _kv_struct(kv) -> tuple[_KV, int, int, int, int]:
-    """(struct, B, Hkv, N, d) for a dense tensor, a Q4Cache or a PagedCache."""
+    """(struct, B, Hkv, N, d) for a dense tensor or a cache tuple."""
     s = _KV()
-    if isinstance(kv, PagedCache):
-        pool, bt, N = kv
+    if isinstance(kv, Fp8Cache):
+        c, sc, dt = kv
+        B, H, N, d = c.shape
+        if c.dtype != torch.float8_e4m3fn or sc.dtype != torch.float32:
+            raise TypeError("Fp8Cache wants float8_e4m3fn codes and float32 scales")
+        if c.stride(3) != 1 or c.stride(2) != d:
+            raise ValueError("codes must have token stride d and channel stride 1")
+        if (tuple(sc.shape) != (B, H, (N + PAGE_SIZE - 1) // PAGE_SIZE)
+                or (sc.stride(2) != 1 and sc.shape[2] > 1) or sc.device != c.device):
+            raise ValueError("scale must be [B, Hkv, ceil(N / 16)] with unit block stride")
+        s.format, s.dtype = DKV_KV_FP8, _dtype_code(dt)
+        s.data, s.stride_b, s.stride_h = c.data_ptr(), c.stride(0), c.stride(1)
+        s.scale, s.sstride_b, s.sstride_h = sc.data_ptr(), sc.stride(0), sc.stride(1)
+        return s, B, H, N, d
+    if isinstance(kv, (PagedCache, Fp8PagedCache)):
+        if isinstance(kv, PagedCache):
+            pool, bt, N = kv
+            s.format, s.dtype = DKV_KV_PAGED, _dtype_code(pool.dtype)
+        else:
+            pool, sc, bt, N, dt = kv
+            if pool.dtype != torch.float8_e4m3fn or sc.dtype != torch.float32:
+                raise TypeError("Fp8PagedCache wants a float8_e4m3fn pool and float32 scales")
+            if tuple(sc.shape) != tuple(pool.shape[:2]) or sc.device != pool.device:
+                raise ValueError("scale must be [num_blocks, Hkv]")
+            s.format, s.dtype = DKV_KV_FP8_PAGED, _dtype_code(dt)
+            s.scale, s.sstride_b, s.sstride_h = sc.data_ptr(), sc.stride(0), sc.stride(1)
         nb, H, S, d = pool.shape
         if S != PAGE_SIZE or pool.stride(3) != 1 or pool.stride(2) != d:
             raise ValueError("pool must be [num_blocks, Hkv, 16, d] with token stride d")
@@ -196,7 +275,6 @@ def _kv_struct(kv) -> tuple[_KV, int, int, int, int]:
         P = (int(N) + PAGE_SIZE - 1) // PAGE_SIZE
         if bt.shape[1] < P:
             raise ValueError("block_table has fewer than ceil(seq_len / 16) columns")
-        s.format, s.dtype = DKV_KV_PAGED, _dtype_code(pool.dtype)
         s.data = pool.data_ptr()
         s.stride_b, s.stride_h = pool.stride(0), pool.stride(1)
         s.block_table, s.block_table_stride, s.num_blocks = bt.data_ptr(), bt.stride(0), nb
@@ -226,9 +304,27 @@ def _kv_struct(kv) -> tuple[_KV, int, int, int, int]:
 
 
 def _device_of(kv) -> torch.device:
-    if isinstance(kv, Q4Cache):
+    if isinstance(kv, (Q4Cache, Fp8Cache)):
         return kv.codes.device
-    return kv.pool.device if isinstance(kv, PagedCache) else kv.device
+    return kv.pool.device if isinstance(kv, (PagedCache, Fp8PagedCache)) else kv.device
+
+
+def _is_fp8(kv) -> bool:
+    return isinstance(kv, (Fp8Cache, Fp8PagedCache))
+
+
+def _dtype_of(kv) -> torch.dtype:
+    """The 16-bit type that goes with a cache: its queries' and metadata's."""
+    if isinstance(kv, Q4Cache):
+        return torch.float16
+    if isinstance(kv, PagedCache):
+        return kv.pool.dtype
+    return kv.dtype
+
+
+def _check_query(q: torch.Tensor, K) -> None:
+    if _is_fp8(K) and (q.dtype != K.dtype or q.device != _device_of(K)):
+        raise ValueError(f"q must be {K.dtype} on the cache's device")
 
 
 def _params(q: Optional[torch.Tensor], B, Hkv, N, d, out: Optional[torch.Tensor],
@@ -254,15 +350,21 @@ def _params(q: Optional[torch.Tensor], B, Hkv, N, d, out: Optional[torch.Tensor]
 
 
 def workspace_bytes(B: int, Hq: int, Hkv: int, d: int, N: int, top_k: int = 0,
-                    page_size: int = PAGE_SIZE) -> int:
-    """Workspace bytes dkv_decode_attn_full (top_k = 0) or _select needs."""
+                    page_size: int = PAGE_SIZE, fp8: bool = False) -> int:
+    """Workspace bytes dkv_decode_attn_full (top_k = 0) or _select needs (fp8:
+    on an 8-bit cache)."""
     p = _Params()
     p.batch, p.num_q_heads, p.num_kv_heads, p.head_dim, p.seq_len = B, Hq, Hkv, d, N
     p.page_size, p.scale = page_size, 1.0
-    n = lib().dkv_workspace_bytes(ctypes.byref(p), int(top_k))
+    n = _workspace_need(p, int(top_k), fp8)
     if n == 0:
         raise DkvError(2, "dkv_workspace_bytes")
     return int(n)
+
+
+def _workspace_need(p: _Params, top_k: int, fp8: bool) -> int:
+    f = lib().dkv_workspace_bytes_fp8 if fp8 else lib().dkv_workspace_bytes
+    return f(ctypes.byref(p), top_k)
 
 
 def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.Tensor:
@@ -277,15 +379,14 @@ def kv_meta_build(K, page_size: int = PAGE_SIZE, seq_lens: Optional[torch.Tensor
     """Page metadata (meta_min, meta_max), each [B, Hkv, P, d]."""
     ks, B, H, N, d = _kv_struct(K)
     dev = _device_of(K)
-    dt = (torch.float16 if isinstance(K, Q4Cache)
-          else K.pool.dtype if isinstance(K, PagedCache) else K.dtype)
+    dt = _dtype_of(K)
     P = (N + page_size - 1) // page_size
     mn = torch.empty(B, H, P, d, dtype=dt, device=dev)
     mx = torch.empty(B, H, P, d, dtype=dt, device=dev)
     p = _params(None, B, H, N, d, None, None, seq_lens=seq_lens)
     p.page_size = page_size
-    _check(lib().dkv_kv_meta_build(ctypes.byref(p), ctypes.byref(ks), mn.data_ptr(),
-                                   mx.data_ptr(), _stream(mn)), "dkv_kv_meta_build")
+    _call("dkv_kv_meta_build", dev, ctypes.byref(p), ctypes.byref(ks), mn.data_ptr(),
+          mx.data_ptr())
     return mn, mx
 
 
@@ -301,9 +402,100 @@ def kv_meta_append(K, meta, page_size: int = PAGE_SIZE,
         raise ValueError("meta must be contiguous [B, Hkv, P, d]")
     p = _params(None, B, H, N, d, None, None, seq_lens=seq_lens)
     p.page_size = page_size
-    _check(lib().dkv_kv_meta_append(ctypes.byref(p), ctypes.byref(ks), mn.data_ptr(),
-                                    mx.data_ptr(), _stream(mn)), "dkv_kv_meta_append")
+    if _is_fp8(K) and not mn.dtype == mx.dtype == K.dtype:
+        raise ValueError(f"meta of this cache is {K.dtype}")
+    _call("dkv_kv_meta_append", mn.device, ctypes.byref(p), ctypes.byref(ks), mn.data_ptr(),
+          mx.data_ptr())
     return mn, mx
+
+
+def rope_table(length: int, rotary_dim: int, base: float = 10000.0, device=None):
+    """(cos, sin) float32 [length, rotary_dim / 2] of the angles
+    p * base^(-2 i / rotary_dim), computed in 64 bits, for kv_append(rope=...).
+    Any other table of that shape (scaled or extended positions) serves as well."""
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    a = torch.arange(length, dtype=torch.float64)[:, None] * base ** (-i / rotary_dim)
+    return a.cos().float().to(device), a.sin().float().to(device)
+
+
+def _rows(t: torch.Tensor, name: str, shape, dt: torch.dtype, dev: torch.device) -> tuple:
+    if (t.dtype != dt or t.device != dev or t.shape != shape or t.stride(3) != 1):
+        raise ValueError(f"{name} must be {dt} {tuple(shape)} on {dev} with channel stride 1")
+    return t.stride()[:3]
+
+
+def _lengths(t: Optional[torch.Tensor], name: str, B: int, dev: torch.device) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.shape != (B,) or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [B] on {dev}")
+    return t.data_ptr()
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, K, V, seq_lens: Optional[torch.Tensor] = None,
+              new_lens: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+              q_out: Optional[torch.Tensor] = None, rope=None, interleaved: bool = False,
+              workspace: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Append new tokens' keys k and values v [B, T, Hkv, d] to the caches K and
+    V, in place, rotating keys and queries by their positions; one launch.
+
+    seq_lens (int32 [B] on the device): each sequence's length with its new
+    tokens, as the step's other calls take it; None: the caches' whole length.
+    new_lens (int32 [B]): how many of the T rows each sequence has; None: all.
+    The tokens take the positions seq_lens - new_lens .. seq_lens - 1.
+    q [B, T, Hq, d]: queries of the same positions, returned rotated (in q_out
+    if given, which may be q itself).
+    rope: (cos, sin) float32 [positions, r / 2], r <= d the rotary width, as
+    rope_table makes them; None: no rotation.  interleaved: pairs (2i, 2i + 1)
+    instead of (i, i + r / 2).
+    workspace: where sequences that do not fit, and block-table entries outside
+    the pool, are recorded (read_device_status); nothing of them is written.
+    K and V: both dense tensors, PagedCache, Fp8Cache or Fp8PagedCache."""
+    ks, B, H, N, d = _kv_struct(K)
+    vs, B2, H2, N2, d2 = _kv_struct(V)
+    if (B, H, N, d) != (B2, H2, N2, d2):
+        raise ValueError("K and V shapes differ")
+    dev, dt = _device_of(K), _dtype_of(K)
+    if dev.type != "cuda" or _device_of(V) != dev:
+        raise ValueError("K and V must be on one CUDA device")
+    if k.dim() != 4:
+        raise ValueError("k must be [B, T, Hkv, d]")
+    T = k.shape[1]
+    a = _Append(B, 0, H, d, N, T)
+    a.k, a.v = k.data_ptr(), v.data_ptr()
+    a.k_stride_b, a.k_stride_t, a.k_stride_h = _rows(k, "k", (B, T, H, d), dt, dev)
+    a.v_stride_b, a.v_stride_t, a.v_stride_h = _rows(v, "v", (B, T, H, d), dt, dev)
+    if q is not None:
+        shape = (B, T, q.shape[2], d)
+        a.num_q_heads, a.q = shape[2], q.data_ptr()
+        a.q_stride_b, a.q_stride_t, a.q_stride_h = _rows(q, "q", shape, dt, dev)
+        if q_out is None:
+            # (rows that no token has are left as they are)
+            q_out = torch.empty(shape, dtype=dt, device=dev)
+        a.o_stride_b, a.o_stride_t, a.o_stride_h = _rows(q_out, "q_out", shape, dt, dev)
+        a.q_out = q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if rope is not None:
+        cos, sin = rope
+        if (cos.shape != sin.shape or cos.dim() != 2 or cos.device != dev or sin.device != dev
+                or cos.dtype != torch.float32 or sin.dtype != torch.float32
+                or not cos.is_contiguous() or not sin.is_contiguous()):
+            raise ValueError("rope must be two contiguous float32 [positions, r / 2] tables")
+        a.rope_len, a.rotary_dim = cos.shape[0], 2 * cos.shape[1]
+        a.interleaved, a.cos, a.sin = int(interleaved), cos.data_ptr(), sin.data_ptr()
+    a.seq_lens = _lengths(seq_lens, "seq_lens", B, dev)
+    a.new_lens = _lengths(new_lens, "new_lens", B, dev)
+    ws = None
+    if workspace is not None:
+        if (workspace.device != dev
+                or workspace.numel() * workspace.element_size() < DKV_WORKSPACE_HEADER_BYTES):
+            raise ValueError("workspace must hold 256 bytes on the caches' device")
+        ws = workspace.data_ptr()
+    if T == 0:  # (an empty tensor has no address)
+        return q_out
+    _call("dkv_kv_append", dev, ctypes.byref(a), ctypes.byref(ks), ctypes.byref(vs), ws)
+    return q_out
 
 
 def hot_state(B: int, Hkv: int, N: int, device) -> torch.Tensor:
@@ -358,14 +550,14 @@ def decode_attn_full(q, K, V, scale: Optional[float] = None,
     vs, B2, H2, N2, d2 = _kv_struct(V)
     if (B, H, N, d) != (B2, H2, N2, d2):
         raise ValueError("K and V shapes differ")
+    _check_query(q, K)
     if out is None:
         out = torch.empty(B, q.shape[1], d, dtype=out_dtype, device=q.device)
     p = _params(q, B, H, N, d, out, scale, flags, seq_lens)
-    nbytes = lib().dkv_workspace_bytes(ctypes.byref(p), 0)
+    nbytes = _workspace_need(p, 0, _is_fp8(K))
     ws = _workspace(nbytes, q.device, workspace)
-    _check(lib().dkv_decode_attn_full(ctypes.byref(p), q.data_ptr(), ctypes.byref(ks),
-                                      ctypes.byref(vs), out.data_ptr(), _dtype_code(out.dtype),
-                                      ws.data_ptr(), nbytes, _stream(q)), "dkv_decode_attn_full")
+    _call("dkv_decode_attn_full", q.device, ctypes.byref(p), q.data_ptr(), ctypes.byref(ks),
+          ctypes.byref(vs), out.data_ptr(), _dtype_code(out.dtype), ws.data_ptr(), nbytes)
     return out
 
 
@@ -389,6 +581,7 @@ def decode_attn_select(q, K, V, meta, top_k: int, scale: Optional[float] = None,
     vs, B2, H2, N2, d2 = _kv_struct(V)
     if (B, H, N, d) != (B2, H2, N2, d2):
         raise ValueError("K and V shapes differ")
+    _check_query(q, K)
     P = (N + page_size - 1) // page_size
     m8 = meta if isinstance(meta, Meta8) else None
     if m8 is not None and hot is not None:
@@ -401,6 +594,8 @@ def decode_attn_select(q, K, V, meta, top_k: int, scale: Optional[float] = None,
         mn, mx = meta
         if tuple(mn.shape) != (B, H, P, d) or not mn.is_contiguous() or not mx.is_contiguous():
             raise ValueError("meta must be contiguous [B, Hkv, P, d]")
+        if _is_fp8(K) and not mn.dtype == mx.dtype == K.dtype:
+            raise ValueError(f"meta of this cache is {K.dtype}")
     if out is None:
         out = torch.empty(B, q.shape[1], d, dtype=out_dtype, device=q.device)
     kk = min(int(top_k), P)
@@ -408,27 +603,22 @@ def decode_attn_select(q, K, V, meta, top_k: int, scale: Optional[float] = None,
         selected = torch.empty(B, q.shape[1], kk, dtype=torch.int32, device=q.device)
     p = _params(q, B, H, N, d, out, scale, flags, seq_lens)
     p.page_size = page_size
-    nbytes = lib().dkv_workspace_bytes(ctypes.byref(p), int(top_k))
+    nbytes = _workspace_need(p, int(top_k), _is_fp8(K))
     ws = _workspace(nbytes, q.device, workspace)
     sel_ptr = selected.data_ptr() if selected is not None else None
+    out_args = (int(top_k), out.data_ptr(), _dtype_code(out.dtype), sel_ptr)
     if m8 is not None:
-        _check(lib().dkv_decode_attn_select_meta8(
-            ctypes.byref(p), q.data_ptr(), ctypes.byref(ks), ctypes.byref(vs),
-            m8.code_min.data_ptr(), m8.code_max.data_ptr(), m8.lo.data_ptr(),
-            m8.step.data_ptr(), int(top_k), out.data_ptr(), _dtype_code(out.dtype), sel_ptr,
-            ws.data_ptr(), nbytes, _stream(q)), "dkv_decode_attn_select_meta8")
+        _call("dkv_decode_attn_select_meta8", q.device, ctypes.byref(p), q.data_ptr(),
+              ctypes.byref(ks), ctypes.byref(vs), m8.code_min.data_ptr(), m8.code_max.data_ptr(),
+              m8.lo.data_ptr(), m8.step.data_ptr(), *out_args, ws.data_ptr(), nbytes)
     elif hot is not None:
-        _check(lib().dkv_decode_attn_select_hot(
-            ctypes.byref(p), q.data_ptr(), ctypes.byref(ks), ctypes.byref(vs), mn.data_ptr(),
-            mx.data_ptr(), int(top_k), out.data_ptr(), _dtype_code(out.dtype), sel_ptr,
-            hot.data_ptr(), hot.numel(), int(step), ws.data_ptr(), nbytes, _stream(q)),
-            "dkv_decode_attn_select_hot")
+        _call("dkv_decode_attn_select_hot", q.device, ctypes.byref(p), q.data_ptr(),
+              ctypes.byref(ks), ctypes.byref(vs), mn.data_ptr(), mx.data_ptr(), *out_args,
+              hot.data_ptr(), hot.numel(), int(step), ws.data_ptr(), nbytes)
     else:
-        _check(lib().dkv_decode_attn_select(ctypes.byref(p), q.data_ptr(), ctypes.byref(ks),
-                                            ctypes.byref(vs), mn.data_ptr(), mx.data_ptr(),
-                                            int(top_k), out.data_ptr(), _dtype_code(out.dtype),
-                                            sel_ptr, ws.data_ptr(), nbytes, _stream(q)),
-               "dkv_decode_attn_select")
+        _call("dkv_decode_attn_select", q.device, ctypes.byref(p), q.data_ptr(),
+              ctypes.byref(ks), ctypes.byref(vs), mn.data_ptr(), mx.data_ptr(), *out_args,
+              ws.data_ptr(), nbytes)
     return (out, selected) if return_selected else out
 
 

@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/dkv.h"
@@ -48,7 +49,14 @@ struct WsLayout {
   bool ok = true;        // false: the sizes exceed what the kernels cover
 };
 
-WsLayout layout_for(const dkv_params& p, int top_k) {
+bool is_fp8(const dkv_kv* kv) {
+  return kv->format == DKV_KV_FP8 || kv->format == DKV_KV_FP8_PAGED;
+}
+bool is_paged(const dkv_kv* kv) {
+  return kv->format == DKV_KV_PAGED || kv->format == DKV_KV_FP8_PAGED;
+}
+
+WsLayout layout_for(const dkv_params& p, int top_k, bool fp8 = false) {
   WsLayout L;
   const int d = p.head_dim;
   const int64_t P = ceil_div(p.seq_len, p.page_size);   // selection (metadata) pages
@@ -56,7 +64,8 @@ WsLayout layout_for(const dkv_params& p, int top_k) {
   const int64_t rows = static_cast<int64_t>(p.batch) * p.num_q_heads;
   const int64_t units = static_cast<int64_t>(p.batch) * p.num_kv_heads;
   if (top_k <= 0) {
-    L.pages_per_chunk = dkv::full_pages_per_chunk(P16, d);
+    L.pages_per_chunk = fp8 ? dkv::fp8_pages_per_chunk(P16, d, p.batch)
+                            : dkv::full_pages_per_chunk(P16, d);
     L.n_chunks = static_cast<int>(ceil_div(P16, L.pages_per_chunk));
   } else {
     const int G = p.num_q_heads / p.num_kv_heads;
@@ -69,8 +78,9 @@ WsLayout layout_for(const dkv_params& p, int top_k) {
         std::min(p.page_size < dkv::kPage ? union_sel : union_sel * (p.page_size / dkv::kPage),
                  P16);
     L.union_stride = static_cast<int>(union_max);
-    L.pages_per_chunk = dkv::select_pages_per_chunk(union_max, d);
-    if (L.pages_per_chunk > dkv::kMaxSelectList) L.ok = false;
+    L.pages_per_chunk = fp8 ? dkv::fp8_pages_per_chunk(union_max, d, p.batch)
+                            : dkv::select_pages_per_chunk(union_max, d);
+    if (!fp8 && L.pages_per_chunk > dkv::kMaxSelectList) L.ok = false;
     L.n_chunks = static_cast<int>(ceil_div(union_max, L.pages_per_chunk));
   }
   if (L.n_chunks > dkv::kMaxChunks) L.ok = false;
@@ -152,17 +162,26 @@ dkv_status check_kv(const dkv_params* p, const dkv_kv* kv) {
     if (kv->stride_b % 8 || kv->stride_h % 8) return DKV_ERR_ALIGN;
     return DKV_OK;
   }
-  if (kv->format == DKV_KV_PAGED) {
+  if (is_paged(kv) || kv->format == DKV_KV_FP8) {
     if (kv->dtype != DKV_BF16 && kv->dtype != DKV_FP16) return DKV_ERR_DTYPE;
-    if (kv->stride_b % 8 || kv->stride_h % 8) return DKV_ERR_ALIGN;
+    const int64_t unit = is_fp8(kv) ? 16 : 8;  // 16 bytes
+    if (kv->stride_b % unit || kv->stride_h % unit) return DKV_ERR_ALIGN;
+  }
+  if (is_paged(kv)) {
     if (kv->block_table == nullptr) return DKV_ERR_NULL;
     if (reinterpret_cast<uintptr_t>(kv->block_table) & 3u) return DKV_ERR_ALIGN;
     if (kv->num_blocks < 1 || kv->block_table_stride < 0) return DKV_ERR_SHAPE;
     // the [B, P] table's rows may not overlap (P = ceil(N / 16) cache pages)
     if (p->batch > 1 && kv->block_table_stride < ceil_div(p->seq_len, dkv::kPage))
       return DKV_ERR_SHAPE;
+  }
+  if (is_fp8(kv)) {
+    if (kv->scale == nullptr) return DKV_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(kv->scale) & 3u) return DKV_ERR_ALIGN;
+    if (kv->sstride_b < 0 || kv->sstride_h < 0) return DKV_ERR_SHAPE;
     return DKV_OK;
   }
+  if (kv->format == DKV_KV_PAGED) return DKV_OK;
   if (kv->format == DKV_KV_Q4G64) {
     if (kv->dtype != DKV_FP16) return DKV_ERR_DTYPE;
     if (kv->gmin == nullptr || kv->gmax == nullptr) return DKV_ERR_NULL;
@@ -271,6 +290,34 @@ bool encode_code_map(CUtensorMap* map, const dkv_params* p, const void* codes, i
   return r == CUDA_SUCCESS;
 }
 
+// Map over the e4m3 codes of an 8-bit cache [B, Hkv, N, d] viewed as {d bytes, N
+// tokens, 1, Hkv, B}, or over a pool as {d bytes, 16 tokens, 1, Hkv, blocks};
+// box {d, 16, 1, 1, 1} (one page of one kv head), d-byte swizzle.
+bool encode_fp8_map(CUtensorMap* map, const dkv_params* p, const dkv_kv* kv) {
+  if (!get_encode()) return false;
+  const cuuint64_t d = static_cast<cuuint64_t>(p->head_dim);
+  const cuuint64_t dims[5] = {d,
+                              static_cast<cuuint64_t>(is_paged(kv) ? dkv::kPage : p->seq_len), 1,
+                              static_cast<cuuint64_t>(p->num_kv_heads),
+                              static_cast<cuuint64_t>(is_paged(kv) ? kv->num_blocks : p->batch)};
+  cuuint64_t st[4] = {d, d, static_cast<cuuint64_t>(kv->stride_h),
+                      static_cast<cuuint64_t>(kv->stride_b)};
+  // A size-1 dimension's stride still has to be a valid (16-byte multiple) value.
+  if (dims[3] == 1 && st[2] == 0) st[2] = 16;
+  if (dims[4] == 1 && st[3] == 0) st[3] = 16;
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(dkv::kPage), 1, 1,
+                             1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(kv->data),
+                              dims, st, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+dkv::Fp8View fp8_view(const dkv_kv* kv) { return {kv->scale, kv->sstride_b, kv->sstride_h}; }
+
 int out_code(int32_t out_dtype) {
   return out_dtype == DKV_FP32 ? 2 : (out_dtype == DKV_FP16 ? 1 : 0);
 }
@@ -287,6 +334,12 @@ size_t dkv_workspace_bytes(const dkv_params* p, int32_t top_k) {
   return L.ok ? L.total : 0;
 }
 
+size_t dkv_workspace_bytes_fp8(const dkv_params* p, int32_t top_k) {
+  if (check_params(p) != DKV_OK || top_k < 0) return 0;
+  const WsLayout L = layout_for(*p, top_k, true);
+  return L.ok ? L.total : 0;
+}
+
 static dkv_status meta_impl(const dkv_params* p, const dkv_kv* K, void* meta_min,
                             void* meta_max, bool last_only, void* stream) {
   dkv_status st = check_params(p);
@@ -294,6 +347,29 @@ static dkv_status meta_impl(const dkv_params* p, const dkv_kv* K, void* meta_min
   if ((st = check_kv(p, K)) != DKV_OK) return st;
   if (meta_min == nullptr || meta_max == nullptr) return DKV_ERR_NULL;
   if (!aligned16(meta_min) || !aligned16(meta_max)) return DKV_ERR_ALIGN;
+  if (is_fp8(K)) {
+    dkv::MetaFp8Args f{};
+    f.codes = static_cast<const uint8_t*>(K->data);
+    f.sb = K->stride_b;
+    f.sh = K->stride_h;
+    f.scale = fp8_view(K);
+    f.B = p->batch;
+    f.Hkv = p->num_kv_heads;
+    f.N = p->seq_len;
+    f.P = static_cast<int>(ceil_div(p->seq_len, p->page_size));
+    f.S = p->page_size;
+    f.meta_min = meta_min;
+    f.meta_max = meta_max;
+    f.lens = p->seq_lens;
+    f.last_only = last_only ? 1 : 0;
+    if (is_paged(K)) {
+      f.bt = K->block_table;
+      f.bts = K->block_table_stride;
+      f.nblocks = K->num_blocks;
+    }
+    return cuda_status(dkv::launch_meta_fp8(p->head_dim, K->dtype == DKV_FP16, f,
+                                            static_cast<cudaStream_t>(stream)));
+  }
   dkv::MetaArgs a{};
   a.data = K->data;
   a.gmin = K->gmin;
@@ -341,12 +417,12 @@ static dkv_status attn_common(const dkv_params* p, const void* q, const dkv_kv* 
   if ((st = check_kv(p, V)) != DKV_OK) return st;
   if (K->format != V->format || K->dtype != V->dtype) return DKV_ERR_DTYPE;
   if (p->seq_lens != nullptr && K->format == DKV_KV_Q4G64) return DKV_ERR_UNSUPPORTED;
-  if (K->format == DKV_KV_PAGED) {
+  if (is_paged(K)) {
     // K and V share one block table; an item's blocks fit the page list
     if (K->block_table != V->block_table || K->block_table_stride != V->block_table_stride ||
         K->num_blocks != V->num_blocks)
       return DKV_ERR_SHAPE;
-    if (L.pages_per_chunk > dkv::kMaxSelectList) return DKV_ERR_UNSUPPORTED;
+    if (!is_fp8(K) && L.pages_per_chunk > dkv::kMaxSelectList) return DKV_ERR_UNSUPPORTED;
   }
   if (out_dtype != DKV_FP32 && out_dtype != DKV_BF16 && out_dtype != DKV_FP16)
     return DKV_ERR_DTYPE;
@@ -380,10 +456,15 @@ static bool cache_views(const dkv_params* p, const dkv_kv* K, const dkv_kv* V, C
     a->v4 = q4_view(V);
     return true;
   }
-  if (K->format == DKV_KV_PAGED) {
+  if (is_paged(K)) {
     a->bt = K->block_table;
     a->bts = K->block_table_stride;
     a->nblocks = K->num_blocks;
+  }
+  if (is_fp8(K)) {
+    a->k8 = fp8_view(K);
+    a->v8 = fp8_view(V);
+    return encode_fp8_map(mk, p, K) && encode_fp8_map(mv, p, V);
   }
   return encode_page_map(mk, p, K) && encode_page_map(mv, p, V);
 }
@@ -421,17 +502,19 @@ static dkv_status run_attention(const dkv_params* p, const dkv::AttnArgs& a, boo
   // (sparse: a.union_count tells the merge how many chunks of a unit hold pages)
   const int sms = current_sm_count();
   if (sms <= 0) return DKV_ERR_CUDA;
-  const bool q4 = a.k4.codes != nullptr;
+  const bool q4 = a.k4.codes != nullptr, fp8 = a.k8.scale != nullptr;
   dkv::AttnArgs ao = a;
   ao.out = out;
   ao.out_dtype = out_code(out_dtype);
   ao.o_sb = p->o_stride_b;
   ao.o_sh = p->o_stride_h;
   dkv_status st = cuda_status(
-      q4 ? dkv::launch_attn_q4(p->head_dim, sparse, ao, sms, s)
-         : dkv::launch_attn(p->head_dim, f16, sparse, ao, mk, mv, sms, s));
+      q4    ? dkv::launch_attn_q4(p->head_dim, sparse, ao, sms, s)
+      : fp8 ? dkv::launch_attn_fp8(p->head_dim, f16, sparse, ao, mk, mv, sms, s)
+            : dkv::launch_attn(p->head_dim, f16, sparse, ao, mk, mv, sms, s));
   if (st != DKV_OK) return st;
-  if (q4 && sparse && a.n_chunks == 1) return DKV_OK;  // the attention wrote out itself
+  // (where a unit is one item, the attention wrote out itself)
+  if (a.n_chunks == 1 && (fp8 || (q4 && sparse))) return DKV_OK;
   dkv::MergeArgs m{};
   m.part_ml = a.part_ml;
   m.part_o = a.part_o;
@@ -447,6 +530,7 @@ static dkv_status run_attention(const dkv_params* p, const dkv::AttnArgs& a, boo
   m.Hkv = a.Hkv;
   m.lens = a.lens;
   m.N = a.N;
+  m.zero_empty = fp8 ? 1 : 0;
   return cuda_status(dkv::launch_merge(p->head_dim, m, p->batch * p->num_q_heads, s));
 }
 
@@ -455,7 +539,7 @@ dkv_status dkv_decode_attn_full(const dkv_params* p, const void* q, const dkv_kv
                                 void* workspace, size_t workspace_bytes, void* stream) {
   dkv_status st = check_params(p);
   if (st != DKV_OK) return st;
-  const WsLayout L = layout_for(*p, 0);
+  const WsLayout L = layout_for(*p, 0, K != nullptr && is_fp8(K));
   if ((st = attn_common(p, q, K, V, out, out_dtype, workspace, workspace_bytes, 0, L)) != DKV_OK)
     return st;
   CUtensorMap mk, mv;
@@ -502,12 +586,12 @@ static dkv_status select_impl(const dkv_params* p, const void* q, const dkv_kv* 
   dkv_status st = check_params(p);
   if (st != DKV_OK) return st;
   if (top_k < 1) return DKV_ERR_SHAPE;
-  const WsLayout L = layout_for(*p, top_k);
+  const WsLayout L = layout_for(*p, top_k, K != nullptr && is_fp8(K));
   if ((st = attn_common(p, q, K, V, out, out_dtype, workspace, workspace_bytes, top_k, L)) !=
       DKV_OK)
     return st;
   if (hot != nullptr) {
-    if (K->format == DKV_KV_Q4G64) return DKV_ERR_UNSUPPORTED;
+    if (K->format == DKV_KV_Q4G64 || is_fp8(K)) return DKV_ERR_UNSUPPORTED;
     if (hot->state == nullptr) return DKV_ERR_NULL;
     if (reinterpret_cast<uintptr_t>(hot->state) & 15u) return DKV_ERR_ALIGN;
     if (hot->bytes < hot_bytes(*p)) return DKV_ERR_WORKSPACE;
@@ -893,6 +977,133 @@ dkv_status dkv_decode_attn_topk_tokens(const dkv_params* p, const void* q, const
   return cuda_status(dkv::launch_token_attn(d, f16, aa, rows, s));
 }
 
+// Whether the elements of a tensor that is written -- rows of `inner` elements
+// over the dimensions (count, stride) -- all have places of their own.
+struct Dim {
+  int64_t count, stride;
+};
+static bool distinct(int64_t inner, std::initializer_list<Dim> dims) {
+  Dim d[3];
+  int n = 0;
+  for (const Dim& x : dims)
+    if (x.count > 1) d[n++] = x;
+  std::sort(d, d + n, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  int64_t extent = inner;
+  for (int i = 0; i < n; ++i) {
+    if (d[i].stride < extent) return false;
+    extent += (d[i].count - 1) * d[i].stride;
+  }
+  return true;
+}
+
+dkv_status dkv_kv_append(const dkv_append* p, const dkv_kv* K, const dkv_kv* V, void* workspace,
+                         void* stream) {
+  if (p == nullptr) return DKV_ERR_NULL;
+  dkv_params pp{};
+  pp.batch = p->batch;
+  pp.num_q_heads = pp.num_kv_heads = p->num_kv_heads;
+  pp.head_dim = p->head_dim;
+  pp.seq_len = p->seq_len;
+  pp.page_size = dkv::kPage;
+  pp.seq_lens = p->seq_lens;
+  dkv_status st = check_params(&pp);
+  if (st != DKV_OK) return st;
+  if ((st = check_kv(&pp, K)) != DKV_OK) return st;
+  if ((st = check_kv(&pp, V)) != DKV_OK) return st;
+  if (K->format != V->format || K->dtype != V->dtype) return DKV_ERR_DTYPE;
+  if (K->format == DKV_KV_Q4G64) return DKV_ERR_UNSUPPORTED;
+  if (is_paged(K) &&
+      (K->block_table != V->block_table || K->block_table_stride != V->block_table_stride ||
+       K->num_blocks != V->num_blocks))
+    return DKV_ERR_SHAPE;
+  if (p->num_q_heads < 0 || p->num_q_heads > 65535 || p->new_tokens < 0) return DKV_ERR_SHAPE;
+  if (p->rotary_dim < 0 || p->rotary_dim > p->head_dim || p->rotary_dim % 16 != 0 ||
+      p->interleaved < 0 || p->interleaved > 1)
+    return DKV_ERR_SHAPE;
+  const bool queries = p->num_q_heads > 0;
+  if (p->k == nullptr || p->v == nullptr) return DKV_ERR_NULL;
+  if (queries && (p->q == nullptr || p->q_out == nullptr)) return DKV_ERR_NULL;
+  if (p->rotary_dim > 0 && (p->cos == nullptr || p->sin == nullptr)) return DKV_ERR_NULL;
+  if (!aligned16(p->k) || !aligned16(p->v) || !aligned16(workspace) ||
+      (queries && (!aligned16(p->q) || !aligned16(p->q_out))) ||
+      (p->rotary_dim > 0 && (!aligned16(p->cos) || !aligned16(p->sin))) ||
+      (reinterpret_cast<uintptr_t>(p->new_lens) & 3u))
+    return DKV_ERR_ALIGN;
+  const int64_t strides[12] = {p->k_stride_b, p->k_stride_t, p->k_stride_h, p->v_stride_b,
+                               p->v_stride_t, p->v_stride_h, p->q_stride_b, p->q_stride_t,
+                               p->q_stride_h, p->o_stride_b, p->o_stride_t, p->o_stride_h};
+  for (int i = 0; i < (queries ? 12 : 6); ++i) {
+    if (strides[i] < 0) return DKV_ERR_SHAPE;
+    if (strides[i] % 8) return DKV_ERR_ALIGN;
+  }
+  // Without lengths on the device the fit is known here.
+  if (p->seq_lens == nullptr && p->new_lens == nullptr && p->new_tokens > p->seq_len)
+    return DKV_ERR_SHAPE;
+  if (p->rotary_dim > 0 &&
+      (p->rope_len < 1 || (p->seq_lens == nullptr && p->rope_len < p->seq_len)))
+    return DKV_ERR_SHAPE;
+  // What is written has no element twice.
+  const int64_t d = p->head_dim, B = p->batch, H = p->num_kv_heads;
+  const int64_t P = ceil_div(p->seq_len, dkv::kPage);
+  for (const dkv_kv* kv : {K, V}) {
+    const int64_t tokens = is_paged(kv) ? dkv::kPage : p->seq_len;
+    const int64_t outer = is_paged(kv) ? kv->num_blocks : B;
+    if (!distinct(tokens * d, {{outer, kv->stride_b}, {H, kv->stride_h}})) return DKV_ERR_SHAPE;
+    if (is_fp8(kv) &&
+        !distinct(is_paged(kv) ? 1 : P, {{outer, kv->sstride_b}, {H, kv->sstride_h}}))
+      return DKV_ERR_SHAPE;
+  }
+  if (queries && !distinct(d, {{B, p->o_stride_b},
+                               {p->new_tokens, p->o_stride_t},
+                               {p->num_q_heads, p->o_stride_h}}))
+    return DKV_ERR_SHAPE;
+  if (p->new_tokens == 0) return DKV_OK;
+  const int64_t heads = 2 * H + p->num_q_heads;
+  const int64_t pages = (static_cast<int64_t>(p->new_tokens) + 14) / 16 + 1;
+  const int64_t most = (static_cast<int64_t>(1) << 31) - 256;  // a grid's threads or CTAs
+  if (p->new_tokens > most / (heads * (d / 16)) || B * pages > most / heads)
+    return DKV_ERR_UNSUPPORTED;
+  dkv::AppendArgs a{};
+  a.k = {static_cast<const uint16_t*>(p->k), p->k_stride_b, p->k_stride_t, p->k_stride_h};
+  a.v = {static_cast<const uint16_t*>(p->v), p->v_stride_b, p->v_stride_t, p->v_stride_h};
+  if (queries) {
+    a.q = {static_cast<const uint16_t*>(p->q), p->q_stride_b, p->q_stride_t, p->q_stride_h};
+    a.q_out = static_cast<uint16_t*>(p->q_out);
+    a.o_sb = p->o_stride_b;
+    a.o_st = p->o_stride_t;
+    a.o_sh = p->o_stride_h;
+  }
+  a.B = p->batch;
+  a.T = p->new_tokens;
+  a.Hq = p->num_q_heads;
+  a.Hkv = p->num_kv_heads;
+  a.N = p->seq_len;
+  a.pages = static_cast<int>(pages);
+  a.r = p->rotary_dim;
+  a.rope_len = p->rope_len;
+  a.cos = p->cos;
+  a.sin = p->sin;
+  a.lens = p->seq_lens;
+  a.news = p->new_lens;
+  a.K = {const_cast<void*>(K->data), K->stride_b, K->stride_h, const_cast<float*>(K->scale),
+         K->sstride_b, K->sstride_h};
+  a.V = {const_cast<void*>(V->data), V->stride_b, V->stride_h, const_cast<float*>(V->scale),
+         V->sstride_b, V->sstride_h};
+  if (is_paged(K)) {
+    a.bt = K->block_table;
+    a.bts = K->block_table_stride;
+    a.nblocks = K->num_blocks;
+  }
+  // code * 2^e is exact in the cache's type from its smallest subnormal, 2^-9 *
+  // 2^e, to its largest, 448 * 2^e (bf16: normal values only)
+  const bool f16 = K->dtype == DKV_FP16;
+  a.e_lo = f16 ? -15 : -117;
+  a.e_hi = f16 ? 7 : 119;
+  a.status = static_cast<uint32_t*>(workspace);
+  return cuda_status(dkv::launch_append(p->head_dim, f16, is_fp8(K), p->interleaved != 0, a,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
 dkv_status dkv_read_device_status(void* workspace, void* stream) {
   if (workspace == nullptr) return DKV_ERR_NULL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -909,6 +1120,14 @@ dkv_status dkv_attn_ctas_per_sm(int32_t head_dim, int32_t dtype, int32_t format,
                                 int32_t* ctas_per_sm) {
   if (ctas_per_sm == nullptr) return DKV_ERR_NULL;
   if (head_dim != 64 && head_dim != 128) return DKV_ERR_UNSUPPORTED;
+  if (format == DKV_KV_FP8 || format == DKV_KV_FP8_PAGED) {
+    if (dtype != DKV_BF16 && dtype != DKV_FP16) return DKV_ERR_UNSUPPORTED;
+    int m = 0;
+    if (dkv::attn_fp8_ctas_per_sm(head_dim, dtype == DKV_FP16, sparse != 0, &m) != cudaSuccess)
+      return DKV_ERR_CUDA;
+    *ctas_per_sm = m;
+    return DKV_OK;
+  }
   if (format == DKV_KV_DENSE ? (dtype != DKV_BF16 && dtype != DKV_FP16)
                              : (format != DKV_KV_Q4G64 || dtype != DKV_FP16))
     return DKV_ERR_UNSUPPORTED;

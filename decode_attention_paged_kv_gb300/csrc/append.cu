@@ -1,0 +1,340 @@
+// append.cu -- appending new tokens' keys and values to a KV cache, with the
+// position rotation of keys and queries applied on the way.
+//
+// Sequence b's n new tokens take the positions p = N_b - n .. N_b - 1.  With a
+// rotary width r, channels (x_a, x_b) of pair i < r / 2 -- (i, i + r/2), or
+// (2 i, 2 i + 1) interleaved -- of a key or query become
+//   y_a = x_a cos(p, i) - x_b sin(p, i),   y_b = x_b cos(p, i) + x_a sin(p, i),
+// each product, sum and difference rounded to fp32, the result once to its
+// 16-bit type (or to e4m3).  Other channels and the values are copied.
+//
+// An 8-bit cache keeps one scale per 16-token block and kv head,
+//   s = 2^e, e = the smallest exponent with amax <= 448 * 2^e,
+// clamped into the range where code * s is exact in the cache's 16-bit type;
+// code = e4m3(y / s), rounded to nearest even, saturated.  A power of two makes
+// y / s exact and raising s later nearly so: older codes of a block whose scale
+// rises are stored again as e4m3(code * s_old / s), which rounds only values
+// that become subnormal.  A block's scale never falls while it holds tokens;
+// its first token sets it anew.
+//
+// Two kernels.  append_token_kernel: d/16 threads a token and head, 16
+// channels (two 16-byte vectors, the two halves of 8 rotation pairs) each;
+// nothing is shared between tokens, so it serves 16-bit caches of any length
+// and the single-token call of an 8-bit cache, where the d/16 threads agree on
+// the scale by shuffles.  append_block_kernel: one CTA of d threads per touched
+// block and head of an 8-bit cache, a thread per token and 16 channels; the
+// block's amax is reduced through shared memory while the values wait in
+// registers, so they are read once.  Both are bound by memory traffic (long
+// calls) or by the latency of the dependent loads length -> block table ->
+// scale (single tokens).
+
+#include "dkv_device.cuh"
+#include "dkv_kernels.h"
+
+namespace dkv {
+namespace {
+
+constexpr int kTokenThreads = 256;
+
+// Sequence b's new tokens: positions [start, start + n).  Lengths that do not
+// fit the cache, the table of angles or the rows given leave the sequence
+// alone and are reported as a failed check.
+struct NewTokens {
+  int start, n;
+};
+__device__ __forceinline__ NewTokens new_tokens(const AppendArgs& a, int b) {
+  const int len = a.lens != nullptr ? a.lens[b] : a.N;
+  int n = a.news != nullptr ? a.news[b] : a.T;
+  if (len <= 0 || n == 0) return {0, 0};  // an unused batch entry, or nothing new
+  if (n < 0 || n > a.T || n > len || len > a.N || (a.r > 0 && len > a.rope_len)) {
+    set_status(a.status, kStatusCheck);
+    return {0, 0};
+  }
+  return {len - n, n};
+}
+
+// The 16 channels of a thread: 8 from c1 on and 8 from c2 on.
+struct Chunks {
+  int c1, c2;
+};
+template <bool IL>
+__device__ __forceinline__ Chunks chunks_of(int j, int r, bool rotated) {
+  if (!IL && rotated) return {8 * j, r / 2 + 8 * j};
+  return {16 * j, 16 * j + 8};
+}
+
+template <bool F16>
+__device__ __forceinline__ void load16(const uint16_t* row, Chunks c, float (&x)[16]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(row + c.c1);
+  const uint4 w = *reinterpret_cast<const uint4*>(row + c.c2);
+  const uint32_t v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = lo16<F16>(v[i]);
+    x[2 * i + 1] = hi16<F16>(v[i]);
+  }
+}
+
+template <bool F16>
+__device__ __forceinline__ void store16(uint16_t* row, Chunks c, const float (&x)[16]) {
+  uint32_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = pack2<F16>(x[2 * i], x[2 * i + 1]);
+  *reinterpret_cast<uint4*>(row + c.c1) = make_uint4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<uint4*>(row + c.c2) = make_uint4(v[4], v[5], v[6], v[7]);
+}
+
+// Rotate the 8 pairs of slot j at position pos.  (Intrinsics: no contraction
+// into fused multiply-adds, so a step has one result whatever the compiler.)
+template <bool IL>
+__device__ __forceinline__ void rotate16(const AppendArgs& a, int pos, int j, float (&x)[16]) {
+  const int64_t at = static_cast<int64_t>(pos) * (a.r / 2) + 8 * j;
+  float c[8], s[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(a.cos + at + i));
+    const float4 w = __ldg(reinterpret_cast<const float4*>(a.sin + at + i));
+    c[i] = u.x, c[i + 1] = u.y, c[i + 2] = u.z, c[i + 3] = u.w;
+    s[i] = w.x, s[i + 1] = w.y, s[i + 2] = w.z, s[i + 3] = w.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float& p = x[IL ? 2 * i : i];
+    float& q = x[IL ? 2 * i + 1 : 8 + i];
+    const float u = p, w = q;
+    p = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(w, s[i]));
+    q = __fadd_rn(__fmul_rn(w, c[i]), __fmul_rn(u, s[i]));
+  }
+}
+
+// The scale a block needs for values of magnitude up to amax (its bits).
+__device__ __forceinline__ float scale_for(uint32_t amax_bits, int e_lo, int e_hi) {
+  // amax = 2^k * f: 448 = 1.75 * 2^8, so e = k - 8, or k - 7 when f > 1.75
+  const int k = static_cast<int>(amax_bits >> 23) - 127;
+  const int e = k - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __int_as_float((127 + min(max(e, e_lo), e_hi)) << 23);
+}
+
+// Four values as e4m3 codes (nearest even, saturated), the first in the low byte.
+__device__ __forceinline__ uint32_t to_e4m3x4(float x0, float x1, float x2, float x3) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x1), "f"(x0));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
+  return make_float2(lo16<true>(h), hi16<true>(h));
+}
+
+// x / s: for a power of two the exact product with 1 / s.
+struct Divider {
+  float s, inv;
+  bool pow2;
+  __device__ __forceinline__ explicit Divider(float s_) : s(s_) {
+    pow2 = (__float_as_uint(s_) & 0x7fffffu) == 0u;
+    inv = __fdiv_rn(1.f, s_);
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    return pow2 ? __fmul_rn(x, inv) : __fdiv_rn(x, s);
+  }
+};
+
+// The thread's 16 channels as codes.
+__device__ __forceinline__ void store_codes(uint8_t* row, Chunks c, const Divider& by,
+                                            const float (&x)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float* y = x + 8 * h;
+    *reinterpret_cast<uint2*>(row + (h ? c.c2 : c.c1)) =
+        make_uint2(to_e4m3x4(by(y[0]), by(y[1]), by(y[2]), by(y[3])),
+                   to_e4m3x4(by(y[4]), by(y[5]), by(y[6]), by(y[7])));
+  }
+}
+
+// Codes stored under the scale s_old, stored again under by.s.
+__device__ __forceinline__ void rescale_codes(uint8_t* row, Chunks c, float s_old,
+                                              const Divider& by) {
+  float x[16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint2 w = *reinterpret_cast<const uint2*>(row + (h ? c.c2 : c.c1));
+    const uint32_t v[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = from_e4m3x2(v[i]);
+      x[8 * h + 2 * i] = __fmul_rn(f.x, s_old);
+      x[8 * h + 2 * i + 1] = __fmul_rn(f.y, s_old);
+    }
+  }
+  store_codes(row, c, by, x);
+}
+
+__device__ __forceinline__ uint32_t amax_bits(const float (&x)[16]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
+  return __float_as_uint(m);
+}
+
+// Where page `page` of sequence b lies in a cache: the index that its block
+// stride multiplies and the element offset of its first token within.  -1 in
+// `blk`: the table names no block of the pool (reported; nothing is written).
+struct PageAt {
+  int64_t blk, tok;
+};
+__device__ __forceinline__ PageAt page_at(const AppendArgs& a, int b, int page, int d) {
+  if (a.bt == nullptr) return {b, static_cast<int64_t>(page) * kPage * d};
+  const int blk = a.bt[b * a.bts + page];
+  if (blk < 0 || blk >= a.nblocks) {
+    set_status(a.status, kStatusCheck);
+    return {-1, 0};
+  }
+  return {blk, 0};
+}
+__device__ __forceinline__ float* scale_at(const AppendArgs& a, const AppendCache& c, PageAt at,
+                                           int page, int h) {
+  return c.scale + at.blk * c.ssb + h * c.ssh + (a.bt == nullptr ? page : 0);
+}
+
+template <int D, bool F16, bool EIGHT, bool IL>
+__global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const AppendArgs a) {
+  constexpr int L = D / 16;  // threads of a token and head
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t idx = blockIdx.x * kTokenThreads + threadIdx.x;
+  const int b = blockIdx.y;
+  const int j = idx % L;
+  const uint32_t heads = 2 * a.Hkv + a.Hq;
+  const uint32_t row = idx / L;
+  const int t = static_cast<int>(row / heads);
+  const int hx = static_cast<int>(row % heads);
+  const NewTokens nt = new_tokens(a, b);
+  const bool on = t < nt.n;  // (8-bit: every lane stays for the shuffles)
+  if (!EIGHT && !on) return;
+  const int pos = nt.start + t;
+  const bool is_q = hx >= 2 * a.Hkv, is_v = !is_q && hx >= a.Hkv;
+  const int h = is_q ? hx - 2 * a.Hkv : (is_v ? hx - a.Hkv : hx);
+  const bool rotated = !is_v && 16 * j < a.r;
+  const Chunks c = chunks_of<IL>(j, a.r, rotated);
+  float x[16] = {};
+  if (on) {
+    const AppendRows& src = is_q ? a.q : (is_v ? a.v : a.k);
+    load16<F16>(src.p + b * src.sb + t * src.st + h * src.sh, c, x);
+    if (rotated) rotate16<IL>(a, pos, j, x);
+    if (is_q) store16<F16>(a.q_out + b * a.o_sb + t * a.o_st + h * a.o_sh, c, x);
+  }
+  const AppendCache& cache = is_v ? a.V : a.K;
+  const int page = pos / kPage, slot = pos % kPage;
+  PageAt at{-1, 0};
+  if (on && !is_q) at = page_at(a, b, page, D);
+  if constexpr (!EIGHT) {
+    if (at.blk >= 0)
+      store16<F16>(static_cast<uint16_t*>(cache.p) + at.blk * cache.sb + h * cache.sh + at.tok +
+                       slot * D,
+                   c, x);
+  } else {
+    uint32_t m = amax_bits(x);
+#pragma unroll
+    for (int o = 1; o < L; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool put = at.blk >= 0;  // (the L lanes of a row agree on it)
+    float* sp = put ? scale_at(a, cache, at, page, h) : nullptr;
+    const float old = put && slot > 0 ? *sp : 0.f;
+    __syncwarp();  // every lane of the row has read the old scale
+    if (put) {
+      const float s = fmaxf(scale_for(m, a.e_lo, a.e_hi), old);
+      const Divider by(s);
+      uint8_t* rows = static_cast<uint8_t*>(cache.p) + at.blk * cache.sb + h * cache.sh + at.tok;
+      if (s > old)
+        for (int i = 0; i < slot; ++i) rescale_codes(rows + i * D, c, old, by);
+      store_codes(rows + slot * D, c, by, x);
+      if (j == 0 && s != old) *sp = s;
+    }
+  }
+}
+
+template <int D, bool F16, bool IL>
+__global__ void __launch_bounds__(D) append_block_kernel(const AppendArgs a) {
+  constexpr int L = D / 16;
+  __shared__ uint32_t warp_amax[D / 32];
+  griddep_launch_dependents();
+  griddep_wait();
+  // (sequence, touched page, head), heads fastest: a row's heads lie together
+  const uint32_t heads = 2 * a.Hkv + a.Hq;
+  const int hx = static_cast<int>(blockIdx.x % heads);
+  const int y = static_cast<int>(blockIdx.x / heads % static_cast<uint32_t>(a.pages));
+  const int b = static_cast<int>(blockIdx.x / heads / static_cast<uint32_t>(a.pages));
+  const NewTokens nt = new_tokens(a, b);
+  const int page = nt.start / kPage + y;
+  if (nt.n == 0 || page * kPage >= nt.start + nt.n) return;  // no token of this page
+  const int j = threadIdx.x % L, i = threadIdx.x / L;
+  const int pos = page * kPage + i, t = pos - nt.start;
+  const bool on = t >= 0 && t < nt.n;
+  const bool is_q = hx >= 2 * a.Hkv, is_v = !is_q && hx >= a.Hkv;
+  const int h = is_q ? hx - 2 * a.Hkv : (is_v ? hx - a.Hkv : hx);
+  const bool rotated = !is_v && 16 * j < a.r;
+  const Chunks c = chunks_of<IL>(j, a.r, rotated);
+  const AppendRows& src = is_q ? a.q : (is_v ? a.v : a.k);
+  float x[16] = {};
+  if (on) {
+    load16<F16>(src.p + b * src.sb + t * src.st + h * src.sh, c, x);
+    if (rotated) rotate16<IL>(a, pos, j, x);
+  }
+  if (is_q) {
+    if (on) store16<F16>(a.q_out + b * a.o_sb + t * a.o_st + h * a.o_sh, c, x);
+    return;
+  }
+  const AppendCache& cache = is_v ? a.V : a.K;
+  const PageAt at = page_at(a, b, page, D);
+  if (at.blk < 0) return;
+  float* sp = scale_at(a, cache, at, page, h);
+  const int kept = max(0, nt.start - page * kPage);  // tokens the block held before
+  const float old = kept > 0 ? *sp : 0.f;
+  const uint32_t wm = __reduce_max_sync(0xffffffffu, amax_bits(x));
+  if (threadIdx.x % 32 == 0) warp_amax[threadIdx.x / 32] = wm;
+  __syncthreads();  // (every thread has read the old scale)
+  uint32_t m = warp_amax[0];
+#pragma unroll
+  for (int w = 1; w < D / 32; ++w) m = max(m, warp_amax[w]);
+  const float s = fmaxf(scale_for(m, a.e_lo, a.e_hi), old);
+  const Divider by(s);
+  uint8_t* row = static_cast<uint8_t*>(cache.p) + at.blk * cache.sb + h * cache.sh + at.tok + i * D;
+  if (on)
+    store_codes(row, c, by, x);
+  else if (i < kept && s > old)
+    rescale_codes(row, c, old, by);
+  if (threadIdx.x == 0 && s != old) *sp = s;
+}
+
+template <int D, bool F16, bool IL>
+cudaError_t launch_t(bool eight, const AppendArgs& a, cudaStream_t s) {
+  const uint32_t heads = 2 * a.Hkv + a.Hq;
+  if (eight && a.T > 1)
+    return launch_pdl(append_block_kernel<D, F16, IL>,
+                      dim3(static_cast<uint32_t>(a.B) * a.pages * heads), dim3(D), 0, s, a);
+  const dim3 grid(static_cast<unsigned>(
+                      ceil_div(static_cast<int64_t>(a.T) * heads * (D / 16), kTokenThreads)),
+                  a.B);
+  return eight ? launch_pdl(append_token_kernel<D, F16, true, IL>, grid, dim3(kTokenThreads), 0, s, a)
+               : launch_pdl(append_token_kernel<D, F16, false, IL>, grid, dim3(kTokenThreads), 0, s,
+                            a);
+}
+
+}  // namespace
+
+cudaError_t launch_append(int d, bool f16, bool eight, bool interleaved, const AppendArgs& a,
+                          cudaStream_t s) {
+  if (d == 128) {
+    if (f16) return interleaved ? launch_t<128, true, true>(eight, a, s)
+                                : launch_t<128, true, false>(eight, a, s);
+    return interleaved ? launch_t<128, false, true>(eight, a, s)
+                       : launch_t<128, false, false>(eight, a, s);
+  }
+  if (f16) return interleaved ? launch_t<64, true, true>(eight, a, s)
+                              : launch_t<64, true, false>(eight, a, s);
+  return interleaved ? launch_t<64, false, true>(eight, a, s)
+                     : launch_t<64, false, false>(eight, a, s);
+}
+
+}  // namespace dkv

@@ -1186,6 +1186,11 @@ __global__ void __launch_bounds__(1024) merge_kernel(const MergeArgs m) {
   griddep_launch_dependents();
   griddep_wait();  // the attention grid has finished writing its partials
   const int row = blockIdx.x, stride = m.n_chunks;
+  if (m.zero_empty && m.lens != nullptr && m.lens[row / m.Hq] <= 0) {  // no token: a zero row
+    if (threadIdx.x < D)
+      store_out(m.out, m.out_dtype, row / m.Hq * m.o_sb + row % m.Hq * m.o_sh + threadIdx.x, 0.f);
+    return;
+  }
   int nc = stride;  // chunks holding pages
   if (m.union_count != nullptr) {
     const int b = row / m.Hq, h = row % m.Hq;
@@ -1259,6 +1264,10 @@ __global__ void __launch_bounds__(kSmallMergeThreads) merge_small_kernel(const M
   if (row >= rows) return;
   const int stride = m.n_chunks;
   const int b = row / m.Hq, h = row % m.Hq;
+  if (m.zero_empty && m.lens != nullptr && m.lens[b] <= 0) {  // no token: a zero row
+    store_out(m.out, m.out_dtype, b * m.o_sb + h * m.o_sh + c, 0.f);
+    return;
+  }
   const int count = m.union_count != nullptr
                         ? __ldcg(m.union_count + b * m.Hkv + h / m.G)
                         : (m.lens != nullptr

@@ -51,6 +51,20 @@ inline int select_pages_per_chunk(int64_t union_max, int d) {
   const int64_t need = ceil_div(union_max, kMaxChunks);
   return static_cast<int>(need > base ? need : base);
 }
+// Pages of an 8-bit cache a work item streams, of `pages` at most per (batch, kv
+// head): 256 KiB of codes, less where the batch is small, so that 8 kv heads
+// still fill two CTAs on each of 152 multiprocessors.  Depends on the pages, d
+// and the batch only, so here too one kv head at a time gives bitwise the
+// all-heads result.  A multiple of 8: two pages a stage for each of four warps.
+inline int fp8_pages_per_chunk(int64_t pages, int d, int batch) {
+  const int64_t base = d == 128 ? 64 : 128;
+  int64_t want = ceil_div(2 * 152 * 2, 8 * static_cast<int64_t>(batch));
+  want = want > 32 ? 32 : want;  // (the single-pass merge)
+  int64_t per = ceil_div(ceil_div(pages, want), 8) * 8;
+  if (per > base) per = base;
+  const int64_t need = ceil_div(ceil_div(pages, kMaxChunks), 8) * 8;
+  return static_cast<int>(need > per ? need : per);
+}
 // The per-(batch, kv head) selection kernel holds a head's P scores in a
 // warp's registers, 64 a lane at most; longer contexts take the separate
 // score / top-K / union kernels.
@@ -75,6 +89,14 @@ struct Q4View {
   int64_t gsb, gsh;            // gmin / gmax strides, elements
 };
 
+// The block scales of one K or V cache in the 8-bit format: of batch entry b (a
+// dense cache) or pool block b, kv head h, at b * sb + h * sh, plus the page of a
+// dense cache.
+struct Fp8View {
+  const float* scale;
+  int64_t sb, sh;              // elements
+};
+
 struct AttnArgs {
   const void* q;
   int64_t q_sb, q_sh;          // elements
@@ -85,8 +107,9 @@ struct AttnArgs {
   int n_items;                 // B * Hkv * n_chunks work items
   float* part_ml;              // [B, Hq, n_chunks, 2]  (max in log2 units, sum)
   float* part_o;               // [B, Hq, n_chunks, d]  unnormalised
-  // sparse 4-bit path with n_chunks == 1: each item is its rows' whole result,
-  // written normalised to out (strides in elements), no partials, no merge
+  // sparse 4-bit path and 8-bit caches with n_chunks == 1: each item is its
+  // rows' whole result, written normalised to out (strides in elements), no
+  // partials, no merge
   void* out;
   int out_dtype;               // 0 bf16, 1 fp16, 2 fp32
   int64_t o_sb, o_sh;
@@ -107,6 +130,7 @@ struct AttnArgs {
   // and waits unit by unit; nullptr: it waits for the whole previous grid.
   const uint32_t* unit_ready;  // [B * Hkv] or nullptr
   Q4View k4, v4;               // 4-bit caches (the dense path uses the tensor maps)
+  Fp8View k8, v8;              // 8-bit caches (their codes come through the tensor maps)
   // paged caches: page j of batch entry b is pool block bt[b * bts + j] (the
   // tensor maps then view the pool); nullptr for a [B, Hkv, N, d] cache
   const int32_t* bt;
@@ -143,6 +167,7 @@ struct MergeArgs {
   // exact path with per-sequence lengths: ceil(ceil(N_b / 16) / ppc) chunks per row
   const int32_t* lens;
   int N;
+  int zero_empty;              // 1: a length of 0 gives a zero row (8-bit caches)
 };
 
 struct ScoreArgs {
@@ -265,6 +290,52 @@ struct MetaArgs {
   int last_only;               // 1: only the page holding each sequence's last token
 };
 
+// Metadata of an 8-bit cache, in the cache's 16-bit type.
+struct MetaFp8Args {
+  const uint8_t* codes;
+  int64_t sb, sh;              // code strides (batch entry or pool block, kv head), bytes
+  Fp8View scale;
+  int B, Hkv, N, P, S;         // as MetaArgs
+  void* meta_min;
+  void* meta_max;
+  const int32_t* bt;
+  int64_t bts;
+  int nblocks;
+  const int32_t* lens;
+  int last_only;
+};
+
+// New tokens' rows [B, T, heads, d] (strides in elements).
+struct AppendRows {
+  const uint16_t* p;
+  int64_t sb, st, sh;
+};
+// A cache that is written: values or codes, and an 8-bit cache's scales.
+struct AppendCache {
+  void* p;
+  int64_t sb, sh;              // batch entry or pool block, kv head: elements or bytes
+  float* scale;
+  int64_t ssb, ssh;
+};
+struct AppendArgs {
+  AppendRows k, v, q;
+  uint16_t* q_out;
+  int64_t o_sb, o_st, o_sh;
+  int B, T, Hq, Hkv, N;        // Hq = 0: no queries; N: tokens a sequence's cache holds
+  int pages;                   // pages that T tokens of a sequence can touch
+  int r, rope_len;             // rotary width (0: no rotation), rows of cos / sin
+  const float* cos;            // [rope_len, r / 2]
+  const float* sin;
+  const int32_t* lens;         // lengths with the new tokens [B], or nullptr (all N)
+  const int32_t* news;         // new tokens of each sequence [B], or nullptr (all T)
+  AppendCache K, V;
+  const int32_t* bt;           // paged caches: block table, row stride bts
+  int64_t bts;
+  int nblocks;
+  int e_lo, e_hi;              // exponents a block scale may take
+  uint32_t* status;            // nullptr: errors are not reported
+};
+
 // Launch `kern` with programmatic stream serialisation, so it may begin while
 // the previous kernel in the stream drains (every kernel here calls
 // griddep_wait() before touching data a predecessor could have written).
@@ -288,6 +359,10 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 cudaError_t launch_attn(int d, bool f16, bool sparse, const AttnArgs& a, const CUtensorMap& mk,
                         const CUtensorMap& mv, int num_sms, cudaStream_t s);
 cudaError_t launch_attn_q4(int d, bool sparse, const AttnArgs& a, int num_sms, cudaStream_t s);
+// mk / mv: maps over the codes, box {d bytes, 16 tokens, 1, 1, 1}, d-byte swizzle.
+cudaError_t launch_attn_fp8(int d, bool f16, bool sparse, const AttnArgs& a, const CUtensorMap& mk,
+                            const CUtensorMap& mv, int num_sms, cudaStream_t s);
+cudaError_t attn_fp8_ctas_per_sm(int d, bool f16, bool sparse, int* out);
 // Resident attention CTAs per SM for one instantiation (1 .. kAttnCtasPerSm).
 cudaError_t attn_ctas_per_sm(int d, bool f16, bool sparse, bool q4, int* out);
 cudaError_t launch_merge(int d, const MergeArgs& m, int rows, cudaStream_t s);
@@ -305,6 +380,9 @@ cudaError_t launch_unit_select(int d, bool f16, bool m8, const UnitSelectArgs& a
                                const CUtensorMap& mmx, const CUtensorMap& mmn, cudaStream_t s);
 
 cudaError_t launch_meta(bool q4, bool f16, const MetaArgs& a, cudaStream_t s);
+cudaError_t launch_meta_fp8(int d, bool f16, const MetaFp8Args& a, cudaStream_t s);
+cudaError_t launch_append(int d, bool f16, bool eight, bool interleaved, const AppendArgs& a,
+                          cudaStream_t s);
 cudaError_t launch_quant4(int64_t rows, int d, const void* x, void* codes, void* gmin,
                           void* gmax, cudaStream_t s);
 cudaError_t launch_dequant4(int64_t rows, int d, const void* codes, const void* gmin,

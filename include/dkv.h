@@ -29,6 +29,11 @@
  *                           "FlexGen: High-Throughput Generative Inference of
  *                           Large Language Models with a Single GPU" (解读),
  *                           4-bit 近似方法.
+ *   dkv_kv_append           new tokens' keys and values into a cache (16-bit or
+ *                           8-bit), with the position rotation of keys and
+ *                           queries applied on the way.  The pages' decode
+ *                           steps start from a cache that already holds the
+ *                           step's token; this is the call that puts it there.
  *
  * Conventions shared by every entry point:
  *   - Every data pointer is a DEVICE pointer owned by the caller, 16-byte
@@ -60,8 +65,9 @@
  *   - Supported: d in {64, 128}; S in {4, 8, 16, 32, 64} (the page of the metadata
  *     and of selection; the cache itself is read in pages of 16 tokens, and a
  *     paged cache's blocks hold 16 tokens); Hq % Hkv == 0 and Hq / Hkv <= 8;
- *     1 <= N < 2^31; bf16 or fp16 dense caches (q in the same dtype), or the
- *     4-bit format with fp16 q.  A ragged last page is masked.
+ *     1 <= N < 2^31; bf16 or fp16 dense caches (q in the same dtype), the
+ *     4-bit format with fp16 q, or the 8-bit format with q in the cache's
+ *     declared 16-bit dtype.  A ragged last page is masked.
  */
 #ifndef DKV_H_
 #define DKV_H_
@@ -95,7 +101,7 @@ typedef enum dkv_kv_format {
   DKV_KV_DENSE = 0, /* data: [B, Hkv, N, d] elements of `dtype` (bf16 or fp16) */
   DKV_KV_Q4G64 = 1, /* data: codes [B, Hkv, N, d/2] bytes, channel 2i in the low
                        nibble of byte i; gmin / gmax: [B, Hkv, N, d/64] fp16 */
-  DKV_KV_PAGED = 2  /* a pool of pages (blocks) of S = 16 tokens, `dtype` bf16 or
+  DKV_KV_PAGED = 2, /* a pool of pages (blocks) of S = 16 tokens, `dtype` bf16 or
                        fp16: block n of kv head h starts at data + n * stride_b +
                        h * stride_h (elements), token stride d.  block_table
                        [B, P] int32 (row stride block_table_stride, at least
@@ -109,23 +115,44 @@ typedef enum dkv_kv_format {
                        last page may hold anything past N: it is never used.
                        K and V of one call share the table.  ("TinyServe"
                        结构化内存布局: the cache as pages of S tokens.) */
+  DKV_KV_FP8 = 3,   /* 8 bits a channel: data: [B, Hkv, N, d] e4m3 codes, strides
+                       in bytes (multiples of 16), token stride d; scale:
+                       [B, Hkv, P16] fp32, P16 = ceil(N / 16), one per block of
+                       16 tokens and kv head (sstride_b, sstride_h in elements,
+                       block stride 1).  A value is code * scale; scales are
+                       >= 0 (one below 2^-126 counts as 0).  dkv_kv_append
+                       writes powers of two, 2^e with e in [-117, 119] (dtype
+                       bf16) or [-15, 7] (fp16: values above 57344 saturate),
+                       whose values are exact in `dtype`.  `dtype` is the type
+                       of q and of the page metadata.  No page defines this
+                       format; it is the plainest 8-bit form of a paged cache. */
+  DKV_KV_FP8_PAGED = 4 /* the same in a pool of 16-token blocks: block n of kv
+                       head h starts at data + n * stride_b + h * stride_h
+                       (bytes), its scale is scale[n * sstride_b + h *
+                       sstride_h]; block_table as for DKV_KV_PAGED. */
+                    /* Both 8-bit formats, with per-sequence lengths: N_b <= 0 is
+                       an empty sequence.  Its out rows are 0 and its metadata is
+                       not written (its `selected` rows are those of length 1);
+                       other formats clamp N_b to 1. */
 } dkv_kv_format;
 
 /* One K or V cache. */
 typedef struct dkv_kv {
   int32_t format;           /* dkv_kv_format */
-  int32_t dtype;            /* DENSE: DKV_BF16 | DKV_FP16.  Q4G64: DKV_FP16 */
+  int32_t dtype;            /* DKV_BF16 | DKV_FP16 (Q4G64: DKV_FP16) */
   const void* data;         /* device pointer, see dkv_kv_format */
   const void* gmin;         /* Q4G64 only (else NULL) */
   const void* gmax;         /* Q4G64 only (else NULL) */
-  int64_t stride_b;         /* of data: elements (DENSE) or bytes (Q4G64 codes) */
-  int64_t stride_h;         /*   token stride is d (DENSE) or d/2 (codes) */
+  int64_t stride_b;         /* of data: elements (DENSE, PAGED) or bytes (codes) */
+  int64_t stride_h;         /*   token stride is d, or d/2 (Q4G64 codes) */
   int64_t gstride_b;        /* of gmin / gmax, in fp16 elements; Q4G64 only, */
   int64_t gstride_h;        /*   multiples of 8 (16 bytes: contiguous bounds need
                                N * d / 64 % 8 == 0); token stride is d/64 */
-  const int32_t* block_table;   /* PAGED only (else NULL): [B, P] block indices */
-  int64_t block_table_stride;   /* PAGED only: elements from one batch row to the next */
-  int32_t num_blocks;           /* PAGED only: blocks in the pool */
+  const int32_t* block_table;   /* PAGED, FP8_PAGED (else NULL): [B, P] block indices */
+  int64_t block_table_stride;   /* paged: elements from one batch row to the next */
+  int32_t num_blocks;           /* paged: blocks in the pool */
+  const float* scale;           /* FP8, FP8_PAGED only: block scales, 4-byte aligned */
+  int64_t sstride_b, sstride_h; /* of scale, in elements */
 } dkv_kv;
 
 /* Problem description shared by the attention and metadata calls. */
@@ -175,8 +202,60 @@ typedef struct dkv_params {
    path; top_k >= 1: the sparse path).  0 if `p` is invalid.  Host only. */
 size_t dkv_workspace_bytes(const dkv_params* p, int32_t top_k);
 
+/* The same for the 8-bit cache formats, whose work is cut finer. */
+size_t dkv_workspace_bytes_fp8(const dkv_params* p, int32_t top_k);
+
+/* New tokens for a cache: sequence b's n_b new tokens take the positions
+   N_b - n_b .. N_b - 1, N_b being its length with them (as every other call of
+   the step takes it).  Key and query pairs are rotated by their position's
+   angles: channels (i, i + r/2), or (2i, 2i + 1) when interleaved, i < r/2,
+     y_a = x_a cos - x_b sin,  y_b = x_b cos + x_a sin
+   (fp32, each operation rounded; then rounded once to the stored type);
+   channels from r on and the values are stored as they are. */
+typedef struct dkv_append {
+  int32_t batch;            /* B in [1, 65535] */
+  int32_t num_q_heads;      /* Hq; 0: no queries */
+  int32_t num_kv_heads;     /* Hkv >= 1 */
+  int32_t head_dim;         /* d in {64, 128} */
+  int32_t seq_len;          /* N: tokens the cache holds per sequence */
+  int32_t new_tokens;       /* T >= 0: rows of k, v, q per sequence */
+  int32_t rotary_dim;       /* r: a multiple of 16 up to d; 0: no rotation */
+  int32_t rope_len;         /* positions in cos / sin */
+  int32_t interleaved;      /* 0: pairs (i, i + r/2); 1: pairs (2i, 2i + 1) */
+  const void *k, *v, *q;    /* [B, T, Hkv | Hkv | Hq, d] in the caches' dtype */
+  void* q_out;              /* [B, T, Hq, d]: the rotated queries; may be q itself */
+  int64_t k_stride_b, k_stride_t, k_stride_h;   /* elements, multiples of 8 */
+  int64_t v_stride_b, v_stride_t, v_stride_h;
+  int64_t q_stride_b, q_stride_t, q_stride_h;
+  int64_t o_stride_b, o_stride_t, o_stride_h;
+  const float *cos, *sin;   /* [rope_len, r/2] contiguous, 16-byte aligned */
+  const int32_t* seq_lens;  /* DEVICE [B]: N_b (NULL: all N) */
+  const int32_t* new_lens;  /* DEVICE [B]: n_b in [0, T] (NULL: all T) */
+} dkv_append;
+
+/* Appends to K and V (one format and dtype: DKV_KV_DENSE, DKV_KV_PAGED,
+   DKV_KV_FP8 or DKV_KV_FP8_PAGED; paged caches share one block table) and writes
+   q_out, in one launch.  Rows t >= n_b of k, v and q are not read, those of
+   q_out not written; nor is any cache slot other than the new tokens' (an 8-bit
+   block whose scale rises has its older tokens' codes stored again under the
+   new scale: e4m3(code * old / new)).  A block takes one scale for all its
+   tokens: the larger of the scale it has (if it held tokens before) and
+   2^e, e the smallest exponent with max |y| <= 448 * 2^e over the new ones.
+   Codes are rounded to nearest even and saturate at +-448; inputs are finite.
+   - N_b <= 0 or n_b = 0: nothing of sequence b is touched.
+   - n_b outside [0, T], n_b > N_b, N_b > N or (rotated) N_b > rope_len: nothing
+     of sequence b is touched; a block-table entry outside [0, num_blocks): no
+     token of that page is written (its queries are).  Both record
+     DKV_ERR_DEVICE_CHECK in the status word of `workspace`
+     (DKV_WORKSPACE_HEADER_BYTES suffice; NULL: not recorded).
+   - A block that two sequences of the batch append to is a race: share only
+     whole blocks of a common prefix. */
+dkv_status dkv_kv_append(const dkv_append* p, const dkv_kv* K, const dkv_kv* V, void* workspace,
+                         void* stream);
+
 /* Page metadata.  meta_min / meta_max: [B, Hkv, P, d] contiguous, in K's dtype
-   (fp16 for a Q4G64 cache, built from the dequantised fp16 keys).  m_j / M_j
+   (fp16 for a Q4G64 cache, built from the dequantised fp16 keys; an 8-bit
+   cache's values rounded outward where its scales are not powers of two).  m_j / M_j
    are exact: minimum and maximum of the stored values (total order, -0 < +0).
    Uses p->batch, num_kv_heads, head_dim, seq_len, page_size. */
 dkv_status dkv_kv_meta_build(const dkv_params* p, const dkv_kv* K, void* meta_min,
@@ -235,7 +314,7 @@ dkv_status dkv_decode_attn_select(const dkv_params* p, const void* q, const dkv_
    - step: 1 for the first step, +1 for each step after (a page counts as
      held when its stamp is step - 1).
    - 16-bit caches only (DKV_KV_DENSE or DKV_KV_PAGED; DKV_ERR_UNSUPPORTED for
-     DKV_KV_Q4G64).  One hot_state serves one call at a time. */
+     the others).  One hot_state serves one call at a time. */
 size_t dkv_hot_state_bytes(const dkv_params* p);
 dkv_status dkv_decode_attn_select_hot(const dkv_params* p, const void* q, const dkv_kv* K,
                                       const dkv_kv* V, const void* meta_min,
