@@ -153,6 +153,8 @@ _lock = threading.Lock()
 def lib() -> ctypes.CDLL:
     """The loaded libdkv.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build_mod.LIB
@@ -214,71 +216,87 @@ def _stream(t: torch.Tensor) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
-def _call(where: str, dev: torch.device, *args) -> None:
-    """One library call on the current stream of `dev`, which is made the
-    current device for it; raises on an error status."""
-    fn = getattr(lib(), where)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, stream)
+def _call(where: str, dev: int, *args) -> None:
+    """One library call on the current stream of CUDA device `dev`, which is
+    made the current device for it; raises on an error status."""
+    if dev < 0:
+        raise ValueError(f"{where} wants CUDA tensors")
+    fn = getattr(_lib or lib(), where)
+    # (the raw stream handle: a Stream object costs more than the launch)
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != DKV_OK:
         raise DkvError(st, where)
 
 
+_DTYPE_CODES = {torch.bfloat16: DKV_BF16, torch.float16: DKV_FP16, torch.float32: DKV_FP32}
+
+
 def _dtype_code(dt: torch.dtype) -> int:
-    if dt == torch.bfloat16:
-        return DKV_BF16
-    if dt == torch.float16:
-        return DKV_FP16
-    if dt == torch.float32:
-        return DKV_FP32
-    raise TypeError(f"unsupported dtype {dt}")
+    code = _DTYPE_CODES.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    return code
+
+
+_FP8 = torch.float8_e4m3fn
+_FP32 = torch.float32
 
 
 def _kv_struct(kv) -> tuple[_KV, int, int, int, int]:
     """(struct, B, Hkv, N, d) for a dense tensor or a cache tuple."""
-    s = _KV()
+    if isinstance(kv, (PagedCache, Fp8PagedCache)):
+        scale = ssb = ssh = 0
+        if isinstance(kv, PagedCache):
+            pool, bt, N = kv
+            fmt, dt = DKV_KV_PAGED, pool.dtype
+            nb, H, S, d = pool.shape
+        else:
+            pool, sc, bt, N, dt = kv
+            fmt = DKV_KV_FP8_PAGED
+            nb, H, S, d = pool.shape
+            if pool.dtype != _FP8 or sc.dtype != _FP32:
+                raise TypeError("Fp8PagedCache wants a float8_e4m3fn pool and float32 scales")
+            if sc.shape != (nb, H) or sc.get_device() != pool.get_device():
+                raise ValueError("scale must be [num_blocks, Hkv]")
+            scale = sc.data_ptr()
+            ssb, ssh = sc.stride()
+        sb, sh, st, one = pool.stride()
+        if S != PAGE_SIZE or one != 1 or st != d:
+            raise ValueError("pool must be [num_blocks, Hkv, 16, d] with token stride d")
+        if bt.dtype != torch.int32 or bt.dim() != 2:
+            raise ValueError("block_table must be int32 [B, P] with unit column stride")
+        bts, one = bt.stride()
+        B, cols = bt.shape
+        if one != 1:
+            raise ValueError("block_table must be int32 [B, P] with unit column stride")
+        if bt.get_device() != pool.get_device():
+            raise ValueError("block_table must be on the pool's device")
+        N = int(N)
+        if cols < (N + PAGE_SIZE - 1) // PAGE_SIZE:
+            raise ValueError("block_table has fewer than ceil(seq_len / 16) columns")
+        return (_KV(fmt, _dtype_code(dt), pool.data_ptr(), None, None, sb, sh, 0, 0,
+                    bt.data_ptr(), bts, nb, scale, ssb, ssh), B, H, N, d)
     if isinstance(kv, Fp8Cache):
         c, sc, dt = kv
         B, H, N, d = c.shape
-        if c.dtype != torch.float8_e4m3fn or sc.dtype != torch.float32:
+        sb, sh, st, one = c.stride()
+        if c.dtype != _FP8 or sc.dtype != _FP32:
             raise TypeError("Fp8Cache wants float8_e4m3fn codes and float32 scales")
-        if c.stride(3) != 1 or c.stride(2) != d:
+        if one != 1 or st != d:
             raise ValueError("codes must have token stride d and channel stride 1")
-        if (tuple(sc.shape) != (B, H, (N + PAGE_SIZE - 1) // PAGE_SIZE)
-                or (sc.stride(2) != 1 and sc.shape[2] > 1) or sc.device != c.device):
+        P = (N + PAGE_SIZE - 1) // PAGE_SIZE
+        if sc.shape != (B, H, P) or sc.get_device() != c.get_device():
             raise ValueError("scale must be [B, Hkv, ceil(N / 16)] with unit block stride")
-        s.format, s.dtype = DKV_KV_FP8, _dtype_code(dt)
-        s.data, s.stride_b, s.stride_h = c.data_ptr(), c.stride(0), c.stride(1)
-        s.scale, s.sstride_b, s.sstride_h = sc.data_ptr(), sc.stride(0), sc.stride(1)
-        return s, B, H, N, d
-    if isinstance(kv, (PagedCache, Fp8PagedCache)):
-        if isinstance(kv, PagedCache):
-            pool, bt, N = kv
-            s.format, s.dtype = DKV_KV_PAGED, _dtype_code(pool.dtype)
-        else:
-            pool, sc, bt, N, dt = kv
-            if pool.dtype != torch.float8_e4m3fn or sc.dtype != torch.float32:
-                raise TypeError("Fp8PagedCache wants a float8_e4m3fn pool and float32 scales")
-            if tuple(sc.shape) != tuple(pool.shape[:2]) or sc.device != pool.device:
-                raise ValueError("scale must be [num_blocks, Hkv]")
-            s.format, s.dtype = DKV_KV_FP8_PAGED, _dtype_code(dt)
-            s.scale, s.sstride_b, s.sstride_h = sc.data_ptr(), sc.stride(0), sc.stride(1)
-        nb, H, S, d = pool.shape
-        if S != PAGE_SIZE or pool.stride(3) != 1 or pool.stride(2) != d:
-            raise ValueError("pool must be [num_blocks, Hkv, 16, d] with token stride d")
-        if bt.dtype != torch.int32 or bt.dim() != 2 or bt.stride(1) != 1:
-            raise ValueError("block_table must be int32 [B, P] with unit column stride")
-        P = (int(N) + PAGE_SIZE - 1) // PAGE_SIZE
-        if bt.shape[1] < P:
-            raise ValueError("block_table has fewer than ceil(seq_len / 16) columns")
-        s.data = pool.data_ptr()
-        s.stride_b, s.stride_h = pool.stride(0), pool.stride(1)
-        s.block_table, s.block_table_stride, s.num_blocks = bt.data_ptr(), bt.stride(0), nb
-        return s, bt.shape[0], H, int(N), d
+        ssb, ssh, one = sc.stride()
+        if one != 1 and P > 1:
+            raise ValueError("scale must be [B, Hkv, ceil(N / 16)] with unit block stride")
+        return (_KV(DKV_KV_FP8, _dtype_code(dt), c.data_ptr(), None, None, sb, sh, 0, 0, None, 0,
+                    0, sc.data_ptr(), ssb, ssh), B, H, N, d)
+    s = _KV()
     if isinstance(kv, Q4Cache):
         c, gmn, gmx = kv
         B, H, N, half = c.shape
@@ -303,10 +321,13 @@ def _kv_struct(kv) -> tuple[_KV, int, int, int, int]:
     return s, B, H, N, d
 
 
+def _data_of(kv) -> torch.Tensor:
+    """A cache's values or codes."""
+    return kv if isinstance(kv, torch.Tensor) else kv[0]
+
+
 def _device_of(kv) -> torch.device:
-    if isinstance(kv, (Q4Cache, Fp8Cache)):
-        return kv.codes.device
-    return kv.pool.device if isinstance(kv, (PagedCache, Fp8PagedCache)) else kv.device
+    return _data_of(kv).device
 
 
 def _is_fp8(kv) -> bool:
@@ -322,31 +343,39 @@ def _dtype_of(kv) -> torch.dtype:
     return kv.dtype
 
 
-def _check_query(q: torch.Tensor, K) -> None:
-    if _is_fp8(K) and (q.dtype != K.dtype or q.device != _device_of(K)):
-        raise ValueError(f"q must be {K.dtype} on the cache's device")
+def _check_fp8(q: torch.Tensor, K, V, *others: Optional[torch.Tensor]) -> None:
+    """The 8-bit calls' tensors lie on one device, q in the cache's type."""
+    if q.dtype != K.dtype:
+        raise ValueError(f"q must be {K.dtype}")
+    dev = q.get_device()
+    if dev < 0 or K[0].get_device() != dev or _data_of(V).get_device() != dev or any(
+            t is not None and t.get_device() != dev for t in others):
+        raise ValueError("q, the caches and the other tensors must be on one CUDA device")
 
 
 def _params(q: Optional[torch.Tensor], B, Hkv, N, d, out: Optional[torch.Tensor],
             scale: Optional[float], flags: int = 0,
             seq_lens: Optional[torch.Tensor] = None) -> _Params:
-    p = _Params()
+    lens = None
     if seq_lens is not None:
-        if (seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (B,) or not seq_lens.is_cuda
+        if (seq_lens.dtype != torch.int32 or seq_lens.shape != (B,) or not seq_lens.is_cuda
                 or not seq_lens.is_contiguous()):
             raise ValueError("seq_lens must be a contiguous int32 CUDA tensor [B]")
-        p.seq_lens = seq_lens.data_ptr()
-    p.batch, p.num_kv_heads, p.head_dim, p.seq_len, p.page_size = B, Hkv, d, N, PAGE_SIZE
-    p.num_q_heads = q.shape[1] if q is not None else Hkv
+        lens = seq_lens.data_ptr()
+    Hq, qsb, qsh, osb, osh = Hkv, 0, 0, 0, 0
     if q is not None:
-        if q.shape[0] != B or q.shape[2] != d or q.stride(2) != 1:
+        qB, Hq, qd = q.shape
+        qsb, qsh, one = q.stride()
+        if qB != B or qd != d or one != 1:
             raise ValueError(f"q shape {tuple(q.shape)} does not match the cache")
-        p.q_stride_b, p.q_stride_h = q.stride(0), q.stride(1)
     if out is not None:
-        p.o_stride_b, p.o_stride_h = out.stride(0), out.stride(1)
-    p.scale = float(scale) if scale is not None else 1.0 / math.sqrt(d)
-    p.flags = flags
-    return p
+        if out.shape != q.shape:
+            raise ValueError(f"out must be {tuple(q.shape)}")
+        osb, osh, one = out.stride()
+        if one != 1:
+            raise ValueError("out must have channel stride 1")
+    return _Params(B, Hq, Hkv, d, N, PAGE_SIZE, qsb, qsh, osb, osh,
+                   1.0 / math.sqrt(d) if scale is None else float(scale), flags, lens)
 
 
 def workspace_bytes(B: int, Hq: int, Hkv: int, d: int, N: int, top_k: int = 0,
@@ -385,7 +414,7 @@ def kv_meta_build(K, page_size: int = PAGE_SIZE, seq_lens: Optional[torch.Tensor
     mx = torch.empty(B, H, P, d, dtype=dt, device=dev)
     p = _params(None, B, H, N, d, None, None, seq_lens=seq_lens)
     p.page_size = page_size
-    _call("dkv_kv_meta_build", dev, ctypes.byref(p), ctypes.byref(ks), mn.data_ptr(),
+    _call("dkv_kv_meta_build", mn.get_device(), ctypes.byref(p), ctypes.byref(ks), mn.data_ptr(),
           mx.data_ptr())
     return mn, mx
 
@@ -402,9 +431,12 @@ def kv_meta_append(K, meta, page_size: int = PAGE_SIZE,
         raise ValueError("meta must be contiguous [B, Hkv, P, d]")
     p = _params(None, B, H, N, d, None, None, seq_lens=seq_lens)
     p.page_size = page_size
-    if _is_fp8(K) and not mn.dtype == mx.dtype == K.dtype:
-        raise ValueError(f"meta of this cache is {K.dtype}")
-    _call("dkv_kv_meta_append", mn.device, ctypes.byref(p), ctypes.byref(ks), mn.data_ptr(),
+    if _is_fp8(K):
+        if not mn.dtype == mx.dtype == K.dtype:
+            raise ValueError(f"meta of this cache is {K.dtype}")
+        if not mn.get_device() == mx.get_device() == K[0].get_device():
+            raise ValueError("meta must be on the cache's device")
+    _call("dkv_kv_meta_append", mn.get_device(), ctypes.byref(p), ctypes.byref(ks), mn.data_ptr(),
           mx.data_ptr())
     return mn, mx
 
@@ -418,17 +450,19 @@ def rope_table(length: int, rotary_dim: int, base: float = 10000.0, device=None)
     return a.cos().float().to(device), a.sin().float().to(device)
 
 
-def _rows(t: torch.Tensor, name: str, shape, dt: torch.dtype, dev: torch.device) -> tuple:
-    if (t.dtype != dt or t.device != dev or t.shape != shape or t.stride(3) != 1):
-        raise ValueError(f"{name} must be {dt} {tuple(shape)} on {dev} with channel stride 1")
-    return t.stride()[:3]
+def _rows(t: torch.Tensor, name: str, shape: tuple, dt: torch.dtype, dev: int) -> tuple:
+    """A rows tensor's address and (batch, token, head) strides."""
+    sb, st, sh, one = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
+    if one != 1 or t.shape != shape or t.dtype != dt or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dt} {tuple(shape)} on cuda:{dev} with channel stride 1")
+    return t.data_ptr(), sb, st, sh
 
 
-def _lengths(t: Optional[torch.Tensor], name: str, B: int, dev: torch.device) -> Optional[int]:
+def _lengths(t: Optional[torch.Tensor], name: str, B: int, dev: int) -> Optional[int]:
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.shape != (B,) or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor [B] on {dev}")
+    if t.dtype != torch.int32 or t.shape != (B,) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [B] on cuda:{dev}")
     return t.data_ptr()
 
 
@@ -455,40 +489,40 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, K, V, seq_lens: Optional[torch.T
     vs, B2, H2, N2, d2 = _kv_struct(V)
     if (B, H, N, d) != (B2, H2, N2, d2):
         raise ValueError("K and V shapes differ")
-    dev, dt = _device_of(K), _dtype_of(K)
-    if dev.type != "cuda" or _device_of(V) != dev:
+    dt = _dtype_of(K)
+    dev = _data_of(K).get_device()
+    if dev < 0 or _data_of(V).get_device() != dev:
         raise ValueError("K and V must be on one CUDA device")
     if k.dim() != 4:
         raise ValueError("k must be [B, T, Hkv, d]")
     T = k.shape[1]
-    a = _Append(B, 0, H, d, N, T)
-    a.k, a.v = k.data_ptr(), v.data_ptr()
-    a.k_stride_b, a.k_stride_t, a.k_stride_h = _rows(k, "k", (B, T, H, d), dt, dev)
-    a.v_stride_b, a.v_stride_t, a.v_stride_h = _rows(v, "v", (B, T, H, d), dt, dev)
+    kp, ksb, kst, ksh = _rows(k, "k", (B, T, H, d), dt, dev)
+    vp, vsb, vst, vsh = _rows(v, "v", (B, T, H, d), dt, dev)
+    Hq = qp = qsb = qst = qsh = op = osb = ost = osh = 0
     if q is not None:
-        shape = (B, T, q.shape[2], d)
-        a.num_q_heads, a.q = shape[2], q.data_ptr()
-        a.q_stride_b, a.q_stride_t, a.q_stride_h = _rows(q, "q", shape, dt, dev)
+        Hq = q.shape[2]
+        qp, qsb, qst, qsh = _rows(q, "q", (B, T, Hq, d), dt, dev)
         if q_out is None:
             # (rows that no token has are left as they are)
-            q_out = torch.empty(shape, dtype=dt, device=dev)
-        a.o_stride_b, a.o_stride_t, a.o_stride_h = _rows(q_out, "q_out", shape, dt, dev)
-        a.q_out = q_out.data_ptr()
+            q_out = torch.empty(B, T, Hq, d, dtype=dt, device=q.device)
+        op, osb, ost, osh = _rows(q_out, "q_out", (B, T, Hq, d), dt, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
+    r = length = cp = sp = 0
     if rope is not None:
         cos, sin = rope
-        if (cos.shape != sin.shape or cos.dim() != 2 or cos.device != dev or sin.device != dev
-                or cos.dtype != torch.float32 or sin.dtype != torch.float32
+        if (cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != _FP32 or sin.dtype != _FP32
+                or cos.get_device() != dev or sin.get_device() != dev
                 or not cos.is_contiguous() or not sin.is_contiguous()):
             raise ValueError("rope must be two contiguous float32 [positions, r / 2] tables")
-        a.rope_len, a.rotary_dim = cos.shape[0], 2 * cos.shape[1]
-        a.interleaved, a.cos, a.sin = int(interleaved), cos.data_ptr(), sin.data_ptr()
-    a.seq_lens = _lengths(seq_lens, "seq_lens", B, dev)
-    a.new_lens = _lengths(new_lens, "new_lens", B, dev)
+        length, r = cos.shape
+        r, cp, sp = 2 * r, cos.data_ptr(), sin.data_ptr()
+    a = _Append(B, Hq, H, d, N, T, r, length, interleaved, kp, vp, qp, op, ksb, kst, ksh, vsb, vst,
+                vsh, qsb, qst, qsh, osb, ost, osh, cp, sp, _lengths(seq_lens, "seq_lens", B, dev),
+                _lengths(new_lens, "new_lens", B, dev))
     ws = None
     if workspace is not None:
-        if (workspace.device != dev
+        if (workspace.get_device() != dev
                 or workspace.numel() * workspace.element_size() < DKV_WORKSPACE_HEADER_BYTES):
             raise ValueError("workspace must hold 256 bytes on the caches' device")
         ws = workspace.data_ptr()
@@ -550,13 +584,14 @@ def decode_attn_full(q, K, V, scale: Optional[float] = None,
     vs, B2, H2, N2, d2 = _kv_struct(V)
     if (B, H, N, d) != (B2, H2, N2, d2):
         raise ValueError("K and V shapes differ")
-    _check_query(q, K)
+    if _is_fp8(K):
+        _check_fp8(q, K, V, out, workspace, seq_lens)
     if out is None:
         out = torch.empty(B, q.shape[1], d, dtype=out_dtype, device=q.device)
     p = _params(q, B, H, N, d, out, scale, flags, seq_lens)
     nbytes = _workspace_need(p, 0, _is_fp8(K))
     ws = _workspace(nbytes, q.device, workspace)
-    _call("dkv_decode_attn_full", q.device, ctypes.byref(p), q.data_ptr(), ctypes.byref(ks),
+    _call("dkv_decode_attn_full", q.get_device(), ctypes.byref(p), q.data_ptr(), ctypes.byref(ks),
           ctypes.byref(vs), out.data_ptr(), _dtype_code(out.dtype), ws.data_ptr(), nbytes)
     return out
 
@@ -581,7 +616,8 @@ def decode_attn_select(q, K, V, meta, top_k: int, scale: Optional[float] = None,
     vs, B2, H2, N2, d2 = _kv_struct(V)
     if (B, H, N, d) != (B2, H2, N2, d2):
         raise ValueError("K and V shapes differ")
-    _check_query(q, K)
+    if _is_fp8(K):
+        _check_fp8(q, K, V, out, workspace, seq_lens, selected, *meta)
     P = (N + page_size - 1) // page_size
     m8 = meta if isinstance(meta, Meta8) else None
     if m8 is not None and hot is not None:
@@ -601,6 +637,9 @@ def decode_attn_select(q, K, V, meta, top_k: int, scale: Optional[float] = None,
     kk = min(int(top_k), P)
     if return_selected and selected is None:
         selected = torch.empty(B, q.shape[1], kk, dtype=torch.int32, device=q.device)
+    if selected is not None and (selected.dtype != torch.int32 or not selected.is_contiguous()
+                                 or selected.shape != (B, q.shape[1], kk)):
+        raise ValueError("selected must be a contiguous int32 [B, Hq, min(top_k, P)]")
     p = _params(q, B, H, N, d, out, scale, flags, seq_lens)
     p.page_size = page_size
     nbytes = _workspace_need(p, int(top_k), _is_fp8(K))
@@ -608,15 +647,15 @@ def decode_attn_select(q, K, V, meta, top_k: int, scale: Optional[float] = None,
     sel_ptr = selected.data_ptr() if selected is not None else None
     out_args = (int(top_k), out.data_ptr(), _dtype_code(out.dtype), sel_ptr)
     if m8 is not None:
-        _call("dkv_decode_attn_select_meta8", q.device, ctypes.byref(p), q.data_ptr(),
+        _call("dkv_decode_attn_select_meta8", q.get_device(), ctypes.byref(p), q.data_ptr(),
               ctypes.byref(ks), ctypes.byref(vs), m8.code_min.data_ptr(), m8.code_max.data_ptr(),
               m8.lo.data_ptr(), m8.step.data_ptr(), *out_args, ws.data_ptr(), nbytes)
     elif hot is not None:
-        _call("dkv_decode_attn_select_hot", q.device, ctypes.byref(p), q.data_ptr(),
+        _call("dkv_decode_attn_select_hot", q.get_device(), ctypes.byref(p), q.data_ptr(),
               ctypes.byref(ks), ctypes.byref(vs), mn.data_ptr(), mx.data_ptr(), *out_args,
               hot.data_ptr(), hot.numel(), int(step), ws.data_ptr(), nbytes)
     else:
-        _call("dkv_decode_attn_select", q.device, ctypes.byref(p), q.data_ptr(),
+        _call("dkv_decode_attn_select", q.get_device(), ctypes.byref(p), q.data_ptr(),
               ctypes.byref(ks), ctypes.byref(vs), mn.data_ptr(), mx.data_ptr(), *out_args,
               ws.data_ptr(), nbytes)
     return (out, selected) if return_selected else out
