@@ -52,13 +52,16 @@ struct ItemDesc {
   int n_pages;  // pages in the item
 };
 
-template <int D>
+template <int D, bool MHA>
 struct Fp8Cfg {
+  // Three CTAs fit an SM where a thread needs at most 128 registers.
+  static constexpr int kCtas = MHA || D == 64 ? 3 : 2;
   static constexpr int kPagesPerStage = 2;
   static constexpr int kTileBytes = kPage * D;      // one tensor's page of codes
   static constexpr int kSlotBytes = 2 * kTileBytes;  // K codes | V codes
   static constexpr int kStageBytes = kPagesPerStage * kSlotBytes;
-  static constexpr int kStages = 96 * 1024 / kStageBytes;  // 12 (d = 128), 24 (d = 64)
+  static constexpr int kRing = MHA ? 64 * 1024 : (D == 64 ? 48 * 1024 : 96 * 1024);
+  static constexpr int kStages = kRing / kStageBytes;
   static constexpr int kSub = kStages / kConsumerWarps;    // stages per consumer warp
   static constexpr int kIssueLanes = kStages < 16 ? kStages : 16;
   static constexpr int kBarOffset = kStages * kStageBytes;
@@ -66,7 +69,8 @@ struct Fp8Cfg {
   static constexpr int kDescOffset = kMetaOffset + kStages * kPagesPerStage * 16;
   static constexpr int kMergeOffset = kDescOffset + 2 * 8;
   static constexpr int kMergeRow = D + 3;  // o[D], max m, sum l, exponent r
-  static constexpr int kListOffset = kMergeOffset + (kConsumerWarps - 1) * 8 * kMergeRow * 4;
+  static constexpr int kListOffset =
+      (kMergeOffset + (kConsumerWarps - 1) * (MHA ? 1 : 8) * kMergeRow * 4 + 15) / 16 * 16;
   static constexpr int kBlockOffset = kListOffset + 16 * kListPages;
   static constexpr int kMiscOffset = kBlockOffset + 4 * kListPages;
   static constexpr int kSmemBytes = 1024 + kMiscOffset + 16;
@@ -74,7 +78,7 @@ struct Fp8Cfg {
   static_assert(kStages % kConsumerWarps == 0, "one sub-ring per consumer warp");
   static_assert(kIssueLanes % kConsumerWarps == 0, "an issuing lane feeds one warp");
   static_assert(kMetaOffset % 16 == 0 && kListOffset % 16 == 0, "16-byte rows");
-  static_assert((kSmemBytes + 1024) * kAttnCtasPerSm <= 228 * 1024, "the CTAs fit an SM");
+  static_assert((kSmemBytes + 1024) * kCtas <= 228 * 1024, "the CTAs fit an SM");
 };
 
 // Shared address of 16-byte chunk c of token t in a tile of 16 rows of D bytes
@@ -128,6 +132,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
+// The largest of a warp's values (no NaN), in every lane: one integer reduction
+// over order-preserving keys (a float's bits, the magnitude bits flipped when
+// negative; the map is its own inverse).
+__device__ __forceinline__ float warp_max(float x) {
+  const int b = __float_as_int(x);
+  const int k = __reduce_max_sync(0xffffffffu, b >= 0 ? b : b ^ 0x7fffffff);
+  return __int_as_float(k >= 0 ? k : k ^ 0x7fffffff);
+}
+
 __device__ __forceinline__ void store_out(void* out, int out_dtype, int64_t off, float v) {
   if (out_dtype == 2) {
     static_cast<float*>(out)[off] = v;
@@ -138,11 +151,11 @@ __device__ __forceinline__ void store_out(void* out, int out_dtype, int64_t off,
   }
 }
 
-template <int D, bool F16, bool SPARSE>
-__global__ void __launch_bounds__(kAttnThreads, D == 64 ? kAttnCtasPerSm : 0)
+template <int D, bool F16, bool SPARSE, bool MHA>
+__global__ void __launch_bounds__(kAttnThreads, MHA || D == 64 ? Fp8Cfg<D, MHA>::kCtas : 0)
     attn_fp8_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv) {
-  using C = Fp8Cfg<D>;
+  using C = Fp8Cfg<D, MHA>;
   constexpr int kQ = C::kPagesPerStage;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -362,7 +375,7 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? kAttnCtasPerSm : 0)
 
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, t4 = lane & 3;
-  const bool head_ok = g < a.G;
+  const bool head_ok = MHA || g < a.G;
   const int mtx = lane >> 3, mrow = lane & 7;
   // Channel of output tile cn, column 2 t4 + e.
   auto out_channel = [t4](int cn, int e) { return 16 * (cn >> 1) + 4 * t4 + 2 * e + (cn & 1); };
@@ -393,7 +406,8 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? kAttnCtasPerSm : 0)
     float qscale = a.scale_log2;
     {
       const uint16_t* qrow = static_cast<const uint16_t*>(a.q) + b * a.q_sb +
-                             static_cast<int64_t>(kvh * a.G + (head_ok ? g : 0)) * a.q_sh + 4 * t4;
+                             static_cast<int64_t>(kvh * a.G + (head_ok && !MHA ? g : 0)) * a.q_sh +
+                             4 * t4;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         const uint2 w = head_ok ? *reinterpret_cast<const uint2*>(qrow + 16 * c) : make_uint2(0u, 0u);
@@ -421,9 +435,10 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? kAttnCtasPerSm : 0)
       }
     }
     float m_run = -INFINITY, mv_run = -INFINITY, r_run = 0.f, l_run = 0.f;
-    float acc[D / 8][4];
+    constexpr int kAccTiles = MHA ? D / 16 : D / 8;
+    float acc[kAccTiles][4];
 #pragma unroll
-    for (int cn = 0; cn < D / 8; ++cn) acc[cn][0] = acc[cn][1] = acc[cn][2] = acc[cn][3] = 0.f;
+    for (int cn = 0; cn < kAccTiles; ++cn) acc[cn][0] = acc[cn][1] = acc[cn][2] = acc[cn][3] = 0.f;
 
     bool aborted = false;
     for (int sq = warp; sq * kQ < n_pages; sq += kConsumerWarps) {
@@ -442,6 +457,111 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? kAttnCtasPerSm : 0)
       const int cnt = min(kQ, n_pages - sq * kQ);
       const uint32_t st = sbase + s * C::kStageBytes;
 
+      if constexpr (MHA) {
+        // S = K q, the query in every column: lane (g, t4) gets the scores of
+        // tokens g (d[0]) and g + 8 (d[2]) of both pages and keeps one of the
+        // 32: token g + 8 (t4 & 1) of page t4 >> 1.
+        float sc[kQ][4];
+#pragma unroll
+        for (int t = 0; t < kQ; ++t) {
+          sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+          if (t < cnt) {
+#pragma unroll
+            for (int c = 0; c < D / 16; c += 2) {
+              uint32_t r[4];  // [chunk c, c + 1][tokens 0-7, 8-15]
+              ldsm_x4(code_addr<D>(st + t * C::kSlotBytes, 8 * (mtx & 1) + mrow, c + (mtx >> 1)),
+                      r[0], r[1], r[2], r[3]);
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                mma16816<true>(sc[t], e4m3_lo2(r[2 * i]), e4m3_lo2(r[2 * i + 1]),
+                               e4m3_hi2(r[2 * i]), e4m3_hi2(r[2 * i + 1]), qa[c + i][0],
+                               qa[c + i][1]);
+            }
+          }
+        }
+        const int4 meta = stage_meta[s * kQ + (t4 >> 1)];
+        const bool mine = (t4 >> 1) < cnt;
+        const int in_page = g + 8 * (t4 & 1);
+        const int sl = SPARSE ? a.sub_log2 : 0;
+        const bool on = !SPARSE || ((meta.y >> (sl ? in_page >> (4 - sl) : 0)) & 1);
+        const bool past = mine && meta.x * kPage + in_page >= Nb;
+        const float raw = (t4 & 2) ? ((t4 & 1) ? sc[1][2] : sc[1][0])
+                                   : ((t4 & 1) ? sc[0][2] : sc[0][0]);
+        const float sv = mine && on && !past ? raw * (qscale * __int_as_float(meta.z)) : -INFINITY;
+        // vs = 2^ve * vf (a scale below 2^-126 counts as 0)
+        const uint32_t vb = static_cast<uint32_t>(meta.w);
+        const int ex = (vb >> 23) & 0xff;
+        const float ve = static_cast<float>(ex - 127);
+        const float vf = ex == 0 ? 0.f : __uint_as_float((vb & 0x807fffffu) | 0x3f800000u);
+        const float m_new = fmaxf(m_run, warp_max(sv));
+        const float mv_new = fmaxf(mv_run, warp_max(sv + ve));
+        const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+        const float r_new = (m_new == -INFINITY) ? 0.f : ceilf(mv_new - m_new);
+        const float x = sv - m_use;
+        const float down = m_run - m_use;
+        l_run = l_run * exp2_fast(down) + exp2_fast(x);  // (this lane's tokens)
+        if (m_new != m_run || r_new != r_run) {          // warp-uniform
+          const float alpha = exp2_fast(down + (r_run - r_new));
+#pragma unroll
+          for (int cn = 0; cn < kAccTiles; ++cn) {
+            acc[cn][0] *= alpha;
+            acc[cn][1] *= alpha;
+            acc[cn][2] *= alpha;
+            acc[cn][3] *= alpha;
+          }
+        }
+        m_run = m_new;
+        mv_run = mv_new;
+        r_run = r_new;
+        if (__any_sync(0xffffffffu, past)) {
+          // Slots past the sequence's end hold anything: zero those V codes
+          // (their weights are 0, but 0 * NaN is not).
+          for (int t = 0; t < cnt; ++t) {
+            const int nt = min(kPage, Nb - stage_meta[s * kQ + t].x * kPage);
+            uint8_t* vt = smem + s * C::kStageBytes + t * C::kSlotBytes + C::kTileBytes;
+            for (int i = lane; i < (kPage - nt) * (D / 16); i += 32)
+              *reinterpret_cast<uint4*>(vt + nt * D + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          // (before the slot goes back to the copy engine)
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        // The weight as two fp16 halves, hi below lo.  O^T += V^T P: B holds the
+        // hi halves in even columns and the lo halves in odd ones (columns 0 and
+        // 1 are read at the end).
+        const float w = exp2_fast(x + (ve - r_run)) * vf;
+        const __half wh = __float2half_rn(w);
+        const __half2 w2 = __halves2half2(wh, __float2half_rn(w - __half2float(wh)));
+        const uint32_t wp = *reinterpret_cast<const uint32_t*>(&w2);
+        const uint32_t pick = (g & 1) ? 0x7632u : 0x5410u;
+#pragma unroll
+        for (int t = 0; t < kQ; ++t) {
+          // tokens 2 t4, 2 t4 + 1 (b0) and 2 t4 + 8, 2 t4 + 9 (b1) of page t
+          const int src = 8 * t4 + 2 * t;
+          const uint32_t w0 = __shfl_sync(0xffffffffu, wp, src);
+          const uint32_t w1 = __shfl_sync(0xffffffffu, wp, src + 4);
+          const uint32_t w8 = __shfl_sync(0xffffffffu, wp, src + 1);
+          const uint32_t w9 = __shfl_sync(0xffffffffu, wp, src + 5);
+          if (t < cnt) {
+            const uint32_t b0 = __byte_perm(w0, w1, pick), b1 = __byte_perm(w8, w9, pick);
+            const uint32_t vt = st + t * C::kSlotBytes + C::kTileBytes;
+#pragma unroll
+            for (int c = 0; c < D / 16; c += 2) {
+              uint32_t r[4];  // [chunk c, c + 1][tokens 0-7, 8-15]
+              ldsm_x4_trans(code_addr<D>(vt, 8 * (mtx & 1) + mrow, c + (mtx >> 1)), r[0], r[1],
+                            r[2], r[3]);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                // rows: the even (g) and the odd (g + 8) channels of the chunk
+                const uint32_t y0 = __byte_perm(r[2 * i], 0u, 0x3120);
+                const uint32_t y8 = __byte_perm(r[2 * i + 1], 0u, 0x3120);
+                mma16816<true>(acc[c + i], e4m3_lo2(y0), e4m3_hi2(y0), e4m3_lo2(y8), e4m3_hi2(y8),
+                               b0, b1);
+              }
+            }
+          }
+        }
+      } else {
       // S = Q K^T: sc[t][h][e] = score of head g, page t's token 8 h + 2 t4 + e.
       float sc[kQ][2][4];
 #pragma unroll
@@ -567,10 +687,73 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? kAttnCtasPerSm : 0)
           }
         }
       }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty0 + 8 * s);
     }
 
+    if constexpr (MHA) {
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) l_run += __shfl_xor_sync(0xffffffffu, l_run, o);
+      if (consumers_any(aborted)) return;
+      // Lanes (g, 0): channels 16 c + 2 g (d[0] + d[1]) and + 1 (d[2] + d[3]).
+      // Warps 1-3 hand their states to warp 0, which merges them with its own
+      // (ascending warp order) and writes the item's partial.
+      if (warp > 0) {
+        float* r = mrg + (warp - 1) * C::kMergeRow;
+        if (lane == 0) {
+          r[D] = m_run;
+          r[D + 1] = l_run;
+          r[D + 2] = r_run;
+        }
+        if (t4 == 0) {
+#pragma unroll
+          for (int cn = 0; cn < kAccTiles; ++cn) {
+            r[16 * cn + 2 * g] = acc[cn][0] + acc[cn][1];
+            r[16 * cn + 2 * g + 1] = acc[cn][2] + acc[cn][3];
+          }
+        }
+      }
+      consumers_sync();
+      if (warp == 0) {
+        float M = m_run;
+#pragma unroll
+        for (int w = 1; w < kConsumerWarps; ++w) M = fmaxf(M, mrg[(w - 1) * C::kMergeRow + D]);
+        // f: 2^(m - M + r), the weight of a warp's o
+        float f[kConsumerWarps];
+        f[0] = (m_run == -INFINITY) ? 0.f : exp2f((m_run - M) + r_run);
+        float L = (m_run == -INFINITY) ? 0.f : exp2f(m_run - M) * l_run;
+#pragma unroll
+        for (int w = 1; w < kConsumerWarps; ++w) {
+          const float* r = mrg + (w - 1) * C::kMergeRow;
+          f[w] = (r[D] == -INFINITY) ? 0.f : exp2f((r[D] - M) + r[D + 2]);
+          L += (r[D] == -INFINITY) ? 0.f : exp2f(r[D] - M) * r[D + 1];
+        }
+        const int64_t pi = (static_cast<int64_t>(b) * a.Hq + kvh) * a.n_chunks + chunk;
+        float* po = a.part_o + pi * D;
+        const int64_t oo = b * a.o_sb + kvh * a.o_sh;
+        if (t4 == 0) {
+#pragma unroll
+          for (int cn = 0; cn < kAccTiles; ++cn) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int c = 16 * cn + 2 * g + e;
+              float O = f[0] * (acc[cn][2 * e] + acc[cn][2 * e + 1]);
+#pragma unroll
+              for (int w = 1; w < kConsumerWarps; ++w) O += f[w] * mrg[(w - 1) * C::kMergeRow + c];
+              if (whole)
+                store_out(a.out, a.out_dtype, oo + c, L > 0.f ? O / L : 0.f);  // (no token: 0)
+              else
+                po[c] = O;
+            }
+          }
+        }
+        if (lane == 0 && !whole) {
+          a.part_ml[2 * pi] = M;
+          a.part_ml[2 * pi + 1] = L;
+        }
+      }
+    } else {
     l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
     l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
 
@@ -629,21 +812,22 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? kAttnCtasPerSm : 0)
         a.part_ml[2 * pi + 1] = L;
       }
     }
+    }
     consumers_sync();  // merge area free again; the descriptor slot was read by all
     if (threadIdx.x == 0) mbar_arrive(dempty0 + 8 * slot);
   }
 }
 
-// Resident CTAs per SM of one instantiation, at most kAttnCtasPerSm; computed once.
-template <int D, bool F16, bool SPARSE>
+// Resident CTAs per SM of one instantiation, at most Fp8Cfg::kCtas; computed once.
+template <int D, bool F16, bool SPARSE, bool MHA>
 cudaError_t ctas_per_sm_t(int* out) {
-  using C = Fp8Cfg<D>;
+  using C = Fp8Cfg<D, MHA>;
   static int cached = 0;  // benign race: every thread computes the same value
   if (cached > 0) {
     *out = cached;
     return cudaSuccess;
   }
-  auto kern = attn_fp8_kernel<D, F16, SPARSE>;
+  auto kern = attn_fp8_kernel<D, F16, SPARSE, MHA>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -651,47 +835,75 @@ cudaError_t ctas_per_sm_t(int* out) {
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kAttnThreads, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   if (n < 1) return cudaErrorInvalidConfiguration;
-  cached = n < kAttnCtasPerSm ? n : kAttnCtasPerSm;
+  cached = n < C::kCtas ? n : C::kCtas;
   *out = cached;
   return cudaSuccess;
 }
 
-template <int D, bool F16, bool SPARSE>
+template <int D, bool F16, bool SPARSE, bool MHA>
 cudaError_t launch_t(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int num_sms,
                      cudaStream_t s) {
   int per_sm = 0;
-  const cudaError_t e = ctas_per_sm_t<D, F16, SPARSE>(&per_sm);
+  const cudaError_t e = ctas_per_sm_t<D, F16, SPARSE, MHA>(&per_sm);
   if (e != cudaSuccess) return e;
   const int64_t want = static_cast<int64_t>(num_sms) * per_sm;
   const int grid = static_cast<int>(a.n_items < want ? a.n_items : want);
-  return launch_pdl(attn_fp8_kernel<D, F16, SPARSE>, dim3(grid), dim3(kAttnThreads),
-                    Fp8Cfg<D>::kSmemBytes, s, a, mk, mv);
+  return launch_pdl(attn_fp8_kernel<D, F16, SPARSE, MHA>, dim3(grid), dim3(kAttnThreads),
+                    Fp8Cfg<D, MHA>::kSmemBytes, s, a, mk, mv);
 }
+
+// One call of f.template run<D, F16, SPARSE, MHA>() for the run-time values.
+template <typename F>
+cudaError_t dispatch(int d, bool f16, bool sparse, bool mha, const F& f) {
+  const int key = (d == 128 ? 8 : 0) + (f16 ? 4 : 0) + (sparse ? 2 : 0) + (mha ? 1 : 0);
+  switch (key) {
+    case 0: return f.template run<64, false, false, false>();
+    case 1: return f.template run<64, false, false, true>();
+    case 2: return f.template run<64, false, true, false>();
+    case 3: return f.template run<64, false, true, true>();
+    case 4: return f.template run<64, true, false, false>();
+    case 5: return f.template run<64, true, false, true>();
+    case 6: return f.template run<64, true, true, false>();
+    case 7: return f.template run<64, true, true, true>();
+    case 8: return f.template run<128, false, false, false>();
+    case 9: return f.template run<128, false, false, true>();
+    case 10: return f.template run<128, false, true, false>();
+    case 11: return f.template run<128, false, true, true>();
+    case 12: return f.template run<128, true, false, false>();
+    case 13: return f.template run<128, true, false, true>();
+    case 14: return f.template run<128, true, true, false>();
+    default: return f.template run<128, true, true, true>();
+  }
+}
+
+struct Launch {
+  const AttnArgs& a;
+  const CUtensorMap &mk, &mv;
+  int num_sms;
+  cudaStream_t s;
+  template <int D, bool F16, bool SPARSE, bool MHA>
+  cudaError_t run() const {
+    return launch_t<D, F16, SPARSE, MHA>(a, mk, mv, num_sms, s);
+  }
+};
+struct Ctas {
+  int* out;
+  template <int D, bool F16, bool SPARSE, bool MHA>
+  cudaError_t run() const {
+    return ctas_per_sm_t<D, F16, SPARSE, MHA>(out);
+  }
+};
 
 }  // namespace
 
 cudaError_t launch_attn_fp8(int d, bool f16, bool sparse, const AttnArgs& a, const CUtensorMap& mk,
                             const CUtensorMap& mv, int num_sms, cudaStream_t s) {
-  if (d == 128) {
-    if (f16) return sparse ? launch_t<128, true, true>(a, mk, mv, num_sms, s)
-                           : launch_t<128, true, false>(a, mk, mv, num_sms, s);
-    return sparse ? launch_t<128, false, true>(a, mk, mv, num_sms, s)
-                  : launch_t<128, false, false>(a, mk, mv, num_sms, s);
-  }
-  if (f16) return sparse ? launch_t<64, true, true>(a, mk, mv, num_sms, s)
-                         : launch_t<64, true, false>(a, mk, mv, num_sms, s);
-  return sparse ? launch_t<64, false, true>(a, mk, mv, num_sms, s)
-                : launch_t<64, false, false>(a, mk, mv, num_sms, s);
+  // one query head per kv head: the single-head layout
+  return dispatch(d, f16, sparse, a.G == 1, Launch{a, mk, mv, num_sms, s});
 }
 
 cudaError_t attn_fp8_ctas_per_sm(int d, bool f16, bool sparse, int* out) {
-  if (d == 128) {
-    if (f16) return sparse ? ctas_per_sm_t<128, true, true>(out)
-                           : ctas_per_sm_t<128, true, false>(out);
-    return sparse ? ctas_per_sm_t<128, false, true>(out) : ctas_per_sm_t<128, false, false>(out);
-  }
-  if (f16) return sparse ? ctas_per_sm_t<64, true, true>(out) : ctas_per_sm_t<64, true, false>(out);
-  return sparse ? ctas_per_sm_t<64, false, true>(out) : ctas_per_sm_t<64, false, false>(out);
+  return dispatch(d, f16, sparse, false, Ctas{out});
 }
 
 }  // namespace dkv

@@ -58,7 +58,7 @@ inline int select_pages_per_chunk(int64_t union_max, int d) {
 // all-heads result.  A multiple of 8: two pages a stage for each of four warps.
 inline int fp8_pages_per_chunk(int64_t pages, int d, int batch) {
   const int64_t base = d == 128 ? 64 : 128;
-  int64_t want = ceil_div(2 * 152 * 2, 8 * static_cast<int64_t>(batch));
+  int64_t want = ceil_div(2 * 152, 8 * static_cast<int64_t>(batch));
   want = want > 32 ? 32 : want;  // (the single-pass merge)
   int64_t per = ceil_div(ceil_div(pages, want), 8) * 8;
   if (per > base) per = base;
