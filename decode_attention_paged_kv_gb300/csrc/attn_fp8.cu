@@ -8,30 +8,46 @@
 //
 // The scales never touch the codes.  ks multiplies the page's scores.  vs =
 // 2^e * f (1 <= |f| < 2, or f = 0) goes into the softmax weights: beside the
-// usual running max m of the scores s (log2 units) and sum l of 2^(s - m), the
-// output accumulates w = f * 2^((s - m) + (e - r)) with an integer r kept at
-// ceil(max(s + e) - m), so the weights that meet the codes stay below 2 and
-// the largest is near 1 whatever the scales are: a page of large values with
-// little weight costs the others no bits.  s - m is exact near the maximum and
-// e - r always, so a second maximum adds no rounding.  At the end of an item
-// o = 2^r * sum w code, the usual partial.
+// usual sum l of 2^(s - m) (s: the scores in log2 units), the output accumulates
+// w = f * 2^((s - m) + (e - r)) with an integer r, so the weights that meet the
+// codes are near 1 at the largest contribution whatever the scales are: a page
+// of large values with little weight costs the others no bits.  s - m is exact
+// near the maximum and e - r always, so r adds no rounding.  At the end of an
+// item o = 2^r * sum w code, the usual partial.
+//
+// m and r are references, not the exact maxima: they move only when a score
+// passes m, or a weight passes 1, by more than 2^kSlack (fp16 holds w < 2^9
+// without loss), which after a warp's first pages is rare.  So a step needs no
+// reduction across lanes, only a vote, and rarely rescales.
 //
 // Structure as in the 16-bit kernel: a persistent grid pulls work items
 // (batch, kv head, chunk of pages) from a counter; one producer warp streams
 // pages by TMA tensor copies (one 16 x d byte box a tensor and page, d-byte
-// swizzle) into per-warp sub-rings of shared-memory stages; four consumer warps
-// compute.  Codes become fp16 in registers (exact: e4m3 is a subset of fp16):
-//   * S = Q K^T: one ldmatrix word of lane (g, t4) is four consecutive channels
-//     16 c + 4 t4 .. + 3 of token g, which two conversions turn into the B
-//     fragment of k-step c; the query's A fragments take the same channel order.
-//   * O += P V: one transposed ldmatrix word is the channel pair (2 g, 2 g + 1)
-//     of tokens 2 t4 and 2 t4 + 1; a byte permute and two conversions make the B
-//     fragments of two output tiles, the even and the odd channels of 16 c ..
-//     16 c + 15 (output tile 2 c + e, column n is channel 16 c + 2 n + e).
-// A bf16 query is scaled by a power of two per head so that its largest
-// component lies in [2^14, 2^15): exact in fp16 for every component within 2^28
-// of it; the scores are scaled back.  The weights are split into fp16 hi + lo
-// (A rows 0-7 / 8-15), 22 significant bits.
+// swizzle) into per-warp sub-rings of two-page shared-memory stages; four
+// consumer warps compute.  Codes become fp16 in registers (exact: e4m3 is a
+// subset of fp16) and are always the MMA's A operand, so that all of its 16 rows
+// work; the query heads are the columns:
+//   * S^T = K Q^T, tokens x heads.  One ldmatrix word of lane (g, t4) is four
+//     consecutive channels 16 c + 4 t4 .. + 3 of token g, which two conversions
+//     turn into the A fragments of k-step c; the query's B fragments take the
+//     same channel order.
+//   * O^T = V^T P^T, channels x heads.  One transposed ldmatrix word is the
+//     channel pair (2 g, 2 g + 1) of tokens 2 t4 and 2 t4 + 1; a byte permute
+//     and two conversions make the A fragments whose rows g and g + 8 are the
+//     channels 16 c + 2 g and 16 c + 2 g + 1.
+// The weights are split into fp16 hi + lo (22 significant bits).  Columns, by
+// the query heads GL that a kv head may have in an instantiation:
+//   GL = 8  columns are heads; hi and lo are two products into one sum.
+//   GL = 4  columns 0-3 hold the hi halves and 4-7 the lo halves of 4 heads: one
+//           product.  The query fills both column halves, so lanes t4 < 2 find
+//           the first page's scores of all heads and t4 >= 2 the second's: 4 of
+//           the stage's 128 scores a lane.
+//   GL = 1  even columns hi, odd columns lo; the query fills every column and
+//           each lane keeps one of the stage's 32 scores.
+// Weights reach the B fragments by 8 x 8 transposes (movmatrix), or shuffles for
+// one head.  A bf16 query is scaled by a power of two per head so that its
+// largest component lies in [2^14, 2^15): exact in fp16 for every component
+// within 2^28 of it; the scores are scaled back.
 //
 // Every mbarrier wait is bounded; on expiry the kernel records a timeout in
 // the status word, stops issuing, drains the copies it issued and exits.
@@ -46,22 +62,25 @@ namespace {
 
 constexpr uint64_t kDrainLimitNs = 200000000ull;  // 200 ms for the whole drain
 constexpr int kListPages = 128;                   // pages of an item listed at a time
+constexpr float kSlack = 8.f;      // how far, in log2 units, a reference may be passed
+constexpr float kUnset = -1e30f;   // a reference before the first token
 
 struct ItemDesc {
   int item;     // work item, -1: no more work
   int n_pages;  // pages in the item
 };
 
-template <int D, bool MHA>
+// GL: query heads a kv head may have (1, 4 or 8).
+template <int D, int GL>
 struct Fp8Cfg {
-  // Three CTAs fit an SM where a thread needs at most 128 registers.
-  static constexpr int kCtas = MHA || D == 64 ? 3 : 2;
   static constexpr int kPagesPerStage = 2;
   static constexpr int kTileBytes = kPage * D;      // one tensor's page of codes
   static constexpr int kSlotBytes = 2 * kTileBytes;  // K codes | V codes
   static constexpr int kStageBytes = kPagesPerStage * kSlotBytes;
-  static constexpr int kRing = MHA ? 64 * 1024 : (D == 64 ? 48 * 1024 : 96 * 1024);
-  static constexpr int kStages = kRing / kStageBytes;
+  // Three CTAs an SM, each with 64 KiB of pages in flight; 8 heads of 128
+  // channels need more shared memory for the warps' merge: two CTAs with 96 KiB.
+  static constexpr int kCtas = GL == 8 && D == 128 ? 2 : 3;
+  static constexpr int kStages = (kCtas == 2 ? 96 : 64) * 1024 / kStageBytes;
   static constexpr int kSub = kStages / kConsumerWarps;    // stages per consumer warp
   static constexpr int kIssueLanes = kStages < 16 ? kStages : 16;
   static constexpr int kBarOffset = kStages * kStageBytes;
@@ -70,7 +89,7 @@ struct Fp8Cfg {
   static constexpr int kMergeOffset = kDescOffset + 2 * 8;
   static constexpr int kMergeRow = D + 3;  // o[D], max m, sum l, exponent r
   static constexpr int kListOffset =
-      (kMergeOffset + (kConsumerWarps - 1) * (MHA ? 1 : 8) * kMergeRow * 4 + 15) / 16 * 16;
+      (kMergeOffset + (kConsumerWarps - 1) * GL * kMergeRow * 4 + 15) / 16 * 16;
   static constexpr int kBlockOffset = kListOffset + 16 * kListPages;
   static constexpr int kMiscOffset = kBlockOffset + 4 * kListPages;
   static constexpr int kSmemBytes = 1024 + kMiscOffset + 16;
@@ -132,13 +151,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
-// The largest of a warp's values (no NaN), in every lane: one integer reduction
-// over order-preserving keys (a float's bits, the magnitude bits flipped when
-// negative; the map is its own inverse).
-__device__ __forceinline__ float warp_max(float x) {
-  const int b = __float_as_int(x);
-  const int k = __reduce_max_sync(0xffffffffu, b >= 0 ? b : b ^ 0x7fffffff);
-  return __int_as_float(k >= 0 ? k : k ^ 0x7fffffff);
+// The transpose of an 8 x 8 matrix of 16-bit values, two of a row a lane.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 __device__ __forceinline__ void store_out(void* out, int out_dtype, int64_t off, float v) {
@@ -151,11 +168,11 @@ __device__ __forceinline__ void store_out(void* out, int out_dtype, int64_t off,
   }
 }
 
-template <int D, bool F16, bool SPARSE, bool MHA>
-__global__ void __launch_bounds__(kAttnThreads, MHA || D == 64 ? Fp8Cfg<D, MHA>::kCtas : 0)
-    attn_fp8_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap mk,
-                    const __grid_constant__ CUtensorMap mv) {
-  using C = Fp8Cfg<D, MHA>;
+template <int D, bool F16, bool SPARSE, int GL>
+__global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_kernel(
+    const AttnArgs a, const __grid_constant__ CUtensorMap mk,
+    const __grid_constant__ CUtensorMap mv) {
+  using C = Fp8Cfg<D, GL>;
   constexpr int kQ = C::kPagesPerStage;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -375,10 +392,11 @@ __global__ void __launch_bounds__(kAttnThreads, MHA || D == 64 ? Fp8Cfg<D, MHA>:
 
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, t4 = lane & 3;
-  const bool head_ok = MHA || g < a.G;
   const int mtx = lane >> 3, mrow = lane & 7;
-  // Channel of output tile cn, column 2 t4 + e.
-  auto out_channel = [t4](int cn, int e) { return 16 * (cn >> 1) + 4 * t4 + 2 * e + (cn & 1); };
+  // This lane's score columns 2 t4 + e are heads h0 + e, on page `pt` of a stage
+  // (GL = 8: on both).
+  const int h0 = GL == 8 ? 2 * t4 : (GL == 4 ? 2 * (t4 & 1) : 0);
+  const int pt = t4 >> 1;
   int mycnt = 0;  // stages this warp has taken from its sub-ring
   // Exits are taken by all four consumer warps together (consumers_any), so no
   // warp is ever left waiting at a consumer barrier.
@@ -400,13 +418,15 @@ __global__ void __launch_bounds__(kAttnThreads, MHA || D == 64 ? Fp8Cfg<D, MHA>:
     const int kvh = unit % a.Hkv, b = unit / a.Hkv;
     const int Nb = seq_len_of(a.lens, b, a.N);  // tokens this sequence attends
 
-    // The query's A fragments: k-step c of lane (g, t4) is channels
-    // 16 c + 4 t4 .. + 3 of head g (row 8 + g is unused), in fp16.
+    // The query's B fragments: k-step c of lane (g, t4) is channels
+    // 16 c + 4 t4 .. + 3 of the head of column g, in fp16.
     uint32_t qa[D / 16][2];
-    float qscale = a.scale_log2;
+    float qs[2];  // the lane's heads' factor from products to log2 units
     {
+      const int head = GL == 1 ? 0 : g & (GL - 1);
+      const bool head_ok = head < a.G;
       const uint16_t* qrow = static_cast<const uint16_t*>(a.q) + b * a.q_sb +
-                             static_cast<int64_t>(kvh * a.G + (head_ok && !MHA ? g : 0)) * a.q_sh +
+                             static_cast<int64_t>(kvh * a.G + (head_ok ? head : 0)) * a.q_sh +
                              4 * t4;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
@@ -414,6 +434,7 @@ __global__ void __launch_bounds__(kAttnThreads, MHA || D == 64 ? Fp8Cfg<D, MHA>:
         qa[c][0] = w.x;
         qa[c][1] = w.y;
       }
+      qs[0] = qs[1] = a.scale_log2;
       if constexpr (!F16) {
         // 2^up brings the head's largest component into [2^14, 2^15)
         uint32_t top = 0;  // its bits: bf16 magnitudes order as integers
@@ -426,7 +447,10 @@ __global__ void __launch_bounds__(kAttnThreads, MHA || D == 64 ? Fp8Cfg<D, MHA>:
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int up = min(126, 14 + 127 - static_cast<int>(top >> 7));
         const float f = __int_as_float((127 + up) << 23);
-        qscale *= __int_as_float((127 - up) << 23);
+        const float down = a.scale_log2 * __int_as_float((127 - up) << 23);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          qs[e] = __shfl_sync(0xffffffffu, down, 4 * (GL == 1 ? 0 : h0 + e));
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
 #pragma unroll
@@ -434,11 +458,17 @@ __global__ void __launch_bounds__(kAttnThreads, MHA || D == 64 ? Fp8Cfg<D, MHA>:
             qa[c][i] = pack2<true>(lo16<false>(qa[c][i]) * f, hi16<false>(qa[c][i]) * f);
       }
     }
-    float m_run = -INFINITY, mv_run = -INFINITY, r_run = 0.f, l_run = 0.f;
-    constexpr int kAccTiles = MHA ? D / 16 : D / 8;
-    float acc[kAccTiles][4];
+    // Per head of the lane: the references m and r, the largest s + e that r was
+    // set for, and the lane's part of the sum l.
+    constexpr int kE = GL == 1 ? 1 : 2;             // heads of a lane
+    constexpr int kT = GL == 8 ? kQ : 1;            // pages of a lane
+    constexpr int kN = GL == 1 ? 1 : 2;             // tokens of a lane, page and head
+    float m_ref[kE], mv_ref[kE], r_ref[kE], l_run[kE];
 #pragma unroll
-    for (int cn = 0; cn < kAccTiles; ++cn) acc[cn][0] = acc[cn][1] = acc[cn][2] = acc[cn][3] = 0.f;
+    for (int e = 0; e < kE; ++e) m_ref[e] = mv_ref[e] = kUnset, r_ref[e] = l_run[e] = 0.f;
+    float acc[D / 16][4];  // tile c: channels 16 c + 2 g (0, 1) and + 1 (2, 3), columns 2 t4 + e
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
 
     bool aborted = false;
     for (int sq = warp; sq * kQ < n_pages; sq += kConsumerWarps) {
@@ -457,117 +487,12 @@ __global__ void __launch_bounds__(kAttnThreads, MHA || D == 64 ? Fp8Cfg<D, MHA>:
       const int cnt = min(kQ, n_pages - sq * kQ);
       const uint32_t st = sbase + s * C::kStageBytes;
 
-      if constexpr (MHA) {
-        // S = K q, the query in every column: lane (g, t4) gets the scores of
-        // tokens g (d[0]) and g + 8 (d[2]) of both pages and keeps one of the
-        // 32: token g + 8 (t4 & 1) of page t4 >> 1.
-        float sc[kQ][4];
-#pragma unroll
-        for (int t = 0; t < kQ; ++t) {
-          sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
-          if (t < cnt) {
-#pragma unroll
-            for (int c = 0; c < D / 16; c += 2) {
-              uint32_t r[4];  // [chunk c, c + 1][tokens 0-7, 8-15]
-              ldsm_x4(code_addr<D>(st + t * C::kSlotBytes, 8 * (mtx & 1) + mrow, c + (mtx >> 1)),
-                      r[0], r[1], r[2], r[3]);
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                mma16816<true>(sc[t], e4m3_lo2(r[2 * i]), e4m3_lo2(r[2 * i + 1]),
-                               e4m3_hi2(r[2 * i]), e4m3_hi2(r[2 * i + 1]), qa[c + i][0],
-                               qa[c + i][1]);
-            }
-          }
-        }
-        const int4 meta = stage_meta[s * kQ + (t4 >> 1)];
-        const bool mine = (t4 >> 1) < cnt;
-        const int in_page = g + 8 * (t4 & 1);
-        const int sl = SPARSE ? a.sub_log2 : 0;
-        const bool on = !SPARSE || ((meta.y >> (sl ? in_page >> (4 - sl) : 0)) & 1);
-        const bool past = mine && meta.x * kPage + in_page >= Nb;
-        const float raw = (t4 & 2) ? ((t4 & 1) ? sc[1][2] : sc[1][0])
-                                   : ((t4 & 1) ? sc[0][2] : sc[0][0]);
-        const float sv = mine && on && !past ? raw * (qscale * __int_as_float(meta.z)) : -INFINITY;
-        // vs = 2^ve * vf (a scale below 2^-126 counts as 0)
-        const uint32_t vb = static_cast<uint32_t>(meta.w);
-        const int ex = (vb >> 23) & 0xff;
-        const float ve = static_cast<float>(ex - 127);
-        const float vf = ex == 0 ? 0.f : __uint_as_float((vb & 0x807fffffu) | 0x3f800000u);
-        const float m_new = fmaxf(m_run, warp_max(sv));
-        const float mv_new = fmaxf(mv_run, warp_max(sv + ve));
-        const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-        const float r_new = (m_new == -INFINITY) ? 0.f : ceilf(mv_new - m_new);
-        const float x = sv - m_use;
-        const float down = m_run - m_use;
-        l_run = l_run * exp2_fast(down) + exp2_fast(x);  // (this lane's tokens)
-        if (m_new != m_run || r_new != r_run) {          // warp-uniform
-          const float alpha = exp2_fast(down + (r_run - r_new));
-#pragma unroll
-          for (int cn = 0; cn < kAccTiles; ++cn) {
-            acc[cn][0] *= alpha;
-            acc[cn][1] *= alpha;
-            acc[cn][2] *= alpha;
-            acc[cn][3] *= alpha;
-          }
-        }
-        m_run = m_new;
-        mv_run = mv_new;
-        r_run = r_new;
-        if (__any_sync(0xffffffffu, past)) {
-          // Slots past the sequence's end hold anything: zero those V codes
-          // (their weights are 0, but 0 * NaN is not).
-          for (int t = 0; t < cnt; ++t) {
-            const int nt = min(kPage, Nb - stage_meta[s * kQ + t].x * kPage);
-            uint8_t* vt = smem + s * C::kStageBytes + t * C::kSlotBytes + C::kTileBytes;
-            for (int i = lane; i < (kPage - nt) * (D / 16); i += 32)
-              *reinterpret_cast<uint4*>(vt + nt * D + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          // (before the slot goes back to the copy engine)
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
-        // The weight as two fp16 halves, hi below lo.  O^T += V^T P: B holds the
-        // hi halves in even columns and the lo halves in odd ones (columns 0 and
-        // 1 are read at the end).
-        const float w = exp2_fast(x + (ve - r_run)) * vf;
-        const __half wh = __float2half_rn(w);
-        const __half2 w2 = __halves2half2(wh, __float2half_rn(w - __half2float(wh)));
-        const uint32_t wp = *reinterpret_cast<const uint32_t*>(&w2);
-        const uint32_t pick = (g & 1) ? 0x7632u : 0x5410u;
-#pragma unroll
-        for (int t = 0; t < kQ; ++t) {
-          // tokens 2 t4, 2 t4 + 1 (b0) and 2 t4 + 8, 2 t4 + 9 (b1) of page t
-          const int src = 8 * t4 + 2 * t;
-          const uint32_t w0 = __shfl_sync(0xffffffffu, wp, src);
-          const uint32_t w1 = __shfl_sync(0xffffffffu, wp, src + 4);
-          const uint32_t w8 = __shfl_sync(0xffffffffu, wp, src + 1);
-          const uint32_t w9 = __shfl_sync(0xffffffffu, wp, src + 5);
-          if (t < cnt) {
-            const uint32_t b0 = __byte_perm(w0, w1, pick), b1 = __byte_perm(w8, w9, pick);
-            const uint32_t vt = st + t * C::kSlotBytes + C::kTileBytes;
-#pragma unroll
-            for (int c = 0; c < D / 16; c += 2) {
-              uint32_t r[4];  // [chunk c, c + 1][tokens 0-7, 8-15]
-              ldsm_x4_trans(code_addr<D>(vt, 8 * (mtx & 1) + mrow, c + (mtx >> 1)), r[0], r[1],
-                            r[2], r[3]);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                // rows: the even (g) and the odd (g + 8) channels of the chunk
-                const uint32_t y0 = __byte_perm(r[2 * i], 0u, 0x3120);
-                const uint32_t y8 = __byte_perm(r[2 * i + 1], 0u, 0x3120);
-                mma16816<true>(acc[c + i], e4m3_lo2(y0), e4m3_hi2(y0), e4m3_lo2(y8), e4m3_hi2(y8),
-                               b0, b1);
-              }
-            }
-          }
-        }
-      } else {
-      // S = Q K^T: sc[t][h][e] = score of head g, page t's token 8 h + 2 t4 + e.
-      float sc[kQ][2][4];
+      // S^T = K Q^T: sc[t][0 .. 3] = tokens g and g + 8 (2, 3) of page t in
+      // columns 2 t4 and 2 t4 + 1 (1, 3).
+      float sc[kQ][4];
 #pragma unroll
       for (int t = 0; t < kQ; ++t) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) sc[t][h][0] = sc[t][h][1] = sc[t][h][2] = sc[t][h][3] = 0.f;
+        sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
         if (t < cnt) {
 #pragma unroll
           for (int c = 0; c < D / 16; c += 2) {
@@ -576,242 +501,285 @@ __global__ void __launch_bounds__(kAttnThreads, MHA || D == 64 ? Fp8Cfg<D, MHA>:
                     r[0], r[1], r[2], r[3]);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                mma16816<true>(sc[t][h], qa[c + i][0], 0u, qa[c + i][1], 0u, e4m3_lo2(r[2 * i + h]),
-                               e4m3_hi2(r[2 * i + h]));
+              mma16816<true>(sc[t], e4m3_lo2(r[2 * i]), e4m3_lo2(r[2 * i + 1]),
+                             e4m3_hi2(r[2 * i]), e4m3_hi2(r[2 * i + 1]), qa[c + i][0],
+                             qa[c + i][1]);
           }
         }
       }
 
-      // Scores in log2 units, masked; the two running maxima.  Token t of a
-      // page counts for head g if bit (g << sub_log2) + (t >> (4 - sub_log2))
-      // of its mask is set.
-      const int sl = SPARSE ? a.sub_log2 : 0;
-      float sv[kQ][4], ve[kQ], vf[kQ];
-      float pmax = -INFINITY, vmax = -INFINITY;
+      // The lane's scores in log2 units: sv[t][e][n] of page t (GL = 8; else page
+      // pt), head h0 + e, token g + 8 n (GL = 1: token g + 8 (t4 & 1)).
+      float sv[kT][kE][kN], ve[kT], vf[kT];
+      bool ragged = false;
 #pragma unroll
-      for (int t = 0; t < kQ; ++t) {
-        const int4 meta = t < cnt ? stage_meta[s * kQ + t] : make_int4(0, 0, 0, 0);
-        const uint32_t hmask = static_cast<uint32_t>(meta.y);
-        const uint32_t hbits =
-            head_ok ? (hmask >> ((g << sl) + (sl == 2 ? (t4 >> 1) : 0))) : 0u;
-        const bool on_lo = hbits & 1u, on_hi = (hbits >> sl) & 1u;
-        const float f = qscale * __int_as_float(meta.z);
+      for (int t = 0; t < kT; ++t) {
+        const int page_t = GL == 8 ? t : pt;
+        const bool have = page_t < cnt;
+        const int4 meta = stage_meta[s * kQ + page_t];
+        const float ks = __int_as_float(meta.z);
         // vs = 2^ve * vf (a scale below 2^-126 counts as 0)
         const uint32_t vb = static_cast<uint32_t>(meta.w);
         const int ex = (vb >> 23) & 0xff;
         ve[t] = static_cast<float>(ex - 127);
         vf[t] = ex == 0 ? 0.f : __uint_as_float((vb & 0x807fffffu) | 0x3f800000u);
-        float tmax = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int tok = meta.x * kPage + 8 * (e >> 1) + 2 * t4 + (e & 1);
-          const bool on = e < 2 ? on_lo : on_hi;
-          sv[t][e] = (on && tok < Nb) ? sc[t][e >> 1][e & 1] * f : -INFINITY;
-          tmax = fmaxf(tmax, sv[t][e]);
-        }
-        pmax = fmaxf(pmax, tmax);
-        vmax = fmaxf(vmax, tmax + ve[t]);
-      }
-      pmax = fmaxf(pmax, __shfl_xor_sync(0xffffffffu, pmax, 1));
-      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-      pmax = fmaxf(pmax, __shfl_xor_sync(0xffffffffu, pmax, 2));
-      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-      const float m_new = fmaxf(m_run, pmax), mv_new = fmaxf(mv_run, vmax);
-      // (mv is -inf exactly when m is: no token yet)
-      const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-      const float r_new = (m_new == -INFINITY) ? 0.f : ceilf(mv_new - m_new);
-      float psum = 0.f;
+        for (int e = 0; e < kE; ++e)
 #pragma unroll
-      for (int t = 0; t < kQ; ++t)
+          for (int n = 0; n < kN; ++n) {
+            const int i = GL == 1 ? 0 : 2 * n + e;
+            float raw = GL == 8 ? sc[t][i] : (pt ? sc[1][i] : sc[0][i]);
+            if constexpr (GL == 1) raw = (t4 & 1) ? (pt ? sc[1][2] : sc[0][2]) : raw;
+            sv[t][e][n] = raw * (qs[e] * ks);
+          }
+        const bool past = have && (meta.x + 1) * kPage > Nb;
+        ragged |= past;
+        if (SPARSE || !have || past) {
+          // Token i of a page counts for head h if it lies in the sequence and
+          // bit (h << sub_log2) + (i >> (4 - sub_log2)) of the mask is set.
+          const int sl = SPARSE ? a.sub_log2 : 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sv[t][e] -= m_use;
-          psum += exp2_fast(sv[t][e]);
-        }
-      const float down = m_run - m_use;
-      l_run = l_run * exp2_fast(down) + psum;
-      if (__any_sync(0xffffffffu, m_new != m_run || r_new != r_run)) {
-        const float alpha = exp2_fast(down + (r_run - r_new));
+          for (int n = 0; n < kN; ++n) {
+            const int i = g + 8 * (GL == 1 ? t4 & 1 : n);
+            const bool in = have && meta.x * kPage + i < Nb;
 #pragma unroll
-        for (int cn = 0; cn < D / 8; ++cn) {
-          acc[cn][0] *= alpha;
-          acc[cn][1] *= alpha;
-          acc[cn][2] *= alpha;
-          acc[cn][3] *= alpha;
+            for (int e = 0; e < kE; ++e) {
+              const bool on =
+                  !SPARSE || ((meta.y >> (((h0 + e) << sl) + (sl ? i >> (4 - sl) : 0))) & 1);
+              if (!in || !on) sv[t][e][n] = -INFINITY;
+            }
+          }
         }
       }
-      m_run = m_new;
-      mv_run = mv_new;
-      r_run = r_new;
+      ragged = __any_sync(0xffffffffu, ragged);
 
-      // O += P V, with P = hi + lo (A rows 0-7 and 8-15).
+      // x = s - m, y = x + (e - r): 2^x into l, f 2^y into the weights.
+      float x[kT][kE][kN], y[kT][kE][kN], top = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int e = 0; e < kE; ++e)
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            x[t][e][n] = sv[t][e][n] - m_ref[e];
+            y[t][e][n] = x[t][e][n] + (ve[t] - r_ref[e]);
+            top = fmaxf(top, fmaxf(x[t][e][n], y[t][e][n]));
+          }
+      if (__any_sync(0xffffffffu, top > kSlack)) {
+        // New references: the running maxima with this stage's.
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          float pm = -INFINITY, pv = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < kT; ++t)
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+              pm = fmaxf(pm, sv[t][e][n]);
+              pv = fmaxf(pv, sv[t][e][n] + ve[t]);
+            }
+#pragma unroll
+          for (int o = GL == 8 ? 4 : (GL == 4 ? 2 : 1); o < 32; o *= 2) {
+            pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, o));
+            pv = fmaxf(pv, __shfl_xor_sync(0xffffffffu, pv, o));
+          }
+          if (pm != -INFINITY) {
+            const float m_new = fmaxf(m_ref[e], pm);
+            mv_ref[e] = fmaxf(mv_ref[e], pv);
+            const float r_new = ceilf(mv_ref[e] - m_new);
+            const float down = m_ref[e] - m_new;  // (unset: 2^down is 0)
+            l_run[e] *= exp2_fast(down);
+            const float alpha = exp2_fast(down + (r_ref[e] - r_new));
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              acc[c][e] *= alpha;
+              acc[c][2 + e] *= alpha;
+              if constexpr (GL == 1) acc[c][1] *= alpha, acc[c][3] *= alpha;
+            }
+            m_ref[e] = m_new;
+            r_ref[e] = r_new;
+          }
+#pragma unroll
+          for (int t = 0; t < kT; ++t)
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+              x[t][e][n] = sv[t][e][n] - m_ref[e];
+              y[t][e][n] = x[t][e][n] + (ve[t] - r_ref[e]);
+            }
+        }
+      }
+      if (ragged) {
+        // Slots past the sequence's end hold anything: zero those V codes
+        // (their weights are 0, but 0 * NaN is not).
+        for (int t = 0; t < cnt; ++t) {
+          const int nt = min(kPage, Nb - stage_meta[s * kQ + t].x * kPage);
+          uint8_t* vt = smem + s * C::kStageBytes + t * C::kSlotBytes + C::kTileBytes;
+          for (int i = lane; i < (kPage - nt) * (D / 16); i += 32)
+            *reinterpret_cast<uint4*>(vt + nt * D + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        // (before the slot goes back to the copy engine)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
+      float w[kT][kE][kN];
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int e = 0; e < kE; ++e)
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            l_run[e] += exp2_fast(x[t][e][n]);
+            w[t][e][n] = exp2_fast(y[t][e][n]) * vf[t];
+          }
+
+      // B fragments of P^T: pb[t][n] = tokens 2 t4 + 8 n, + 1 of page t in column
+      // g; GL = 8: pl the lo halves.
+      uint32_t pb[kQ][2], pl[kQ][2];
+      if constexpr (GL == 1) {
+        const __half wh = __float2half_rn(w[0][0][0]);
+        const __half2 w2 = __halves2half2(wh, __float2half_rn(w[0][0][0] - __half2float(wh)));
+        const uint32_t wp = *reinterpret_cast<const uint32_t*>(&w2);
+        const uint32_t pick = (g & 1) ? 0x7632u : 0x5410u;
+#pragma unroll
+        for (int t = 0; t < kQ; ++t)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            pb[t][n] = __byte_perm(__shfl_sync(0xffffffffu, wp, 8 * t4 + 2 * t + n),
+                                   __shfl_sync(0xffffffffu, wp, 8 * t4 + 4 + 2 * t + n), pick);
+      } else if constexpr (GL == 4) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          uint32_t hi, lo;
+          split_pair<true>(w[0][0][n], w[0][1][n], hi, lo);
+          // page 0's lo halves for lanes t4 >= 2, page 1's hi halves for t4 < 2
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, pt ? hi : lo, 2);
+          pb[0][n] = movmatrix_trans(pt ? other : hi);
+          pb[1][n] = movmatrix_trans(pt ? lo : other);
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < kQ; ++t)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            uint32_t hi, lo;
+            split_pair<true>(w[t][0][n], w[t][1][n], hi, lo);
+            pb[t][n] = movmatrix_trans(hi);
+            pl[t][n] = movmatrix_trans(lo);
+          }
+      }
+
+      // O^T += V^T P^T
 #pragma unroll
       for (int t = 0; t < kQ; ++t) {
         if (t < cnt) {
-          const uint32_t vb = st + t * C::kSlotBytes + C::kTileBytes;
-          const int page = stage_meta[s * kQ + t].x;
-          if ((page + 1) * kPage > Nb) {
-            // Slots past the sequence's end hold anything: zero those V codes
-            // (their weights are 0, but 0 * NaN is not).
-            const int nt = Nb - page * kPage;
-            uint8_t* vt = smem + s * C::kStageBytes + t * C::kSlotBytes + C::kTileBytes;
-            for (int i = lane; i < (kPage - nt) * (D / 16); i += 32)
-              *reinterpret_cast<uint4*>(vt + nt * D + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-            // (before the slot goes back to the copy engine)
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-          }
-          const float shift = ve[t] - r_run;
-          float w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = exp2_fast(sv[t][e] + shift) * vf[t];
-          uint32_t a0, a1, a2, a3;
-          split_pair<true>(w[0], w[1], a0, a1);
-          split_pair<true>(w[2], w[3], a2, a3);
+          const uint32_t vt = st + t * C::kSlotBytes + C::kTileBytes;
 #pragma unroll
           for (int c = 0; c < D / 16; c += 2) {
             uint32_t r[4];  // [chunk c, c + 1][tokens 0-7, 8-15]
-            ldsm_x4_trans(code_addr<D>(vb, 8 * (mtx & 1) + mrow, c + (mtx >> 1)), r[0], r[1], r[2],
+            ldsm_x4_trans(code_addr<D>(vt, 8 * (mtx & 1) + mrow, c + (mtx >> 1)), r[0], r[1], r[2],
                           r[3]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               // bytes (token 2 t4: even, odd; token 2 t4 + 1: even, odd channel)
               // to (even, even; odd, odd)
-              const uint32_t x = __byte_perm(r[2 * i], 0u, 0x3120);
-              const uint32_t y = __byte_perm(r[2 * i + 1], 0u, 0x3120);
-              mma16816<true>(acc[2 * (c + i)], a0, a1, a2, a3, e4m3_lo2(x), e4m3_lo2(y));
-              mma16816<true>(acc[2 * (c + i) + 1], a0, a1, a2, a3, e4m3_hi2(x), e4m3_hi2(y));
+              const uint32_t y0 = __byte_perm(r[2 * i], 0u, 0x3120);
+              const uint32_t y8 = __byte_perm(r[2 * i + 1], 0u, 0x3120);
+              const uint32_t a0 = e4m3_lo2(y0), a1 = e4m3_hi2(y0);
+              const uint32_t a2 = e4m3_lo2(y8), a3 = e4m3_hi2(y8);
+              mma16816<true>(acc[c + i], a0, a1, a2, a3, pb[t][0], pb[t][1]);
+              if constexpr (GL == 8)
+                mma16816<true>(acc[c + i], a0, a1, a2, a3, pl[t][0], pl[t][1]);
             }
           }
         }
-      }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty0 + 8 * s);
     }
 
-    if constexpr (MHA) {
+    // Sum up over the lanes: l over the tokens; o over the hi and lo columns,
+    // which leaves head h0 + e's channels 16 c + 2 g + i in acc[c][2 i + e] of
+    // the lanes t4 < kOwners.
 #pragma unroll
-      for (int o = 1; o < 32; o *= 2) l_run += __shfl_xor_sync(0xffffffffu, l_run, o);
-      if (consumers_any(aborted)) return;
-      // Lanes (g, 0): channels 16 c + 2 g (d[0] + d[1]) and + 1 (d[2] + d[3]).
-      // Warps 1-3 hand their states to warp 0, which merges them with its own
-      // (ascending warp order) and writes the item's partial.
-      if (warp > 0) {
-        float* r = mrg + (warp - 1) * C::kMergeRow;
-        if (lane == 0) {
-          r[D] = m_run;
-          r[D + 1] = l_run;
-          r[D + 2] = r_run;
-        }
-        if (t4 == 0) {
+    for (int e = 0; e < kE; ++e)
 #pragma unroll
-          for (int cn = 0; cn < kAccTiles; ++cn) {
-            r[16 * cn + 2 * g] = acc[cn][0] + acc[cn][1];
-            r[16 * cn + 2 * g + 1] = acc[cn][2] + acc[cn][3];
-          }
-        }
-      }
-      consumers_sync();
-      if (warp == 0) {
-        float M = m_run;
+      for (int o = GL == 8 ? 4 : (GL == 4 ? 2 : 1); o < 32; o *= 2)
+        l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], o);
+    if constexpr (GL == 4) {
 #pragma unroll
-        for (int w = 1; w < kConsumerWarps; ++w) M = fmaxf(M, mrg[(w - 1) * C::kMergeRow + D]);
-        // f: 2^(m - M + r), the weight of a warp's o
-        float f[kConsumerWarps];
-        f[0] = (m_run == -INFINITY) ? 0.f : exp2f((m_run - M) + r_run);
-        float L = (m_run == -INFINITY) ? 0.f : exp2f(m_run - M) * l_run;
+      for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-        for (int w = 1; w < kConsumerWarps; ++w) {
-          const float* r = mrg + (w - 1) * C::kMergeRow;
-          f[w] = (r[D] == -INFINITY) ? 0.f : exp2f((r[D] - M) + r[D + 2]);
-          L += (r[D] == -INFINITY) ? 0.f : exp2f(r[D] - M) * r[D + 1];
-        }
-        const int64_t pi = (static_cast<int64_t>(b) * a.Hq + kvh) * a.n_chunks + chunk;
-        float* po = a.part_o + pi * D;
-        const int64_t oo = b * a.o_sb + kvh * a.o_sh;
-        if (t4 == 0) {
+        for (int i = 0; i < 4; ++i) acc[c][i] += __shfl_xor_sync(0xffffffffu, acc[c][i], 2);
+    } else if constexpr (GL == 1) {
 #pragma unroll
-          for (int cn = 0; cn < kAccTiles; ++cn) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int c = 16 * cn + 2 * g + e;
-              float O = f[0] * (acc[cn][2 * e] + acc[cn][2 * e + 1]);
-#pragma unroll
-              for (int w = 1; w < kConsumerWarps; ++w) O += f[w] * mrg[(w - 1) * C::kMergeRow + c];
-              if (whole)
-                store_out(a.out, a.out_dtype, oo + c, L > 0.f ? O / L : 0.f);  // (no token: 0)
-              else
-                po[c] = O;
-            }
-          }
-        }
-        if (lane == 0 && !whole) {
-          a.part_ml[2 * pi] = M;
-          a.part_ml[2 * pi + 1] = L;
-        }
-      }
-    } else {
-    l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
-    l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+      for (int c = 0; c < D / 16; ++c) acc[c][0] += acc[c][1], acc[c][2] += acc[c][3];
+    }
+    constexpr int kOwners = GL == 8 ? 4 : (GL == 4 ? 2 : 1);
 
     // Warps 1-3 hand their states to warp 0, which merges them with its own
     // (ascending warp order) and writes the item's partial.
     if (consumers_any(aborted)) return;
-    if (warp > 0) {
-      float* r = mrg + ((warp - 1) * 8 + g) * C::kMergeRow;
-      if (t4 == 0) {
-        r[D] = m_run;
-        r[D + 1] = l_run;
-        r[D + 2] = r_run;
-      }
+    if (warp > 0 && t4 < kOwners) {
 #pragma unroll
-      for (int cn = 0; cn < D / 8; ++cn) {
-        r[out_channel(cn, 0)] = acc[cn][0] + acc[cn][2];
-        r[out_channel(cn, 1)] = acc[cn][1] + acc[cn][3];
+      for (int e = 0; e < kE; ++e) {
+        float* r = mrg + ((warp - 1) * GL + h0 + e) * C::kMergeRow;
+        if (g == 0) {
+          r[D] = m_ref[e];
+          r[D + 1] = l_run[e];
+          r[D + 2] = r_ref[e];
+        }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          r[16 * c + 2 * g] = acc[c][e];
+          r[16 * c + 2 * g + 1] = acc[c][2 + e];
+        }
       }
     }
     consumers_sync();
-    if (warp == 0 && head_ok) {
-      float M = m_run;
+    if (warp == 0 && t4 < kOwners) {
 #pragma unroll
-      for (int w = 1; w < kConsumerWarps; ++w)
-        M = fmaxf(M, mrg[((w - 1) * 8 + g) * C::kMergeRow + D]);
-      // f: 2^(m - M + r), the weight of a warp's o
-      float f[kConsumerWarps];
-      f[0] = (m_run == -INFINITY) ? 0.f : exp2f((m_run - M) + r_run);
-      float L = (m_run == -INFINITY) ? 0.f : exp2f(m_run - M) * l_run;
+      for (int e = 0; e < kE; ++e) {
+        if (h0 + e >= a.G) continue;
+        const float* rows = mrg + (h0 + e) * C::kMergeRow;  // of warp 1
+        float M = m_ref[e];
 #pragma unroll
-      for (int w = 1; w < kConsumerWarps; ++w) {
-        const float* r = mrg + ((w - 1) * 8 + g) * C::kMergeRow;
-        f[w] = (r[D] == -INFINITY) ? 0.f : exp2f((r[D] - M) + r[D + 2]);
-        L += (r[D] == -INFINITY) ? 0.f : exp2f(r[D] - M) * r[D + 1];
-      }
-      const int64_t pi = (static_cast<int64_t>(b) * a.Hq + kvh * a.G + g) * a.n_chunks + chunk;
-      float* po = a.part_o + pi * D;
-      const int64_t oo = b * a.o_sb + (kvh * a.G + g) * a.o_sh;
+        for (int v = 1; v < kConsumerWarps; ++v)
+          M = fmaxf(M, rows[(v - 1) * GL * C::kMergeRow + D]);
+        // f: 2^(m - M + r), the weight of a warp's o (unset: 0, or o is 0)
+        float f[kConsumerWarps];
+        f[0] = exp2f((m_ref[e] - M) + r_ref[e]);
+        float L = exp2f(m_ref[e] - M) * l_run[e];
 #pragma unroll
-      for (int cn = 0; cn < D / 8; ++cn) {
+        for (int v = 1; v < kConsumerWarps; ++v) {
+          const float* r = rows + (v - 1) * GL * C::kMergeRow;
+          f[v] = exp2f((r[D] - M) + r[D + 2]);
+          L += exp2f(r[D] - M) * r[D + 1];
+        }
+        const int64_t row = static_cast<int64_t>(b) * a.Hq + kvh * a.G + h0 + e;
+        const int64_t pi = row * a.n_chunks + chunk;
+        float* po = a.part_o + pi * D;
+        const int64_t oo = b * a.o_sb + (kvh * a.G + h0 + e) * a.o_sh;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = out_channel(cn, e);
-          float O = f[0] * (acc[cn][e] + acc[cn][2 + e]);
+        for (int c = 0; c < D / 16; ++c) {
+          float2 O = make_float2(f[0] * acc[c][e], f[0] * acc[c][2 + e]);
+          const int ch = 16 * c + 2 * g;
 #pragma unroll
-          for (int w = 1; w < kConsumerWarps; ++w)
-            O += f[w] * mrg[((w - 1) * 8 + g) * C::kMergeRow + c];
-          if (whole)
-            store_out(a.out, a.out_dtype, oo + c, L > 0.f ? O / L : 0.f);  // (no token: 0)
-          else
-            po[c] = O;
+          for (int v = 1; v < kConsumerWarps; ++v) {
+            const float* r = rows + (v - 1) * GL * C::kMergeRow + ch;
+            O.x += f[v] * r[0];
+            O.y += f[v] * r[1];
+          }
+          if (whole) {  // (no token: 0)
+            store_out(a.out, a.out_dtype, oo + ch, L > 0.f ? O.x / L : 0.f);
+            store_out(a.out, a.out_dtype, oo + ch + 1, L > 0.f ? O.y / L : 0.f);
+          } else {
+            *reinterpret_cast<float2*>(po + ch) = O;
+          }
+        }
+        if (g == 0 && !whole) {
+          a.part_ml[2 * pi] = M > kUnset ? M : -INFINITY;
+          a.part_ml[2 * pi + 1] = L;
         }
       }
-      if (t4 == 0 && !whole) {
-        a.part_ml[2 * pi] = M;
-        a.part_ml[2 * pi + 1] = L;
-      }
-    }
     }
     consumers_sync();  // merge area free again; the descriptor slot was read by all
     if (threadIdx.x == 0) mbar_arrive(dempty0 + 8 * slot);
@@ -819,15 +787,15 @@ __global__ void __launch_bounds__(kAttnThreads, MHA || D == 64 ? Fp8Cfg<D, MHA>:
 }
 
 // Resident CTAs per SM of one instantiation, at most Fp8Cfg::kCtas; computed once.
-template <int D, bool F16, bool SPARSE, bool MHA>
+template <int D, bool F16, bool SPARSE, int GL>
 cudaError_t ctas_per_sm_t(int* out) {
-  using C = Fp8Cfg<D, MHA>;
+  using C = Fp8Cfg<D, GL>;
   static int cached = 0;  // benign race: every thread computes the same value
   if (cached > 0) {
     *out = cached;
     return cudaSuccess;
   }
-  auto kern = attn_fp8_kernel<D, F16, SPARSE, MHA>;
+  auto kern = attn_fp8_kernel<D, F16, SPARSE, GL>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -840,40 +808,33 @@ cudaError_t ctas_per_sm_t(int* out) {
   return cudaSuccess;
 }
 
-template <int D, bool F16, bool SPARSE, bool MHA>
+template <int D, bool F16, bool SPARSE, int GL>
 cudaError_t launch_t(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int num_sms,
                      cudaStream_t s) {
   int per_sm = 0;
-  const cudaError_t e = ctas_per_sm_t<D, F16, SPARSE, MHA>(&per_sm);
+  const cudaError_t e = ctas_per_sm_t<D, F16, SPARSE, GL>(&per_sm);
   if (e != cudaSuccess) return e;
   const int64_t want = static_cast<int64_t>(num_sms) * per_sm;
   const int grid = static_cast<int>(a.n_items < want ? a.n_items : want);
-  return launch_pdl(attn_fp8_kernel<D, F16, SPARSE, MHA>, dim3(grid), dim3(kAttnThreads),
-                    Fp8Cfg<D, MHA>::kSmemBytes, s, a, mk, mv);
+  return launch_pdl(attn_fp8_kernel<D, F16, SPARSE, GL>, dim3(grid), dim3(kAttnThreads),
+                    Fp8Cfg<D, GL>::kSmemBytes, s, a, mk, mv);
 }
 
-// One call of f.template run<D, F16, SPARSE, MHA>() for the run-time values.
+// f.run<D, F16, SPARSE, GL>() for the run-time values, G query heads a kv head.
+template <bool SPARSE, int GL, typename F>
+cudaError_t dispatch_type(int d, bool f16, const F& f) {
+  if (d == 128)
+    return f16 ? f.template run<128, true, SPARSE, GL>() : f.template run<128, false, SPARSE, GL>();
+  return f16 ? f.template run<64, true, SPARSE, GL>() : f.template run<64, false, SPARSE, GL>();
+}
+template <bool SPARSE, typename F>
+cudaError_t dispatch_group(int G, int d, bool f16, const F& f) {
+  if (G == 1) return dispatch_type<SPARSE, 1>(d, f16, f);
+  return G <= 4 ? dispatch_type<SPARSE, 4>(d, f16, f) : dispatch_type<SPARSE, 8>(d, f16, f);
+}
 template <typename F>
-cudaError_t dispatch(int d, bool f16, bool sparse, bool mha, const F& f) {
-  const int key = (d == 128 ? 8 : 0) + (f16 ? 4 : 0) + (sparse ? 2 : 0) + (mha ? 1 : 0);
-  switch (key) {
-    case 0: return f.template run<64, false, false, false>();
-    case 1: return f.template run<64, false, false, true>();
-    case 2: return f.template run<64, false, true, false>();
-    case 3: return f.template run<64, false, true, true>();
-    case 4: return f.template run<64, true, false, false>();
-    case 5: return f.template run<64, true, false, true>();
-    case 6: return f.template run<64, true, true, false>();
-    case 7: return f.template run<64, true, true, true>();
-    case 8: return f.template run<128, false, false, false>();
-    case 9: return f.template run<128, false, false, true>();
-    case 10: return f.template run<128, false, true, false>();
-    case 11: return f.template run<128, false, true, true>();
-    case 12: return f.template run<128, true, false, false>();
-    case 13: return f.template run<128, true, false, true>();
-    case 14: return f.template run<128, true, true, false>();
-    default: return f.template run<128, true, true, true>();
-  }
+cudaError_t dispatch(bool sparse, int G, int d, bool f16, const F& f) {
+  return sparse ? dispatch_group<true>(G, d, f16, f) : dispatch_group<false>(G, d, f16, f);
 }
 
 struct Launch {
@@ -881,16 +842,16 @@ struct Launch {
   const CUtensorMap &mk, &mv;
   int num_sms;
   cudaStream_t s;
-  template <int D, bool F16, bool SPARSE, bool MHA>
+  template <int D, bool F16, bool SPARSE, int GL>
   cudaError_t run() const {
-    return launch_t<D, F16, SPARSE, MHA>(a, mk, mv, num_sms, s);
+    return launch_t<D, F16, SPARSE, GL>(a, mk, mv, num_sms, s);
   }
 };
 struct Ctas {
   int* out;
-  template <int D, bool F16, bool SPARSE, bool MHA>
+  template <int D, bool F16, bool SPARSE, int GL>
   cudaError_t run() const {
-    return ctas_per_sm_t<D, F16, SPARSE, MHA>(out);
+    return ctas_per_sm_t<D, F16, SPARSE, GL>(out);
   }
 };
 
@@ -898,12 +859,11 @@ struct Ctas {
 
 cudaError_t launch_attn_fp8(int d, bool f16, bool sparse, const AttnArgs& a, const CUtensorMap& mk,
                             const CUtensorMap& mv, int num_sms, cudaStream_t s) {
-  // one query head per kv head: the single-head layout
-  return dispatch(d, f16, sparse, a.G == 1, Launch{a, mk, mv, num_sms, s});
+  return dispatch(sparse, a.G, d, f16, Launch{a, mk, mv, num_sms, s});
 }
 
 cudaError_t attn_fp8_ctas_per_sm(int d, bool f16, bool sparse, int* out) {
-  return dispatch(d, f16, sparse, false, Ctas{out});
+  return dispatch(sparse, 8, d, f16, Ctas{out});  // the most shared memory
 }
 
 }  // namespace dkv
