@@ -292,8 +292,9 @@ bool encode_code_map(CUtensorMap* map, const dkv_params* p, const void* codes, i
 
 // Map over the e4m3 codes of an 8-bit cache [B, Hkv, N, d] viewed as {d bytes, N
 // tokens, 1, Hkv, B}, or over a pool as {d bytes, 16 tokens, 1, Hkv, blocks};
-// box {d, 16, 1, 1, 1} (one page of one kv head), d-byte swizzle.
-bool encode_fp8_map(CUtensorMap* map, const dkv_params* p, const dkv_kv* kv) {
+// box {d, 16, 1, 1, 1} (one page of one kv head), or two pages high for a cache
+// read in order; d-byte swizzle.
+bool encode_fp8_map(CUtensorMap* map, const dkv_params* p, const dkv_kv* kv, bool pairs) {
   if (!get_encode()) return false;
   const cuuint64_t d = static_cast<cuuint64_t>(p->head_dim);
   const cuuint64_t dims[5] = {d,
@@ -305,8 +306,8 @@ bool encode_fp8_map(CUtensorMap* map, const dkv_params* p, const dkv_kv* kv) {
   // A size-1 dimension's stride still has to be a valid (16-byte multiple) value.
   if (dims[3] == 1 && st[2] == 0) st[2] = 16;
   if (dims[4] == 1 && st[3] == 0) st[3] = 16;
-  const cuuint32_t box[5] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(dkv::kPage), 1, 1,
-                             1};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(d),
+                             static_cast<cuuint32_t>(pairs ? 2 * dkv::kPage : dkv::kPage), 1, 1, 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(kv->data),
                               dims, st, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -447,8 +448,8 @@ static dkv::Q4View q4_view(const dkv_kv* kv) {
 }
 
 // Tensor maps for a dense cache; a 4-bit cache is described by Q4 views instead.
-static bool cache_views(const dkv_params* p, const dkv_kv* K, const dkv_kv* V, CUtensorMap* mk,
-                        CUtensorMap* mv, dkv::AttnArgs* a) {
+static bool cache_views(const dkv_params* p, const dkv_kv* K, const dkv_kv* V, bool sparse,
+                        CUtensorMap* mk, CUtensorMap* mv, dkv::AttnArgs* a) {
   if (K->format == DKV_KV_Q4G64) {
     memset(mk, 0, sizeof *mk);
     memset(mv, 0, sizeof *mv);
@@ -464,7 +465,8 @@ static bool cache_views(const dkv_params* p, const dkv_kv* K, const dkv_kv* V, C
   if (is_fp8(K)) {
     a->k8 = fp8_view(K);
     a->v8 = fp8_view(V);
-    return encode_fp8_map(mk, p, K) && encode_fp8_map(mv, p, V);
+    const bool pairs = !sparse && !is_paged(K);
+    return encode_fp8_map(mk, p, K, pairs) && encode_fp8_map(mv, p, V, pairs);
   }
   return encode_page_map(mk, p, K) && encode_page_map(mv, p, V);
 }
@@ -546,7 +548,7 @@ dkv_status dkv_decode_attn_full(const dkv_params* p, const void* q, const dkv_kv
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   dkv::AttnArgs a = attn_args(p, q, L, ws);
-  if (!cache_views(p, K, V, &mk, &mv, &a)) return DKV_ERR_CUDA;
+  if (!cache_views(p, K, V, false, &mk, &mv, &a)) return DKV_ERR_CUDA;
   return run_attention(p, a, false, K->dtype == DKV_FP16, mk, mv, out, out_dtype, s);
 }
 
@@ -622,7 +624,7 @@ static dkv_status select_impl(const dkv_params* p, const void* q, const dkv_kv* 
   int* ucount = reinterpret_cast<int*>(ws + L.union_count);
 
   dkv::AttnArgs a = attn_args(p, q, L, ws);
-  if (!cache_views(p, K, V, &mk, &mv, &a)) return DKV_ERR_CUDA;
+  if (!cache_views(p, K, V, true, &mk, &mv, &a)) return DKV_ERR_CUDA;
   a.sub_log2 = p->page_size == 4 ? 2 : (p->page_size == 8 ? 1 : 0);
   if (hot != nullptr) {
     uint8_t* hs = static_cast<uint8_t*>(hot->state);

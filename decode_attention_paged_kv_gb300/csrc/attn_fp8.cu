@@ -61,7 +61,8 @@ namespace dkv {
 namespace {
 
 constexpr uint64_t kDrainLimitNs = 200000000ull;  // 200 ms for the whole drain
-constexpr int kListPages = 128;                   // pages of an item listed at a time
+constexpr int kListPages = 64;                    // pages of an item listed at a time
+constexpr int kMaxRagged = 128;    // sequences whose items are counted by their lengths
 constexpr float kSlack = 8.f;      // how far, in log2 units, a reference may be passed
 constexpr float kUnset = -1e30f;   // a reference before the first token
 
@@ -75,8 +76,9 @@ template <int D, int GL>
 struct Fp8Cfg {
   static constexpr int kPagesPerStage = 2;
   static constexpr int kTileBytes = kPage * D;      // one tensor's page of codes
-  static constexpr int kSlotBytes = 2 * kTileBytes;  // K codes | V codes
-  static constexpr int kStageBytes = kPagesPerStage * kSlotBytes;
+  // K codes of both pages | V codes of both
+  static constexpr int kVOffset = kPagesPerStage * kTileBytes;
+  static constexpr int kStageBytes = 2 * kVOffset;
   // Three CTAs an SM, each with 64 KiB of pages in flight; 8 heads of 128
   // channels need more shared memory for the warps' merge: two CTAs with 96 KiB.
   static constexpr int kCtas = GL == 8 && D == 128 ? 2 : 3;
@@ -91,9 +93,10 @@ struct Fp8Cfg {
   static constexpr int kListOffset =
       (kMergeOffset + (kConsumerWarps - 1) * GL * kMergeRow * 4 + 15) / 16 * 16;
   static constexpr int kBlockOffset = kListOffset + 16 * kListPages;
-  static constexpr int kMiscOffset = kBlockOffset + 4 * kListPages;
+  static constexpr int kFirstOffset = kBlockOffset + 4 * kListPages;
+  static constexpr int kMiscOffset = kFirstOffset + 4 * kMaxRagged;
   static constexpr int kSmemBytes = 1024 + kMiscOffset + 16;
-  static_assert(kSlotBytes % 1024 == 0, "tiles keep the swizzle's alignment");
+  static_assert(kTileBytes % 1024 == 0, "tiles keep the swizzle's alignment");
   static_assert(kStages % kConsumerWarps == 0, "one sub-ring per consumer warp");
   static_assert(kIssueLanes % kConsumerWarps == 0, "an issuing lane feeds one warp");
   static_assert(kMetaOffset % 16 == 0 && kListOffset % 16 == 0, "16-byte rows");
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
   int4* stage_meta = reinterpret_cast<int4*>(smem + C::kMetaOffset);
   volatile ItemDesc* desc = reinterpret_cast<volatile ItemDesc*>(smem + C::kDescOffset);
   float* mrg = reinterpret_cast<float*>(smem + C::kMergeOffset);
-  int4* list = reinterpret_cast<int4*>(smem + C::kListOffset);  // the same, of the item's pages
+  int4* list = reinterpret_cast<int4*>(smem + C::kListOffset);  // the same, of listed pages
   int* blocks = reinterpret_cast<int*>(smem + C::kBlockOffset);  // paged: their pool blocks
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOffset);
 
@@ -221,140 +224,262 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
     // Lane 0 fetches items and publishes their descriptors.  Stage q of an
     // item (pages 2 q, 2 q + 1) goes to consumer warp q % 4; lanes
     // 0 .. kIssueLanes - 1 issue one stage each per round.
+    //
+    // An item's pages are listed in parts of kListPages: page, mask, block and
+    // scales.  That takes four or five dependent loads (work counter -> length
+    // or union -> block table -> scales), about 3 us, in which the ring would
+    // run dry; so the next part is listed step by step between the rounds of
+    // the current one, each step using what the one before loaded.
     const uint64_t pol = l2_evict_first_policy();
+    // (the maps' boxes are two pages high for a dense cache read in order)
+    const bool pair_boxes = !SPARSE && a.bt == nullptr;
     const int my_w = lane & 3;  // consumer warp this lane feeds
     const bool issuer = lane < C::kIssueLanes;
     int wc = 0;           // stages issued so far to warp my_w
     bool failed = false;  // a lane gave up waiting for a free slot
-    for (int k = 0;; ++k) {
-      int item = 0, n = 0, b = 0, kvh = 0, first = 0, unit = 0;
-      while (true) {
-        if (lane == 0) item = static_cast<int>(atomicAdd(a.work_counter, 1u));
-        item = __shfl_sync(0xffffffffu, item, 0);
-        if (item >= a.n_items) {
-          item = -1;
-          n = 0;
-          break;
+    // Exact attention over sequences of their own lengths: tickets count the
+    // chunks that hold pages, sequence by sequence (heads inside), so no ticket
+    // is spent on an empty one.  seq_end[b]: the chunks of sequences 0 .. b.
+    int* seq_end = reinterpret_cast<int*>(smem + C::kFirstOffset);
+    const bool by_length = !SPARSE && a.lens != nullptr && a.B <= kMaxRagged && !whole;
+    int n_tickets = a.n_items;
+    if (by_length) {
+      int sum = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int bb = b0 + lane;
+        int c = 0;
+        if (bb < a.B)
+          c = static_cast<int>(ceil_div(ceil_div(max(0, min(a.lens[bb], a.N)), kPage),
+                                        a.pages_per_chunk));
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int up = __shfl_up_sync(0xffffffffu, c, o);
+          if (lane >= o) c += up;
         }
-        const int chunk = item % a.n_chunks;
-        unit = item / a.n_chunks;
-        kvh = unit % a.Hkv;
-        b = unit / a.Hkv;
-        first = chunk * a.pages_per_chunk;
-        const bool empty_seq = a.lens != nullptr && a.lens[b] <= 0;  // nothing to attend
-        if constexpr (SPARSE) {
-          if (unit_flags) {
-            int rdy = 1;
-            if (lane == 0) rdy = flag_wait_bounded(a.unit_ready + unit, a.wait_limit_ns, abort_flag);
-            if (!__shfl_sync(0xffffffffu, rdy, 0)) {
-              if (lane == 0 && *abort_flag == 0) {
-                set_status(a.status, kStatusTimeout);
-                *abort_flag = 1;
+        if (bb < a.B) seq_end[bb] = sum + c;
+        sum += __shfl_sync(0xffffffffu, c, 31);
+      }
+      __syncwarp();
+      n_tickets = sum * a.Hkv;  // (at most n_items)
+    }
+    constexpr int kPer = kListPages / 32;
+    // The part being listed, and where its listing has got to.
+    int item = 0, n = 0, b = 0, kvh = 0, unit = 0, first = 0, l0 = 0;
+    int step = 0;
+    // Taking an item before the current one is done costs balance at the end:
+    // only where a CTA gets several, and not while selections are still coming.
+    const bool ahead = !SPARSE && a.n_items >= 4 * static_cast<int>(gridDim.x);
+    int ticket = 0, count = 0, len = 0;
+    int page[kPer], mask[kPer], blk[kPer];
+    float ks[kPer], vs[kPer];
+    constexpr int kListed = 6;
+    // One step; with `block`, a step that has to wait does.
+    auto advance = [&](bool block) {
+      switch (step) {
+        case 0:  // a new item
+          if (lane == 0) ticket = static_cast<int>(atomicAdd(a.work_counter, 1u));
+          step = 1;
+          break;
+        case 1: {
+          item = __shfl_sync(0xffffffffu, ticket, 0);
+          l0 = 0;
+          if (item >= n_tickets) {
+            item = -1;
+            n = 0;
+            step = kListed;
+            break;
+          }
+          if (by_length) {
+            // the first sequence that ends past the ticket's chunk
+            const int at = item / a.Hkv;
+            kvh = item % a.Hkv;
+            b = 0;
+            for (int b0 = 0; b0 < a.B; b0 += 32) {
+              const int bb = b0 + lane;
+              b += __popc(__ballot_sync(0xffffffffu, bb < a.B && seq_end[bb] <= at));
+            }
+            const int c = at - (b > 0 ? seq_end[b - 1] : 0);
+            unit = b * a.Hkv + kvh;
+            item = unit * a.n_chunks + c;
+            first = c * a.pages_per_chunk;
+          } else {
+            unit = item / a.n_chunks;
+            first = item % a.n_chunks * a.pages_per_chunk;
+            kvh = unit % a.Hkv;
+            b = unit / a.Hkv;
+          }
+          len = a.lens != nullptr ? a.lens[b] : a.N;
+          step = SPARSE ? 2 : 3;
+          if constexpr (!SPARSE) break;
+          [[fallthrough]];
+        }
+        case 2:  // sparse: the union's size, once the unit's selection is there
+          if constexpr (SPARSE) {
+            if (unit_flags) {
+              int rdy = 1;
+              if (lane == 0)
+                rdy = block ? flag_wait_bounded(a.unit_ready + unit, a.wait_limit_ns, abort_flag)
+                            : ld_acquire_gpu(a.unit_ready + unit) != 0u;
+              if (!__shfl_sync(0xffffffffu, rdy, 0)) {
+                if (!block) break;  // asked again
+                if (lane == 0 && *abort_flag == 0) {
+                  set_status(a.status, kStatusTimeout);
+                  *abort_flag = 1;
+                }
+                item = -1;  // stop: publish the end of work
+                n = 0;
+                step = kListed;
+                break;
               }
-              item = -1;  // stop: publish the end of work
-              n = 0;
+            }
+            count = __ldcg(a.union_count + unit);
+          }
+          step = 3;
+          break;
+        case 3:  // the part's pages
+          if (l0 == 0) {
+            if constexpr (!SPARSE) count = static_cast<int>(ceil_div(min(len, a.N), kPage));
+            n = len <= 0 ? 0 : max(0, min(count - first, a.pages_per_chunk));
+            if (n == 0 && !whole) {  // no partial is read for it
+              step = 0;
               break;
             }
           }
-          n = max(0, min(__ldcg(a.union_count + unit) - first, a.pages_per_chunk));
-        } else {
-          const int Pb = static_cast<int>(ceil_div(seq_len_of(a.lens, b, a.N), kPage));
-          n = max(0, min(Pb - first, a.pages_per_chunk));
-        }
-        if (empty_seq) n = 0;
-        if (n == 0 && !whole) continue;  // no partial is read for it
-        break;
-      }
-      const int slot = k & 1;
-      int ok = 1;
-      if (lane == 0 && k >= 2) {
-        ok = mbar_wait_bounded(dempty0 + 8 * slot, ((k >> 1) - 1) & 1, a.wait_limit_ns,
-                               abort_flag);
-        if (!ok && *abort_flag == 0) {
-          set_status(a.status, kStatusTimeout);
-          *abort_flag = 1;
-        }
-      }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      if (lane == 0) {
-        desc[slot].item = item;
-        desc[slot].n_pages = n;
-        mbar_arrive(dfull0 + 8 * slot);  // release: consumers see the descriptor
-      }
-      if (item < 0) break;
-      const float* ks = a.k8.scale + kvh * a.k8.sh;
-      const float* vs = a.v8.scale + kvh * a.v8.sh;
-      bool lok = true;
-      for (int l0 = 0; l0 < n && lok; l0 += kListPages) {
-        // The pages of this part of the item, with their scales and blocks:
-        // one round of loads for all of them, while the ring still holds the
-        // previous item's pages.
-        const int ln = min(kListPages, n - l0);
-        __syncwarp();
-        for (int j = lane; j < ln; j += 32) {
-          int page = first + l0 + j, mask = 0xff;
-          if constexpr (SPARSE) {
-            const int2 e = __ldcg(a.union_list + static_cast<int64_t>(unit) * a.union_stride +
-                                  first + l0 + j);
-            page = e.x;
-            mask = e.y;
-          }
-          int64_t ko, vo;
-          if (a.bt != nullptr) {
-            // An entry outside [0, num_blocks) is clamped into it, so no copy
-            // leaves the pool, and reported as a failed check.
-            const int raw = a.bt[b * a.bts + page];
-            if (raw < 0 || raw >= a.nblocks) set_status(a.status, kStatusCheck);
-            const int blk = min(max(raw, 0), a.nblocks - 1);
-            blocks[j] = blk;
-            ko = blk * a.k8.sb;
-            vo = blk * a.v8.sb;
-          } else {
-            ko = b * a.k8.sb + page;
-            vo = b * a.v8.sb + page;
-          }
-          list[j] = make_int4(page, mask, __float_as_int(ks[ko]), __float_as_int(vs[vo]));
-        }
-        __syncwarp();
-        for (int j0 = 0; j0 < ln; j0 += C::kIssueLanes * kQ) {
-          const int j = j0 + lane * kQ;  // first page of this lane's stage
-          if (issuer && j < ln) {
-            const int c = wc + (j / kQ >> 2);            // (a list is a whole number of rounds)
-            const int s = my_w * C::kSub + c % C::kSub;  // warp my_w's sub-ring, in order
-            if (c >= C::kSub &&
-                !mbar_wait_bounded(empty0 + 8 * s, ((c / C::kSub) - 1) & 1, a.wait_limit_ns,
-                                   abort_flag)) {
-              lok = false;
-            } else {
-              const int cnt = min(kQ, ln - j);
 #pragma unroll
-              for (int t = 0; t < kQ; ++t)
-                if (t < cnt) stage_meta[s * kQ + t] = list[j + t];
-              mbar_arrive_expect_tx(full0 + 8 * s, cnt * C::kSlotBytes);
+          for (int i = 0; i < kPer; ++i) {
+            const int j = l0 + lane + 32 * i;
+            page[i] = first + j;
+            mask[i] = 0xff;
+            if constexpr (SPARSE) {
+              if (j < n) {
+                const int2 e = __ldcg(a.union_list +
+                                      static_cast<int64_t>(unit) * a.union_stride + first + j);
+                page[i] = e.x;
+                mask[i] = e.y;
+              }
+            }
+          }
+          step = 4;
+          if constexpr (SPARSE) break;
+          [[fallthrough]];
+        case 4:
+          if (a.bt != nullptr) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (l0 + lane + 32 * i < n) blk[i] = a.bt[b * a.bts + page[i]];
+          }
+          step = 5;
+          break;
+        case 5: {
+          const float* kscale = a.k8.scale + kvh * a.k8.sh;
+          const float* vscale = a.v8.scale + kvh * a.v8.sh;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            if (l0 + lane + 32 * i >= n) continue;
+            if (a.bt != nullptr) {
+              // An entry outside [0, num_blocks) is clamped into it, so no copy
+              // leaves the pool, and reported as a failed check.
+              if (blk[i] < 0 || blk[i] >= a.nblocks) set_status(a.status, kStatusCheck);
+              blk[i] = min(max(blk[i], 0), a.nblocks - 1);
+              ks[i] = kscale[blk[i] * a.k8.sb];
+              vs[i] = vscale[blk[i] * a.v8.sb];
+            } else {
+              ks[i] = kscale[b * a.k8.sb + page[i]];
+              vs[i] = vscale[b * a.v8.sb + page[i]];
+            }
+          }
+          step = kListed;
+          break;
+        }
+        default: break;
+      }
+    };
+    while (step != kListed) advance(true);
+    for (int k = -1;;) {
+      // The listed part becomes the current one: its registers go to the list.
+      const int c_item = item, c_n = n, c_b = b, c_kvh = kvh, c_l0 = l0;
+      const int ln = min(kListPages, n - l0);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int j = lane + 32 * i;
+        if (j < ln) {
+          list[j] = make_int4(page[i], mask[i], __float_as_int(ks[i]), __float_as_int(vs[i]));
+          blocks[j] = blk[i];
+        }
+      }
+      __syncwarp();
+      if (c_l0 == 0) {  // a new item: publish it
+        const int slot = ++k & 1;
+        int ok = 1;
+        if (lane == 0 && k >= 2) {
+          ok = mbar_wait_bounded(dempty0 + 8 * slot, ((k >> 1) - 1) & 1, a.wait_limit_ns,
+                                 abort_flag);
+          if (!ok && *abort_flag == 0) {
+            set_status(a.status, kStatusTimeout);
+            *abort_flag = 1;
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        if (lane == 0) {
+          desc[slot].item = c_item;
+          desc[slot].n_pages = c_n;
+          mbar_arrive(dfull0 + 8 * slot);  // release: consumers see the descriptor
+        }
+        if (c_item < 0) break;
+      }
+      // What is listed next: the item's next part, or a new item.
+      l0 += kListPages;
+      step = l0 < n ? 3 : 0;
+      bool lok = true;
+      for (int j0 = 0; j0 < ln; j0 += C::kIssueLanes * kQ) {
+        const int j = j0 + lane * kQ;  // first page of this lane's stage
+        if (issuer && j < ln) {
+          const int c = wc + (j / kQ >> 2);
+          const int s = my_w * C::kSub + c % C::kSub;  // warp my_w's sub-ring, in order
+          if (c >= C::kSub &&
+              !mbar_wait_bounded(empty0 + 8 * s, ((c / C::kSub) - 1) & 1, a.wait_limit_ns,
+                                 abort_flag)) {
+            lok = false;
+          } else {
+            const int cnt = min(kQ, ln - j);
+#pragma unroll
+            for (int t = 0; t < kQ; ++t)
+              if (t < cnt) stage_meta[s * kQ + t] = list[j + t];
+            const uint32_t dst = sbase + s * C::kStageBytes;
+            const uint32_t bar = full0 + 8 * s;
+            // {channel, token, -, kv head, batch} of the cache, or
+            // {channel, token in block, -, kv head, block} of a pool
+            if (pair_boxes) {  // a box of both pages (past the end: zeros)
+              mbar_arrive_expect_tx(bar, C::kStageBytes);
+              const int y = list[j].x * kPage;
+              tma_load_5d_hint(dst, &mk, bar, 0, y, 0, c_kvh, c_b, pol);
+              tma_load_5d_hint(dst + C::kVOffset, &mv, bar, 0, y, 0, c_kvh, c_b, pol);
+            } else {
+              mbar_arrive_expect_tx(bar, cnt * 2 * C::kTileBytes);
 #pragma unroll
               for (int t = 0; t < kQ; ++t) {
                 if (t < cnt) {
-                  // {channel, token, -, kv head, batch} of the cache, or
-                  // {channel, token in block, -, kv head, block} of a pool
-                  const uint32_t dst = sbase + s * C::kStageBytes + t * C::kSlotBytes;
                   const int y = a.bt != nullptr ? 0 : list[j + t].x * kPage;
-                  const int z = a.bt != nullptr ? blocks[j + t] : b;
-                  tma_load_5d_hint(dst, &mk, full0 + 8 * s, 0, y, 0, kvh, z, pol);
-                  tma_load_5d_hint(dst + C::kTileBytes, &mv, full0 + 8 * s, 0, y, 0, kvh, z, pol);
+                  const int z = a.bt != nullptr ? blocks[j + t] : c_b;
+                  const uint32_t d = dst + t * C::kTileBytes;
+                  tma_load_5d_hint(d, &mk, bar, 0, y, 0, c_kvh, z, pol);
+                  tma_load_5d_hint(d + C::kVOffset, &mv, bar, 0, y, 0, c_kvh, z, pol);
                 }
               }
             }
           }
-          lok = __all_sync(0xffffffffu, lok);
-          if (!lok) break;
         }
-        const int nq = static_cast<int>(ceil_div(ln, kQ));  // stages of this part
-        wc += nq > my_w ? (nq - my_w + 3) >> 2 : 0;
+        lok = __all_sync(0xffffffffu, lok);
+        if (!lok) break;
+        if (step != kListed && (ahead || step > 0)) advance(false);
       }
-      if (!__all_sync(0xffffffffu, lok)) {
+      const int nq = static_cast<int>(ceil_div(ln, kQ));  // stages of this part
+      wc += nq > my_w ? (nq - my_w + 3) >> 2 : 0;
+      if (!lok) {
         failed = true;
         break;
       }
+      while (step != kListed) advance(true);
     }
     if (lane == 0 && failed && *abort_flag == 0) {
       set_status(a.status, kStatusTimeout);
@@ -497,7 +622,7 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
 #pragma unroll
           for (int c = 0; c < D / 16; c += 2) {
             uint32_t r[4];  // [chunk c, c + 1][tokens 0-7, 8-15]
-            ldsm_x4(code_addr<D>(st + t * C::kSlotBytes, 8 * (mtx & 1) + mrow, c + (mtx >> 1)),
+            ldsm_x4(code_addr<D>(st + t * C::kTileBytes, 8 * (mtx & 1) + mrow, c + (mtx >> 1)),
                     r[0], r[1], r[2], r[3]);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -612,7 +737,7 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
         // (their weights are 0, but 0 * NaN is not).
         for (int t = 0; t < cnt; ++t) {
           const int nt = min(kPage, Nb - stage_meta[s * kQ + t].x * kPage);
-          uint8_t* vt = smem + s * C::kStageBytes + t * C::kSlotBytes + C::kTileBytes;
+          uint8_t* vt = smem + s * C::kStageBytes + C::kVOffset + t * C::kTileBytes;
           for (int i = lane; i < (kPage - nt) * (D / 16); i += 32)
             *reinterpret_cast<uint4*>(vt + nt * D + i * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -671,7 +796,7 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
 #pragma unroll
       for (int t = 0; t < kQ; ++t) {
         if (t < cnt) {
-          const uint32_t vt = st + t * C::kSlotBytes + C::kTileBytes;
+          const uint32_t vt = st + C::kVOffset + t * C::kTileBytes;
 #pragma unroll
           for (int c = 0; c < D / 16; c += 2) {
             uint32_t r[4];  // [chunk c, c + 1][tokens 0-7, 8-15]

@@ -359,7 +359,8 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 cudaError_t launch_attn(int d, bool f16, bool sparse, const AttnArgs& a, const CUtensorMap& mk,
                         const CUtensorMap& mv, int num_sms, cudaStream_t s);
 cudaError_t launch_attn_q4(int d, bool sparse, const AttnArgs& a, int num_sms, cudaStream_t s);
-// mk / mv: maps over the codes, box {d bytes, 16 tokens, 1, 1, 1}, d-byte swizzle.
+// mk / mv: maps over the codes, box {d bytes, 16 tokens, 1, 1, 1} (32 tokens for
+// exact attention over a dense cache), d-byte swizzle.
 cudaError_t launch_attn_fp8(int d, bool f16, bool sparse, const AttnArgs& a, const CUtensorMap& mk,
                             const CUtensorMap& mv, int num_sms, cudaStream_t s);
 cudaError_t attn_fp8_ctas_per_sm(int d, bool f16, bool sparse, int* out);
