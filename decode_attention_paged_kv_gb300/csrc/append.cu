@@ -22,11 +22,11 @@
 // nothing is shared between tokens, so it serves 16-bit caches of any length
 // and the single-token call of an 8-bit cache, where the d/16 threads agree on
 // the scale by shuffles.  append_block_kernel: one CTA of d threads per touched
-// block and head of an 8-bit cache, a thread per token and 16 channels; the
-// block's amax is reduced through shared memory while the values wait in
-// registers, so they are read once.  Both are bound by memory traffic (long
-// calls) or by the latency of the dependent loads length -> block table ->
-// scale (single tokens).
+// block of an 8-bit cache and four heads, a thread per token and 16 channels of
+// each; the blocks' amax are reduced through shared memory while the values wait
+// in registers, so they are read once, and the heads share the token's angles.
+// Both are bound by memory traffic (long calls) or by the latency of the
+// dependent loads length -> block table -> scale (single tokens).
 
 #include "dkv_device.cuh"
 #include "dkv_kernels.h"
@@ -63,11 +63,15 @@ __device__ __forceinline__ Chunks chunks_of(int j, int r, bool rotated) {
   return {16 * j, 16 * j + 8};
 }
 
+struct Raw {
+  uint4 u, w;
+};
+__device__ __forceinline__ Raw load_raw(const uint16_t* row, Chunks c) {
+  return {*reinterpret_cast<const uint4*>(row + c.c1), *reinterpret_cast<const uint4*>(row + c.c2)};
+}
 template <bool F16>
-__device__ __forceinline__ void load16(const uint16_t* row, Chunks c, float (&x)[16]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(row + c.c1);
-  const uint4 w = *reinterpret_cast<const uint4*>(row + c.c2);
-  const uint32_t v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void widen(const Raw& r, float (&x)[16]) {
+  const uint32_t v[8] = {r.u.x, r.u.y, r.u.z, r.u.w, r.w.x, r.w.y, r.w.z, r.w.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     x[2 * i] = lo16<F16>(v[i]);
@@ -84,26 +88,33 @@ __device__ __forceinline__ void store16(uint16_t* row, Chunks c, const float (&x
   *reinterpret_cast<uint4*>(row + c.c2) = make_uint4(v[4], v[5], v[6], v[7]);
 }
 
-// Rotate the 8 pairs of slot j at position pos.  (Intrinsics: no contraction
-// into fused multiply-adds, so a step has one result whatever the compiler.)
-template <bool IL>
-__device__ __forceinline__ void rotate16(const AppendArgs& a, int pos, int j, float (&x)[16]) {
-  const int64_t at = static_cast<int64_t>(pos) * (a.r / 2) + 8 * j;
+// cos and sin of the 8 pairs of slot j at position pos.
+struct Angles {
   float c[8], s[8];
+};
+__device__ __forceinline__ Angles angles_of(const AppendArgs& a, int pos, int j) {
+  Angles t;
+  const int64_t at = static_cast<int64_t>(pos) * (a.r / 2) + 8 * j;
 #pragma unroll
   for (int i = 0; i < 8; i += 4) {
     const float4 u = __ldg(reinterpret_cast<const float4*>(a.cos + at + i));
     const float4 w = __ldg(reinterpret_cast<const float4*>(a.sin + at + i));
-    c[i] = u.x, c[i + 1] = u.y, c[i + 2] = u.z, c[i + 3] = u.w;
-    s[i] = w.x, s[i + 1] = w.y, s[i + 2] = w.z, s[i + 3] = w.w;
+    t.c[i] = u.x, t.c[i + 1] = u.y, t.c[i + 2] = u.z, t.c[i + 3] = u.w;
+    t.s[i] = w.x, t.s[i + 1] = w.y, t.s[i + 2] = w.z, t.s[i + 3] = w.w;
   }
+  return t;
+}
+// Rotate a slot's 8 pairs.  (Intrinsics: no contraction into fused
+// multiply-adds, so a step has one result whatever the compiler.)
+template <bool IL>
+__device__ __forceinline__ void rotate16(const Angles& t, float (&x)[16]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float& p = x[IL ? 2 * i : i];
     float& q = x[IL ? 2 * i + 1 : 8 + i];
     const float u = p, w = q;
-    p = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(w, s[i]));
-    q = __fadd_rn(__fmul_rn(w, c[i]), __fmul_rn(u, s[i]));
+    p = __fsub_rn(__fmul_rn(u, t.c[i]), __fmul_rn(w, t.s[i]));
+    q = __fadd_rn(__fmul_rn(w, t.c[i]), __fmul_rn(u, t.s[i]));
   }
 }
 
@@ -221,8 +232,8 @@ __global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const Appen
   float x[16] = {};
   if (on) {
     const AppendRows& src = is_q ? a.q : (is_v ? a.v : a.k);
-    load16<F16>(src.p + b * src.sb + t * src.st + h * src.sh, c, x);
-    if (rotated) rotate16<IL>(a, pos, j, x);
+    widen<F16>(load_raw(src.p + b * src.sb + t * src.st + h * src.sh, c), x);
+    if (rotated) rotate16<IL>(angles_of(a, pos, j), x);
     if (is_q) store16<F16>(a.q_out + b * a.o_sb + t * a.o_st + h * a.o_sh, c, x);
   }
   const AppendCache& cache = is_v ? a.V : a.K;
@@ -254,65 +265,100 @@ __global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const Appen
   }
 }
 
+constexpr int kHeads = 4;  // heads of a block kernel's CTA
+
 template <int D, bool F16, bool IL>
 __global__ void __launch_bounds__(D) append_block_kernel(const AppendArgs a) {
-  constexpr int L = D / 16;
-  __shared__ uint32_t warp_amax[D / 32];
+  constexpr int L = D / 16, kWarps = D / 32;
+  __shared__ uint32_t warp_amax[kWarps][kHeads];
   griddep_launch_dependents();
   griddep_wait();
-  // (sequence, touched page, head), heads fastest: a row's heads lie together
-  const uint32_t heads = 2 * a.Hkv + a.Hq;
-  const int hx = static_cast<int>(blockIdx.x % heads);
-  const int y = static_cast<int>(blockIdx.x / heads % static_cast<uint32_t>(a.pages));
-  const int b = static_cast<int>(blockIdx.x / heads / static_cast<uint32_t>(a.pages));
+  // (sequence, touched page, four heads of k, v or q), heads fastest
+  const uint32_t kv_groups = (a.Hkv + kHeads - 1) / kHeads;
+  const uint32_t groups = 2 * kv_groups + (a.Hq + kHeads - 1) / kHeads;
+  const uint32_t gx = blockIdx.x % groups;
+  const int y = static_cast<int>(blockIdx.x / groups % static_cast<uint32_t>(a.pages));
+  const int b = static_cast<int>(blockIdx.x / groups / static_cast<uint32_t>(a.pages));
   const NewTokens nt = new_tokens(a, b);
   const int page = nt.start / kPage + y;
   if (nt.n == 0 || page * kPage >= nt.start + nt.n) return;  // no token of this page
   const int j = threadIdx.x % L, i = threadIdx.x / L;
   const int pos = page * kPage + i, t = pos - nt.start;
   const bool on = t >= 0 && t < nt.n;
-  const bool is_q = hx >= 2 * a.Hkv, is_v = !is_q && hx >= a.Hkv;
-  const int h = is_q ? hx - 2 * a.Hkv : (is_v ? hx - a.Hkv : hx);
+  const bool is_q = gx >= 2 * kv_groups, is_v = !is_q && gx >= kv_groups;
+  const int h0 = static_cast<int>(is_q ? gx - 2 * kv_groups : (is_v ? gx - kv_groups : gx)) * kHeads;
+  const int nh = min(kHeads, (is_q ? a.Hq : a.Hkv) - h0);
   const bool rotated = !is_v && 16 * j < a.r;
   const Chunks c = chunks_of<IL>(j, a.r, rotated);
   const AppendRows& src = is_q ? a.q : (is_v ? a.v : a.k);
-  float x[16] = {};
+  Raw raw[kHeads] = {};
+  Angles ang;
   if (on) {
-    load16<F16>(src.p + b * src.sb + t * src.st + h * src.sh, c, x);
-    if (rotated) rotate16<IL>(a, pos, j, x);
+    const uint16_t* row = src.p + b * src.sb + t * src.st + h0 * src.sh;
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h)
+      if (h < nh) raw[h] = load_raw(row + h * src.sh, c);
+    if (rotated) ang = angles_of(a, pos, j);
   }
   if (is_q) {
-    if (on) store16<F16>(a.q_out + b * a.o_sb + t * a.o_st + h * a.o_sh, c, x);
+    if (!on) return;
+    uint16_t* out = a.q_out + b * a.o_sb + t * a.o_st + h0 * a.o_sh;
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      if (h >= nh) break;
+      float x[16];
+      widen<F16>(raw[h], x);
+      if (rotated) rotate16<IL>(ang, x);
+      store16<F16>(out + h * a.o_sh, c, x);
+    }
     return;
   }
   const AppendCache& cache = is_v ? a.V : a.K;
   const PageAt at = page_at(a, b, page, D);
   if (at.blk < 0) return;
-  float* sp = scale_at(a, cache, at, page, h);
+  float* sp = scale_at(a, cache, at, page, h0);
   const int kept = max(0, nt.start - page * kPage);  // tokens the block held before
-  const float old = kept > 0 ? *sp : 0.f;
-  const uint32_t wm = __reduce_max_sync(0xffffffffu, amax_bits(x));
-  if (threadIdx.x % 32 == 0) warp_amax[threadIdx.x / 32] = wm;
-  __syncthreads();  // (every thread has read the old scale)
-  uint32_t m = warp_amax[0];
+  float old[kHeads];
 #pragma unroll
-  for (int w = 1; w < D / 32; ++w) m = max(m, warp_amax[w]);
-  const float s = fmaxf(scale_for(m, a.e_lo, a.e_hi), old);
-  const Divider by(s);
-  uint8_t* row = static_cast<uint8_t*>(cache.p) + at.blk * cache.sb + h * cache.sh + at.tok + i * D;
-  if (on)
-    store_codes(row, c, by, x);
-  else if (i < kept && s > old)
-    rescale_codes(row, c, old, by);
-  if (threadIdx.x == 0 && s != old) *sp = s;
+  for (int h = 0; h < kHeads; ++h) {
+    old[h] = kept > 0 && h < nh ? sp[h * cache.ssh] : 0.f;
+    float x[16];
+    widen<F16>(raw[h], x);
+    if (rotated) rotate16<IL>(ang, x);  // (again below: cheaper than 16 registers a head)
+    const uint32_t wm = __reduce_max_sync(0xffffffffu, on ? amax_bits(x) : 0u);
+    if (threadIdx.x % 32 == 0) warp_amax[threadIdx.x / 32][h] = wm;
+  }
+  __syncthreads();  // (every thread has read the old scales)
+  uint8_t* rows = static_cast<uint8_t*>(cache.p) + at.blk * cache.sb + h0 * cache.sh + at.tok + i * D;
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    if (h >= nh) break;
+    uint32_t m = warp_amax[0][h];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) m = max(m, warp_amax[w][h]);
+    const float s = fmaxf(scale_for(m, a.e_lo, a.e_hi), old[h]);
+    const Divider by(s);
+    uint8_t* row = rows + h * cache.sh;
+    if (on) {
+      float x[16];
+      widen<F16>(raw[h], x);
+      if (rotated) rotate16<IL>(ang, x);
+      store_codes(row, c, by, x);
+    } else if (i < kept && s > old[h]) {
+      rescale_codes(row, c, old[h], by);
+    }
+    if (threadIdx.x == 0 && s != old[h]) sp[h * cache.ssh] = s;
+  }
 }
 
 template <int D, bool F16, bool IL>
 cudaError_t launch_t(bool eight, const AppendArgs& a, cudaStream_t s) {
   const uint32_t heads = 2 * a.Hkv + a.Hq;
-  if (eight && a.T > 1)
+  if (eight && a.T > 1) {
+    const uint32_t groups = 2 * ((a.Hkv + kHeads - 1) / kHeads) + (a.Hq + kHeads - 1) / kHeads;
     return launch_pdl(append_block_kernel<D, F16, IL>,
-                      dim3(static_cast<uint32_t>(a.B) * a.pages * heads), dim3(D), 0, s, a);
+                      dim3(static_cast<uint32_t>(a.B) * a.pages * groups), dim3(D), 0, s, a);
+  }
   const dim3 grid(static_cast<unsigned>(
                       ceil_div(static_cast<int64_t>(a.T) * heads * (D / 16), kTokenThreads)),
                   a.B);

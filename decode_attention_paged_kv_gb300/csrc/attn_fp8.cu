@@ -842,7 +842,10 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
 
     // Warps 1-3 hand their states to warp 0, which merges them with its own
     // (ascending warp order) and writes the item's partial.
+    // The barrier also tells that warp 0 is done with the merge area, and that all
+    // have read the item's descriptor.
     if (consumers_any(aborted)) return;
+    if (threadIdx.x == 0) mbar_arrive(dempty0 + 8 * slot);
     if (warp > 0 && t4 < kOwners) {
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
@@ -906,8 +909,6 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
         }
       }
     }
-    consumers_sync();  // merge area free again; the descriptor slot was read by all
-    if (threadIdx.x == 0) mbar_arrive(dempty0 + 8 * slot);
   }
 }
 
