@@ -1102,7 +1102,9 @@ dkv_status dkv_kv_append(const dkv_append* p, const dkv_kv* K, const dkv_kv* V, 
   a.e_lo = f16 ? -15 : -117;
   a.e_hi = f16 ? 7 : 119;
   a.status = static_cast<uint32_t*>(workspace);
-  return cuda_status(dkv::launch_append(p->head_dim, f16, is_fp8(K), p->interleaved != 0, a,
+  const int sms = current_sm_count();
+  if (sms <= 0) return DKV_ERR_CUDA;
+  return cuda_status(dkv::launch_append(p->head_dim, f16, is_fp8(K), p->interleaved != 0, a, sms,
                                         static_cast<cudaStream_t>(stream)));
 }
 

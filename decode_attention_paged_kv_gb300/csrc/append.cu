@@ -265,99 +265,159 @@ __global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const Appen
   }
 }
 
-constexpr int kHeads = 4;  // heads of a block kernel's CTA
+constexpr int kHeads = 4;      // heads of a block kernel's work item
+constexpr int kMaxSeqs = 128;  // sequences whose touched pages are counted first
+// CTAs of the persistent grid on an SM: 128 registers a thread, or 102.
+template <int D, bool EIGHT>
+constexpr int block_ctas() {
+  return (EIGHT ? 4 : 5) * (128 / D);
+}
 
-template <int D, bool F16, bool IL>
-__global__ void __launch_bounds__(D) append_block_kernel(const AppendArgs a) {
+template <int D, bool F16, bool EIGHT, bool IL>
+__global__ void __launch_bounds__(D, block_ctas<D, EIGHT>()) append_block_kernel(const AppendArgs a) {
   constexpr int L = D / 16, kWarps = D / 32;
-  __shared__ uint32_t warp_amax[kWarps][kHeads];
+  __shared__ uint32_t warp_amax[2][kWarps][kHeads];
+  __shared__ int page_end[kMaxSeqs];  // pages that sequences 0 .. b touch
+  __shared__ NewTokens seqs[kMaxSeqs];
   griddep_launch_dependents();
   griddep_wait();
-  // (sequence, touched page, four heads of k, v or q), heads fastest
+  // Work items: (sequence, touched page, four heads of k, v or q), heads fastest.
+  // Up to kMaxSeqs sequences, only the pages they touch are counted.
+  const bool counted = a.B <= kMaxSeqs;
   const uint32_t kv_groups = (a.Hkv + kHeads - 1) / kHeads;
   const uint32_t groups = 2 * kv_groups + (a.Hq + kHeads - 1) / kHeads;
-  const uint32_t gx = blockIdx.x % groups;
-  const int y = static_cast<int>(blockIdx.x / groups % static_cast<uint32_t>(a.pages));
-  const int b = static_cast<int>(blockIdx.x / groups / static_cast<uint32_t>(a.pages));
-  const NewTokens nt = new_tokens(a, b);
-  const int page = nt.start / kPage + y;
-  if (nt.n == 0 || page * kPage >= nt.start + nt.n) return;  // no token of this page
-  const int j = threadIdx.x % L, i = threadIdx.x / L;
-  const int pos = page * kPage + i, t = pos - nt.start;
-  const bool on = t >= 0 && t < nt.n;
-  const bool is_q = gx >= 2 * kv_groups, is_v = !is_q && gx >= kv_groups;
-  const int h0 = static_cast<int>(is_q ? gx - 2 * kv_groups : (is_v ? gx - kv_groups : gx)) * kHeads;
-  const int nh = min(kHeads, (is_q ? a.Hq : a.Hkv) - h0);
-  const bool rotated = !is_v && 16 * j < a.r;
-  const Chunks c = chunks_of<IL>(j, a.r, rotated);
-  const AppendRows& src = is_q ? a.q : (is_v ? a.v : a.k);
-  Raw raw[kHeads] = {};
-  Angles ang;
-  if (on) {
-    const uint16_t* row = src.p + b * src.sb + t * src.st + h0 * src.sh;
+  const int lane = threadIdx.x % 32;
+  uint32_t n_items = static_cast<uint32_t>(a.B) * a.pages * groups;
+  if (counted) {
+    if (threadIdx.x < 32) {
+      int sum = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int b = b0 + lane;
+        int c = 0;
+        if (b < a.B) {
+          const NewTokens nt = new_tokens(a, b);
+          seqs[b] = nt;
+          if (nt.n > 0) c = (nt.start + nt.n - 1) / kPage - nt.start / kPage + 1;
+        }
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h)
-      if (h < nh) raw[h] = load_raw(row + h * src.sh, c);
-    if (rotated) ang = angles_of(a, pos, j);
+        for (int o = 1; o < 32; o *= 2) {
+          const int up = __shfl_up_sync(0xffffffffu, c, o);
+          if (lane >= o) c += up;
+        }
+        if (b < a.B) page_end[b] = sum + c;
+        sum += __shfl_sync(0xffffffffu, c, 31);
+      }
+    }
+    __syncthreads();
+    n_items = static_cast<uint32_t>(page_end[a.B - 1]) * groups;
   }
-  if (is_q) {
-    if (!on) return;
-    uint16_t* out = a.q_out + b * a.o_sb + t * a.o_st + h0 * a.o_sh;
+  const int j = threadIdx.x % L, i = threadIdx.x / L;
+  int turn = 0;
+  for (uint32_t item = blockIdx.x; item < n_items; item += gridDim.x) {
+    const uint32_t gx = item % groups;
+    int y = static_cast<int>(item / groups), b;
+    NewTokens nt;
+    if (counted) {  // the first sequence that ends past the page
+      b = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32)
+        b += __popc(__ballot_sync(0xffffffffu, b0 + lane < a.B && page_end[b0 + lane] <= y));
+      if (b > 0) y -= page_end[b - 1];
+      nt = seqs[b];
+    } else {
+      b = y / a.pages;
+      y %= a.pages;
+      nt = new_tokens(a, b);
+    }
+    const int page = nt.start / kPage + y;
+    if (nt.n == 0 || page * kPage >= nt.start + nt.n) continue;  // no token of this page
+    const int pos = page * kPage + i, t = pos - nt.start;
+    const bool on = t >= 0 && t < nt.n;
+    const bool is_q = gx >= 2 * kv_groups, is_v = !is_q && gx >= kv_groups;
+    const int h0 =
+        static_cast<int>(is_q ? gx - 2 * kv_groups : (is_v ? gx - kv_groups : gx)) * kHeads;
+    const int nh = min(kHeads, (is_q ? a.Hq : a.Hkv) - h0);
+    const bool rotated = !is_v && 16 * j < a.r;
+    const Chunks c = chunks_of<IL>(j, a.r, rotated);
+    const AppendRows& src = is_q ? a.q : (is_v ? a.v : a.k);
+    Raw raw[kHeads] = {};
+    Angles ang;
+    if (on) {
+      const uint16_t* row = src.p + b * src.sb + t * src.st + h0 * src.sh;
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h)
+        if (h < nh) raw[h] = load_raw(row + h * src.sh, c);
+      if (rotated) ang = angles_of(a, pos, j);
+    }
+    const AppendCache& cache = is_v ? a.V : a.K;
+    PageAt at{-1, 0};
+    if (!is_q) at = page_at(a, b, page, D);
+    if (is_q || (!EIGHT && at.blk >= 0)) {  // 16-bit rows
+      uint16_t* out = is_q ? a.q_out + b * a.o_sb + t * a.o_st + h0 * a.o_sh
+                           : static_cast<uint16_t*>(cache.p) + at.blk * cache.sb + h0 * cache.sh +
+                                 at.tok + i * D;
+      const int64_t osh = is_q ? a.o_sh : cache.sh;
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h) {
+        if (!on || h >= nh) break;
+        float x[16];
+        widen<F16>(raw[h], x);
+        if (rotated) rotate16<IL>(ang, x);
+        store16<F16>(out + h * osh, c, x);
+      }
+      continue;
+    }
+    if (!EIGHT || at.blk < 0) continue;
+    float* sp = scale_at(a, cache, at, page, h0);
+    const int kept = max(0, nt.start - page * kPage);  // tokens the block held before
+    float old[kHeads];
+    turn ^= 1;
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      old[h] = kept > 0 && h < nh ? sp[h * cache.ssh] : 0.f;
+      float x[16];
+      widen<F16>(raw[h], x);
+      if (rotated) rotate16<IL>(ang, x);  // (again below: cheaper than 16 registers a head)
+      const uint32_t wm = __reduce_max_sync(0xffffffffu, on ? amax_bits(x) : 0u);
+      if (lane == 0) warp_amax[turn][threadIdx.x / 32][h] = wm;
+    }
+    // Every thread has read the old scales; the other turn's maxima are free once
+    // all have passed this barrier again.
+    __syncthreads();
+    uint8_t* rows =
+        static_cast<uint8_t*>(cache.p) + at.blk * cache.sb + h0 * cache.sh + at.tok + i * D;
 #pragma unroll
     for (int h = 0; h < kHeads; ++h) {
       if (h >= nh) break;
-      float x[16];
-      widen<F16>(raw[h], x);
-      if (rotated) rotate16<IL>(ang, x);
-      store16<F16>(out + h * a.o_sh, c, x);
+      uint32_t m = warp_amax[turn][0][h];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) m = max(m, warp_amax[turn][w][h]);
+      const float s = fmaxf(scale_for(m, a.e_lo, a.e_hi), old[h]);
+      const Divider by(s);
+      uint8_t* row = rows + h * cache.sh;
+      if (on) {
+        float x[16];
+        widen<F16>(raw[h], x);
+        if (rotated) rotate16<IL>(ang, x);
+        store_codes(row, c, by, x);
+      } else if (i < kept && s > old[h]) {
+        rescale_codes(row, c, old[h], by);
+      }
+      if (threadIdx.x == 0 && s != old[h]) sp[h * cache.ssh] = s;
     }
-    return;
-  }
-  const AppendCache& cache = is_v ? a.V : a.K;
-  const PageAt at = page_at(a, b, page, D);
-  if (at.blk < 0) return;
-  float* sp = scale_at(a, cache, at, page, h0);
-  const int kept = max(0, nt.start - page * kPage);  // tokens the block held before
-  float old[kHeads];
-#pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
-    old[h] = kept > 0 && h < nh ? sp[h * cache.ssh] : 0.f;
-    float x[16];
-    widen<F16>(raw[h], x);
-    if (rotated) rotate16<IL>(ang, x);  // (again below: cheaper than 16 registers a head)
-    const uint32_t wm = __reduce_max_sync(0xffffffffu, on ? amax_bits(x) : 0u);
-    if (threadIdx.x % 32 == 0) warp_amax[threadIdx.x / 32][h] = wm;
-  }
-  __syncthreads();  // (every thread has read the old scales)
-  uint8_t* rows = static_cast<uint8_t*>(cache.p) + at.blk * cache.sb + h0 * cache.sh + at.tok + i * D;
-#pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
-    if (h >= nh) break;
-    uint32_t m = warp_amax[0][h];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) m = max(m, warp_amax[w][h]);
-    const float s = fmaxf(scale_for(m, a.e_lo, a.e_hi), old[h]);
-    const Divider by(s);
-    uint8_t* row = rows + h * cache.sh;
-    if (on) {
-      float x[16];
-      widen<F16>(raw[h], x);
-      if (rotated) rotate16<IL>(ang, x);
-      store_codes(row, c, by, x);
-    } else if (i < kept && s > old[h]) {
-      rescale_codes(row, c, old[h], by);
-    }
-    if (threadIdx.x == 0 && s != old[h]) sp[h * cache.ssh] = s;
   }
 }
 
 template <int D, bool F16, bool IL>
-cudaError_t launch_t(bool eight, const AppendArgs& a, cudaStream_t s) {
+cudaError_t launch_t(bool eight, const AppendArgs& a, int num_sms, cudaStream_t s) {
   const uint32_t heads = 2 * a.Hkv + a.Hq;
-  if (eight && a.T > 1) {
-    const uint32_t groups = 2 * ((a.Hkv + kHeads - 1) / kHeads) + (a.Hq + kHeads - 1) / kHeads;
-    return launch_pdl(append_block_kernel<D, F16, IL>,
-                      dim3(static_cast<uint32_t>(a.B) * a.pages * groups), dim3(D), 0, s, a);
+  if (a.T > 1) {
+    const int64_t groups = 2 * ceil_div(a.Hkv, kHeads) + ceil_div(a.Hq, kHeads);
+    const int64_t items = static_cast<int64_t>(a.B) * a.pages * groups;
+    const int64_t most = static_cast<int64_t>(num_sms) *
+                         (eight ? block_ctas<D, true>() : block_ctas<D, false>());
+    const dim3 grid(static_cast<unsigned>(items < most ? items : most));
+    return eight ? launch_pdl(append_block_kernel<D, F16, true, IL>, grid, dim3(D), 0, s, a)
+                 : launch_pdl(append_block_kernel<D, F16, false, IL>, grid, dim3(D), 0, s, a);
   }
   const dim3 grid(static_cast<unsigned>(
                       ceil_div(static_cast<int64_t>(a.T) * heads * (D / 16), kTokenThreads)),
@@ -370,17 +430,17 @@ cudaError_t launch_t(bool eight, const AppendArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_append(int d, bool f16, bool eight, bool interleaved, const AppendArgs& a,
-                          cudaStream_t s) {
+                          int num_sms, cudaStream_t s) {
   if (d == 128) {
-    if (f16) return interleaved ? launch_t<128, true, true>(eight, a, s)
-                                : launch_t<128, true, false>(eight, a, s);
-    return interleaved ? launch_t<128, false, true>(eight, a, s)
-                       : launch_t<128, false, false>(eight, a, s);
+    if (f16) return interleaved ? launch_t<128, true, true>(eight, a, num_sms, s)
+                                : launch_t<128, true, false>(eight, a, num_sms, s);
+    return interleaved ? launch_t<128, false, true>(eight, a, num_sms, s)
+                       : launch_t<128, false, false>(eight, a, num_sms, s);
   }
-  if (f16) return interleaved ? launch_t<64, true, true>(eight, a, s)
-                              : launch_t<64, true, false>(eight, a, s);
-  return interleaved ? launch_t<64, false, true>(eight, a, s)
-                     : launch_t<64, false, false>(eight, a, s);
+  if (f16) return interleaved ? launch_t<64, true, true>(eight, a, num_sms, s)
+                              : launch_t<64, true, false>(eight, a, num_sms, s);
+  return interleaved ? launch_t<64, false, true>(eight, a, num_sms, s)
+                     : launch_t<64, false, false>(eight, a, num_sms, s);
 }
 
 }  // namespace dkv

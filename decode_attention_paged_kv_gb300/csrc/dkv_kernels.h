@@ -383,7 +383,7 @@ cudaError_t launch_unit_select(int d, bool f16, bool m8, const UnitSelectArgs& a
 cudaError_t launch_meta(bool q4, bool f16, const MetaArgs& a, cudaStream_t s);
 cudaError_t launch_meta_fp8(int d, bool f16, const MetaFp8Args& a, cudaStream_t s);
 cudaError_t launch_append(int d, bool f16, bool eight, bool interleaved, const AppendArgs& a,
-                          cudaStream_t s);
+                          int num_sms, cudaStream_t s);
 cudaError_t launch_quant4(int64_t rows, int d, const void* x, void* codes, void* gmin,
                           void* gmax, cudaStream_t s);
 cudaError_t launch_dequant4(int64_t rows, int d, const void* codes, const void* gmin,
