@@ -410,7 +410,9 @@ __global__ void __launch_bounds__(D, block_ctas<D, EIGHT>()) append_block_kernel
 template <int D, bool F16, bool IL>
 cudaError_t launch_t(bool eight, const AppendArgs& a, int num_sms, cudaStream_t s) {
   const uint32_t heads = 2 * a.Hkv + a.Hq;
-  if (a.T > 1) {
+  // Few tokens into a 16-bit cache: 4 a sequence of 64 take 2.7 us here against
+  // 3.7 in the persistent kernel, 8K prompts 302 us against 270.
+  if (a.T > (eight ? 1 : 16)) {
     const int64_t groups = 2 * ceil_div(a.Hkv, kHeads) + ceil_div(a.Hq, kHeads);
     const int64_t items = static_cast<int64_t>(a.B) * a.pages * groups;
     const int64_t most = static_cast<int64_t>(num_sms) *

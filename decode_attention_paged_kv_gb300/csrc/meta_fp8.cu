@@ -16,7 +16,7 @@
 namespace dkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 __device__ __forceinline__ __half2 codes2(uint32_t w) {  // the low half's two codes
   uint32_t r;
@@ -40,8 +40,9 @@ __device__ __forceinline__ uint32_t pack_outward(float lo, float hi) {
   }
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, 2) meta_fp8_kernel(const MetaFp8Args a) {
+// MULTI: pages of several blocks (S > 16).
+template <int D, bool F16, bool MULTI>
+__global__ void __launch_bounds__(kThreads, MULTI ? 3 : 5) meta_fp8_kernel(const MetaFp8Args a) {
   constexpr int kVec = D / 16;  // 16-byte vectors per row
   griddep_launch_dependents();
   griddep_wait();
@@ -61,10 +62,12 @@ __global__ void __launch_bounds__(kThreads, 2) meta_fp8_kernel(const MetaFp8Args
     if (t0 >= Nb || (a.lens != nullptr && a.lens[b] <= 0)) continue;
     const int nt = min(a.S, Nb - t0);
     float mn[16], mx[16];
+    if constexpr (MULTI) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) mn[i] = INFINITY, mx[i] = -INFINITY;
+      for (int i = 0; i < 16; ++i) mn[i] = INFINITY, mx[i] = -INFINITY;
+    }
 #pragma unroll 1
-    for (int c0 = 0; c0 < nt; c0 += kPage) {
+    for (int c0 = 0; c0 < (MULTI ? nt : 1); c0 += kPage) {
       const int cp = (t0 + c0) / kPage;  // cache page
       const int ntc = min(kPage, nt - c0);
       int64_t at, so;
@@ -78,16 +81,16 @@ __global__ void __launch_bounds__(kThreads, 2) meta_fp8_kernel(const MetaFp8Args
       }
       const uint8_t* src = a.codes + at + h * a.sh + 16 * v;
       const float s = a.scale.scale[so + h * a.scale.sh];
-      uint4 x[kPage];
-#pragma unroll
-      for (int t = 0; t < kPage; ++t)
-        if (t < ntc) x[t] = __ldcs(reinterpret_cast<const uint4*>(src + t * D));
       __half2 lo[8], hi[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         lo[u] = __half2half2(__ushort_as_half(0x7c00));  // +inf
         hi[u] = __half2half2(__ushort_as_half(0xfc00));  // -inf
       }
+      uint4 x[kPage];
+#pragma unroll
+      for (int t = 0; t < kPage; ++t)
+        if (t < ntc) x[t] = __ldcs(reinterpret_cast<const uint4*>(src + t * D));
 #pragma unroll
       for (int t = 0; t < kPage; ++t) {
         if (t < ntc) {
@@ -102,10 +105,12 @@ __global__ void __launch_bounds__(kThreads, 2) meta_fp8_kernel(const MetaFp8Args
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        mn[2 * u] = fminf(mn[2 * u], __fmul_rd(__low2float(lo[u]), s));
-        mn[2 * u + 1] = fminf(mn[2 * u + 1], __fmul_rd(__high2float(lo[u]), s));
-        mx[2 * u] = fmaxf(mx[2 * u], __fmul_ru(__low2float(hi[u]), s));
-        mx[2 * u + 1] = fmaxf(mx[2 * u + 1], __fmul_ru(__high2float(hi[u]), s));
+        const float m0 = __fmul_rd(__low2float(lo[u]), s), m1 = __fmul_rd(__high2float(lo[u]), s);
+        const float M0 = __fmul_ru(__low2float(hi[u]), s), M1 = __fmul_ru(__high2float(hi[u]), s);
+        mn[2 * u] = MULTI ? fminf(mn[2 * u], m0) : m0;
+        mn[2 * u + 1] = MULTI ? fminf(mn[2 * u + 1], m1) : m1;
+        mx[2 * u] = MULTI ? fmaxf(mx[2 * u], M0) : M0;
+        mx[2 * u + 1] = MULTI ? fmaxf(mx[2 * u + 1], M1) : M1;
       }
     }
     const int64_t o = (bh * a.P + page) * D + 16 * v;
@@ -123,18 +128,24 @@ __global__ void __launch_bounds__(kThreads, 2) meta_fp8_kernel(const MetaFp8Args
   }
 }
 
+template <bool MULTI>
+cudaError_t launch_t(int d, bool f16, const MetaFp8Args& a, dim3 grid, cudaStream_t s) {
+  const dim3 block(kThreads);
+  if (d == 128)
+    return f16 ? launch_pdl(meta_fp8_kernel<128, true, MULTI>, grid, block, 0, s, a)
+               : launch_pdl(meta_fp8_kernel<128, false, MULTI>, grid, block, 0, s, a);
+  return f16 ? launch_pdl(meta_fp8_kernel<64, true, MULTI>, grid, block, 0, s, a)
+             : launch_pdl(meta_fp8_kernel<64, false, MULTI>, grid, block, 0, s, a);
+}
+
 }  // namespace
 
 cudaError_t launch_meta_fp8(int d, bool f16, const MetaFp8Args& a, cudaStream_t s) {
   const int64_t work =
       static_cast<int64_t>(a.B) * a.Hkv * (a.last_only ? 1 : a.P) * (d / 16);
   const int64_t blocks = ceil_div(work, kThreads);
-  const dim3 grid(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30))), block(kThreads);
-  if (d == 128)
-    return f16 ? launch_pdl(meta_fp8_kernel<128, true>, grid, block, 0, s, a)
-               : launch_pdl(meta_fp8_kernel<128, false>, grid, block, 0, s, a);
-  return f16 ? launch_pdl(meta_fp8_kernel<64, true>, grid, block, 0, s, a)
-             : launch_pdl(meta_fp8_kernel<64, false>, grid, block, 0, s, a);
+  const dim3 grid(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30)));
+  return a.S > kPage ? launch_t<true>(d, f16, a, grid, s) : launch_t<false>(d, f16, a, grid, s);
 }
 
 }  // namespace dkv
