@@ -21,6 +21,8 @@ strides, token stride d), ``Q4Cache`` tuples in the 4-bit format,
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 import threading
@@ -147,6 +149,7 @@ class _Append(ctypes.Structure):
 
 
 _lib = None
+_binding = None
 _lock = threading.Lock()
 
 
@@ -203,6 +206,26 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+def _load_binding():
+    """The native marshalling of a decode step's calls (csrc/binding.cpp)."""
+    global _binding
+    lib()
+    with _lock:
+        if _binding is None:
+            path = _build_mod.BINDING
+            if not os.path.exists(path):
+                raise RuntimeError(
+                    f"{os.path.basename(path)} not found at {path}; build it with "
+                    "`python -m decode_attention_paged_kv_gb300.build`")
+            loader = importlib.machinery.ExtensionFileLoader(f"{__name__}._binding", path)
+            spec = importlib.util.spec_from_loader(loader.name, loader)
+            m = importlib.util.module_from_spec(spec)
+            loader.exec_module(m)
+            m.setup(Q4Cache, PagedCache, Fp8Cache, Fp8PagedCache, Meta8, DkvError)
+            _binding = m
+    return _binding
+
+
 def status_string(status: int) -> str:
     return lib().dkv_status_string(int(status)).decode()
 
@@ -216,22 +239,6 @@ def _stream(t: torch.Tensor) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
-def _call(where: str, dev: int, *args) -> None:
-    """One library call on the current stream of CUDA device `dev`, which is
-    made the current device for it; raises on an error status."""
-    if dev < 0:
-        raise ValueError(f"{where} wants CUDA tensors")
-    fn = getattr(_lib or lib(), where)
-    # (the raw stream handle: a Stream object costs more than the launch)
-    if torch._C._cuda_getDevice() == dev:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if st != DKV_OK:
-        raise DkvError(st, where)
-
-
 _DTYPE_CODES = {torch.bfloat16: DKV_BF16, torch.float16: DKV_FP16, torch.float32: DKV_FP32}
 
 
@@ -242,115 +249,10 @@ def _dtype_code(dt: torch.dtype) -> int:
     return code
 
 
-_FP8 = torch.float8_e4m3fn
-_FP32 = torch.float32
-
-
 def _kv_struct(kv) -> tuple[_KV, int, int, int, int]:
-    """(struct, B, Hkv, N, d) for a dense tensor or a cache tuple."""
-    if isinstance(kv, (PagedCache, Fp8PagedCache)):
-        scale = ssb = ssh = 0
-        if isinstance(kv, PagedCache):
-            pool, bt, N = kv
-            fmt, dt = DKV_KV_PAGED, pool.dtype
-            nb, H, S, d = pool.shape
-        else:
-            pool, sc, bt, N, dt = kv
-            fmt = DKV_KV_FP8_PAGED
-            nb, H, S, d = pool.shape
-            if pool.dtype != _FP8 or sc.dtype != _FP32:
-                raise TypeError("Fp8PagedCache wants a float8_e4m3fn pool and float32 scales")
-            if sc.shape != (nb, H) or sc.get_device() != pool.get_device():
-                raise ValueError("scale must be [num_blocks, Hkv]")
-            scale = sc.data_ptr()
-            ssb, ssh = sc.stride()
-        sb, sh, st, one = pool.stride()
-        if S != PAGE_SIZE or one != 1 or st != d:
-            raise ValueError("pool must be [num_blocks, Hkv, 16, d] with token stride d")
-        if bt.dtype != torch.int32 or bt.dim() != 2:
-            raise ValueError("block_table must be int32 [B, P] with unit column stride")
-        bts, one = bt.stride()
-        B, cols = bt.shape
-        if one != 1:
-            raise ValueError("block_table must be int32 [B, P] with unit column stride")
-        if bt.get_device() != pool.get_device():
-            raise ValueError("block_table must be on the pool's device")
-        N = int(N)
-        if cols < (N + PAGE_SIZE - 1) // PAGE_SIZE:
-            raise ValueError("block_table has fewer than ceil(seq_len / 16) columns")
-        return (_KV(fmt, _dtype_code(dt), pool.data_ptr(), None, None, sb, sh, 0, 0,
-                    bt.data_ptr(), bts, nb, scale, ssb, ssh), B, H, N, d)
-    if isinstance(kv, Fp8Cache):
-        c, sc, dt = kv
-        B, H, N, d = c.shape
-        sb, sh, st, one = c.stride()
-        if c.dtype != _FP8 or sc.dtype != _FP32:
-            raise TypeError("Fp8Cache wants float8_e4m3fn codes and float32 scales")
-        if one != 1 or st != d:
-            raise ValueError("codes must have token stride d and channel stride 1")
-        P = (N + PAGE_SIZE - 1) // PAGE_SIZE
-        if sc.shape != (B, H, P) or sc.get_device() != c.get_device():
-            raise ValueError("scale must be [B, Hkv, ceil(N / 16)] with unit block stride")
-        ssb, ssh, one = sc.stride()
-        if one != 1 and P > 1:
-            raise ValueError("scale must be [B, Hkv, ceil(N / 16)] with unit block stride")
-        return (_KV(DKV_KV_FP8, _dtype_code(dt), c.data_ptr(), None, None, sb, sh, 0, 0, None, 0,
-                    0, sc.data_ptr(), ssb, ssh), B, H, N, d)
-    s = _KV()
-    if isinstance(kv, Q4Cache):
-        c, gmn, gmx = kv
-        B, H, N, half = c.shape
-        d = half * 2
-        if c.dtype != torch.uint8 or gmn.dtype != torch.float16 or gmx.dtype != torch.float16:
-            raise TypeError("Q4Cache wants uint8 codes and fp16 gmin/gmax")
-        if c.stride(3) != 1 or c.stride(2) != half:
-            raise ValueError("codes must have token stride d/2 and channel stride 1")
-        if gmn.stride() != gmx.stride() or gmn.stride(3) != 1 or gmn.stride(2) != d // 64:
-            raise ValueError("gmin / gmax must share strides with token stride d/64")
-        s.format, s.dtype = DKV_KV_Q4G64, DKV_FP16
-        s.data, s.gmin, s.gmax = c.data_ptr(), gmn.data_ptr(), gmx.data_ptr()
-        s.stride_b, s.stride_h = c.stride(0), c.stride(1)
-        s.gstride_b, s.gstride_h = gmn.stride(0), gmn.stride(1)
-        return s, B, H, N, d
-    B, H, N, d = kv.shape
-    if kv.stride(3) != 1 or kv.stride(2) != d:
-        raise ValueError("K/V must have token stride d and channel stride 1")
-    s.format, s.dtype = DKV_KV_DENSE, _dtype_code(kv.dtype)
-    s.data = kv.data_ptr()
-    s.stride_b, s.stride_h = kv.stride(0), kv.stride(1)
-    return s, B, H, N, d
-
-
-def _data_of(kv) -> torch.Tensor:
-    """A cache's values or codes."""
-    return kv if isinstance(kv, torch.Tensor) else kv[0]
-
-
-def _device_of(kv) -> torch.device:
-    return _data_of(kv).device
-
-
-def _is_fp8(kv) -> bool:
-    return isinstance(kv, (Fp8Cache, Fp8PagedCache))
-
-
-def _dtype_of(kv) -> torch.dtype:
-    """The 16-bit type that goes with a cache: its queries' and metadata's."""
-    if isinstance(kv, Q4Cache):
-        return torch.float16
-    if isinstance(kv, PagedCache):
-        return kv.pool.dtype
-    return kv.dtype
-
-
-def _check_fp8(q: torch.Tensor, K, V, *others: Optional[torch.Tensor]) -> None:
-    """The 8-bit calls' tensors lie on one device, q in the cache's type."""
-    if q.dtype != K.dtype:
-        raise ValueError(f"q must be {K.dtype}")
-    dev = q.get_device()
-    if dev < 0 or K[0].get_device() != dev or _data_of(V).get_device() != dev or any(
-            t is not None and t.get_device() != dev for t in others):
-        raise ValueError("q, the caches and the other tensors must be on one CUDA device")
+    """(struct, B, Hkv, N, d) of a dense tensor or a cache tuple."""
+    fields, B, H, N, d = (_binding or _load_binding()).describe_cache(kv)
+    return _KV(*fields), B, H, N, d
 
 
 def _params(q: Optional[torch.Tensor], B, Hkv, N, d, out: Optional[torch.Tensor],
@@ -406,17 +308,7 @@ def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.
 
 def kv_meta_build(K, page_size: int = PAGE_SIZE, seq_lens: Optional[torch.Tensor] = None):
     """Page metadata (meta_min, meta_max), each [B, Hkv, P, d]."""
-    ks, B, H, N, d = _kv_struct(K)
-    dev = _device_of(K)
-    dt = _dtype_of(K)
-    P = (N + page_size - 1) // page_size
-    mn = torch.empty(B, H, P, d, dtype=dt, device=dev)
-    mx = torch.empty(B, H, P, d, dtype=dt, device=dev)
-    p = _params(None, B, H, N, d, None, None, seq_lens=seq_lens)
-    p.page_size = page_size
-    _call("dkv_kv_meta_build", mn.get_device(), ctypes.byref(p), ctypes.byref(ks), mn.data_ptr(),
-          mx.data_ptr())
-    return mn, mx
+    return (_binding or _load_binding()).kv_meta_build(K, page_size, seq_lens)
 
 
 def kv_meta_append(K, meta, page_size: int = PAGE_SIZE,
@@ -424,20 +316,8 @@ def kv_meta_append(K, meta, page_size: int = PAGE_SIZE,
     """After a decode step appended tokens: rebuild, in place, only the page
     of `meta` (from kv_meta_build) holding each sequence's last token (N_b - 1,
     N_b from seq_lens, else the cache length)."""
-    ks, B, H, N, d = _kv_struct(K)
     mn, mx = meta
-    P = (N + page_size - 1) // page_size
-    if tuple(mn.shape) != (B, H, P, d) or not mn.is_contiguous() or not mx.is_contiguous():
-        raise ValueError("meta must be contiguous [B, Hkv, P, d]")
-    p = _params(None, B, H, N, d, None, None, seq_lens=seq_lens)
-    p.page_size = page_size
-    if _is_fp8(K):
-        if not mn.dtype == mx.dtype == K.dtype:
-            raise ValueError(f"meta of this cache is {K.dtype}")
-        if not mn.get_device() == mx.get_device() == K[0].get_device():
-            raise ValueError("meta must be on the cache's device")
-    _call("dkv_kv_meta_append", mn.get_device(), ctypes.byref(p), ctypes.byref(ks), mn.data_ptr(),
-          mx.data_ptr())
+    (_binding or _load_binding()).kv_meta_append(K, (mn, mx), page_size, seq_lens)
     return mn, mx
 
 
@@ -448,22 +328,6 @@ def rope_table(length: int, rotary_dim: int, base: float = 10000.0, device=None)
     i = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
     a = torch.arange(length, dtype=torch.float64)[:, None] * base ** (-i / rotary_dim)
     return a.cos().float().to(device), a.sin().float().to(device)
-
-
-def _rows(t: torch.Tensor, name: str, shape: tuple, dt: torch.dtype, dev: int) -> tuple:
-    """A rows tensor's address and (batch, token, head) strides."""
-    sb, st, sh, one = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
-    if one != 1 or t.shape != shape or t.dtype != dt or t.get_device() != dev:
-        raise ValueError(f"{name} must be {dt} {tuple(shape)} on cuda:{dev} with channel stride 1")
-    return t.data_ptr(), sb, st, sh
-
-
-def _lengths(t: Optional[torch.Tensor], name: str, B: int, dev: int) -> Optional[int]:
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or t.shape != (B,) or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor [B] on cuda:{dev}")
-    return t.data_ptr()
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, K, V, seq_lens: Optional[torch.Tensor] = None,
@@ -485,51 +349,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, K, V, seq_lens: Optional[torch.T
     workspace: where sequences that do not fit, and block-table entries outside
     the pool, are recorded (read_device_status); nothing of them is written.
     K and V: both dense tensors, PagedCache, Fp8Cache or Fp8PagedCache."""
-    ks, B, H, N, d = _kv_struct(K)
-    vs, B2, H2, N2, d2 = _kv_struct(V)
-    if (B, H, N, d) != (B2, H2, N2, d2):
-        raise ValueError("K and V shapes differ")
-    dt = _dtype_of(K)
-    dev = _data_of(K).get_device()
-    if dev < 0 or _data_of(V).get_device() != dev:
-        raise ValueError("K and V must be on one CUDA device")
-    if k.dim() != 4:
-        raise ValueError("k must be [B, T, Hkv, d]")
-    T = k.shape[1]
-    kp, ksb, kst, ksh = _rows(k, "k", (B, T, H, d), dt, dev)
-    vp, vsb, vst, vsh = _rows(v, "v", (B, T, H, d), dt, dev)
-    Hq = qp = qsb = qst = qsh = op = osb = ost = osh = 0
-    if q is not None:
-        Hq = q.shape[2]
-        qp, qsb, qst, qsh = _rows(q, "q", (B, T, Hq, d), dt, dev)
-        if q_out is None:
-            # (rows that no token has are left as they are)
-            q_out = torch.empty(B, T, Hq, d, dtype=dt, device=q.device)
-        op, osb, ost, osh = _rows(q_out, "q_out", (B, T, Hq, d), dt, dev)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    r = length = cp = sp = 0
-    if rope is not None:
-        cos, sin = rope
-        if (cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != _FP32 or sin.dtype != _FP32
-                or cos.get_device() != dev or sin.get_device() != dev
-                or not cos.is_contiguous() or not sin.is_contiguous()):
-            raise ValueError("rope must be two contiguous float32 [positions, r / 2] tables")
-        length, r = cos.shape
-        r, cp, sp = 2 * r, cos.data_ptr(), sin.data_ptr()
-    a = _Append(B, Hq, H, d, N, T, r, length, interleaved, kp, vp, qp, op, ksb, kst, ksh, vsb, vst,
-                vsh, qsb, qst, qsh, osb, ost, osh, cp, sp, _lengths(seq_lens, "seq_lens", B, dev),
-                _lengths(new_lens, "new_lens", B, dev))
-    ws = None
-    if workspace is not None:
-        if (workspace.get_device() != dev
-                or workspace.numel() * workspace.element_size() < DKV_WORKSPACE_HEADER_BYTES):
-            raise ValueError("workspace must hold 256 bytes on the caches' device")
-        ws = workspace.data_ptr()
-    if T == 0:  # (an empty tensor has no address)
-        return q_out
-    _call("dkv_kv_append", dev, ctypes.byref(a), ctypes.byref(ks), ctypes.byref(vs), ws)
-    return q_out
+    return (_binding or _load_binding()).kv_append(k, v, K, V, seq_lens, new_lens, q, q_out, rope,
+                                                   interleaved, workspace)
 
 
 def hot_state(B: int, Hkv: int, N: int, device) -> torch.Tensor:
@@ -580,20 +401,8 @@ def decode_attn_full(q, K, V, scale: Optional[float] = None,
                      seq_lens: Optional[torch.Tensor] = None):
     """Exact decode attention; returns out [B, Hq, d] (seq_lens: int32 [B] on the
     device, tokens each sequence attends; None: all N)."""
-    ks, B, H, N, d = _kv_struct(K)
-    vs, B2, H2, N2, d2 = _kv_struct(V)
-    if (B, H, N, d) != (B2, H2, N2, d2):
-        raise ValueError("K and V shapes differ")
-    if _is_fp8(K):
-        _check_fp8(q, K, V, out, workspace, seq_lens)
-    if out is None:
-        out = torch.empty(B, q.shape[1], d, dtype=out_dtype, device=q.device)
-    p = _params(q, B, H, N, d, out, scale, flags, seq_lens)
-    nbytes = _workspace_need(p, 0, _is_fp8(K))
-    ws = _workspace(nbytes, q.device, workspace)
-    _call("dkv_decode_attn_full", q.get_device(), ctypes.byref(p), q.data_ptr(), ctypes.byref(ks),
-          ctypes.byref(vs), out.data_ptr(), _dtype_code(out.dtype), ws.data_ptr(), nbytes)
-    return out
+    return (_binding or _load_binding()).decode_attn_full(q, K, V, scale, out_dtype, out, workspace,
+                                                          flags, seq_lens)
 
 
 def decode_attn_select(q, K, V, meta, top_k: int, scale: Optional[float] = None,
@@ -612,53 +421,9 @@ def decode_attn_select(q, K, V, meta, top_k: int, scale: Optional[float] = None,
     from hot_state())."""
     if group_select:
         flags |= DKV_FLAG_GROUP_SELECT
-    ks, B, H, N, d = _kv_struct(K)
-    vs, B2, H2, N2, d2 = _kv_struct(V)
-    if (B, H, N, d) != (B2, H2, N2, d2):
-        raise ValueError("K and V shapes differ")
-    if _is_fp8(K):
-        _check_fp8(q, K, V, out, workspace, seq_lens, selected, *meta)
-    P = (N + page_size - 1) // page_size
-    m8 = meta if isinstance(meta, Meta8) else None
-    if m8 is not None and hot is not None:
-        raise ValueError("cross-step reuse takes 16-bit metadata")
-    if m8 is not None:
-        if (tuple(m8.code_min.shape) != (B, H, P, d) or tuple(m8.lo.shape) != (B, H, P)
-                or not all(t.is_contiguous() for t in m8)):
-            raise ValueError("Meta8 must hold contiguous [B, Hkv, P, d] codes, [B, Hkv, P] grid")
-    else:
-        mn, mx = meta
-        if tuple(mn.shape) != (B, H, P, d) or not mn.is_contiguous() or not mx.is_contiguous():
-            raise ValueError("meta must be contiguous [B, Hkv, P, d]")
-        if _is_fp8(K) and not mn.dtype == mx.dtype == K.dtype:
-            raise ValueError(f"meta of this cache is {K.dtype}")
-    if out is None:
-        out = torch.empty(B, q.shape[1], d, dtype=out_dtype, device=q.device)
-    kk = min(int(top_k), P)
-    if return_selected and selected is None:
-        selected = torch.empty(B, q.shape[1], kk, dtype=torch.int32, device=q.device)
-    if selected is not None and (selected.dtype != torch.int32 or not selected.is_contiguous()
-                                 or selected.shape != (B, q.shape[1], kk)):
-        raise ValueError("selected must be a contiguous int32 [B, Hq, min(top_k, P)]")
-    p = _params(q, B, H, N, d, out, scale, flags, seq_lens)
-    p.page_size = page_size
-    nbytes = _workspace_need(p, int(top_k), _is_fp8(K))
-    ws = _workspace(nbytes, q.device, workspace)
-    sel_ptr = selected.data_ptr() if selected is not None else None
-    out_args = (int(top_k), out.data_ptr(), _dtype_code(out.dtype), sel_ptr)
-    if m8 is not None:
-        _call("dkv_decode_attn_select_meta8", q.get_device(), ctypes.byref(p), q.data_ptr(),
-              ctypes.byref(ks), ctypes.byref(vs), m8.code_min.data_ptr(), m8.code_max.data_ptr(),
-              m8.lo.data_ptr(), m8.step.data_ptr(), *out_args, ws.data_ptr(), nbytes)
-    elif hot is not None:
-        _call("dkv_decode_attn_select_hot", q.get_device(), ctypes.byref(p), q.data_ptr(),
-              ctypes.byref(ks), ctypes.byref(vs), mn.data_ptr(), mx.data_ptr(), *out_args,
-              hot.data_ptr(), hot.numel(), int(step), ws.data_ptr(), nbytes)
-    else:
-        _call("dkv_decode_attn_select", q.get_device(), ctypes.byref(p), q.data_ptr(),
-              ctypes.byref(ks), ctypes.byref(vs), mn.data_ptr(), mx.data_ptr(), *out_args,
-              ws.data_ptr(), nbytes)
-    return (out, selected) if return_selected else out
+    return (_binding or _load_binding()).decode_attn_select(
+        q, K, V, meta, top_k, scale, out_dtype, out, return_selected, selected, workspace, flags,
+        seq_lens, page_size, hot, step)
 
 
 def decode_attn_topk_tokens(q, K, V, top_k: int, scale: Optional[float] = None,

@@ -1,4 +1,5 @@
-"""Build libdkv.so in-tree: nvcc for sm_103a, one object per .cu in parallel.
+"""Build libdkv.so in-tree (nvcc for sm_103a, one object per .cu in parallel) and
+the Python binding beside it (g++, against the installed torch).
 
     python -m decode_attention_paged_kv_gb300.build [--force]
 """
@@ -8,6 +9,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -15,8 +17,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libdkv.so")
+BINDING = os.path.join(BUILD, "_binding.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+CXX = os.environ.get("CXX", "g++")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I" + INCLUDE,
          "--expt-relaxed-constexpr"]
@@ -28,15 +32,15 @@ def sources():
 
 def _deps():
     dep = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
-           if f.endswith((".cu", ".cuh", ".h"))]
+           if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
     dep.append(os.path.join(INCLUDE, "dkv.h"))
     return dep
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
@@ -56,8 +60,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(max_workers=min(9, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding, verbose)
         objs = list(ex.map(compile_one, sources()))
+        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [NVCC, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
            "-Xlinker", "-rpath=/usr/local/cuda/lib64"]
@@ -65,7 +71,40 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
+
+
+def _run(cmd, what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding(verbose: bool) -> str:
+    import torch
+    torch_include = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "binding.o")
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + INCLUDE, "-I" + torch_include,
+           "-I" + os.path.join(torch_include, "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I/usr/local/cuda/include",
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    _run(cmd, "the binding's compilation")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    _run([CXX, "-shared", obj, "-o", tmp, "-L" + BUILD, "-l:libdkv.so", "-Wl,-rpath,$ORIGIN",
+          "-L" + torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+          "-Wl,-rpath," + torch_lib], "the binding's link")
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":
