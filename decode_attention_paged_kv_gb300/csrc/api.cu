@@ -715,6 +715,9 @@ static dkv_status select_impl(const dkv_params* p, const void* q, const dkv_kv* 
     sa.G = G;
     sa.P = P;
     sa.scores = reinterpret_cast<float*>(ws + L.scores);
+    sa.lens = p->seq_lens;
+    sa.N = p->seq_len;
+    sa.S = p->page_size;
     if (m8 == nullptr) {
       if ((st = cuda_status(dkv::launch_score(p->head_dim, f16, sa, s))) != DKV_OK) return st;
     } else {

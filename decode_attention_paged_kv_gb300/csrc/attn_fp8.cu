@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
     int step = 0;
     // Taking an item before the current one is done costs balance at the end:
     // only where a CTA gets several, and not while selections are still coming.
-    const bool ahead = !SPARSE && a.n_items >= 4 * static_cast<int>(gridDim.x);
+    const bool ahead = !unit_flags && a.n_items >= 4 * static_cast<int>(gridDim.x);
     int ticket = 0, count = 0, len = 0;
     int page[kPer], mask[kPer], blk[kPer];
     float ks[kPer], vs[kPer];

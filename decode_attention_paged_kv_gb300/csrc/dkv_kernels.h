@@ -178,6 +178,8 @@ struct ScoreArgs {
   int B, Hq, Hkv, G, P;
   float* scores;               // [B, Hq, P]
   int exact;                   // 1: meta_max holds single keys (m = M): score q . k once
+  const int32_t* lens;         // per-sequence lengths [B] or nullptr; N = the longest
+  int N, S;                    // (with lens: pages past ceil(N_b / S) are not scored)
 };
 
 // 8-bit page metadata: per page a grid dec(c) = fma(c, step, lo) and, per

@@ -722,6 +722,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const ScoreArgs
   griddep_launch_dependents();
   griddep_wait();
   if (page0 >= a.P) return;
+  // (a shorter sequence: nothing reads the scores of pages past its own)
+  if (a.lens != nullptr && page0 >= ceil_div(seq_len_of(a.lens, b, a.N), a.S)) return;
   uint32_t bq[D / 16][4];
   load_q_pm<D, EXACT>(a.q, a.q_sb, a.q_sh, b, kvh, a.G, lane, bq);
   const int64_t mbase = (static_cast<int64_t>(b) * a.Hkv + kvh) * a.P * D;
