@@ -273,11 +273,19 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
     int page[kPer], mask[kPer], blk[kPer];
     float ks[kPer], vs[kPer];
     constexpr int kListed = 6;
+    bool fresh = true;  // no ticket taken yet
+    const bool counted = n_tickets > static_cast<int>(gridDim.x);  // CTAs take several
     // One step; with `block`, a step that has to wait does.
     auto advance = [&](bool block) {
       switch (step) {
-        case 0:  // a new item
-          if (lane == 0) ticket = static_cast<int>(atomicAdd(a.work_counter, 1u));
+        case 0:  // a new item: the CTA's own number first, then from the counter
+          if (fresh)
+            ticket = blockIdx.x;
+          else if (!counted)
+            ticket = n_tickets;
+          else if (lane == 0)
+            ticket = static_cast<int>(gridDim.x + atomicAdd(a.work_counter, 1u));
+          fresh = false;
           step = 1;
           break;
         case 1: {
@@ -500,7 +508,7 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
       }
     }
     __syncwarp();
-    if (lane == 0) {
+    if (lane == 0 && counted) {
       // The last CTA to stop fetching work resets the counters for the next
       // call (every earlier fetch is ordered before its ticket by the fence).
       __threadfence();
