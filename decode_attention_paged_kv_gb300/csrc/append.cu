@@ -139,7 +139,7 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
   return make_float2(lo16<true>(h), hi16<true>(h));
 }
 
-// x / s: for a power of two the exact product with 1 / s.
+// Division by s: for a power of two the exact product with 1 / s.
 struct Divider {
   float s, inv;
   bool pow2;
@@ -147,21 +147,27 @@ struct Divider {
     pow2 = (__float_as_uint(s_) & 0x7fffffu) == 0u;
     inv = __fdiv_rn(1.f, s_);
   }
-  __device__ __forceinline__ float operator()(float x) const {
-    return pow2 ? __fmul_rn(x, inv) : __fdiv_rn(x, s);
-  }
 };
+
+// (Out of line: only a scale that this file did not write needs it.)
+__device__ __noinline__ float divide(float x, float s) { return __fdiv_rn(x, s); }
 
 // The thread's 16 channels as codes.
 __device__ __forceinline__ void store_codes(uint8_t* row, Chunks c, const Divider& by,
                                             const float (&x)[16]) {
+  float y[16];
+  if (by.pow2) {  // (one branch for all 16)
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float* y = x + 8 * h;
-    *reinterpret_cast<uint2*>(row + (h ? c.c2 : c.c1)) =
-        make_uint2(to_e4m3x4(by(y[0]), by(y[1]), by(y[2]), by(y[3])),
-                   to_e4m3x4(by(y[4]), by(y[5]), by(y[6]), by(y[7])));
+    for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(x[i], by.inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = divide(x[i], by.s);
   }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    *reinterpret_cast<uint2*>(row + (h ? c.c2 : c.c1)) =
+        make_uint2(to_e4m3x4(y[8 * h], y[8 * h + 1], y[8 * h + 2], y[8 * h + 3]),
+                   to_e4m3x4(y[8 * h + 4], y[8 * h + 5], y[8 * h + 6], y[8 * h + 7]));
 }
 
 // Codes stored under the scale s_old, stored again under by.s.
@@ -369,15 +375,14 @@ __global__ void __launch_bounds__(D, block_ctas<D, EIGHT>()) append_block_kernel
     if (!EIGHT || at.blk < 0) continue;
     float* sp = scale_at(a, cache, at, page, h0);
     const int kept = max(0, nt.start - page * kPage);  // tokens the block held before
-    float old[kHeads];
+    float old[kHeads], x[kHeads][16];
     turn ^= 1;
 #pragma unroll
     for (int h = 0; h < kHeads; ++h) {
       old[h] = kept > 0 && h < nh ? sp[h * cache.ssh] : 0.f;
-      float x[16];
-      widen<F16>(raw[h], x);
-      if (rotated) rotate16<IL>(ang, x);  // (again below: cheaper than 16 registers a head)
-      const uint32_t wm = __reduce_max_sync(0xffffffffu, on ? amax_bits(x) : 0u);
+      widen<F16>(raw[h], x[h]);
+      if (rotated) rotate16<IL>(ang, x[h]);
+      const uint32_t wm = __reduce_max_sync(0xffffffffu, on ? amax_bits(x[h]) : 0u);
       if (lane == 0) warp_amax[turn][threadIdx.x / 32][h] = wm;
     }
     // Every thread has read the old scales; the other turn's maxima are free once
@@ -395,10 +400,7 @@ __global__ void __launch_bounds__(D, block_ctas<D, EIGHT>()) append_block_kernel
       const Divider by(s);
       uint8_t* row = rows + h * cache.sh;
       if (on) {
-        float x[16];
-        widen<F16>(raw[h], x);
-        if (rotated) rotate16<IL>(ang, x);
-        store_codes(row, c, by, x);
+        store_codes(row, c, by, x[h]);
       } else if (i < kept && s > old[h]) {
         rescale_codes(row, c, old[h], by);
       }

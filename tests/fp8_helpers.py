@@ -146,6 +146,12 @@ def rotated(x, pos, rope, interleaved):
     return y
 
 
+def quotient(y, s):
+    """fp32 y [Hkv, ...] over the scales s [Hkv], rounded to fp32 (exact for
+    powers of two), as 64-bit values."""
+    return (y.float() / s.float()[:, None, None]).double()
+
+
 def append(k, v, K, V, lens, news, q=None, q_out=None, rope=None, interleaved=False):
     """The reference of kv_append on CPU tensors, in place.  K, V: logical
     caches: values [B, Hkv, L, d], or (codes uint8 [B, Hkv, L, d], scale
@@ -172,8 +178,9 @@ def append(k, v, K, V, lens, news, q=None, q_out=None, rope=None, interleaved=Fa
                     old = scale[b, :, p].double()
                     s = torch.maximum(s, old)
                     at = codes[b, :, p * PAGE:lo]
-                    again = encode(TABLE[at.long()] * (old / s)[:, None, None])
+                    again = encode(quotient(TABLE[at.long()].float()
+                                            * old.float()[:, None, None], s))
                     rise = (s > old)[:, None, None]
                     codes[b, :, p * PAGE:lo] = torch.where(rise, again.view(torch.uint8), at)
                 scale[b, :, p] = s.float()
-                codes[b, :, lo:hi] = encode(new.double() / s[:, None, None]).view(torch.uint8)
+                codes[b, :, lo:hi] = encode(quotient(new, s)).view(torch.uint8)

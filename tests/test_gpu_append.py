@@ -160,6 +160,16 @@ def test_append_without_lengths(kind, B, Hq, Hkv, N, T, dev, dkv):
         False, seed=N)
 
 
+@pytest.mark.parametrize("kind", ["paged", "fp8"])
+@pytest.mark.parametrize("T", [1, 18])
+def test_more_sequences_than_are_counted(kind, T, dev, dkv):
+    g = torch.Generator().manual_seed(T)
+    lens = torch.randint(T, 41, (131,), generator=g)
+    news = torch.randint(0, T + 1, (131,), generator=g)
+    lens[3], news[3], news[130] = 0, T, T
+    run(dkv, dev, kind, 131, 1, 1, 64, 40, T, lens.tolist(), news.tolist(), torch.bfloat16, 64, False)
+
+
 @pytest.mark.parametrize("kind", ["dense", "fp8_paged"])
 def test_queries_in_place(kind, dev, dkv):
     run(dkv, dev, kind, 2, 4, 2, 128, 64, 6, [50, 6], None, torch.bfloat16, 128, False,
@@ -177,6 +187,26 @@ def test_scales_at_their_ends(dt, scale, T, dev, dkv):
         scale=scale, seed=3)
     run(dkv, dev, "fp8", 4, 2, 2, 128, 40, T, [40, 22, 5, 17], None, dt, 0, False, scale=scale,
         seed=4)
+
+
+@pytest.mark.parametrize("T", [1, 6])
+@pytest.mark.parametrize("factor", [3.0, 0.37])
+def test_scales_of_another_maker(T, factor, dev, dkv):
+    # blocks whose scale is no power of two keep it while it is large enough
+    gen = torch.Generator().manual_seed(T)
+    table = table_for(3, 64, gen)
+    K = Cache(dkv, "fp8_paged", 3, 2, 64, 64, torch.bfloat16, gen, dev, table)
+    V = Cache(dkv, "fp8_paged", 3, 2, 64, 64, torch.bfloat16, gen, dev, table)
+    V.obj = V.obj._replace(block_table=K.obj.block_table)
+    for c in (K, V):
+        c.scale[table.view(-1).long().to(dev)] *= factor
+        c.ref[1].mul_(factor)
+    x = torch.randn(3, T, 2, 64, generator=gen).to(torch.bfloat16)
+    lens = torch.tensor([30, 64, 17], dtype=torch.int32)
+    dkv.kv_append(x.to(dev), x.to(dev), K.obj, V.obj, seq_lens=lens.to(dev))
+    ref.append(x, x, K.ref, V.ref, lens, [T] * 3)
+    K.check()
+    V.check()
 
 
 def test_largest_value_at_a_scale_border(dev, dkv):

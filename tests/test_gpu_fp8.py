@@ -199,6 +199,49 @@ def test_paged_head_wise_and_strided_bitwise(dev, dkv):
     assert torch.all(o[:, Hq] == 5.0) and torch.all(o[:, :, d:] == 5.0)
 
 
+def test_more_sequences_than_are_counted(dev, dkv):
+    # past 128 sequences items are not counted by length; some of them empty
+    B, Hq, H, d, N = 131, 4, 2, 64, 600
+    q, K, V = make(B, Hq, H, d, N, torch.bfloat16, seed=5)
+    g = torch.Generator().manual_seed(5)
+    lens = torch.randint(0, N + 1, (B,), generator=g)
+    lens[7], lens[130] = 0, N
+    lt = lens.to(torch.int32).to(dev)
+    kv, vv = ref.values(*K), ref.values(*V)
+    want = ref.attention(q, kv, vv, 1 / 8, lens.tolist())
+    for paged in (False, True):
+        Kd, Vd = caches(dkv, dev, K, V, torch.bfloat16, paged)
+        out = dkv.decode_attn_full(q.to(dev), Kd, Vd, seq_lens=lt)
+        assert not out[7].any()
+        assert (out.cpu().double() - want).abs().max() <= ref.tolerance(q, kv, vv, 1 / 8)
+
+
+def test_blocks_past_two_gib(dev, dkv):
+    # the tokens lie in the last blocks of pools whose offsets pass 2^31
+    H, d, N = 8, 128, 70
+    nb = (1 << 31) // (H * 16 * d) + 9
+    q, K, V = make(1, 16, H, d, N, torch.bfloat16, seed=3)
+    bt = torch.arange(nb - 5, nb, dtype=torch.int32).view(1, 5)
+    out = []
+    for c, s in (K, V):
+        pool = torch.zeros(nb, H, 16, d, dtype=torch.uint8, device=dev)
+        scale = torch.zeros(nb, H, device=dev)
+        full = torch.zeros(H, 80, d, dtype=torch.uint8)
+        full[:, :N] = c[0].view(torch.uint8)
+        pool[nb - 5:] = full.view(H, 5, 16, d).transpose(0, 1).to(dev)
+        scale[nb - 5:] = s[0].t().to(dev)
+        out.append((pool, scale))
+    table = bt.to(dev)
+    Kd, Vd = (dkv.Fp8PagedCache(p.view(torch.float8_e4m3fn), s, table, N) for p, s in out)
+    kv, vv = ref.values(*K), ref.values(*V)
+    want = ref.attention(q, kv, vv, 1 / math.sqrt(d))
+    tol = ref.tolerance(q, kv, vv, 1 / math.sqrt(d))
+    assert (dkv.decode_attn_full(q.to(dev), Kd, Vd).cpu().double() - want).abs().max() <= tol
+    meta = dkv.kv_meta_build(Kd)
+    o = dkv.decode_attn_select(q.to(dev), Kd, Vd, meta, 5)
+    assert (o.cpu().double() - want).abs().max() <= tol
+
+
 def deq16(c, s, dt):
     """An 8-bit cache's values in its 16-bit type (exact for powers of two)."""
     x = ref.values(c, s)
