@@ -199,6 +199,29 @@ def test_paged_head_wise_and_strided_bitwise(dev, dkv):
     assert torch.all(o[:, Hq] == 5.0) and torch.all(o[:, :, d:] == 5.0)
 
 
+@pytest.mark.parametrize("Hq", [3, 9, 18])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_many_items_a_cta(Hq, ragged, dev, dkv):
+    # more work items than resident CTAs, every second one of five pages or fewer
+    # (warps without a page run ahead of the others), run twice on one workspace
+    B, H, d, N = 120, 3, 128, 1104
+    q, K, V = make(B, Hq, H, d, N, torch.bfloat16, seed=Hq)
+    lens = None
+    if ragged:
+        lens = torch.randint(1025, N + 1, (B,), generator=torch.Generator().manual_seed(1)).tolist()
+        lens[::9] = [17] * len(lens[::9])
+    lt = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=dev)
+    kv, vv = ref.values(*K), ref.values(*V)
+    scale = 1 / math.sqrt(d)
+    want = ref.attention(q, kv, vv, scale, lens)
+    ws = torch.zeros(dkv.workspace_bytes(B, Hq, H, d, N, fp8=True), dtype=torch.uint8, device=dev)
+    Kd, Vd = caches(dkv, dev, K, V, torch.bfloat16, True)
+    for _ in range(2):
+        out = dkv.decode_attn_full(q.to(dev), Kd, Vd, seq_lens=lt, workspace=ws)
+        assert dkv.read_device_status(ws) == 0
+        assert (out.cpu().double() - want).abs().max() <= ref.tolerance(q, kv, vv, scale)
+
+
 def test_more_sequences_than_are_counted(dev, dkv):
     # past 128 sequences items are not counted by length; some of them empty
     B, Hq, H, d, N = 131, 4, 2, 64, 600
