@@ -19,14 +19,22 @@
 //
 // Two kernels.  append_token_kernel: d/16 threads a token and head, 16
 // channels (two 16-byte vectors, the two halves of 8 rotation pairs) each;
-// nothing is shared between tokens, so it serves 16-bit caches of any length
-// and the single-token call of an 8-bit cache, where the d/16 threads agree on
-// the scale by shuffles.  append_block_kernel: one CTA of d threads per touched
-// block of an 8-bit cache and four heads, a thread per token and 16 channels of
-// each; the blocks' amax are reduced through shared memory while the values wait
-// in registers, so they are read once, and the heads share the token's angles.
-// Both are bound by memory traffic (long calls) or by the latency of the
-// dependent loads length -> block table -> scale (single tokens).
+// nothing is shared between tokens, so it serves the single-token call -- where
+// the d/16 threads of an 8-bit cache agree on the scale by shuffles -- and few
+// tokens into a 16-bit cache.  append_block_kernel: a CTA of d threads takes a
+// touched block and four heads at a time, a thread per token and 16 channels of
+// each; the blocks' amax are reduced through shared memory while the rotated
+// values wait in registers, so they are read and rotated once, and the heads
+// share the token's angles.  Its CTAs are persistent and count the blocks that
+// the sequences touch, so a ragged batch costs nothing for what it lacks.
+//
+// Measured on a GB300 (copy rate 6.79 TB/s), 32 query / 8 kv heads, d = 128:
+// 8 prompts of 8K tokens into an 8-bit cache 231 us (6.4 TB/s), ragged 137 us
+// (6.3), into a 16-bit one 269 us (6.0).  The ragged ones took 248 us with one
+// head a CTA, 166 with four, 152 with persistent CTAs that rotated twice to save
+// registers.  One token of 64 sequences (16-bit) takes 2.0 us, of 16 sequences
+// (8-bit) 2.2 us: the latency of the launch and of the dependent loads length ->
+// block table -> scale.
 
 #include "dkv_device.cuh"
 #include "dkv_kernels.h"

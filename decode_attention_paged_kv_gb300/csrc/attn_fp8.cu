@@ -49,6 +49,17 @@
 // largest component lies in [2^14, 2^15): exact in fp16 for every component
 // within 2^28 of it; the scores are scaled back.
 //
+// Bound by HBM: a token's K and V are 2 d bytes, once.  Measured on a GB300 (copy
+// rate 6.79 TB/s), 32 query / 8 kv heads, d = 128, with the merge: 16 sequences
+// of 32K tokens 158 us dense (6.8 TB/s), 165 us paged (6.5), ragged 116 us
+// (6.1); one of 1M tokens 305 us (7.0); 8 x 32 heads of 8K, d = 64, one query
+// head each, 47 us (5.7).  What the layout is worth there: with the heads on the
+// MMA's M side (8 of 16 rows, four to eight scores a lane, exact running maxima)
+// and two CTAs an SM, 183 us dense and 190 us paged; d = 64 paged pages of 1 KiB
+// are held back by the copy engine's rate of boxes (5.3 TB/s), so a dense cache
+// read in order takes two pages a box (52 -> 47 us at the 8K shape).  A small
+// call costs about 7 us, two kernels' chains of dependent loads.
+//
 // Every mbarrier wait is bounded; on expiry the kernel records a timeout in
 // the status word, stops issuing, drains the copies it issued and exits.
 

@@ -7,8 +7,11 @@
 // 32 or 64 tokens join their blocks in fp32.  Powers of two give the exact min
 // and max; another scale's products are rounded outward (m down, M up), which
 // keeps the bound scores upper bounds.  One thread owns 16 channels (one 16-byte
-// vector a token) of a page with the page's rows in flight together: bound by
-// HBM, 24 instructions a vector.
+// vector a token) of a page with the page's 16 rows in flight together: bound by
+// HBM, 24 instructions a vector.  Measured on a GB300 (copy rate 6.79 TB/s), 16 x
+// 8 kv heads of 32K tokens, d = 128: 104 us (6.4 TB/s) with five CTAs of 128
+// threads an SM; two of 256 threads 121 us, four with eight rows in flight
+// 135 us.
 
 #include "dkv_device.cuh"
 #include "dkv_kernels.h"

@@ -202,7 +202,7 @@ typedef struct dkv_params {
    path; top_k >= 1: the sparse path).  0 if `p` is invalid.  Host only. */
 size_t dkv_workspace_bytes(const dkv_params* p, int32_t top_k);
 
-/* The same for the 8-bit cache formats, whose work is cut finer. */
+/* The same for calls on the 8-bit cache formats, whose work is cut otherwise. */
 size_t dkv_workspace_bytes_fp8(const dkv_params* p, int32_t top_k);
 
 /* New tokens for a cache: sequence b's n_b new tokens take the positions
@@ -400,7 +400,8 @@ dkv_status dkv_kv_dequant4(int64_t rows, int32_t d, const void* codes, const voi
    array of DKV_NOALLOC_SCRATCH_BYTES inside the library, held by every GPU that
    loads it until exit.
    - Returns DKV_ERR_WORKSPACE when the problem needs more scratch than that
-     (dkv_workspace_bytes(p, 0) > DKV_NOALLOC_SCRATCH_BYTES).
+     (dkv_workspace_bytes(p, 0), or dkv_workspace_bytes_fp8(p, 0) for an 8-bit
+     cache, > DKV_NOALLOC_SCRATCH_BYTES).
    - The first call on a device looks up the array's address (with that device
      current); make that first call before any stream capture.  The address is
      kept per device and context: a call under another context (after a device
