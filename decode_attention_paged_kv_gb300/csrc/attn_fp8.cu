@@ -931,25 +931,29 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
   }
 }
 
-// Resident CTAs per SM of one instantiation, at most Fp8Cfg::kCtas; computed once.
+// Resident CTAs per SM of one instantiation, at most Fp8Cfg::kCtas; computed once
+// a device (the shared-memory limit is set per device too).
 template <int D, bool F16, bool SPARSE, int GL>
 cudaError_t ctas_per_sm_t(int* out) {
   using C = Fp8Cfg<D, GL>;
-  static int cached = 0;  // benign race: every thread computes the same value
-  if (cached > 0) {
-    *out = cached;
+  static int cached[64] = {0};  // benign race: every thread computes the same value
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < 64;
+  if (known && cached[dev] > 0) {
+    *out = cached[dev];
     return cudaSuccess;
   }
   auto kern = attn_fp8_kernel<D, F16, SPARSE, GL>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   int n = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kAttnThreads, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   if (n < 1) return cudaErrorInvalidConfiguration;
-  cached = n < C::kCtas ? n : C::kCtas;
-  *out = cached;
+  *out = n < C::kCtas ? n : C::kCtas;
+  if (known) cached[dev] = *out;
   return cudaSuccess;
 }
 

@@ -212,8 +212,9 @@ const int32_t* lengths(PyObject* o, const char* name, int64_t B, int device) {
   if (is_none(o)) return nullptr;
   const at::Tensor& t = tensor(o, name);
   if (t.scalar_type() != at::kInt || t.dim() != 1 || t.size(0) != B || !t.is_contiguous() ||
-      !t.is_cuda() || (device >= 0 && t.get_device() != device)) {
-    PyErr_Format(PyExc_ValueError, "%s must be a contiguous int32 CUDA tensor [B]", name);
+      !t.is_cuda() || t.get_device() != device) {
+    PyErr_Format(PyExc_ValueError,
+                 "%s must be a contiguous int32 CUDA tensor [B] on the cache's device", name);
     throw PyError{};
   }
   return static_cast<const int32_t*>(t.data_ptr());
@@ -227,7 +228,7 @@ dkv_params make_params(const Cache& c, int64_t page_size, PyObject* seq_lens) {
   p.seq_len = int32_size(c.N);
   p.page_size = int32_size(page_size);
   p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.d)));
-  p.seq_lens = lengths(seq_lens, "seq_lens", c.B, c.fp8 ? c.device : -1);
+  p.seq_lens = lengths(seq_lens, "seq_lens", c.B, c.device);
   return p;
 }
 
@@ -247,9 +248,10 @@ void set_out(dkv_params* p, const at::Tensor& q, const at::Tensor& out) {
   p->o_stride_b = out.stride(0), p->o_stride_h = out.stride(1);
 }
 
-// The 8-bit calls' tensors lie on one device, q in the cache's type.
-void check_fp8(const at::Tensor& q, const Pair& c, std::initializer_list<const at::Tensor*> others) {
-  if (q.scalar_type() != c.k.dtype) value_error("q must have the cache's dtype");
+// The tensors of an attention call lie on one device; q has an 8-bit cache's type.
+void check_tensors(const at::Tensor& q, const Pair& c,
+                   std::initializer_list<const at::Tensor*> others) {
+  if (c.k.fp8 && q.scalar_type() != c.k.dtype) value_error("q must have the cache's dtype");
   const int dev = cuda_index(q);
   bool ok = dev >= 0 && c.k.device == dev && c.v.device == dev;
   for (const at::Tensor* t : others) ok = ok && (t == nullptr || cuda_index(*t) == dev);
@@ -458,11 +460,10 @@ PyObject* decode_attn_full(PyObject* const* a) {
   const at::Tensor& q = tensor(a[0], "q");
   const Pair c = parse_pair(a[1], a[2]);
   const at::Tensor* given = optional_tensor(a[5], "out");
-  if (c.k.fp8) check_fp8(q, c, {given, optional_tensor(a[6], "workspace")});
+  check_tensors(q, c, {given, optional_tensor(a[6], "workspace")});
   dkv_params p = make_params(c.k, kPage, a[8]);
   set_query(&p, c.k, q, a[3], integer(a[7]));
   const int dev = cuda_index(q);
-  if (dev < 0) value_error("dkv_decode_attn_full wants CUDA tensors");
   const at::Tensor out = given ? *given : at::empty(q.sizes(), q.options().dtype(scalar_type(a[4])));
   set_out(&p, q, out);
   const size_t need = workspace_need(p, 0, c.k.fp8);
@@ -501,13 +502,11 @@ PyObject* decode_attn_select(PyObject* const* a) {
   } else {
     m = meta_pair(a[3], c.k, P);
   }
-  if (c.k.fp8)
-    check_fp8(q, c, {given, optional_tensor(a[10], "workspace"), chosen, hot, m.mn, m.mx, part[0],
-                     part[1], part[2], part[3]});
+  check_tensors(q, c, {given, optional_tensor(a[10], "workspace"), chosen, hot, m.mn, m.mx,
+                       part[0], part[1], part[2], part[3]});
   dkv_params p = make_params(c.k, S, a[12]);
   set_query(&p, c.k, q, a[5], integer(a[11]));
   const int dev = cuda_index(q);
-  if (dev < 0) value_error("dkv_decode_attn_select wants CUDA tensors");
   const at::Tensor out = given ? *given : at::empty(q.sizes(), q.options().dtype(scalar_type(a[6])));
   set_out(&p, q, out);
   const int64_t kk = top_k < P ? top_k : P;

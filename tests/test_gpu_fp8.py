@@ -459,6 +459,22 @@ def test_python_refusals(dev, dkv):
         dkv.kv_meta_append(Kd, meta)
     with pytest.raises(dkv.DkvError):
         dkv.decode_attn_topk_tokens(qd, Kd, Vd, 4)
+    # tensors of another device, of another shape or stride
+    cpu = dkv.Fp8Cache(K[0], K[1])
+    k16, v16 = (deq16(*c, torch.bfloat16).to(dev) for c in (K, V))
+    for call in (lambda: dkv.decode_attn_full(qd, cpu, Vd), lambda: dkv.decode_attn_full(q, Kd, Vd),
+                 lambda: dkv.decode_attn_full(qd, k16, v16.cpu()),
+                 lambda: dkv.decode_attn_full(qd, k16, v16, out=torch.zeros(1, 2, 64)),
+                 lambda: dkv.decode_attn_full(qd, k16, v16, workspace=torch.zeros(1 << 20)),
+                 lambda: dkv.decode_attn_full(qd, Kd, Vd, out=torch.zeros(1, 1, 64, device=dev)),
+                 lambda: dkv.decode_attn_full(
+                     qd, Kd, Vd, out=torch.zeros(1, 64, 2, device=dev).transpose(1, 2)),
+                 lambda: dkv.decode_attn_full(qd, Kd, Vd, seq_lens=torch.ones(1, dtype=torch.int32)),
+                 lambda: dkv.decode_attn_select(
+                     qd, Kd, Vd, dkv.kv_meta_build(Kd), 2,
+                     selected=torch.zeros(1, 2, 3, dtype=torch.int32, device=dev))):
+        with pytest.raises(ValueError):
+            call()
 
 
 def test_decode_loop(dev, dkv):
