@@ -78,10 +78,14 @@ WsLayout layout_for(const dkv_params& p, int top_k, bool fp8 = false) {
         std::min(p.page_size < dkv::kPage ? union_sel : union_sel * (p.page_size / dkv::kPage),
                  P16);
     L.union_stride = static_cast<int>(union_max);
-    L.pages_per_chunk = fp8 ? dkv::fp8_pages_per_chunk(union_max, d, p.batch)
-                            : dkv::select_pages_per_chunk(union_max, d);
-    if (!fp8 && L.pages_per_chunk > dkv::kMaxSelectList) L.ok = false;
-    L.n_chunks = static_cast<int>(ceil_div(union_max, L.pages_per_chunk));
+    if (fp8) {
+      L.pages_per_chunk = 0;  // equal parts of each unit's union
+      L.n_chunks = dkv::fp8_select_parts(union_max, units);
+    } else {
+      L.pages_per_chunk = dkv::select_pages_per_chunk(union_max, d);
+      if (L.pages_per_chunk > dkv::kMaxSelectList) L.ok = false;
+      L.n_chunks = static_cast<int>(ceil_div(union_max, L.pages_per_chunk));
+    }
   }
   if (L.n_chunks > dkv::kMaxChunks) L.ok = false;
   L.n_items = units * L.n_chunks;

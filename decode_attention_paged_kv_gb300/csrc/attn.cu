@@ -1179,6 +1179,9 @@ __global__ void __launch_bounds__(kAttnThreads, MHA ? 3 : (D == 64 ? kAttnCtasPe
 //   2. thread (slice s, channel c) sums w_k o_k[c] over its <= 32 chunks with
 //      every load in flight; the S slice sums are added in order.
 // out = sum / L.  A fixed order throughout: deterministic.
+__device__ __forceinline__ int pages_of_chunk(const MergeArgs& m, int count) {
+  return m.pages_per_chunk > 0 ? m.pages_per_chunk : fp8_part_pages(count, m.n_chunks);
+}
 template <int D>
 __global__ void __launch_bounds__(1024) merge_kernel(const MergeArgs m) {
   __shared__ float s_w[kMaxChunks], s_l[kMaxChunks], s_o[kMaxChunks / 32][D];
@@ -1195,7 +1198,7 @@ __global__ void __launch_bounds__(1024) merge_kernel(const MergeArgs m) {
   if (m.union_count != nullptr) {
     const int b = row / m.Hq, h = row % m.Hq;
     const int count = m.union_count[b * m.Hkv + h / m.G];
-    nc = min(stride, static_cast<int>(ceil_div(count, m.pages_per_chunk)));
+    nc = min(stride, static_cast<int>(ceil_div(count, pages_of_chunk(m, count))));
   } else if (m.lens != nullptr) {
     const int Pb = static_cast<int>(ceil_div(seq_len_of(m.lens, row / m.Hq, m.N), kPage));
     nc = min(stride, static_cast<int>(ceil_div(Pb, m.pages_per_chunk)));
@@ -1283,7 +1286,7 @@ __global__ void __launch_bounds__(kSmallMergeThreads) merge_small_kernel(const M
     x[k] = k < stride ? __ldcg(po + static_cast<int64_t>(k) * D) : 0.f;
   }
   const int nc = (m.union_count != nullptr || m.lens != nullptr)
-                     ? min(stride, static_cast<int>(ceil_div(count, m.pages_per_chunk)))
+                     ? min(stride, static_cast<int>(ceil_div(count, pages_of_chunk(m, count))))
                      : stride;
   float M = -INFINITY;
 #pragma unroll

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
             first = c * a.pages_per_chunk;
           } else {
             unit = item / a.n_chunks;
-            first = item % a.n_chunks * a.pages_per_chunk;
+            first = item % a.n_chunks * a.pages_per_chunk;  // (sparse: once the union is known)
             kvh = unit % a.Hkv;
             b = unit / a.Hkv;
           }
@@ -357,8 +357,14 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
           break;
         case 3:  // the part's pages
           if (l0 == 0) {
-            if constexpr (!SPARSE) count = static_cast<int>(ceil_div(min(len, a.N), kPage));
-            n = len <= 0 ? 0 : max(0, min(count - first, a.pages_per_chunk));
+            int part = a.pages_per_chunk;
+            if constexpr (SPARSE) {
+              part = fp8_part_pages(count, a.n_chunks);
+              first = item % a.n_chunks * part;
+            } else {
+              count = static_cast<int>(ceil_div(min(len, a.N), kPage));
+            }
+            n = len <= 0 ? 0 : max(0, min(count - first, part));
             if (n == 0 && !whole) {  // no partial is read for it
               step = 0;
               break;
