@@ -52,18 +52,25 @@ inline int select_pages_per_chunk(int64_t union_max, int d) {
   return static_cast<int>(need > base ? need : base);
 }
 // Exact attention: pages of an 8-bit cache a work item streams, of `pages` per
-// (batch, kv head): 256 KiB of codes, less where the batch is small, so that 8 kv heads
-// still fill two CTAs on each of 152 multiprocessors.  Depends on the pages, d
-// and the batch only, so here too one kv head at a time gives bitwise the
-// all-heads result.  A multiple of 8: two pages a stage for each of four warps.
+// (batch, kv head): about 256 KiB of codes.  Where that makes fewer than four
+// waves of items on the 456 resident CTAs (three on each of 152 multiprocessors),
+// counting 8 kv heads, the size is changed to whole waves; less than one is cut
+// finer.  Depends on the pages, d and the batch only, so here too one kv head at
+// a time gives bitwise the all-heads result.  Even: two pages a stage.
+constexpr int64_t kFp8Ctas = 3 * 152;
 inline int fp8_pages_per_chunk(int64_t pages, int d, int batch) {
-  const int64_t base = d == 128 ? 64 : 128;
-  int64_t want = ceil_div(2 * 152, 8 * static_cast<int64_t>(batch));
-  want = want > 32 ? 32 : want;  // (the single-pass merge)
-  int64_t per = ceil_div(ceil_div(pages, want), 8) * 8;
-  if (per > base) per = base;
-  const int64_t need = ceil_div(ceil_div(pages, kMaxChunks), 8) * 8;
-  return static_cast<int>(need > per ? need : per);
+  const int64_t base = d == 128 ? 64 : 128, units = 8 * static_cast<int64_t>(batch);
+  int64_t n = ceil_div(pages, base);  // chunks
+  if (n * units < 4 * kFp8Ctas) {
+    const int64_t waves = n * units / kFp8Ctas;
+    n = (waves > 1 ? waves : 1) * kFp8Ctas / units;
+    const int64_t most = ceil_div(pages, 8);
+    n = n < most ? n : most;
+    if (n > 32 && pages <= 32 * 32) n = 32;  // (the single-pass merge)
+    if (n < 1) n = 1;
+  }
+  if (n > kMaxChunks) n = kMaxChunks;
+  return static_cast<int>(ceil_div(ceil_div(pages, n), 2) * 2);
 }
 // Page-sparse attention over an 8-bit cache: the parts that each (batch, kv head)'s
 // union, of union_max pages at most, is cut into -- equal ones of the pages it
@@ -74,9 +81,8 @@ inline int fp8_pages_per_chunk(int64_t pages, int d, int batch) {
 // 128 pages (the largest possible: 512): 128 units 46.3 us a call and 32 units
 // 30.4, against 50.0 and 38.0 with chunks of 64 pages, 6 of 8 of them empty.
 inline int fp8_select_parts(int64_t union_max, int64_t units) {
-  constexpr int64_t kCtas = 3 * 152;
-  int64_t n = kCtas / units;
-  if (5 * n * units < 4 * kCtas) n = ceil_div(2 * kCtas, units);
+  int64_t n = kFp8Ctas / units;
+  if (5 * n * units < 4 * kFp8Ctas) n = ceil_div(2 * kFp8Ctas, units);
   const int64_t most = ceil_div(union_max, 8);
   n = n < most ? n : most;
   return static_cast<int>(n > 32 ? 32 : (n < 1 ? 1 : n));
