@@ -56,7 +56,7 @@ inline int select_pages_per_chunk(int64_t union_max, int d) {
 // waves of items on the 456 resident CTAs (three on each of 152 multiprocessors),
 // counting 8 kv heads, the size is changed to whole waves; less than one is cut
 // finer.  Depends on the pages, d and the batch only, so here too one kv head at
-// a time gives bitwise the all-heads result.  Even: two pages a stage.
+// a time gives bitwise the all-heads result.
 constexpr int64_t kFp8Ctas = 3 * 152;
 inline int fp8_pages_per_chunk(int64_t pages, int d, int batch) {
   const int64_t base = d == 128 ? 64 : 128, units = 8 * static_cast<int64_t>(batch);
@@ -70,7 +70,8 @@ inline int fp8_pages_per_chunk(int64_t pages, int d, int batch) {
     if (n < 1) n = 1;
   }
   if (n > kMaxChunks) n = kMaxChunks;
-  return static_cast<int>(ceil_div(ceil_div(pages, n), 2) * 2);
+  // two pages a stage for each of four warps
+  return static_cast<int>(ceil_div(ceil_div(pages, n), 8) * 8);
 }
 // Page-sparse attention over an 8-bit cache: the parts that each (batch, kv head)'s
 // union, of union_max pages at most, is cut into -- equal ones of the pages it
