@@ -80,7 +80,7 @@ WsLayout layout_for(const dkv_params& p, int top_k, bool fp8 = false) {
     L.union_stride = static_cast<int>(union_max);
     if (fp8) {
       L.pages_per_chunk = 0;  // equal parts of each unit's union
-      L.n_chunks = dkv::fp8_select_parts(union_max, units);
+      L.n_chunks = dkv::fp8_select_parts(union_max, d, units);
     } else {
       L.pages_per_chunk = dkv::select_pages_per_chunk(union_max, d);
       if (L.pages_per_chunk > dkv::kMaxSelectList) L.ok = false;

@@ -52,13 +52,14 @@
 // Bound by HBM: a token's K and V are 2 d bytes, once.  Measured on a GB300 (copy
 // rate 6.79 TB/s), 32 query / 8 kv heads, d = 128, with the merge: 16 sequences
 // of 32K tokens 158 us dense (6.8 TB/s), 165 us paged (6.5), ragged 116 us
-// (6.1); one of 1M tokens 305 us (7.0); 8 x 32 heads of 8K, d = 64, one query
-// head each, 47 us (5.7).  What the layout is worth there: with the heads on the
-// MMA's M side (8 of 16 rows, four to eight scores a lane, exact running maxima)
-// and two CTAs an SM, 183 us dense and 190 us paged; d = 64 paged pages of 1 KiB
-// are held back by the copy engine's rate of boxes (5.3 TB/s), so a dense cache
-// read in order takes two pages a box (52 -> 47 us at the 8K shape).  A small
-// call costs about 7 us, two kernels' chains of dependent loads.
+// (6.1); one of 1M tokens 303 us (7.1).  At d = 64 a page is the same work for
+// half the bytes, and its chain of dependent steps shows: 16 x 32K 86 us dense
+// (6.3), 95 us paged (5.6); 8 x 32 heads of 8K, one query head each, 47 us (5.7).
+// What the layout is worth, at 16 x 32K, d = 128: with the heads on the MMA's M
+// side (8 of 16 rows, four to eight scores a lane, exact running maxima) and two
+// CTAs an SM, 183 us dense and 190 us paged.  Two pages a box in a dense cache
+// read in order save the 8K shape 5 us.  A small call costs about 7 us, two
+// kernels' chains of dependent loads.
 //
 // Every mbarrier wait is bounded; on expiry the kernel records a timeout in
 // the status word, stops issuing, drains the copies it issued and exits.
@@ -90,10 +91,13 @@ struct Fp8Cfg {
   // K codes of both pages | V codes of both
   static constexpr int kVOffset = kPagesPerStage * kTileBytes;
   static constexpr int kStageBytes = 2 * kVOffset;
-  // Three CTAs an SM, each with 64 KiB of pages in flight; 8 heads of 128
-  // channels need more shared memory for the warps' merge: two CTAs with 96 KiB.
-  static constexpr int kCtas = GL == 8 && D == 128 ? 2 : 3;
-  static constexpr int kStages = (kCtas == 2 ? 96 : 64) * 1024 / kStageBytes;
+  // Three CTAs an SM, each with 64 KiB of pages in flight.  8 heads of 128
+  // channels take more registers and shared memory: two CTAs with 96 KiB.  Up to 4
+  // heads of 64 channels take fewer, and a page's work, the same for half the
+  // bytes, has more latency to hide: four with 48 KiB (16 x 32K paged 101 -> 99
+  // us, the select at 8 x 8K 36.8 -> 34.8).
+  static constexpr int kCtas = D == 64 ? (GL == 8 ? 3 : 4) : (GL == 8 ? 2 : 3);
+  static constexpr int kStages = (kCtas == 2 ? 96 : (kCtas == 3 ? 64 : 48)) * 1024 / kStageBytes;
   static constexpr int kSub = kStages / kConsumerWarps;    // stages per consumer warp
   static constexpr int kIssueLanes = kStages < 16 ? kStages : 16;
   static constexpr int kBarOffset = kStages * kStageBytes;

@@ -53,17 +53,17 @@ inline int select_pages_per_chunk(int64_t union_max, int d) {
 }
 // Exact attention: pages of an 8-bit cache a work item streams, of `pages` per
 // (batch, kv head): about 256 KiB of codes.  Where that makes fewer than four
-// waves of items on the 456 resident CTAs (three on each of 152 multiprocessors),
-// counting 8 kv heads, the size is changed to whole waves; less than one is cut
+// waves of items on the resident CTAs (fp8_ctas), counting 8 kv heads, the size is changed to whole waves; less than one is cut
 // finer.  Depends on the pages, d and the batch only, so here too one kv head at
 // a time gives bitwise the all-heads result.
-constexpr int64_t kFp8Ctas = 3 * 152;
+inline int64_t fp8_ctas(int d) { return 152 * (d == 64 ? 4 : 3); }  // (up to 4 query heads)
 inline int fp8_pages_per_chunk(int64_t pages, int d, int batch) {
   const int64_t base = d == 128 ? 64 : 128, units = 8 * static_cast<int64_t>(batch);
+  const int64_t ctas = fp8_ctas(d);
   int64_t n = ceil_div(pages, base);  // chunks
-  if (n * units < 4 * kFp8Ctas) {
-    const int64_t waves = n * units / kFp8Ctas;
-    n = (waves > 1 ? waves : 1) * kFp8Ctas / units;
+  if (n * units < 4 * ctas) {
+    const int64_t waves = n * units / ctas;
+    n = (waves > 1 ? waves : 1) * ctas / units;
     const int64_t most = ceil_div(pages, 8);
     n = n < most ? n : most;
     if (n > 32 && pages <= 32 * 32) n = 32;  // (the single-pass merge)
@@ -76,14 +76,15 @@ inline int fp8_pages_per_chunk(int64_t pages, int d, int batch) {
 // Page-sparse attention over an 8-bit cache: the parts that each (batch, kv head)'s
 // union, of union_max pages at most, is cut into -- equal ones of the pages it
 // turns out to have (fp8_part_pages), so no item is empty and none much longer
-// than another.  One wave of items where that fills the 456 resident CTAs (three
-// on each of 152 multiprocessors) to 4/5, else about two; 8 pages a part at
+// than another.  One wave of items where that fills the resident CTAs (fp8_ctas)
+// to 4/5, else about two; 8 pages a part at
 // least, and at most 32 parts (the single-pass merge).  Measured on unions of
 // 128 pages (the largest possible: 512): 128 units 46.3 us a call and 32 units
 // 30.4, against 50.0 and 38.0 with chunks of 64 pages, 6 of 8 of them empty.
-inline int fp8_select_parts(int64_t union_max, int64_t units) {
-  int64_t n = kFp8Ctas / units;
-  if (5 * n * units < 4 * kFp8Ctas) n = ceil_div(2 * kFp8Ctas, units);
+inline int fp8_select_parts(int64_t union_max, int d, int64_t units) {
+  const int64_t ctas = fp8_ctas(d);
+  int64_t n = ctas / units;
+  if (5 * n * units < 4 * ctas) n = ceil_div(2 * ctas, units);
   const int64_t most = ceil_div(union_max, 8);
   n = n < most ? n : most;
   return static_cast<int>(n > 32 ? 32 : (n < 1 ? 1 : n));
