@@ -91,13 +91,15 @@ struct Fp8Cfg {
   // K codes of both pages | V codes of both
   static constexpr int kVOffset = kPagesPerStage * kTileBytes;
   static constexpr int kStageBytes = 2 * kVOffset;
-  // Three CTAs an SM, each with 64 KiB of pages in flight.  8 heads of 128
-  // channels take more registers and shared memory: two CTAs with 96 KiB.  Up to 4
-  // heads of 64 channels take fewer, and a page's work, the same for half the
-  // bytes, has more latency to hide: four with 48 KiB (16 x 32K paged 101 -> 99
-  // us, the select at 8 x 8K 36.8 -> 34.8).
-  static constexpr int kCtas = D == 64 ? (GL == 8 ? 3 : 4) : (GL == 8 ? 2 : 3);
-  static constexpr int kStages = (kCtas == 2 ? 96 : (kCtas == 3 ? 64 : 48)) * 1024 / kStageBytes;
+  // Three CTAs an SM, each with 64 KiB of pages in flight.  64 channels take
+  // fewer registers, and a page's work, the same for half the bytes, has more
+  // latency to hide: four with 48 KiB (16 x 32K paged, 4 query heads a kv head,
+  // 101 -> 99 us, the select at 8 x 8K 36.8 -> 34.8).
+  static constexpr int kCtas = D == 64 ? 4 : 3;
+  static constexpr int kStages = (kCtas == 3 ? 64 : 48) * 1024 / kStageBytes;
+  // The warps' states of 8 heads are merged in two turns of 4.
+  static constexpr int kTurns = GL == 8 ? 2 : 1;
+  static constexpr int kMergeRows = GL / kTurns;
   static constexpr int kSub = kStages / kConsumerWarps;    // stages per consumer warp
   static constexpr int kIssueLanes = kStages < 16 ? kStages : 16;
   static constexpr int kBarOffset = kStages * kStageBytes;
@@ -106,7 +108,7 @@ struct Fp8Cfg {
   static constexpr int kMergeOffset = kDescOffset + 2 * 8;
   static constexpr int kMergeRow = D + 3;  // o[D], max m, sum l, exponent r
   static constexpr int kListOffset =
-      (kMergeOffset + (kConsumerWarps - 1) * GL * kMergeRow * 4 + 15) / 16 * 16;
+      (kMergeOffset + (kConsumerWarps - 1) * kMergeRows * kMergeRow * 4 + 15) / 16 * 16;
   static constexpr int kBlockOffset = kListOffset + 16 * kListPages;
   static constexpr int kFirstOffset = kBlockOffset + 4 * kListPages;
   static constexpr int kMiscOffset = kFirstOffset + 4 * kMaxRagged;
@@ -875,39 +877,45 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
     // have read the item's descriptor.
     if (consumers_any(aborted)) return;
     if (threadIdx.x == 0) mbar_arrive(dempty0 + 8 * slot);
-    if (warp > 0 && t4 < kOwners) {
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        float* r = mrg + ((warp - 1) * GL + h0 + e) * C::kMergeRow;
-        if (g == 0) {
-          r[D] = m_ref[e];
-          r[D + 1] = l_run[e];
-          r[D + 2] = r_ref[e];
-        }
+    for (int turn = 0; turn < C::kTurns; ++turn) {
+      // this turn's heads of the lane, and their row in a warp's part of the area
+      const int e0 = C::kTurns == 2 ? turn : 0, e1 = C::kTurns == 2 ? turn + 1 : kE;
+      const int row0 = C::kTurns == 2 ? t4 - turn : h0;  // (+ e)
+      if (turn > 0) consumers_sync();  // warp 0 has read the turn before
+      if (warp > 0 && t4 < kOwners) {
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          r[16 * c + 2 * g] = acc[c][e];
-          r[16 * c + 2 * g + 1] = acc[c][2 + e];
+        for (int e = e0; e < e1; ++e) {
+          float* r = mrg + ((warp - 1) * C::kMergeRows + row0 + e) * C::kMergeRow;
+          if (g == 0) {
+            r[D] = m_ref[e];
+            r[D + 1] = l_run[e];
+            r[D + 2] = r_ref[e];
+          }
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            r[16 * c + 2 * g] = acc[c][e];
+            r[16 * c + 2 * g + 1] = acc[c][2 + e];
+          }
         }
       }
-    }
-    consumers_sync();
-    if (warp == 0 && t4 < kOwners) {
+      consumers_sync();
+      if (warp > 0 || t4 >= kOwners) continue;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {
+      for (int e = e0; e < e1; ++e) {
         if (h0 + e >= a.G) continue;
-        const float* rows = mrg + (h0 + e) * C::kMergeRow;  // of warp 1
+        const float* rows = mrg + (row0 + e) * C::kMergeRow;  // of warp 1
+        constexpr int kNext = C::kMergeRows * C::kMergeRow;   // to the next warp's
         float M = m_ref[e];
 #pragma unroll
-        for (int v = 1; v < kConsumerWarps; ++v)
-          M = fmaxf(M, rows[(v - 1) * GL * C::kMergeRow + D]);
+        for (int v = 1; v < kConsumerWarps; ++v) M = fmaxf(M, rows[(v - 1) * kNext + D]);
         // f: 2^(m - M + r), the weight of a warp's o (unset: 0, or o is 0)
         float f[kConsumerWarps];
         f[0] = exp2f((m_ref[e] - M) + r_ref[e]);
         float L = exp2f(m_ref[e] - M) * l_run[e];
 #pragma unroll
         for (int v = 1; v < kConsumerWarps; ++v) {
-          const float* r = rows + (v - 1) * GL * C::kMergeRow;
+          const float* r = rows + (v - 1) * kNext;
           f[v] = exp2f((r[D] - M) + r[D + 2]);
           L += exp2f(r[D] - M) * r[D + 1];
         }
@@ -921,7 +929,7 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
           const int ch = 16 * c + 2 * g;
 #pragma unroll
           for (int v = 1; v < kConsumerWarps; ++v) {
-            const float* r = rows + (v - 1) * GL * C::kMergeRow + ch;
+            const float* r = rows + (v - 1) * kNext + ch;
             O.x += f[v] * r[0];
             O.y += f[v] * r[1];
           }

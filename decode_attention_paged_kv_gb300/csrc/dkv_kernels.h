@@ -53,10 +53,12 @@ inline int select_pages_per_chunk(int64_t union_max, int d) {
 }
 // Exact attention: pages of an 8-bit cache a work item streams, of `pages` per
 // (batch, kv head): about 256 KiB of codes.  Where that makes fewer than four
-// waves of items on the resident CTAs (fp8_ctas), counting 8 kv heads, the size is changed to whole waves; less than one is cut
-// finer.  Depends on the pages, d and the batch only, so here too one kv head at
+// waves of items on the resident CTAs (fp8_ctas), counting 8 kv heads, the size
+// is changed to whole waves; less than one is cut finer.  Measured at 32K tokens,
+// 32 / 8 heads, d = 128: 2 sequences 36.8 -> 29.2 us, 4 56.4 -> 50.3; 16, nine
+// waves of 64 pages, 165 us (32 pages: 180, 128: 165).  Depends on the pages, d and the batch only, so here too one kv head at
 // a time gives bitwise the all-heads result.
-inline int64_t fp8_ctas(int d) { return 152 * (d == 64 ? 4 : 3); }  // (up to 4 query heads)
+inline int64_t fp8_ctas(int d) { return 152 * (d == 64 ? 4 : 3); }
 inline int fp8_pages_per_chunk(int64_t pages, int d, int batch) {
   const int64_t base = d == 128 ? 64 : 128, units = 8 * static_cast<int64_t>(batch);
   const int64_t ctas = fp8_ctas(d);

@@ -437,7 +437,7 @@ def test_resident_ctas(sparse, dev, dkv):
         for dt in (dkv.DKV_BF16, dkv.DKV_FP16):
             assert dkv.lib().dkv_attn_ctas_per_sm(d, dt, dkv.DKV_KV_FP8, sparse,
                                                   ctypes.byref(n)) == 0
-            assert n.value == (3 if d == 64 else 2)  # (8 heads a kv head)
+            assert n.value == (4 if d == 64 else 3)
 
 
 def test_python_refusals(dev, dkv):
