@@ -243,8 +243,9 @@ void set_query(dkv_params* p, const Cache& c, const at::Tensor& q, PyObject* sca
   p->flags = static_cast<uint32_t>(flags);
 }
 void set_out(dkv_params* p, const at::Tensor& q, const at::Tensor& out) {
-  if (out.sizes() != q.sizes()) value_error("out must have q's shape");
-  if (out.stride(2) != 1) value_error("out must have channel stride 1");
+  if (out.dim() != 3 || out.size(0) < q.size(0) || out.size(1) < q.size(1) ||
+      out.size(2) < q.size(2) || out.stride(2) != 1)
+    value_error("out must hold [B, Hq, d] with channel stride 1");
   p->o_stride_b = out.stride(0), p->o_stride_h = out.stride(1);
 }
 
@@ -514,9 +515,9 @@ PyObject* decode_attn_select(PyObject* const* a) {
   if (wanted < 0) throw PyError{};
   std::optional<at::Tensor> made;
   if (chosen != nullptr) {
-    if (chosen->scalar_type() != at::kInt || !chosen->is_contiguous() || chosen->dim() != 3 ||
-        chosen->size(0) != c.k.B || chosen->size(1) != q.size(1) || chosen->size(2) != kk)
-      value_error("selected must be a contiguous int32 [B, Hq, min(top_k, P)]");
+    if (chosen->scalar_type() != at::kInt || !chosen->is_contiguous() ||
+        chosen->numel() < c.k.B * q.size(1) * kk)
+      value_error("selected must hold a contiguous int32 [B, Hq, min(top_k, P)]");
   } else if (wanted) {
     made = at::empty({c.k.B, q.size(1), kk}, q.options().dtype(at::kInt));
     chosen = &*made;

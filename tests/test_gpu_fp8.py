@@ -472,9 +472,34 @@ def test_python_refusals(dev, dkv):
                  lambda: dkv.decode_attn_full(qd, Kd, Vd, seq_lens=torch.ones(1, dtype=torch.int32)),
                  lambda: dkv.decode_attn_select(
                      qd, Kd, Vd, dkv.kv_meta_build(Kd), 2,
-                     selected=torch.zeros(1, 2, 3, dtype=torch.int32, device=dev))):
+                     selected=torch.zeros(1, 2, 1, dtype=torch.int32, device=dev))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_two_calls_at_once(dev, dkv):
+    # two streams, a workspace each, caches and metadata shared
+    q, K, V = make(4, 8, 2, 128, 9000, torch.bfloat16, seed=4)
+    Kd, Vd = caches(dkv, dev, K, V, torch.bfloat16, True)
+    meta = dkv.kv_meta_build(Kd)
+    qs = [q.to(dev), q.flip(1).contiguous().to(dev)]
+    want = [(dkv.decode_attn_full(x, Kd, Vd), dkv.decode_attn_select(x, Kd, Vd, meta, 20))
+            for x in qs]
+    n = max(dkv.workspace_bytes(4, 8, 2, 128, 9000, k, fp8=True) for k in (0, 20))
+    ws = [torch.zeros(n, dtype=torch.uint8, device=dev) for _ in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append((dkv.decode_attn_full(qs[i], Kd, Vd, workspace=ws[i]),
+                               dkv.decode_attn_select(qs[i], Kd, Vd, meta, 20, workspace=ws[i])))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert dkv.read_device_status(ws[i]) == 0
+        for full, sparse in got[i]:
+            assert torch.equal(full, want[i][0]) and torch.equal(sparse, want[i][1])
 
 
 def test_decode_loop(dev, dkv):
