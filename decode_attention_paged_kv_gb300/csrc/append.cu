@@ -20,8 +20,8 @@
 // Two kernels.  append_token_kernel: d/16 threads a token and head, 16
 // channels (two 16-byte vectors, the two halves of 8 rotation pairs) each;
 // nothing is shared between tokens, so it serves the single-token call -- where
-// the d/16 threads of an 8-bit cache agree on the scale by shuffles -- and few
-// tokens into a 16-bit cache.  append_block_kernel: a CTA of d threads takes a
+// the d/16 threads of an 8-bit cache agree on the scale by shuffles -- and short
+// appends into a 16-bit cache.  append_block_kernel: a CTA of d threads takes a
 // touched block and four heads at a time, a thread per token and 16 channels of
 // each; the blocks' amax are reduced through shared memory while the rotated
 // values wait in registers, so they are read and rotated once, and the heads
@@ -420,9 +420,14 @@ __global__ void __launch_bounds__(D, block_ctas<D, EIGHT>()) append_block_kernel
 template <int D, bool F16, bool IL>
 cudaError_t launch_t(bool eight, const AppendArgs& a, int num_sms, cudaStream_t s) {
   const uint32_t heads = 2 * a.Hkv + a.Hq;
-  // Few tokens into a 16-bit cache: 4 a sequence of 64 take 2.7 us here against
-  // 3.7 in the persistent kernel, 8K prompts 302 us against 270.
-  if (a.T > (eight ? 1 : 16)) {
+  // Into a 16-bit cache, a thread a row segment while all of them are resident at
+  // once (2048 a SM) or there are few tokens a sequence; us here against the
+  // persistent kernel's (32 / 8 heads, d = 128): 64 sequences of 4 tokens 2.7 /
+  // 3.6, 8 of 64 3.0 / 4.0, 1 of 512 3.1 / 4.0; at 64 of 16, just past it, 4.7 /
+  // 5.0, 64 of 32 9.3 / 9.0, 8 prompts of 8K 302 / 270.
+  const int64_t threads = static_cast<int64_t>(a.B) * a.T * heads * (D / 16);
+  const bool by_token = eight ? a.T == 1 : a.T <= 16 || threads <= num_sms * 2048;
+  if (!by_token) {
     const int64_t groups = 2 * ceil_div(a.Hkv, kHeads) + ceil_div(a.Hq, kHeads);
     const int64_t items = static_cast<int64_t>(a.B) * a.pages * groups;
     const int64_t most = static_cast<int64_t>(num_sms) *

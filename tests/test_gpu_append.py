@@ -160,6 +160,42 @@ def test_append_without_lengths(kind, B, Hq, Hkv, N, T, dev, dkv):
         False, seed=N)
 
 
+# More rows than a device holds threads for: 16-bit caches change kernels there.
+@pytest.mark.parametrize("kind", ["dense", "paged"])
+@pytest.mark.parametrize("d,dt,r,il", [(128, torch.bfloat16, 128, False),
+                                       (64, torch.float16, 48, True)])
+@pytest.mark.parametrize("lens,news", [
+    (None, None), ([650, 41, 700, 17, 0], [601, 30, 650, 1, 0]),
+    ([701, 600, 600, 699, 33], [5, 651, 600, -1, 33])])
+def test_many_tokens(kind, d, dt, r, il, lens, news, dev, dkv):
+    ws = torch.zeros(dkv.DKV_WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=dev)
+    bad = run(dkv, dev, kind, 5, 9, 5 if d == 128 else 15, d, 700, 650, lens, news, dt, r, il,
+              seed=d, workspace=ws)
+    assert dkv.read_device_status(ws) == (dkv.DKV_ERR_DEVICE_CHECK if bad else 0)
+
+
+def test_many_tokens_with_a_bad_block(dev, dkv):
+    gen = torch.Generator().manual_seed(3)
+    B, H, N = 4, 11, 700
+    table = table_for(B, N, gen)
+    K = Cache(dkv, "paged", B, H, N, 128, torch.bfloat16, gen, dev, table)
+    V = Cache(dkv, "paged", B, H, N, 128, torch.bfloat16, gen, dev, table)
+    bt = table.clone()
+    bt[1, 2], bt[3, 43] = -1, 1 << 30  # tokens 32 .. 47 of one, the last 12 of another
+    K.obj = K.obj._replace(block_table=bt.to(dev))
+    V.obj = V.obj._replace(block_table=K.obj.block_table)
+    x = torch.randn(B, N, H, 128, generator=gen).to(torch.bfloat16)
+    ws = torch.zeros(256, dtype=torch.uint8, device=dev)
+    q = dkv.kv_append(x.to(dev), x.to(dev), K.obj, V.obj, q=x.to(dev), workspace=ws)
+    assert dkv.read_device_status(ws) == dkv.DKV_ERR_DEVICE_CHECK
+    assert torch.equal(q.cpu(), x)
+    for c in (K, V):
+        keep = c.ref[1, :, 32:48].clone(), c.ref[3, :, 688:].clone()
+        c.ref[:, :, :N] = x.permute(0, 2, 1, 3)
+        c.ref[1, :, 32:48], c.ref[3, :, 688:] = keep
+        c.check()
+
+
 @pytest.mark.parametrize("kind", ["paged", "fp8"])
 @pytest.mark.parametrize("T", [1, 18])
 def test_more_sequences_than_are_counted(kind, T, dev, dkv):
