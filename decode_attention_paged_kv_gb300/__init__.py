@@ -271,8 +271,8 @@ def _params(q: Optional[torch.Tensor], B, Hkv, N, d, out: Optional[torch.Tensor]
         if qB != B or qd != d or one != 1:
             raise ValueError(f"q shape {tuple(q.shape)} does not match the cache")
     if out is not None:
-        if out.shape != q.shape:
-            raise ValueError(f"out must be {tuple(q.shape)}")
+        if out.dim() != 3 or any(a < b for a, b in zip(out.shape, q.shape)):
+            raise ValueError(f"out must hold {tuple(q.shape)}")
         osb, osh, one = out.stride()
         if one != 1:
             raise ValueError("out must have channel stride 1")
@@ -421,6 +421,8 @@ def decode_attn_select(q, K, V, meta, top_k: int, scale: Optional[float] = None,
     from hot_state())."""
     if group_select:
         flags |= DKV_FLAG_GROUP_SELECT
+    if not isinstance(meta, (tuple, list)):
+        meta = tuple(meta)
     return (_binding or _load_binding()).decode_attn_select(
         q, K, V, meta, top_k, scale, out_dtype, out, return_selected, selected, workspace, flags,
         seq_lens, page_size, hot, step)

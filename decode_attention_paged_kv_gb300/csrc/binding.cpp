@@ -67,8 +67,11 @@ at::ScalarType scalar_type(PyObject* o) {
   return reinterpret_cast<THPDtype*>(o)->scalar_type;
 }
 
-int64_t integer(PyObject* o) {
-  const long long v = PyLong_AsLongLong(o);
+int64_t integer(PyObject* o) {  // as int(o)
+  PyObject* n = PyNumber_Long(o);
+  if (n == nullptr) throw PyError{};
+  const long long v = PyLong_AsLongLong(n);
+  Py_DECREF(n);
   if (v == -1 && PyErr_Occurred()) throw PyError{};
   return v;
 }

@@ -502,6 +502,29 @@ def test_two_calls_at_once(dev, dkv):
             assert torch.equal(full, want[i][0]) and torch.equal(sparse, want[i][1])
 
 
+def test_arguments_that_16_bit_calls_take(dev, dkv):
+    # outputs and selections with room to spare, metadata as one tensor, counts
+    # that int() takes
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn(2, 4, 64, generator=g).to(torch.bfloat16).to(dev)
+    K, V = (torch.randn(2, 2, 100, 64, generator=g).to(torch.bfloat16).to(dev) for _ in range(2))
+    mn, mx = dkv.kv_meta_build(K)
+    want = dkv.decode_attn_select(q, K, V, (mn, mx), 3, return_selected=True)
+    got = dkv.decode_attn_select(q, K, V, torch.stack((mn, mx)), np.float64(3.0),
+                                 return_selected=True)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    for f in (lambda **o: dkv.decode_attn_topk_tokens(q, K, V, 5, **o),
+              lambda **o: dkv.decode_attn_full(q, K, V, **o)):
+        out = torch.full((3, 5, 80), 9.0, device=dev)
+        assert f(out=out) is out
+        assert torch.equal(out[:2, :4, :64], f())
+        out[:2, :4, :64] = 9.0
+        assert (out == 9.0).all()
+        for bad in (out[:1], out[:, :3], out[:, :, :32], out[0]):
+            with pytest.raises(ValueError, match="out must hold"):
+                f(out=bad)
+
+
 def test_decode_loop(dev, dkv):
     """A prompt, then steps of append, newest-page metadata, exact and sparse
     attention, captured in two graphs that share a workspace: against 64-bit
