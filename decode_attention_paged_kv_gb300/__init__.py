@@ -185,6 +185,7 @@ def lib() -> ctypes.CDLL:
             L.dkv_workspace_bytes_tokens.argtypes = [P, i32]
             L.dkv_workspace_bytes_tokens.restype = sz
             L.dkv_kv_meta_append.argtypes = [P, KVp, vp, vp, vp]
+            L.dkv_kv_meta_append_tokens.argtypes = [P, KVp, i32, vp, vp, vp, vp]
             L.dkv_hot_state_bytes.argtypes = [P]
             L.dkv_hot_state_bytes.restype = sz
             L.dkv_decode_attn_select_hot.argtypes = [P, vp, KVp, KVp, vp, vp, i32, vp, i32, vp,
@@ -198,6 +199,7 @@ def lib() -> ctypes.CDLL:
             for name in ("dkv_kv_meta_build", "dkv_decode_attn_full", "dkv_decode_attn_select",
                          "dkv_decode_attn_topk_tokens", "dkv_kv_meta8_build",
                          "dkv_decode_attn_select_meta8", "dkv_kv_meta_append",
+                         "dkv_kv_meta_append_tokens",
                          "dkv_decode_attn_select_hot", "dkv_kv_append",
                          "dkv_kv_quant4", "dkv_kv_dequant4", "dkv_read_device_status",
                          "dkv_attn_ctas_per_sm"):
@@ -312,12 +314,18 @@ def kv_meta_build(K, page_size: int = PAGE_SIZE, seq_lens: Optional[torch.Tensor
 
 
 def kv_meta_append(K, meta, page_size: int = PAGE_SIZE,
-                   seq_lens: Optional[torch.Tensor] = None):
-    """After a decode step appended tokens: rebuild, in place, only the page
-    of `meta` (from kv_meta_build) holding each sequence's last token (N_b - 1,
-    N_b from seq_lens, else the cache length)."""
+                   seq_lens: Optional[torch.Tensor] = None, new_tokens: Optional[int] = None,
+                   new_lens: Optional[torch.Tensor] = None):
+    """After an append: rebuild, in place, only the pages of `meta` (from
+    kv_meta_build) that the new tokens changed.
+
+    seq_lens: each sequence's length with them (None: the cache length), as
+    kv_append took it.  new_tokens: the rows T of that append (None: 1, a decode
+    step); new_lens (int32 [B] on the device): how many of them each sequence
+    has (None: all).  The other pages must be built already."""
     mn, mx = meta
-    (_binding or _load_binding()).kv_meta_append(K, (mn, mx), page_size, seq_lens)
+    (_binding or _load_binding()).kv_meta_append(K, (mn, mx), page_size, seq_lens, new_tokens,
+                                                 new_lens)
     return mn, mx
 
 
@@ -348,7 +356,10 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, K, V, seq_lens: Optional[torch.T
     instead of (i, i + r / 2).
     workspace: where sequences that do not fit, and block-table entries outside
     the pool, are recorded (read_device_status); nothing of them is written.
-    K and V: both dense tensors, PagedCache, Fp8Cache or Fp8PagedCache."""
+    K and V: both dense tensors, PagedCache, Fp8Cache or Fp8PagedCache.
+
+    The page metadata of K does not follow by itself: kv_meta_append with
+    new_tokens=T and the same seq_lens and new_lens brings it up to date."""
     return (_binding or _load_binding()).kv_append(k, v, K, V, seq_lens, new_lens, q, q_out, rope,
                                                    interleaved, workspace)
 

@@ -346,12 +346,13 @@ size_t dkv_workspace_bytes_fp8(const dkv_params* p, int32_t top_k) {
 }
 
 static dkv_status meta_impl(const dkv_params* p, const dkv_kv* K, void* meta_min,
-                            void* meta_max, bool last_only, void* stream) {
+                            void* meta_max, const dkv::MetaNew& fresh, void* stream) {
   dkv_status st = check_params(p);
   if (st != DKV_OK) return st;
   if ((st = check_kv(p, K)) != DKV_OK) return st;
   if (meta_min == nullptr || meta_max == nullptr) return DKV_ERR_NULL;
   if (!aligned16(meta_min) || !aligned16(meta_max)) return DKV_ERR_ALIGN;
+  if (fresh.slots > 0 && fresh.T == 0) return DKV_OK;  // nothing was appended
   if (is_fp8(K)) {
     dkv::MetaFp8Args f{};
     f.codes = static_cast<const uint8_t*>(K->data);
@@ -366,7 +367,7 @@ static dkv_status meta_impl(const dkv_params* p, const dkv_kv* K, void* meta_min
     f.meta_min = meta_min;
     f.meta_max = meta_max;
     f.lens = p->seq_lens;
-    f.last_only = last_only ? 1 : 0;
+    f.fresh = fresh;
     if (is_paged(K)) {
       f.bt = K->block_table;
       f.bts = K->block_table_stride;
@@ -392,7 +393,7 @@ static dkv_status meta_impl(const dkv_params* p, const dkv_kv* K, void* meta_min
   a.meta_min = meta_min;
   a.meta_max = meta_max;
   a.lens = p->seq_lens;
-  a.last_only = last_only ? 1 : 0;
+  a.fresh = fresh;
   if (K->format == DKV_KV_PAGED) {
     a.bt = K->block_table;
     a.bts = K->block_table_stride;
@@ -404,12 +405,30 @@ static dkv_status meta_impl(const dkv_params* p, const dkv_kv* K, void* meta_min
 
 dkv_status dkv_kv_meta_build(const dkv_params* p, const dkv_kv* K, void* meta_min,
                              void* meta_max, void* stream) {
-  return meta_impl(p, K, meta_min, meta_max, false, stream);
+  return meta_impl(p, K, meta_min, meta_max, dkv::MetaNew{}, stream);
 }
 
 dkv_status dkv_kv_meta_append(const dkv_params* p, const dkv_kv* K, void* meta_min,
                               void* meta_max, void* stream) {
-  return meta_impl(p, K, meta_min, meta_max, true, stream);
+  return dkv_kv_meta_append_tokens(p, K, 1, nullptr, meta_min, meta_max, stream);
+}
+
+dkv_status dkv_kv_meta_append_tokens(const dkv_params* p, const dkv_kv* K, int32_t new_tokens,
+                                     const int32_t* new_lens, void* meta_min, void* meta_max,
+                                     void* stream) {
+  const dkv_status st = check_params(p);
+  if (st != DKV_OK) return st;
+  if (new_tokens < 0 || new_tokens > p->seq_len) return DKV_ERR_SHAPE;
+  if (reinterpret_cast<uintptr_t>(new_lens) & 3u) return DKV_ERR_ALIGN;
+  dkv::MetaNew m{};
+  m.T = new_tokens;
+  m.news = new_lens;
+  m.align = K != nullptr && is_fp8(K) ? std::max(p->page_size, dkv::kPage) : p->page_size;
+  // the first new token may be the last of its `align` tokens
+  const int64_t span = static_cast<int64_t>(new_tokens) + m.align - 1;
+  m.slots = static_cast<int>(
+      std::min(ceil_div(span, p->page_size), ceil_div(p->seq_len, p->page_size)));
+  return meta_impl(p, K, meta_min, meta_max, m, stream);
 }
 
 static dkv_status attn_common(const dkv_params* p, const void* q, const dkv_kv* K,

@@ -362,7 +362,7 @@ Meta meta_pair(PyObject* o, const Cache& c, int64_t P) {
   return m;
 }
 
-// kv_meta_append(K, meta, page_size, seq_lens)
+// kv_meta_append(K, meta, page_size, seq_lens, new_tokens, new_lens)
 PyObject* kv_meta_append(PyObject* const* a) {
   const Cache c = parse_cache(a[0]);
   const int64_t S = integer(a[2]);
@@ -370,8 +370,13 @@ PyObject* kv_meta_append(PyObject* const* a) {
   const Meta m = meta_pair(a[1], c, S > 0 ? (c.N + S - 1) / S : 0);
   if (cuda_index(*m.mn) != c.device || cuda_index(*m.mx) != c.device)
     value_error("meta must be on the cache's device");
+  const int32_t* news = lengths(a[5], "new_lens", c.B, c.device);
+  if (news != nullptr && is_none(a[4])) value_error("new_lens needs new_tokens");
+  const int64_t T = is_none(a[4]) ? 1 : integer(a[4]);
+  const int32_t fresh = T < 0 ? -1 : int32_size(T);
   call("dkv_kv_meta_append", c.device, [&](void* stream) {
-    return dkv_kv_meta_append(&p, &c.kv, m.mn->data_ptr(), m.mx->data_ptr(), stream);
+    return dkv_kv_meta_append_tokens(&p, &c.kv, fresh, news, m.mn->data_ptr(), m.mx->data_ptr(),
+                                     stream);
   });
   Py_RETURN_NONE;
 }
@@ -583,7 +588,7 @@ PyMethodDef method(const char* name) {
 PyMethodDef g_methods[] = {method<setup, 6>("setup"),
                            method<describe_cache, 1>("describe_cache"),
                            method<kv_meta_build, 3>("kv_meta_build"),
-                           method<kv_meta_append, 4>("kv_meta_append"),
+                           method<kv_meta_append, 6>("kv_meta_append"),
                            method<kv_append, 11>("kv_append"),
                            method<decode_attn_full, 9>("decode_attn_full"),
                            method<decode_attn_select, 16>("decode_attn_select"),

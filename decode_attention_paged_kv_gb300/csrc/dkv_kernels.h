@@ -306,6 +306,25 @@ struct TokenAttnArgs {
   int64_t o_sb, o_sh;
 };
 
+// The pages of metadata that an append changed: with n_b (news, or T for all) of
+// sequence b's tokens new, those from the one holding the first of them, rounded
+// down to `align` tokens, to the one holding its last token.
+struct MetaNew {
+  int slots;                   // most pages an append can change; 0: build every page
+  int T;                       // most new tokens of a sequence
+  const int32_t* news;         // [B], or nullptr: all T
+  int align;                   // S; 8-bit caches: at least 16, since a block whose
+                               // scale rises has its older codes rounded again
+};
+// The first page of metadata (S tokens each) that an append to sequence b, now
+// of Nb tokens, changed; a page past the sequence if it got no token.  (S and
+// `align` are powers of two.)
+__device__ __forceinline__ int page_of(int token, int S) { return token >> (__ffs(S) - 1); }
+__device__ __forceinline__ int first_new_page(const MetaNew& m, int b, int Nb, int S) {
+  const int n = min(min(m.news != nullptr ? m.news[b] : m.T, m.T), Nb);
+  return n > 0 ? page_of((Nb - n) & -m.align, S) : page_of(Nb - 1, S) + 1;
+}
+
 struct MetaArgs {
   const void* data;            // dense K or Q4 codes
   const void* gmin;
@@ -319,7 +338,7 @@ struct MetaArgs {
   int nblocks;
   const int32_t* lens;         // per-sequence lengths [B] or nullptr (all N)
   int S;                       // tokens per metadata page (16, 32 or 64); P = ceil(N / S)
-  int last_only;               // 1: only the page holding each sequence's last token
+  MetaNew fresh;
 };
 
 // Metadata of an 8-bit cache, in the cache's 16-bit type.
@@ -334,7 +353,7 @@ struct MetaFp8Args {
   int64_t bts;
   int nblocks;
   const int32_t* lens;
-  int last_only;
+  MetaNew fresh;
 };
 
 // New tokens' rows [B, T, heads, d] (strides in elements).

@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(kThreads, MULTI ? 3 : 5) meta_fp8_kernel(const
   constexpr int kVec = D / 16;  // 16-byte vectors per row
   griddep_launch_dependents();
   griddep_wait();
-  // every page, or (last_only) one page per (batch, kv head)
-  const int pages = a.last_only ? 1 : a.P;
+  // every page, or those that an append changed
+  const int pages = a.fresh.slots > 0 ? a.fresh.slots : a.P;
   const int64_t total = static_cast<int64_t>(a.B) * a.Hkv * pages * kVec;
   for (int64_t idx = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; idx < total;
        idx += static_cast<int64_t>(gridDim.x) * blockDim.x) {
@@ -59,10 +59,11 @@ __global__ void __launch_bounds__(kThreads, MULTI ? 3 : 5) meta_fp8_kernel(const
     const int h = static_cast<int>(bh % a.Hkv);
     const int b = static_cast<int>(bh / a.Hkv);
     const int Nb = seq_len_of(a.lens, b, a.N);
-    const int page = a.last_only ? (Nb - 1) / a.S : static_cast<int>(idx / kVec % pages);
-    const int t0 = page * a.S;  // a metadata page of S tokens
+    const int page = static_cast<int>(idx / kVec % pages) +
+                     (a.fresh.slots > 0 ? first_new_page(a.fresh, b, Nb, a.S) : 0);
     // past a shorter sequence, or an empty one: not written
-    if (t0 >= Nb || (a.lens != nullptr && a.lens[b] <= 0)) continue;
+    if (page > page_of(Nb - 1, a.S) || (a.lens != nullptr && a.lens[b] <= 0)) continue;
+    const int t0 = page * a.S;  // a metadata page of S tokens
     const int nt = min(a.S, Nb - t0);
     float mn[16], mx[16];
     if constexpr (MULTI) {
@@ -145,7 +146,7 @@ cudaError_t launch_t(int d, bool f16, const MetaFp8Args& a, dim3 grid, cudaStrea
 
 cudaError_t launch_meta_fp8(int d, bool f16, const MetaFp8Args& a, cudaStream_t s) {
   const int64_t work =
-      static_cast<int64_t>(a.B) * a.Hkv * (a.last_only ? 1 : a.P) * (d / 16);
+      static_cast<int64_t>(a.B) * a.Hkv * (a.fresh.slots > 0 ? a.fresh.slots : a.P) * (d / 16);
   const int64_t blocks = ceil_div(work, kThreads);
   const dim3 grid(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30)));
   return a.S > kPage ? launch_t<true>(d, f16, a, grid, s) : launch_t<false>(d, f16, a, grid, s);

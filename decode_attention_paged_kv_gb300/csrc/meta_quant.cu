@@ -80,8 +80,8 @@ __global__ void __launch_bounds__(kMetaThreads, 2) meta_kernel(const MetaArgs a)
   griddep_launch_dependents();
   griddep_wait();
   const int vpr = a.d / 8;  // 16-byte vectors per row
-  // every page, or (last_only) one page per (batch, kv head)
-  const int pages = a.last_only ? 1 : a.P;
+  // every page, or those that an append changed
+  const int pages = a.fresh.slots > 0 ? a.fresh.slots : a.P;
   const int64_t total = static_cast<int64_t>(a.B) * a.Hkv * pages * vpr;
   for (int64_t idx = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; idx < total;
        idx += static_cast<int64_t>(gridDim.x) * blockDim.x) {
@@ -90,11 +90,11 @@ __global__ void __launch_bounds__(kMetaThreads, 2) meta_kernel(const MetaArgs a)
     const int h = static_cast<int>(bh % a.Hkv);
     const int b = static_cast<int>(bh / a.Hkv);
     const int Nb = seq_len_of(a.lens, b, a.N);
-    // the page holding the sequence's newest token, or page idx / vpr % P
-    const int page = a.last_only ? (Nb - 1) / a.S : static_cast<int>(idx / vpr % a.P);
+    const int page = static_cast<int>(idx / vpr % pages) +
+                     (a.fresh.slots > 0 ? first_new_page(a.fresh, b, Nb, a.S) : 0);
+    if (page > page_of(Nb - 1, a.S)) continue;  // past a shorter sequence: not written
     const int64_t pg = bh * a.P + page;  // (b * Hkv + h) * P + page
     const int t0 = page * a.S;  // a metadata page of S tokens
-    if (t0 >= Nb) continue;  // past a shorter sequence: not written
     const int nt = min(a.S, Nb - t0);
     uint32_t kmin[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
     uint32_t kmax[4] = {0u, 0u, 0u, 0u};
@@ -264,17 +264,21 @@ __global__ void __launch_bounds__(kMetaThreads, 4) meta_q4_kernel(const MetaArgs
   for (int bh = blockIdx.y; bh < a.B * a.Hkv; bh += gridDim.y) {
     const int h = bh % a.Hkv, b = bh / a.Hkv;
     const int Nb = seq_len_of(a.lens, b, a.N);
-    // page slot -> page: every page, or (last_only) slot 0 is the newest token's page
-    const int slot = lin / LPP;
-    const int last = (Nb - 1) / a.S;
-    const bool live = a.last_only ? slot == 0 : slot < a.P;
-    const int page = a.last_only ? last : slot;
-    const int nt = live ? max(0, min(a.S, Nb - page * a.S)) : 0;
+    // page slot -> page: from page 0, or from the first that an append changed
+    const bool some = a.fresh.slots > 0;
+    const int slot = lin / LPP, slots = some ? a.fresh.slots : a.P;
+    const int last = page_of(Nb - 1, a.S);
+    const int page0 = some ? first_new_page(a.fresh, b, Nb, a.S) : 0;
+    const bool live = slot < slots && slot <= last - page0;
+    // (lanes past an append's last page follow the ones on it)
+    const int page = some ? min(page0 + slot, last) : slot;
+    const int nt = live ? min(a.S, Nb - page * a.S) : 0;
     // tokens of the warp's first and last pages (pages are consecutive)
-    const int wfirst = a.last_only ? (wpage == 0 ? last : a.P) : wpage;
-    const int wlast = a.last_only ? wfirst : wpage + 32 / LPP - 1;
-    const int nt_first = wfirst < a.P ? max(0, min(a.S, Nb - wfirst * a.S)) : 0;
-    const int nt_last = wlast < a.P ? max(0, min(a.S, Nb - wlast * a.S)) : 0;
+    const int wfirst = page0 + wpage;
+    const int wlast = some ? min(min(wfirst + 32 / LPP, page0 + slots) - 1, last)
+                           : wpage + 32 / LPP - 1;
+    const int nt_first = wpage < slots && wfirst <= last ? min(a.S, Nb - wfirst * a.S) : 0;
+    const int nt_last = wlast <= last ? min(a.S, Nb - wlast * a.S) : 0;
     const int t0 = page * a.S;
     const uint8_t* src = static_cast<const uint8_t*>(a.data) + b * a.sb + h * a.sh +
                          static_cast<int64_t>(t0) * (D / 2) + 8 * u;
@@ -711,9 +715,9 @@ int grid_for(int64_t threads, int block) {
 cudaError_t launch_meta(bool q4, bool f16, const MetaArgs& a, cudaStream_t s) {
   (void)f16;  // min / max on order-preserving keys: identical code for bf16 and fp16
   const int64_t work =
-      static_cast<int64_t>(a.B) * a.Hkv * (a.last_only ? 1 : a.P) * (a.d / 8);
+      static_cast<int64_t>(a.B) * a.Hkv * (a.fresh.slots > 0 ? a.fresh.slots : a.P) * (a.d / 8);
   const dim3 grid(grid_for(work, kMetaThreads)), block(kMetaThreads);
-  if (!q4 && !a.last_only && (a.S == 4 || a.S == 8)) {
+  if (!q4 && a.fresh.slots == 0 && (a.S == 4 || a.S == 8)) {
     // a thread per 16-token cache page and 8 channels
     const int64_t sub_work =
         static_cast<int64_t>(a.B) * a.Hkv * ceil_div(a.N, kPage) * (a.d / 8);
@@ -723,7 +727,7 @@ cudaError_t launch_meta(bool q4, bool f16, const MetaArgs& a, cudaStream_t s) {
   }
   if (!q4) return launch_pdl(meta_kernel, grid, block, 0, s, a);
   // one row of blocks per (batch, kv head): the row's pages, d/16 lanes each
-  const int64_t row = static_cast<int64_t>(a.last_only ? 1 : a.P) * (a.d / 16);
+  const int64_t row = static_cast<int64_t>(a.fresh.slots > 0 ? a.fresh.slots : a.P) * (a.d / 16);
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv;
   const dim3 grid4(static_cast<unsigned>(ceil_div(row, kMetaThreads)),
                    static_cast<unsigned>(rows < 65535 ? rows : 65535));

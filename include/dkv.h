@@ -249,7 +249,9 @@ typedef struct dkv_append {
      DKV_ERR_DEVICE_CHECK in the status word of `workspace`
      (DKV_WORKSPACE_HEADER_BYTES suffice; NULL: not recorded).
    - A block that two sequences of the batch append to is a race: share only
-     whole blocks of a common prefix. */
+     whole blocks of a common prefix.
+   - Page metadata does not follow by itself: dkv_kv_meta_append_tokens with the
+     same T, n_b and N_b brings it up to date. */
 dkv_status dkv_kv_append(const dkv_append* p, const dkv_kv* K, const dkv_kv* V, void* workspace,
                          void* stream);
 
@@ -261,16 +263,27 @@ dkv_status dkv_kv_append(const dkv_append* p, const dkv_kv* K, const dkv_kv* V, 
 dkv_status dkv_kv_meta_build(const dkv_params* p, const dkv_kv* K, void* meta_min,
                              void* meta_max, void* stream);
 
-/* Page metadata after a decode step appended tokens: rebuilds, for every
-   (batch entry b, kv head), only the page holding the sequence's last token
-   N_b - 1 (N_b from seq_lens, else seq_len), the one page an appended token
-   changes; every other page's (m_j, M_j) is left as it is.  Same arguments
-   and layout as dkv_kv_meta_build, whose result it reproduces bit for bit
-   when the other pages are already built.  ("TinyServe: Query-Aware Cache
-   Selection for Efficient LLM Serving", 结构化内存布局 and 系统实现意义: the
-   page metadata is kept alongside the cache as it grows.) */
+/* Page metadata after an append: rebuilds, for every (batch entry b, kv head),
+   only the pages that the newest n_b of the sequence's N_b tokens (N_b from
+   seq_lens, else seq_len) changed; every other page's (m_j, M_j) is left as it
+   is.  These are the pages from the one holding token N_b - n_b to the one
+   holding the last token -- in the 8-bit formats from the first page of that
+   token's 16-token block, whose older tokens are rounded again when its scale
+   rises (pages of 4 and 8 tokens: several a block).  Same arguments and layout
+   as dkv_kv_meta_build, whose result it reproduces bit for bit when the other
+   pages are already built.
+   - new_tokens: T, as the append had it, 0 <= T <= seq_len.  new_lens: DEVICE
+     [B], n_b (NULL: all T).  n_b <= 0: nothing of sequence b is rebuilt; one
+     above T or N_b counts as that.
+   - dkv_kv_meta_append is the call of a decode step: T = 1, no new_lens.
+   ("TinyServe: Query-Aware Cache Selection for Efficient LLM Serving",
+   结构化内存布局 and 系统实现意义: the page metadata is kept alongside the cache
+   as it grows.) */
 dkv_status dkv_kv_meta_append(const dkv_params* p, const dkv_kv* K, void* meta_min,
                               void* meta_max, void* stream);
+dkv_status dkv_kv_meta_append_tokens(const dkv_params* p, const dkv_kv* K, int32_t new_tokens,
+                                     const int32_t* new_lens, void* meta_min, void* meta_max,
+                                     void* stream);
 
 /* Exact decode attention.  out [B, Hq, d] in out_dtype (DKV_FP32 | DKV_BF16 |
    DKV_FP16).  Splits the sequence into fixed chunks whose length depends only
