@@ -76,7 +76,8 @@ constexpr uint64_t kDrainLimitNs = 200000000ull;  // 200 ms for the whole drain
 constexpr int kListPages = 64;                    // pages of an item listed at a time
 constexpr int kMaxRagged = 128;    // sequences whose items are counted by their lengths
 constexpr float kSlack = 8.f;      // how far, in log2 units, a reference may be passed
-constexpr float kUnset = -1e30f;   // a reference before the first token
+constexpr float kUnset = -3.402823466e38f;  // a reference before the first token: the
+                                            // lowest value, so every finite score passes it
 
 struct ItemDesc {
   int item;     // work item, -1: no more work

@@ -1,0 +1,70 @@
+"""Decode attention over 8-bit caches at the edges of its domain, against 64-bit
+forms."""
+
+import pytest
+import torch
+
+import fp8_helpers as ref
+from gpu_helpers import require_cuda
+from test_gpu_fp8 import caches, make
+
+pytestmark = pytest.mark.gpu
+
+PAGE = 16
+
+
+@pytest.fixture(scope="module")
+def dev():
+    return require_cuda()
+
+
+@pytest.fixture(scope="module")
+def dkv():
+    import decode_attention_paged_kv_gb300 as m
+    return m
+
+
+def one_hot_case(N, d, log_score, v_exp, seed, negative):
+    """bf16 q, K, V whose scores are +- 2^log_score * (1 + j / 8), one token
+    a kv head ahead of the others by 2^log_score / 8: the softmax is one-hot.  V
+    blocks are 2^v_exp apart in size, the winners' block the smallest."""
+    B, Hkv = 2, 2
+    g = torch.Generator().manual_seed(seed)
+    half = log_score // 2
+    q = torch.zeros(B, Hkv * 8, d)
+    q[..., 0] = 2.0 ** (log_score - half) * (-1.0 if negative else 1.0)
+    j = torch.randint(1, 7, (B, Hkv, N), generator=g).float()
+    win = torch.randint(0, N, (B, Hkv, 1), generator=g)
+    j.scatter_(2, win, 0.0 if negative else 7.0)
+    k = torch.zeros(B, Hkv, N, d)
+    k[..., 0] = (1 + j / 8) * 2.0 ** half
+    v = torch.randn(B, Hkv, N, d, generator=g)
+    P = -(-N // PAGE)
+    e = torch.randint(-v_exp, v_exp + 1, (B, Hkv, P), generator=g).float()
+    e.scatter_(2, win // PAGE, -float(v_exp))
+    v *= torch.exp2(e).repeat_interleave(PAGE, dim=2)[:, :, :N, None]
+    return q.to(torch.bfloat16), ref.quantise(k, torch.bfloat16), ref.quantise(v, torch.bfloat16), win
+
+
+def check_one_hot(case, N, heads, dev, dkv):
+    q, K, V, win = case
+    q = q.view(2, 2, 8, 64)[:, :, :heads].reshape(2, 2 * heads, 64).contiguous()
+    kv, vv = ref.values(*K), ref.values(*V)
+    want = ref.attention(q, kv, vv, 1.0)
+    pick = vv.gather(2, win[..., None].expand(-1, -1, -1, 64))  # [B, Hkv, 1, d]
+    assert torch.equal(want.view(2, 2, heads, 64), pick.expand(-1, -1, heads, -1))
+    for paged in (False, True):
+        Kd, Vd = caches(dkv, dev, K, V, torch.bfloat16, paged)
+        meta = dkv.kv_meta_build(Kd)
+        for out in (dkv.decode_attn_full(q.to(dev), Kd, Vd, scale=1.0),
+                    dkv.decode_attn_select(q.to(dev), Kd, Vd, meta, 3, scale=1.0)):
+            # the winner's weight is 1 and the others' 0: what is left is the
+            # weight's two halves (22 bits) and the fp32 steps of the joins
+            assert torch.all((out.cpu().double() - want).abs() <= want.abs() * 2.0 ** -18)
+
+
+@pytest.mark.parametrize("heads", [1, 4, 8])
+@pytest.mark.parametrize("N", [40, 9000])  # one work item a unit, and several
+def test_scores_all_below(N, heads, dev, dkv):
+    # every score lies below -1e30
+    check_one_hot(one_hot_case(N, 64, 105, 0, heads, True), N, heads, dev, dkv)
