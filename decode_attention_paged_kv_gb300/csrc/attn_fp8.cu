@@ -615,14 +615,14 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
             qa[c][i] = pack2<true>(lo16<false>(qa[c][i]) * f, hi16<false>(qa[c][i]) * f);
       }
     }
-    // Per head of the lane: the references m and r, the largest s + e that r was
-    // set for, and the lane's part of the sum l.
+    // Per head of the lane: the references m and r, the largest (s - m) + e that r
+    // was set for, and the lane's part of the sum l.
     constexpr int kE = GL == 1 ? 1 : 2;             // heads of a lane
     constexpr int kT = GL == 8 ? kQ : 1;            // pages of a lane
     constexpr int kN = GL == 1 ? 1 : 2;             // tokens of a lane, page and head
-    float m_ref[kE], mv_ref[kE], r_ref[kE], l_run[kE];
+    float m_ref[kE], v_ref[kE], r_ref[kE], l_run[kE];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) m_ref[e] = mv_ref[e] = kUnset, r_ref[e] = l_run[e] = 0.f;
+    for (int e = 0; e < kE; ++e) m_ref[e] = v_ref[e] = kUnset, r_ref[e] = l_run[e] = 0.f;
     float acc[D / 16][4];  // tile c: channels 16 c + 2 g (0, 1) and + 1 (2, 3), columns 2 t4 + e
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
@@ -723,27 +723,37 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
             top = fmaxf(top, fmaxf(x[t][e][n], y[t][e][n]));
           }
       if (__any_sync(0xffffffffu, top > kSlack)) {
-        // New references: the running maxima with this stage's.
+        // New references: the running maxima with this stage's.  (s - m) + e, not s
+        // + e: beside a large s the exponent would have no digits left.
+        constexpr int kFirst = GL == 8 ? 4 : (GL == 4 ? 2 : 1);  // lanes of other heads
+        float m_new[kE], pv[kE];
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
-          float pm = -INFINITY, pv = -INFINITY;
+          float pm = -INFINITY;
 #pragma unroll
           for (int t = 0; t < kT; ++t)
 #pragma unroll
-            for (int n = 0; n < kN; ++n) {
-              pm = fmaxf(pm, sv[t][e][n]);
-              pv = fmaxf(pv, sv[t][e][n] + ve[t]);
-            }
+            for (int n = 0; n < kN; ++n) pm = fmaxf(pm, sv[t][e][n]);
 #pragma unroll
-          for (int o = GL == 8 ? 4 : (GL == 4 ? 2 : 1); o < 32; o *= 2) {
+          for (int o = kFirst; o < 32; o *= 2)
             pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, o));
-            pv = fmaxf(pv, __shfl_xor_sync(0xffffffffu, pv, o));
-          }
-          if (pm != -INFINITY) {
-            const float m_new = fmaxf(m_ref[e], pm);
-            mv_ref[e] = fmaxf(mv_ref[e], pv);
-            const float r_new = ceilf(mv_ref[e] - m_new);
-            const float down = m_ref[e] - m_new;  // (unset: 2^down is 0)
+          m_new[e] = fmaxf(m_ref[e], pm);
+          pv[e] = -INFINITY;  // (stays so where no token of the stage counts)
+#pragma unroll
+          for (int t = 0; t < kT; ++t)
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+              pv[e] = fmaxf(pv[e], (sv[t][e][n] - m_new[e]) + ve[t]);
+#pragma unroll
+          for (int o = kFirst; o < 32; o *= 2)
+            pv[e] = fmaxf(pv[e], __shfl_xor_sync(0xffffffffu, pv[e], o));
+        }
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          if (pv[e] != -INFINITY) {
+            const float down = m_ref[e] - m_new[e];  // (unset: 2^down is 0)
+            v_ref[e] = fmaxf(v_ref[e] + down, pv[e]);
+            const float r_new = ceilf(v_ref[e]);
             l_run[e] *= exp2_fast(down);
             const float alpha = exp2_fast(down + (r_ref[e] - r_new));
 #pragma unroll
@@ -752,7 +762,7 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
               acc[c][2 + e] *= alpha;
               if constexpr (GL == 1) acc[c][1] *= alpha, acc[c][3] *= alpha;
             }
-            m_ref[e] = m_new;
+            m_ref[e] = m_new[e];
             r_ref[e] = r_new;
           }
 #pragma unroll

@@ -68,3 +68,12 @@ def check_one_hot(case, N, heads, dev, dkv):
 def test_scores_all_below(N, heads, dev, dkv):
     # every score lies below -1e30
     check_one_hot(one_hot_case(N, 64, 105, 0, heads, True), N, heads, dev, dkv)
+
+
+@pytest.mark.parametrize("heads", [1, 4, 8])
+@pytest.mark.parametrize("N", [40, 9000])
+@pytest.mark.parametrize("log_score,v_exp,negative", [(105, 20, True), (40, 40, False),
+                                                      (40, 40, True), (100, 40, False)])
+def test_scales_beside_large_scores(log_score, v_exp, negative, N, heads, dev, dkv):
+    # scores so large that a V scale's exponent, added to one, has no digits left
+    check_one_hot(one_hot_case(N, 64, log_score, v_exp, heads, negative), N, heads, dev, dkv)
