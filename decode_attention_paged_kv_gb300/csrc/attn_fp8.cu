@@ -944,9 +944,9 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
             O.x += f[v] * r[0];
             O.y += f[v] * r[1];
           }
-          if (whole) {  // (no token: 0)
-            store_out(a.out, a.out_dtype, oo + ch, L > 0.f ? O.x / L : 0.f);
-            store_out(a.out, a.out_dtype, oo + ch + 1, L > 0.f ? O.y / L : 0.f);
+          if (whole) {  // (an empty sequence: 0; NaN scores have their way)
+            store_out(a.out, a.out_dtype, oo + ch, n_pages > 0 ? O.x / L : 0.f);
+            store_out(a.out, a.out_dtype, oo + ch + 1, n_pages > 0 ? O.y / L : 0.f);
           } else {
             *reinterpret_cast<float2*>(po + ch) = O;
           }

@@ -1,6 +1,8 @@
 """Decode attention over 8-bit caches at the edges of its domain, against 64-bit
 forms."""
 
+import math
+
 import pytest
 import torch
 
@@ -77,3 +79,37 @@ def test_scores_all_below(N, heads, dev, dkv):
 def test_scales_beside_large_scores(log_score, v_exp, negative, N, heads, dev, dkv):
     # scores so large that a V scale's exponent, added to one, has no digits left
     check_one_hot(one_hot_case(N, 64, log_score, v_exp, heads, negative), N, heads, dev, dkv)
+
+
+@pytest.mark.parametrize("Hq", [2, 6, 16])
+@pytest.mark.parametrize("N", [40, 9000])
+def test_not_a_number(N, Hq, dev, dkv):
+    # a NaN query gives NaN rows, a NaN key NaN rows of its kv head's queries, a
+    # NaN value its channel; other rows keep their results
+    B, H, d = 2, 2, 64
+    G = Hq // H
+    q, K, V = make(B, Hq, H, d, N, torch.bfloat16, seed=N + Hq)
+    scale = 1 / math.sqrt(d)
+    for paged in (False, True):
+        Kd, Vd = caches(dkv, dev, K, V, torch.bfloat16, paged)
+        clean = dkv.decode_attn_full(q.to(dev), Kd, Vd)
+        bad = q.clone()
+        bad[1, G - 1, 5] = math.nan
+        out = dkv.decode_attn_full(bad.to(dev), Kd, Vd)
+        assert out[1, G - 1].isnan().all()
+        keep = torch.ones(B, Hq, dtype=torch.bool)
+        keep[1, G - 1] = False
+        assert torch.equal(out[keep], clean[keep])
+        meta = dkv.kv_meta_build(Kd)
+        top_k = -(-N // PAGE)  # every page
+        for t, channels in ((0, slice(None)), (1, slice(9, 10))):
+            c = [x[0].clone() for x in (K, V)]
+            c[t].view(torch.uint8)[0, 1, N // 2, 9] = 0x7F
+            Kb, Vb = caches(dkv, dev, (c[0], K[1]), (c[1], V[1]), torch.bfloat16, paged)
+            for f in (lambda a, b: dkv.decode_attn_full(q.to(dev), a, b),
+                      lambda a, b: dkv.decode_attn_select(q.to(dev), a, b, meta, top_k)):
+                clean, out = f(Kd, Vd), f(Kb, Vb)
+                hit = torch.zeros(B, Hq, d, dtype=torch.bool, device=dev)
+                hit[0, G:, channels] = True
+                assert torch.equal(out.isnan(), hit)
+                assert torch.equal(out[~hit], clean[~hit])
