@@ -450,6 +450,8 @@ def decode_attn_topk_tokens(q, K, V, top_k: int, scale: Optional[float] = None,
     vs, B2, H2, N2, d2 = _kv_struct(V)
     if (B, H, N, d) != (B2, H2, N2, d2):
         raise ValueError("K and V shapes differ")
+    if isinstance(K, torch.Tensor) and q.dtype != K.dtype:
+        raise ValueError("q must have the cache's dtype")
     if out is None:
         out = torch.empty(B, q.shape[1], d, dtype=out_dtype, device=q.device)
     kk = min(int(top_k), N)

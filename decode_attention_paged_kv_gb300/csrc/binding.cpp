@@ -252,10 +252,10 @@ void set_out(dkv_params* p, const at::Tensor& q, const at::Tensor& out) {
   p->o_stride_b = out.stride(0), p->o_stride_h = out.stride(1);
 }
 
-// The tensors of an attention call lie on one device; q has an 8-bit cache's type.
+// The tensors of an attention call lie on one device; q has the cache's type (4-bit: fp16).
 void check_tensors(const at::Tensor& q, const Pair& c,
                    std::initializer_list<const at::Tensor*> others) {
-  if (c.k.fp8 && q.scalar_type() != c.k.dtype) value_error("q must have the cache's dtype");
+  if (q.scalar_type() != c.k.dtype) value_error("q must have the cache's dtype");
   const int dev = cuda_index(q);
   bool ok = dev >= 0 && c.k.device == dev && c.v.device == dev;
   for (const at::Tensor* t : others) ok = ok && (t == nullptr || cuda_index(*t) == dev);
@@ -357,7 +357,7 @@ Meta meta_pair(PyObject* o, const Cache& c, int64_t P) {
     if (t->dim() != 4 || t->size(0) != c.B || t->size(1) != c.H || t->size(2) != P ||
         t->size(3) != c.d || !t->is_contiguous())
       value_error("meta must be contiguous [B, Hkv, P, d]");
-    if (c.fp8 && t->scalar_type() != c.dtype) value_error("meta must have the cache's dtype");
+    if (t->scalar_type() != c.dtype) value_error("meta must have the cache's dtype");
   }
   return m;
 }
@@ -507,6 +507,8 @@ PyObject* decode_attn_select(PyObject* const* a) {
       if (t.dim() != (i < 2 ? 4 : 3) || t.size(0) != c.k.B || t.size(1) != c.k.H ||
           t.size(2) != P || (i < 2 && t.size(3) != c.k.d) || !t.is_contiguous())
         value_error("Meta8 must hold contiguous [B, Hkv, P, d] codes, [B, Hkv, P] grid");
+      if (t.scalar_type() != (i < 2 ? at::kByte : at::kFloat))
+        value_error("Meta8 must have the dtypes uint8 (codes) and float32 (grid)");
     }
   } else {
     m = meta_pair(a[3], c.k, P);
