@@ -304,6 +304,8 @@ def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.
     if workspace is not None:
         if workspace.numel() * workspace.element_size() < nbytes:
             raise ValueError("workspace too small")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         return workspace
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 

@@ -55,6 +55,17 @@ const at::Tensor* optional_tensor(PyObject* o, const char* name) {
   return is_none(o) ? nullptr : &tensor(o, name);
 }
 
+// Memory of which only the size counts (a workspace, a reuse state), or null: it
+// is used from its first byte on, so a view must not leave any out.
+const at::Tensor* scratch(PyObject* o, const char* name) {
+  const at::Tensor* t = optional_tensor(o, name);
+  if (t != nullptr && !t->is_contiguous()) {
+    PyErr_Format(PyExc_ValueError, "%s must be contiguous", name);
+    throw PyError{};
+  }
+  return t;
+}
+
 int dtype_code(at::ScalarType t) {
   if (t == at::kBFloat16) return DKV_BF16;
   if (t == at::kHalf) return DKV_FP16;
@@ -270,7 +281,7 @@ size_t workspace_need(const dkv_params& p, int top_k, bool fp8) {
 at::Tensor workspace_for(PyObject* o, size_t need, const at::Tensor& q) {
   if (is_none(o))
     return at::zeros({static_cast<int64_t>(need)}, q.options().dtype(at::kByte));
-  const at::Tensor& t = tensor(o, "workspace");
+  const at::Tensor& t = *scratch(o, "workspace");
   if (static_cast<size_t>(t.numel()) * t.element_size() < need) value_error("workspace too small");
   return t;
 }
@@ -451,7 +462,7 @@ PyObject* kv_append(PyObject* const* a) {
   p.seq_lens = lengths(a[4], "seq_lens", c.k.B, dev);
   p.new_lens = lengths(a[5], "new_lens", c.k.B, dev);
   void* ws = nullptr;
-  if (const at::Tensor* t = optional_tensor(a[10], "workspace")) {
+  if (const at::Tensor* t = scratch(a[10], "workspace")) {
     if (cuda_index(*t) != dev ||
         static_cast<size_t>(t->numel()) * t->element_size() < DKV_WORKSPACE_HEADER_BYTES)
       value_error("workspace must hold 256 bytes on the caches' device");
@@ -469,7 +480,7 @@ PyObject* decode_attn_full(PyObject* const* a) {
   const at::Tensor& q = tensor(a[0], "q");
   const Pair c = parse_pair(a[1], a[2]);
   const at::Tensor* given = optional_tensor(a[5], "out");
-  check_tensors(q, c, {given, optional_tensor(a[6], "workspace")});
+  check_tensors(q, c, {given, scratch(a[6], "workspace")});
   dkv_params p = make_params(c.k, kPage, a[8]);
   set_query(&p, c.k, q, a[3], integer(a[7]));
   const int dev = cuda_index(q);
@@ -495,7 +506,7 @@ PyObject* decode_attn_select(PyObject* const* a) {
   const int64_t P = S > 0 ? (c.k.N + S - 1) / S : 0;
   const at::Tensor* given = optional_tensor(a[7], "out");
   const at::Tensor* chosen = optional_tensor(a[9], "selected");
-  const at::Tensor* hot = optional_tensor(a[14], "hot");
+  const at::Tensor* hot = scratch(a[14], "hot");
   const bool m8 = is(a[3], g_meta8);
   if (m8 && hot != nullptr) value_error("cross-step reuse takes 16-bit metadata");
   Meta m{};
@@ -513,7 +524,7 @@ PyObject* decode_attn_select(PyObject* const* a) {
   } else {
     m = meta_pair(a[3], c.k, P);
   }
-  check_tensors(q, c, {given, optional_tensor(a[10], "workspace"), chosen, hot, m.mn, m.mx,
+  check_tensors(q, c, {given, scratch(a[10], "workspace"), chosen, hot, m.mn, m.mx,
                        part[0], part[1], part[2], part[3]});
   dkv_params p = make_params(c.k, S, a[12]);
   set_query(&p, c.k, q, a[5], integer(a[11]));

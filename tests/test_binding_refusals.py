@@ -75,3 +75,20 @@ def test_dtypes(kind, dt, dkv):
             with pytest.raises(ValueError, match="dtype"):
                 dkv.decode_attn_select(q, K, V, dkv.Meta8(*(x.to(t) if j == i else x
                                                             for j, x in enumerate(m8))), 2)
+
+
+@pytest.mark.parametrize("kind,dt", KINDS, ids=str)
+def test_scratch_with_gaps(kind, dt, dkv):
+    # a workspace or reuse state is used as one piece: a view with gaps would have
+    # the kernels write between its elements
+    K = cache(dkv, kind, dt)
+    q, mn = torch.zeros(B, HQ, D, dtype=dt), torch.zeros(B, H, P, D, dtype=dt)
+    gaps = torch.zeros(1 << 20, 2, dtype=torch.uint8)[:, 0]
+    for call in (lambda: dkv.decode_attn_full(q, K, K, workspace=gaps),
+                 lambda: dkv.decode_attn_select(q, K, K, (mn, mn), 2, workspace=gaps),
+                 lambda: dkv.decode_attn_select(q, K, K, (mn, mn), 2, hot=gaps, step=1)):
+        with pytest.raises(ValueError, match="contiguous"):
+            call()
+    if kind == "dense":
+        with pytest.raises(ValueError, match="contiguous"):
+            dkv.decode_attn_topk_tokens(q, K, K, 2, workspace=gaps)
