@@ -197,6 +197,10 @@ Cache parse_cache(PyObject* o) {
     if (mn.strides() != mx.strides() || mn.dim() != 4 || mn.stride(3) != 1 ||
         mn.stride(2) != c.d / 64)
       value_error("gmin / gmax must share strides with token stride d/64");
+    for (const at::Tensor* m : {&mn, &mx})
+      if (m->dim() != 4 || m->size(0) < c.B || m->size(1) < c.H || m->size(2) < c.N ||
+          m->size(3) < c.d / 64 || m->device() != t.device())
+        value_error("gmin / gmax must hold [B, Hkv, N, d/64] on the codes' device");
     s.format = DKV_KV_Q4G64;
     c.dtype = at::kHalf;
     s.data = t.data_ptr();

@@ -92,3 +92,22 @@ def test_scratch_with_gaps(kind, dt, dkv):
     if kind == "dense":
         with pytest.raises(ValueError, match="contiguous"):
             dkv.decode_attn_topk_tokens(q, K, K, 2, workspace=gaps)
+
+
+def test_4_bit_bounds(dkv):
+    # gmin / gmax that are smaller than the codes, or elsewhere, would be read past
+    # their end
+    K = cache(dkv, "q4", torch.float16)
+    q = torch.zeros(B, HQ, D, dtype=torch.float16)
+    g = lambda b, h, n: torch.zeros(b, h, n, D // 64, dtype=torch.float16)
+    meta_dev = K.gmin.to("meta")
+    for lo, hi in ((g(B, H, N - 1), g(B, H, N - 1)), (g(B, 1, N), g(B, 1, N)),
+                   (g(1, H, N), g(1, H, N)), (K.gmin, g(1, H, N)), (meta_dev, meta_dev),
+                   (K.gmin, meta_dev)):
+        bad = dkv.Q4Cache(K.codes, lo, hi)
+        for call in (lambda: dkv.decode_attn_full(q, bad, K), lambda: dkv.kv_meta_build(bad)):
+            with pytest.raises(ValueError, match="gmin / gmax must hold"):
+                call()
+    with pytest.raises(ValueError, match="CUDA"):  # room to spare is fine
+        room = g(B + 1, H, N)
+        dkv.kv_meta_build(dkv.Q4Cache(K.codes, room, room))
