@@ -290,6 +290,16 @@ at::Tensor workspace_for(PyObject* o, size_t need, const at::Tensor& q) {
   return t;
 }
 
+// Other Python threads run meanwhile.  (An object, not the macro pair: a tensor
+// without memory throws when its address is taken, and the exception is turned
+// into a Python one, which needs the interpreter's lock.)
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // One library call on the current stream of CUDA device `dev`, which is made the
 // current device for it; raises on an error status.
 template <typename F>
@@ -300,10 +310,10 @@ void call(const char* where, int dev, const F& f) {
   }
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
   void* stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-  dkv_status st;
-  Py_BEGIN_ALLOW_THREADS;
-  st = f(stream);
-  Py_END_ALLOW_THREADS;
+  const dkv_status st = [&] {
+    const Unlocked unlocked;
+    return f(stream);
+  }();
   if (st != DKV_OK) {
     PyObject* e = PyObject_CallFunction(g_error, "is", static_cast<int>(st), where);
     if (e != nullptr) {
