@@ -268,16 +268,22 @@ def _params(q: Optional[torch.Tensor], B, Hkv, N, d, out: Optional[torch.Tensor]
         lens = seq_lens.data_ptr()
     Hq, qsb, qsh, osb, osh = Hkv, 0, 0, 0, 0
     if q is not None:
-        qB, Hq, qd = q.shape
-        qsb, qsh, one = q.stride()
+        qB, Hq, qd = q.shape[:3]
+        qsb, qsh, one = q.stride()[:3]
         if qB != B or qd != d or one != 1:
             raise ValueError(f"q shape {tuple(q.shape)} does not match the cache")
     if out is not None:
-        if out.dim() != 3 or any(a < b for a, b in zip(out.shape, q.shape)):
-            raise ValueError(f"out must hold {tuple(q.shape)}")
-        osb, osh, one = out.stride()
-        if one != 1:
-            raise ValueError("out must have channel stride 1")
+        # (a row of out may be split into more dimensions, [B, Hq, 1, d] say)
+        ok = out.dim() >= 3 and out.shape[0] >= B and out.shape[1] >= Hq
+        run = 1  # elements of a row that follow one another
+        for n, s in reversed(list(zip(out.shape[2:], out.stride()[2:]))):
+            if not ok or run >= d:
+                break
+            ok = s == run or n == 1
+            run *= n
+        if not ok or run < d:
+            raise ValueError(f"out must hold {(B, Hq, d)} with channel stride 1")
+        osb, osh = out.stride()[:2]
     return _Params(B, Hq, Hkv, d, N, PAGE_SIZE, qsb, qsh, osb, osh,
                    1.0 / math.sqrt(d) if scale is None else float(scale), flags, lens)
 

@@ -253,18 +253,28 @@ dkv_params make_params(const Cache& c, int64_t page_size, PyObject* seq_lens) {
 // The query and output of an attention call.
 void set_query(dkv_params* p, const Cache& c, const at::Tensor& q, PyObject* scale,
                int64_t flags) {
-  if (q.dim() != 3 || q.size(0) != c.B || q.size(2) != c.d || q.stride(2) != 1)
+  if (q.dim() < 3 || q.size(0) != c.B || q.size(2) != c.d || q.stride(2) != 1)
     value_error("q's shape does not match the cache");
   p->num_q_heads = int32_size(q.size(1));
   p->q_stride_b = q.stride(0), p->q_stride_h = q.stride(1);
   if (!is_none(scale)) p->scale = static_cast<float>(number(scale));
   p->flags = static_cast<uint32_t>(flags);
 }
+// (A row of out may be split into more dimensions, [B, Hq, 1, d] say: d elements
+// one after the other are what counts.)
 void set_out(dkv_params* p, const at::Tensor& q, const at::Tensor& out) {
-  if (out.dim() != 3 || out.size(0) < q.size(0) || out.size(1) < q.size(1) ||
-      out.size(2) < q.size(2) || out.stride(2) != 1)
-    value_error("out must hold [B, Hq, d] with channel stride 1");
+  bool ok = out.dim() >= 3 && out.size(0) >= q.size(0) && out.size(1) >= q.size(1);
+  int64_t run = 1;  // elements of a row that follow one another
+  for (int64_t i = out.dim() - 1; ok && i >= 2 && run < q.size(2); --i) {
+    ok = out.stride(i) == run || out.size(i) == 1;
+    run *= out.size(i);
+  }
+  if (!ok || run < q.size(2)) value_error("out must hold [B, Hq, d] with channel stride 1");
   p->o_stride_b = out.stride(0), p->o_stride_h = out.stride(1);
+}
+
+at::Tensor new_out(const at::Tensor& q, PyObject* dtype) {
+  return at::empty({q.size(0), q.size(1), q.size(2)}, q.options().dtype(scalar_type(dtype)));
 }
 
 // The tensors of an attention call lie on one device; q has the cache's type (4-bit: fp16).
@@ -498,7 +508,7 @@ PyObject* decode_attn_full(PyObject* const* a) {
   dkv_params p = make_params(c.k, kPage, a[8]);
   set_query(&p, c.k, q, a[3], integer(a[7]));
   const int dev = cuda_index(q);
-  const at::Tensor out = given ? *given : at::empty(q.sizes(), q.options().dtype(scalar_type(a[4])));
+  const at::Tensor out = given ? *given : new_out(q, a[4]);
   set_out(&p, q, out);
   const size_t need = workspace_need(p, 0, c.k.fp8);
   const at::Tensor ws = workspace_for(a[6], need, q);
@@ -543,7 +553,7 @@ PyObject* decode_attn_select(PyObject* const* a) {
   dkv_params p = make_params(c.k, S, a[12]);
   set_query(&p, c.k, q, a[5], integer(a[11]));
   const int dev = cuda_index(q);
-  const at::Tensor out = given ? *given : at::empty(q.sizes(), q.options().dtype(scalar_type(a[6])));
+  const at::Tensor out = given ? *given : new_out(q, a[6]);
   set_out(&p, q, out);
   const int64_t kk = top_k < P ? top_k : P;
   const int wanted = PyObject_IsTrue(a[8]);
