@@ -100,6 +100,11 @@ int32_t int32_size(int64_t v) {
   return static_cast<int32_t>(v);
 }
 
+// A count as the library takes it, which refuses those below 1 with its status.
+int32_t int32_count(int64_t v) {
+  return static_cast<int32_t>(v < -1 ? -1 : (v > INT32_MAX ? INT32_MAX : v));
+}
+
 // A K or V cache, as the package's calls take it.
 struct Cache {
   dkv_kv kv{};
@@ -407,8 +412,7 @@ PyObject* kv_meta_append(PyObject* const* a) {
     value_error("meta must be on the cache's device");
   const int32_t* news = lengths(a[5], "new_lens", c.B, c.device);
   if (news != nullptr && is_none(a[4])) value_error("new_lens needs new_tokens");
-  const int64_t T = is_none(a[4]) ? 1 : integer(a[4]);
-  const int32_t fresh = T < 0 ? -1 : int32_size(T);
+  const int32_t fresh = is_none(a[4]) ? 1 : int32_count(integer(a[4]));
   call("dkv_kv_meta_append", c.device, [&](void* stream) {
     return dkv_kv_meta_append_tokens(&p, &c.kv, fresh, news, m.mn->data_ptr(), m.mx->data_ptr(),
                                      stream);
@@ -526,7 +530,7 @@ PyObject* decode_attn_select(PyObject* const* a) {
   const at::Tensor& q = tensor(a[0], "q");
   const Pair c = parse_pair(a[1], a[2]);
   const int64_t S = integer(a[13]);
-  const int32_t top_k = int32_size(integer(a[4]));
+  const int32_t top_k = int32_count(integer(a[4]));
   const int64_t P = S > 0 ? (c.k.N + S - 1) / S : 0;
   const at::Tensor* given = optional_tensor(a[7], "out");
   const at::Tensor* chosen = optional_tensor(a[9], "selected");
@@ -555,7 +559,7 @@ PyObject* decode_attn_select(PyObject* const* a) {
   const int dev = cuda_index(q);
   const at::Tensor out = given ? *given : new_out(q, a[6]);
   set_out(&p, q, out);
-  const int64_t kk = top_k < P ? top_k : P;
+  const int64_t kk = top_k < 0 ? 0 : (top_k < P ? top_k : P);
   const int wanted = PyObject_IsTrue(a[8]);
   if (wanted < 0) throw PyError{};
   std::optional<at::Tensor> made;
@@ -581,7 +585,7 @@ PyObject* decode_attn_select(PyObject* const* a) {
                                           stream);
     });
   } else if (hot != nullptr) {
-    const int32_t step = int32_size(integer(a[15]));
+    const int32_t step = int32_count(integer(a[15]));
     const size_t bytes = static_cast<size_t>(hot->numel()) * hot->element_size();
     call("dkv_decode_attn_select_hot", dev, [&](void* stream) {
       return dkv_decode_attn_select_hot(&p, qp, &c.k.kv, &c.v.kv, m.mn->data_ptr(),

@@ -59,3 +59,20 @@ def test_rows_of_more_dimensions(dev, dkv):
                     torch.zeros(2, 4, 64, 2, device=dev)[..., :1], torch.zeros(2, 64, device=dev)):
             with pytest.raises(ValueError, match="out must hold"):
                 f(x, out=bad)
+
+
+def test_counts_out_of_range(dev, dkv):
+    # refused with the library's status, as callers that catch DkvError expect; more
+    # pages than there are: all of them
+    q, K, V = problem(dev)
+    meta = dkv.kv_meta_build(K)
+    state = dkv.hot_state(2, 2, 100, dev)
+    for k in (0, -1, -5, -(1 << 40)):
+        for wanted in (False, True):
+            with pytest.raises(dkv.DkvError):
+                dkv.decode_attn_select(q, K, V, meta, k, return_selected=wanted)
+        with pytest.raises(dkv.DkvError):
+            dkv.decode_attn_select(q, K, V, meta, 2, hot=state, step=k)
+    want = dkv.decode_attn_select(q, K, V, meta, 7, return_selected=True)
+    got = dkv.decode_attn_select(q, K, V, meta, (1 << 31) - 1, return_selected=True)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
