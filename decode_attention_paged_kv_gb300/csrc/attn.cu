@@ -49,6 +49,7 @@
 
 #include "dkv_device.cuh"
 #include "dkv_kernels.h"
+#include "per_device.h"
 
 namespace dkv {
 namespace {
@@ -1305,26 +1306,26 @@ __global__ void __launch_bounds__(kSmallMergeThreads) merge_small_kernel(const M
 }
 
 // Resident CTAs per SM of one attention instantiation (its registers and shared
-// memory as compiled), at most kAttnCtasPerSm; computed once.
+// memory as compiled), at most kAttnCtasPerSm; computed once a device, whose
+// shared-memory limit for the kernel is raised then.
 template <int D, bool F16, bool SPARSE, bool Q4, bool MHA = false>
 cudaError_t attn_ctas_per_sm_t(int* out) {
   using C = AttnCfg<D, Q4, Q4 && !SPARSE, MHA>;
-  static int cached = 0;  // benign race: every thread computes the same value
-  if (cached > 0) {
-    *out = cached;
+  static PerDevice known;
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return per_device(known, dev, cudaSuccess, out, [](int* n) {
+    auto kern = attn_kernel<D, F16, SPARSE, Q4, MHA>;
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, kAttnThreads, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (*n < 1) return cudaErrorInvalidConfiguration;
+    if (*n > C::kCtasPerSm) *n = C::kCtasPerSm;
     return cudaSuccess;
-  }
-  auto kern = attn_kernel<D, F16, SPARSE, Q4, MHA>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-  if (e != cudaSuccess) return e;
-  int n = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kAttnThreads, C::kSmemBytes);
-  if (e != cudaSuccess) return e;
-  if (n < 1) return cudaErrorInvalidConfiguration;
-  cached = n < C::kCtasPerSm ? n : C::kCtasPerSm;
-  *out = cached;
-  return cudaSuccess;
+  });
 }
 
 template <int D, bool F16, bool SPARSE, bool Q4, bool MHA = false>

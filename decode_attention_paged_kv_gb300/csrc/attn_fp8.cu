@@ -68,6 +68,7 @@
 
 #include "dkv_device.cuh"
 #include "dkv_kernels.h"
+#include "per_device.h"
 
 namespace dkv {
 namespace {
@@ -965,25 +966,21 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
 template <int D, bool F16, bool SPARSE, int GL>
 cudaError_t ctas_per_sm_t(int* out) {
   using C = Fp8Cfg<D, GL>;
-  static int cached[64] = {0};  // benign race: every thread computes the same value
+  static PerDevice known;
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const bool known = dev >= 0 && dev < 64;
-  if (known && cached[dev] > 0) {
-    *out = cached[dev];
+  return per_device(known, dev, cudaSuccess, out, [](int* n) {
+    auto kern = attn_fp8_kernel<D, F16, SPARSE, GL>;
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, kAttnThreads, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (*n < 1) return cudaErrorInvalidConfiguration;
+    if (*n > C::kCtas) *n = C::kCtas;
     return cudaSuccess;
-  }
-  auto kern = attn_fp8_kernel<D, F16, SPARSE, GL>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-  if (e != cudaSuccess) return e;
-  int n = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kAttnThreads, C::kSmemBytes);
-  if (e != cudaSuccess) return e;
-  if (n < 1) return cudaErrorInvalidConfiguration;
-  *out = n < C::kCtas ? n : C::kCtas;
-  if (known) cached[dev] = *out;
-  return cudaSuccess;
+  });
 }
 
 template <int D, bool F16, bool SPARSE, int GL>
