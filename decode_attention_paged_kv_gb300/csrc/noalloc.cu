@@ -109,7 +109,9 @@ __global__ void poison_on_error_kernel(const unsigned int* status, void* out, in
 extern "C" dkv_status dkv_decode_attn_full_noalloc(const dkv_params* p, const void* q,
                                                    const dkv_kv* K, const dkv_kv* V, void* out,
                                                    int32_t out_dtype, void* stream) {
-  const size_t need = dkv_workspace_bytes(p, 0);
+  const bool eight =
+      K != nullptr && (K->format == DKV_KV_FP8 || K->format == DKV_KV_FP8_PAGED);
+  const size_t need = eight ? dkv_workspace_bytes_fp8(p, 0) : dkv_workspace_bytes(p, 0);
   if (need == 0) {
     // Invalid parameters: let the workspace entry point report which one,
     // before it launches anything.

@@ -1,6 +1,7 @@
 """Decode attention over 8-bit caches at the edges of its domain, against 64-bit
 forms."""
 
+import ctypes
 import math
 
 import pytest
@@ -113,3 +114,39 @@ def test_not_a_number(N, Hq, dev, dkv):
                 hit[0, G:, channels] = True
                 assert torch.equal(out.isnan(), hit)
                 assert torch.equal(out[~hit], clean[~hit])
+
+
+def noalloc(dkv, q, K, V, out):
+    ks, B, H, N, d = dkv._kv_struct(K)
+    vs = dkv._kv_struct(V)[0]
+    p = dkv._params(q, B, H, N, d, out, None)
+    fn = dkv.lib().dkv_decode_attn_full_noalloc
+    fn.argtypes = [ctypes.POINTER(dkv._Params), ctypes.c_void_p, ctypes.POINTER(dkv._KV),
+                   ctypes.POINTER(dkv._KV), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
+    return fn(ctypes.byref(p), q.data_ptr(), ctypes.byref(ks), ctypes.byref(vs), out.data_ptr(),
+              dkv.DKV_FP32, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+
+
+def test_fixed_scratch(dev, dkv):
+    # the size that counts is the 8-bit layout's: it fits where the 16-bit one's
+    # does not, and the other way round
+    limit = 16 << 20
+    for B, Hq, H, N, fits in ((2, 8, 2, 3000, True), (4, 256, 32, 32768, True),
+                              (1, 640, 80, 32768, False)):
+        d = 128
+        need = [dkv.workspace_bytes(B, Hq, H, d, N, fp8=f) for f in (False, True)]
+        assert (need[1] <= limit) == fits and (N == 3000 or (need[0] <= limit) != fits)
+        g = torch.Generator(dev).manual_seed(N)
+        q = torch.randn(B, Hq, d, generator=g, device=dev).to(torch.bfloat16)
+        K, V = (dkv.Fp8Cache(torch.randint(0, 0x7F, (B, H, N, d), generator=g, device=dev,
+                                           dtype=torch.uint8).view(torch.float8_e4m3fn),
+                             torch.full((B, H, -(-N // 16)), 2.0 ** -8, device=dev))
+                for _ in range(2))
+        out = torch.full((B, Hq, d), 5.0, device=dev)
+        status = noalloc(dkv, q, K, V, out)
+        if fits:
+            assert status == dkv.DKV_OK
+            assert torch.equal(out, dkv.decode_attn_full(q, K, V))
+        else:
+            assert status == 6  # DKV_ERR_WORKSPACE
+            assert (out == 5.0).all()
