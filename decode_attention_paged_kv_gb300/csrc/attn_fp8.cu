@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(kAttnThreads, Fp8Cfg<D, GL>::kCtas) attn_fp8_k
             if constexpr (GL == 1) raw = (t4 & 1) ? (pt ? sc[1][2] : sc[0][2]) : raw;
             sv[t][e][n] = raw * (qs[e] * ks);
           }
-        const bool past = have && (meta.x + 1) * kPage > Nb;
+        const bool past = have && Nb - meta.x * kPage < kPage;  // (no sum passes 2^31)
         ragged |= past;
         if (SPARSE || !have || past) {
           // Token i of a page counts for head h if it lies in the sequence and

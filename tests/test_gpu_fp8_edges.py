@@ -150,3 +150,28 @@ def test_fixed_scratch(dev, dkv):
         else:
             assert status == 6  # DKV_ERR_WORKSPACE
             assert (out == 5.0).all()
+
+
+def test_longest_sequence(dev, dkv):
+    # N = 2^31 - 1: the last page holds 15 tokens, and its sixteenth slot is not
+    # attended (NaN there).  Every other page is the same block
+    N, d = (1 << 31) - 1, 64
+    q, K, V = make(1, 1, 1, d, 32, torch.bfloat16, seed=1)
+    for c, _ in (K, V):
+        c.view(torch.uint8)[0, 0, 31] = 0x7F
+    bt = torch.zeros(1, 1 << 27, dtype=torch.int32, device=dev)
+    bt[0, -1] = 1
+    Kd, Vd = (dkv.Fp8PagedCache(c.view(2, 1, 16, d).to(dev), s.view(2, 1).to(dev), bt, N)
+              for c, s in (K, V))
+    out = dkv.decode_attn_full(q.to(dev), Kd, Vd).cpu().double()[0, 0]
+    kv, vv = ref.values(*K)[0, 0], ref.values(*V)[0, 0]
+    p = torch.exp(kv[:31] @ q[0, 0].double() / 8)
+    p[:16] *= (1 << 27) - 1  # times that the first block is attended
+    want = (p @ vv[:31]) / p.sum()
+    # A page of the first block gives the same terms each time, so l and o grow by
+    # equal steps, and from 2^24 steps on a step is below half an ulp of the sum: a
+    # warp takes 2^27 / (256 items * 4) = 2^17 pages of 16 tokens, an item joins four
+    # warps' sums and the merge 256 items': 2^17 sums of at most 2^-24 each, relative
+    # to max |v|, beside tolerance()'s terms
+    tol = ref.tolerance(q, ref.values(*K)[:, :, :31], ref.values(*V)[:, :, :31], 1 / 8)
+    assert (out - want).abs().max() <= tol + 2.0 ** 17 * 2.0 ** -24 * float(vv[:31].abs().max())
