@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(D, block_ctas<D, EIGHT>()) append_block_kernel
       nt = new_tokens(a, b);
     }
     const int page = nt.start / kPage + y;
-    if (nt.n == 0 || page * kPage >= nt.start + nt.n) continue;  // no token of this page
+    // no token of this page (compared as pages: a page's tokens may pass 2^31)
+    if (nt.n == 0 || page > (nt.start + nt.n - 1) / kPage) continue;
     const int pos = page * kPage + i, t = pos - nt.start;
     const bool on = t >= 0 && t < nt.n;
     const bool is_q = gx >= 2 * kv_groups, is_v = !is_q && gx >= kv_groups;
