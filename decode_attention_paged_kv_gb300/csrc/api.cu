@@ -1091,6 +1091,8 @@ dkv_status dkv_kv_append(const dkv_append* p, const dkv_kv* K, const dkv_kv* V, 
   const int64_t most = (static_cast<int64_t>(1) << 31) - 256;  // a grid's threads or CTAs
   if (p->new_tokens > most / (heads * (d / 16)) || B * pages > most / heads)
     return DKV_ERR_UNSUPPORTED;
+  // keys and values have places of their own, and so have their scales
+  if (K->data == V->data || (is_fp8(K) && K->scale == V->scale)) return DKV_ERR_SHAPE;
   dkv::AppendArgs a{};
   a.k = {static_cast<const uint16_t*>(p->k), p->k_stride_b, p->k_stride_t, p->k_stride_h};
   a.v = {static_cast<const uint16_t*>(p->v), p->v_stride_b, p->v_stride_t, p->v_stride_h};

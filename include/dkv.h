@@ -242,6 +242,8 @@ typedef struct dkv_append {
    tokens: the larger of the scale it has (if it held tokens before) and
    2^e, e the smallest exponent with max |y| <= 448 * 2^e over the new ones.
    Codes are rounded to nearest even and saturate at +-448; inputs are finite.
+   K and V are caches of their own: the same data, or the same scales for both,
+   are refused (DKV_ERR_SHAPE).
    - N_b <= 0 or n_b = 0: nothing of sequence b is touched.
    - n_b outside [0, T], n_b > N_b, N_b > N or (rotated) N_b > rope_len: nothing
      of sequence b is touched; a block-table entry outside [0, num_blocks): no
