@@ -33,8 +33,11 @@
 // (6.3), into a 16-bit one 269 us (6.0).  The ragged ones took 248 us with one
 // head a CTA, 166 with four, 152 with persistent CTAs that rotated twice to save
 // registers.  One token of 64 sequences (16-bit) takes 2.0 us, of 16 sequences
-// (8-bit) 2.2 us: the latency of the launch and of the dependent loads length ->
-// block table -> scale.
+// (8-bit) 2.2 us where no scale rises: the latency of the launch and of the
+// dependent loads length -> block table -> scale.  Where one rises, the older rows
+// of its block are stored again one after the other: 0.3 us more for one row, 1.8
+// for 7, 3.8 for 15 (16 sequences; 4.0 of 64), and a batch takes as long as its
+// fullest such block.
 
 #include "dkv_device.cuh"
 #include "dkv_kernels.h"
@@ -422,10 +425,13 @@ template <int D, bool F16, bool IL>
 cudaError_t launch_t(bool eight, const AppendArgs& a, int num_sms, cudaStream_t s) {
   const uint32_t heads = 2 * a.Hkv + a.Hq;
   // Into a 16-bit cache, a thread a row segment while all of them are resident at
-  // once (2048 a SM) or there are few tokens a sequence; us here against the
-  // persistent kernel's (32 / 8 heads, d = 128): 64 sequences of 4 tokens 2.7 /
-  // 3.6, 8 of 64 3.0 / 4.0, 1 of 512 3.1 / 4.0; at 64 of 16, just past it, 4.7 /
-  // 5.0, 64 of 32 9.3 / 9.0, 8 prompts of 8K 302 / 270.
+  // once (2048 a SM) or there are few tokens a sequence, which fill the blocks that
+  // the persistent kernel goes by only in part; us here against that kernel's (32 /
+  // 8 heads, d = 128): 1 sequence of 512 tokens 3.1 / 4.0, 8 of 64 3.0 / 4.0, 64 of 4
+  // 2.6 / 4.2, 64 of 16 4.6 / 5.6, 128 of 8 4.7 / 7.5, 512 of 8 17.3 / 23.8, 1024 of
+  // 1 5.1 / 20.3.  They meet at 16 tokens in large batches (256 17.1 / 17.4, 512 37.7
+  // / 36.5, 1024 73.2 / 68.6); past it 256 of 32 36.2 / 33.6, 8 prompts of 8K 302 /
+  // 270.
   const int64_t threads = static_cast<int64_t>(a.B) * a.T * heads * (D / 16);
   const bool by_token = eight ? a.T == 1 : a.T <= 16 || threads <= num_sms * 2048;
   if (!by_token) {

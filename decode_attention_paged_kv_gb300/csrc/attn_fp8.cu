@@ -166,7 +166,7 @@ __device__ __forceinline__ uint32_t e4m3_hi2(uint32_t w) {
 }
 
 // 2^x, 0 for x = -inf (results below 2^-126 are 0: a weight that small is lost
-// beside the largest, which is at least 1).
+// beside the largest, which is above 1/2: r is rounded up).
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

@@ -56,8 +56,9 @@ inline int select_pages_per_chunk(int64_t union_max, int d) {
 // waves of items on the resident CTAs (fp8_ctas), counting 8 kv heads, the size
 // is changed to whole waves; less than one is cut finer.  Measured at 32K tokens,
 // 32 / 8 heads, d = 128: 2 sequences 36.8 -> 29.2 us, 4 56.4 -> 50.3; 16, nine
-// waves of 64 pages, 165 us (32 pages: 180, 128: 165).  Depends on the pages, d and the batch only, so here too one kv head at
-// a time gives bitwise the all-heads result.
+// waves of 64 pages, 165 us (32 pages: 180, 128: 165).  Depends on the pages, d and
+// the batch only, so here too one kv head at a time gives bitwise the all-heads
+// result; a sequence's result may differ in its last bits from batch to batch.
 inline int64_t fp8_ctas(int d) { return 152 * (d == 64 ? 4 : 3); }
 inline int fp8_pages_per_chunk(int64_t pages, int d, int batch) {
   const int64_t base = d == 128 ? 64 : 128, units = 8 * static_cast<int64_t>(batch);
@@ -79,8 +80,9 @@ inline int fp8_pages_per_chunk(int64_t pages, int d, int batch) {
 // union, of union_max pages at most, is cut into -- equal ones of the pages it
 // turns out to have (fp8_part_pages), so no item is empty and none much longer
 // than another.  One wave of items where that fills the resident CTAs (fp8_ctas)
-// to 4/5, else about two; 8 pages a part at
-// least, and at most 32 parts (the single-pass merge).  Measured on unions of
+// to 4/5, else about two; 8 pages a part at least where the union is as large as it
+// can be (a smaller one's parts go down to two pages, a stage), and at most 32 parts
+// (the single-pass merge).  Measured on unions of
 // 128 pages (the largest possible: 512): 128 units 46.3 us a call and 32 units
 // 30.4, against 50.0 and 38.0 with chunks of 64 pages, 6 of 8 of them empty.
 inline int fp8_select_parts(int64_t union_max, int d, int64_t units) {

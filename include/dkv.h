@@ -289,8 +289,11 @@ dkv_status dkv_kv_meta_append_tokens(const dkv_params* p, const dkv_kv* K, int32
 
 /* Exact decode attention.  out [B, Hq, d] in out_dtype (DKV_FP32 | DKV_BF16 |
    DKV_FP16).  Splits the sequence into fixed chunks whose length depends only
-   on d, so evaluating one kv head at a time (a view with Hkv = 1) gives results
-   bitwise identical to the all-heads call. */
+   on d and seq_len -- in the 8-bit formats on the batch too -- so evaluating one
+   kv head at a time (a view with Hkv = 1) gives results bitwise identical to the
+   all-heads call.  In the 8-bit formats a sequence's result may differ in its last
+   bits (the order of fp32 sums) with the batch it is part of; one call is the same
+   each time. */
 dkv_status dkv_decode_attn_full(const dkv_params* p, const void* q, const dkv_kv* K,
                                 const dkv_kv* V, void* out, int32_t out_dtype,
                                 void* workspace, size_t workspace_bytes, void* stream);
@@ -299,7 +302,10 @@ dkv_status dkv_decode_attn_full(const dkv_params* p, const void* q, const dkv_kv
    scores of all P pages from meta_min / meta_max, the top_k best pages (ties
    to the lower page index; top_k clamped to P), attention over those pages'
    tokens only (softmax normalised over them).  `selected` (nullable) receives
-   the chosen pages [B, Hq, min(top_k, P)] in ascending order. */
+   the chosen pages [B, Hq, min(top_k, P)] in ascending order.  How the pages of a
+   unit are cut depends on top_k and P, in the 8-bit formats also on batch and
+   num_kv_heads: there a row may differ in its last bits from call shape to call
+   shape. */
 dkv_status dkv_decode_attn_select(const dkv_params* p, const void* q, const dkv_kv* K,
                                   const dkv_kv* V, const void* meta_min,
                                   const void* meta_max, int32_t top_k, void* out,
