@@ -418,14 +418,17 @@ dkv_status dkv_kv_meta_append_tokens(const dkv_params* p, const dkv_kv* K, int32
                                      void* stream) {
   const dkv_status st = check_params(p);
   if (st != DKV_OK) return st;
-  if (new_tokens < 0 || new_tokens > p->seq_len) return DKV_ERR_SHAPE;
+  // (an append may have had more rows than the cache has tokens, not all in use)
+  if (new_tokens < 0 ||
+      (p->seq_lens == nullptr && new_lens == nullptr && new_tokens > p->seq_len))
+    return DKV_ERR_SHAPE;
   if (reinterpret_cast<uintptr_t>(new_lens) & 3u) return DKV_ERR_ALIGN;
   dkv::MetaNew m{};
-  m.T = new_tokens;
+  m.T = std::min(new_tokens, p->seq_len);
   m.news = new_lens;
   m.align = K != nullptr && is_fp8(K) ? std::max(p->page_size, dkv::kPage) : p->page_size;
   // the first new token may be the last of its `align` tokens
-  const int64_t span = static_cast<int64_t>(new_tokens) + m.align - 1;
+  const int64_t span = static_cast<int64_t>(m.T) + m.align - 1;
   m.slots = static_cast<int>(
       std::min(ceil_div(span, p->page_size), ceil_div(p->seq_len, p->page_size)));
   return meta_impl(p, K, meta_min, meta_max, m, stream);

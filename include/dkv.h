@@ -274,8 +274,8 @@ dkv_status dkv_kv_meta_build(const dkv_params* p, const dkv_kv* K, void* meta_mi
    rises (pages of 4 and 8 tokens: several a block).  Same arguments and layout
    as dkv_kv_meta_build, whose result it reproduces bit for bit when the other
    pages are already built.
-   - new_tokens: T, as the append had it, 0 <= T <= seq_len.  new_lens: DEVICE
-     [B], n_b (NULL: all T).  n_b <= 0: nothing of sequence b is rebuilt; one
+   - new_tokens: T, as the append had it (at most seq_len if seq_lens and new_lens
+     are NULL).  new_lens: DEVICE [B], n_b (NULL: all T).  n_b <= 0: nothing of sequence b is rebuilt; one
      above T or N_b counts as that.
    - dkv_kv_meta_append is the call of a decode step: T = 1, no new_lens.
    ("TinyServe: Query-Aware Cache Selection for Efficient LLM Serving",

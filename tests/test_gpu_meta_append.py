@@ -214,3 +214,20 @@ def test_draft_steps(S, dev, dkv):
         want = ref.attention(q.cpu(), kv, vv, 1 / math.sqrt(d), lens, pages=sel.tolist(), S=S)
         err = (out.cpu().double() - want).abs().max()
         assert err <= ref.tolerance(q.cpu(), kv, vv, 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("kind", ["dense", "fp8"])
+def test_more_rows_than_tokens(kind, dev, dkv):
+    # a draft buffer of more rows than the cache holds tokens, a few of them in use
+    B, H, d, N, S, T, dt = 2, 2, 64, 40, 8, 64, torch.bfloat16
+    K, V = empty_caches(dkv, kind, B, H, N, d, dt, dev, 1)
+    meta = [torch.full((B, H, 5, d), 9.0, dtype=dt, device=dev) for _ in range(2)]
+    lens = torch.zeros(B, dtype=torch.int32, device=dev)
+    g = torch.Generator().manual_seed(1)
+    for news in ([3, 20], [37, 1]):
+        new = torch.tensor(news, dtype=torch.int32, device=dev)
+        lens += new
+        y = torch.randn(B, T, H, d, generator=g).to(dt).to(dev)
+        dkv.kv_append(y, y, K, V, seq_lens=lens, new_lens=new)
+        dkv.kv_meta_append(K, meta, page_size=S, seq_lens=lens, new_tokens=T, new_lens=new)
+        check_against_build(dkv, K, meta, lens, S)

@@ -25,3 +25,12 @@ def test_validation(dkv, fmt):  # noqa: F811
     assert call(0, mn=None) == NULL and call(0, K=None) == NULL
     assert call(0, mn=ctypes.c_void_p(8)) == ALIGN
     assert call(0, p=_params(dkv, seq_len=0)) == SHAPE
+
+
+def test_more_rows_than_tokens(dkv):  # noqa: F811
+    # as dkv_kv_append: what fits is known on the device, so only an address is wrong here
+    L, kv = dkv.lib(), _kv(dkv, dkv.DKV_KV_DENSE)
+    lens, bad = ctypes.c_void_p(4096), ctypes.c_void_p(8)
+    for p, news in ((_params(dkv), lens), (_params(dkv, seq_lens=4096), None)):
+        assert L.dkv_kv_meta_append_tokens(ctypes.byref(p), ctypes.byref(kv), 5000, news, bad, bad,
+                                           None) == ALIGN
