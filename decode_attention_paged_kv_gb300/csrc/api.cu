@@ -2,33 +2,27 @@
 // argument validation, workspace layout, TMA tensor-map encoding and kernel
 // launches.  Every argument error is returned before anything is launched.
 
-#include <cudaTypedefs.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
 
 #include <algorithm>
-#include <initializer_list>
-#include <mutex>
 
 #include "../../include/dkv.h"
+#include "api_util.h"
 #include "dkv_kernels.h"
 
 namespace {
 
 using dkv::ceil_div;
 
-constexpr uint64_t kWaitLimitNs = 200000000ull;  // 200 ms per bounded device wait
-constexpr size_t kAlign = 256;
+using namespace dkv::api;
+
 static_assert(DKV_WORKSPACE_HEADER_BYTES == kAlign, "status word and counters");
 // Shared memory the per-unit selection kernel may take (one CTA per SM), and
 // the shortest context (pages) it is used for.
 constexpr size_t kUnitSelectSmemLimit = 227 * 1024;
 constexpr int kUnitSelectMinP = 256;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Byte offsets of the regions inside a caller-provided workspace.
 struct WsLayout {
@@ -116,18 +110,6 @@ WsLayout layout_for(const dkv_params& p, int top_k, bool fp8 = false) {
   return L;
 }
 
-// Multiprocessor count of the current device (the persistent attention grid).
-int current_sm_count() {
-  static int cached[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64 && cached[dev] > 0) return cached[dev];
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64) cached[dev] = n;
-  return n;
-}
-
 dkv_status check_params(const dkv_params* p) {
   if (p == nullptr) return DKV_ERR_NULL;
   if (p->batch < 1 || p->num_q_heads < 1 || p->num_kv_heads < 1 || p->seq_len < 1 ||
@@ -199,21 +181,6 @@ dkv_status check_kv(const dkv_params* p, const dkv_kv* kv) {
 }
 
 // ------------------------------------------------------------- tensor maps
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-bool get_encode() {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  return g_encode != nullptr;
-}
-
 // Map over one dense K or V cache [B, Hkv, N, d] viewed as 5-D
 // {64 channels, N tokens, d/64 halves, Hkv, B} with a box of one page
 // {64, 16, d/64, 1, 1} and 128-byte swizzle.
@@ -322,12 +289,6 @@ bool encode_fp8_map(CUtensorMap* map, const dkv_params* p, const dkv_kv* kv, boo
 }
 
 dkv::Fp8View fp8_view(const dkv_kv* kv) { return {kv->scale, kv->sstride_b, kv->sstride_h}; }
-
-int out_code(int32_t out_dtype) {
-  return out_dtype == DKV_FP32 ? 2 : (out_dtype == DKV_FP16 ? 1 : 0);
-}
-
-dkv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DKV_OK : DKV_ERR_CUDA; }
 
 }  // namespace
 
@@ -1006,25 +967,6 @@ dkv_status dkv_decode_attn_topk_tokens(const dkv_params* p, const void* q, const
   aa.o_sb = p->o_stride_b;
   aa.o_sh = p->o_stride_h;
   return cuda_status(dkv::launch_token_attn(d, f16, aa, rows, s));
-}
-
-// Whether the elements of a tensor that is written -- rows of `inner` elements
-// over the dimensions (count, stride) -- all have places of their own.
-struct Dim {
-  int64_t count, stride;
-};
-static bool distinct(int64_t inner, std::initializer_list<Dim> dims) {
-  Dim d[3];
-  int n = 0;
-  for (const Dim& x : dims)
-    if (x.count > 1) d[n++] = x;
-  std::sort(d, d + n, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
-  int64_t extent = inner;
-  for (int i = 0; i < n; ++i) {
-    if (d[i].stride < extent) return false;
-    extent += (d[i].count - 1) * d[i].stride;
-  }
-  return true;
 }
 
 dkv_status dkv_kv_append(const dkv_append* p, const dkv_kv* K, const dkv_kv* V, void* workspace,
