@@ -12,10 +12,17 @@ Public calls (same names as the C ABI, without the ``dkv_`` prefix):
   decode_attn_select(q, K, V, meta, k)  -> out (, selected)
   kv_quant4(x) / kv_dequant4(q4)
   kv_append(k, v, K, V, lens)           new tokens into a cache (-> rotated q)
+  latent_append(c, k_rope, cache, ...)  new tokens into a latent cache
+  latent_decode_attn(q_latent, q_rope, cache, scale)          -> out
+  latent_prompt_attn(q_nope, q_rope, k_nope, k_rope, v, ...)  -> out
+  kv_pages_fork(caches, refs, lens, ...) one step of a block table: rows continue,
+                                        fork, grow, end
+  kv_pages_compact(caches, refs)        pages in use to the pools' front
   workspace_bytes(...), read_device_status(workspace)
 K and V are dense tensors [B, Hkv, N, d] (bf16 / fp16; any batch / head
 strides, token stride d), ``Q4Cache`` tuples in the 4-bit format,
 ``PagedCache`` pools, or ``Fp8Cache`` / ``Fp8PagedCache`` in the 8-bit format.
+Latent caches are dense tensors [B, N, latent + 64] or ``LatentCache`` pools.
 """
 
 from __future__ import annotations
@@ -33,9 +40,12 @@ import torch
 from . import build as _build_mod
 
 __all__ = [
-    "Q4Cache", "PagedCache", "Fp8Cache", "Fp8PagedCache", "Meta8", "DkvError", "lib", "kv_meta_build", "kv_meta8_build",
+    "Q4Cache", "PagedCache", "Fp8Cache", "Fp8PagedCache", "LatentCache", "Meta8", "DkvError", "lib",
+    "kv_meta_build", "kv_meta8_build",
     "kv_append", "kv_meta_append", "rope_table", "hot_state", "hot_stats", "decode_attn_full",
     "decode_attn_select", "decode_attn_topk_tokens", "kv_quant4", "kv_dequant4",
+    "latent_append", "latent_decode_attn", "latent_prompt_attn", "latent_workspace_bytes",
+    "kv_pages_fork", "kv_pages_compact", "pages_workspace_bytes",
     "workspace_bytes", "workspace_bytes_tokens", "read_device_status", "status_string",
     "PAGE_SIZE", "DKV_FLAG_GROUP_SELECT",
 ]
@@ -119,6 +129,20 @@ class Fp8PagedCache(NamedTuple):
     dtype: torch.dtype = torch.bfloat16
 
 
+class LatentCache(NamedTuple):
+    """A cache of one latent vector and one rotated key a token, shared by all
+    heads, held as a pool of blocks.
+
+    pool [num_blocks, S, dc + 64] bf16 / fp16, S = 16, 32 or 64 tokens a block,
+    dc = 256 or 512 latent channels; block_table [B, P] int32: block j of batch
+    entry b is pool block block_table[b, j]; seq_len: the N tokens a sequence can
+    hold.  (A dense latent cache is a tensor [B, N, dc + 64].)
+    """
+    pool: torch.Tensor
+    block_table: torch.Tensor
+    seq_len: int
+
+
 class _Params(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
@@ -146,6 +170,23 @@ class _Append(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("k", "v", "q", "q_out")]
                 + [(f"{t}_stride_{x}", ctypes.c_int64) for t in "kvqo" for x in "bth"]
                 + [(n, ctypes.c_void_p) for n in ("cos", "sin", "seq_lens", "new_lens")])
+
+
+class _LatentCache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("dtype", "latent_dim", "rope_dim", "seq_len",
+                                               "block_size", "num_blocks")]
+                + [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
+                   ("stride_t", ctypes.c_int64), ("block_table", ctypes.c_void_p),
+                   ("block_table_stride", ctypes.c_int64)])
+
+
+class _LatentAttn(ctypes.Structure):
+    _fields_ = ([("batch", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                 ("new_tokens", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                 ("scale", ctypes.c_float), ("out_dtype", ctypes.c_int32)]
+                + [(n, ctypes.c_void_p) for n in ("q_latent", "q_rope", "out")]
+                + [(f"{t}_stride_{x}", ctypes.c_int64) for t in ("ql", "qr", "o") for x in "bth"]
+                + [("seq_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p)])
 
 
 _lib = None
@@ -190,6 +231,11 @@ def lib() -> ctypes.CDLL:
             L.dkv_hot_state_bytes.restype = sz
             L.dkv_decode_attn_select_hot.argtypes = [P, vp, KVp, KVp, vp, vp, i32, vp, i32, vp,
                                                      vp, sz, i32, vp, sz, vp]
+            L.dkv_latent_workspace_bytes.argtypes = [ctypes.POINTER(_LatentAttn),
+                                                     ctypes.POINTER(_LatentCache)]
+            L.dkv_latent_workspace_bytes.restype = sz
+            L.dkv_pages_workspace_bytes.argtypes = [i32, i32, i32]
+            L.dkv_pages_workspace_bytes.restype = sz
             L.dkv_kv_quant4.argtypes = [i64, i32, vp, vp, vp, vp, vp]
             L.dkv_kv_dequant4.argtypes = [i64, i32, vp, vp, vp, vp, vp]
             L.dkv_read_device_status.argtypes = [vp, vp]
@@ -223,7 +269,7 @@ def _load_binding():
             spec = importlib.util.spec_from_loader(loader.name, loader)
             m = importlib.util.module_from_spec(spec)
             loader.exec_module(m)
-            m.setup(Q4Cache, PagedCache, Fp8Cache, Fp8PagedCache, Meta8, DkvError)
+            m.setup(Q4Cache, PagedCache, Fp8Cache, Fp8PagedCache, Meta8, DkvError, LatentCache)
             _binding = m
     return _binding
 
@@ -370,6 +416,125 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, K, V, seq_lens: Optional[torch.T
     new_tokens=T and the same seq_lens and new_lens brings it up to date."""
     return (_binding or _load_binding()).kv_append(k, v, K, V, seq_lens, new_lens, q, q_out, rope,
                                                    interleaved, workspace)
+
+
+def latent_append(c: torch.Tensor, k_rope: torch.Tensor, cache,
+                  seq_lens: Optional[torch.Tensor] = None,
+                  new_lens: Optional[torch.Tensor] = None,
+                  q_rope: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                  rope=None, norm: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  interleaved: bool = False,
+                  workspace: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Append new tokens' latent vectors c [B, T, dc] and shared keys k_rope
+    [B, T, 64] to a latent cache, in place; one launch.
+
+    norm [dc], eps: the latent vectors are stored as c * rsqrt(mean(c^2) + eps) *
+    norm, in 32 bits and rounded once (None: as they are).
+    rope: (cos, sin) float32 [positions, 32] (rope_table(length, 64)), by which
+    the keys, and the queries' rotary parts q_rope [B, T, H, 64], are rotated;
+    the latter are returned (in q_out if given, which may be q_rope itself).
+    seq_lens, new_lens, interleaved, workspace: as for kv_append."""
+    return (_binding or _load_binding()).latent_append(c, k_rope, cache, seq_lens, new_lens,
+                                                       q_rope, q_out, rope, norm, eps,
+                                                       interleaved, workspace)
+
+
+def latent_decode_attn(q_latent: torch.Tensor, q_rope: torch.Tensor, cache, scale: float,
+                       seq_lens: Optional[torch.Tensor] = None,
+                       new_lens: Optional[torch.Tensor] = None,
+                       out_dtype: torch.dtype = torch.float32,
+                       out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, flags: int = 0):
+    """Attention of the T newest tokens of each sequence over a latent cache (the
+    absorbed form); returns out [B, T, H, dc].
+
+    q_latent [B, T, H, dc]: queries times the heads' key expansion; q_rope
+    [B, T, H, 64]: their rotated parts.  Per head, softmax(scale * (q_latent .
+    latent + q_rope . key)) times the latent vectors; out times the heads' value
+    expansion is the layer's result.
+    seq_lens (int32 [B]): each sequence's length with its new tokens (None: all
+    N); new_lens (int32 [B]): how many of the T it has (None: all); new token t
+    sees the sequence's first seq_lens - new_lens + t + 1 tokens.  Rows past
+    new_lens are not written.
+    scale has no default: it goes by the width of the unabsorbed heads, which the
+    cache does not know (1 / sqrt(128 + 64), say)."""
+    return (_binding or _load_binding()).latent_decode_attn(
+        q_latent, q_rope, cache, scale, seq_lens, new_lens, out_dtype, out, workspace, flags)
+
+
+def latent_workspace_bytes(B: int, T: int, H: int, latent_dim: int, N: int) -> int:
+    """Workspace bytes latent_decode_attn needs for up to these sizes."""
+    p, c = _LatentAttn(), _LatentCache()
+    p.batch, p.new_tokens, p.num_heads = B, T, H
+    c.latent_dim, c.rope_dim, c.seq_len = latent_dim, 64, N
+    n = lib().dkv_latent_workspace_bytes(ctypes.byref(p), ctypes.byref(c))
+    if n == 0:
+        raise DkvError(2, "dkv_latent_workspace_bytes")
+    return int(n)
+
+
+def latent_prompt_attn(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Tensor,
+                       k_rope: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                       cu_k: Optional[torch.Tensor], scale: float, causal: bool = True,
+                       out_dtype: torch.dtype = torch.float32,
+                       out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, flags: int = 0):
+    """Attention of prompts with keys and values expanded a head (the expanded
+    form); returns out [rows, H, dn].
+
+    Sequences lie one after another: rows cu_q[b] .. cu_q[b + 1] - 1 of q_nope
+    [rows, H, dn] and q_rope [rows, H, 64] are sequence b's queries, rows cu_k[b]
+    .. of k_nope and v [rows, H, dn] and of the shared k_rope [rows, 64] its keys
+    (cu_k None: as cu_q).  The queries are the last tokens of their sequence, so
+    causal means that query i of n_q sees the first n_k - n_q + i + 1 keys: whole
+    prompts, and the last chunk of prompts whose first tokens are cached already.
+    dn = 64 or 128.  Rows past the last sequence may be there and are left alone.
+    workspace: where bounds that do not fit the tensors are recorded
+    (read_device_status); such a sequence is left alone."""
+    return (_binding or _load_binding()).latent_prompt_attn(
+        q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, scale, causal, out_dtype, out, workspace,
+        flags)
+
+
+def kv_pages_fork(caches, refs: torch.Tensor, seq_lens: torch.Tensor,
+                  parents: Optional[torch.Tensor] = None,
+                  new_lens: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> None:
+    """One step of the block table that `caches` (PagedCache, Fp8PagedCache or
+    LatentCache objects of one table and block size) share, in place: row b becomes
+    the continuation of the first seq_lens[p] tokens of row p = parents[b] (None: b
+    itself; -1: of nothing), with pages for new_lens[b] more tokens (None: 0).
+
+    Whole pages are shared; a last page that is not whole is copied, in every pool,
+    for all but the lowest row that continues it; new pages are the lowest free
+    blocks.  refs (int32 [num_blocks], in place) counts the table entries that hold
+    a block, and whoever else does: pages that no row continues are released by it.
+    Entries past a row's pages become -1.  Lengths are not changed: a row's new one is
+    seq_lens[parents[b]] + new_lens[b].
+    All or nothing: a step that does not fit (too few free blocks, say) changes
+    nothing and is recorded in `workspace` (read_device_status)."""
+    return (_binding or _load_binding()).kv_pages_fork(caches, refs, seq_lens, parents, new_lens,
+                                                       workspace)
+
+
+def kv_pages_compact(caches, refs: torch.Tensor, refs_out: Optional[torch.Tensor] = None,
+                     block_table_out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Move the blocks in use (refs > 0) of the caches' pools to their front, and
+    rename them in the block table and the counts (in place, or into
+    block_table_out and refs_out).  Returns int32 [num_blocks]: every block's new
+    number, -1 where it was free, for whoever else knows blocks by number."""
+    return (_binding or _load_binding()).kv_pages_compact(caches, refs, refs_out, block_table_out,
+                                                          workspace)
+
+
+def pages_workspace_bytes(rows: int, cols: int, num_blocks: int) -> int:
+    """Workspace bytes kv_pages_fork and kv_pages_compact need for a block table
+    [rows, cols] over pools of num_blocks blocks."""
+    n = lib().dkv_pages_workspace_bytes(rows, cols, num_blocks)
+    if n == 0:
+        raise DkvError(2, "dkv_pages_workspace_bytes")
+    return int(n)
 
 
 def hot_state(B: int, Hkv: int, N: int, device) -> torch.Tensor:

@@ -32,6 +32,7 @@ PyObject* g_fp8 = nullptr;
 PyObject* g_fp8_paged = nullptr;
 PyObject* g_meta8 = nullptr;
 PyObject* g_error = nullptr;
+PyObject* g_latent = nullptr;
 
 struct PyError {};  // a Python exception is set
 
@@ -346,8 +347,8 @@ PyObject* incref(PyObject* o) {
 
 // ------------------------------------------------------------------- the calls
 PyObject* setup(PyObject* const* a) {
-  PyObject** to[] = {&g_q4, &g_paged, &g_fp8, &g_fp8_paged, &g_meta8, &g_error};
-  for (int i = 0; i < 6; ++i) {
+  PyObject** to[] = {&g_q4, &g_paged, &g_fp8, &g_fp8_paged, &g_meta8, &g_error, &g_latent};
+  for (int i = 0; i < 7; ++i) {
     Py_INCREF(a[i]);
     *to[i] = a[i];
   }
@@ -603,6 +604,368 @@ PyObject* decode_attn_select(PyObject* const* a) {
   return Py_BuildValue("(NN)", o, made ? THPVariable_Wrap(*made) : incref(a[9]));
 }
 
+// ----------------------------------------------------------------- latent caches
+struct Latent {
+  dkv_latent_cache c{};
+  at::ScalarType dtype = at::kBFloat16;
+  int64_t B = 0, N = 0, width = 0;
+  int device = -1;
+};
+
+// A dense tensor [B, N, dc + 64] or a LatentCache.
+Latent parse_latent(PyObject* o) {
+  Latent l;
+  dkv_latent_cache& c = l.c;
+  const at::Tensor* t;
+  if (THPVariable_Check(o)) {
+    t = &THPVariable_Unpack(o);
+    if (t->dim() != 3 || t->stride(2) != 1)
+      value_error("a latent cache must be [B, N, latent + rope] with channel stride 1");
+    l.B = t->size(0), l.N = t->size(1);
+  } else if (is(o, g_latent)) {
+    t = &tensor(PyTuple_GET_ITEM(o, 0), "pool");
+    const at::Tensor& bt = tensor(PyTuple_GET_ITEM(o, 1), "block_table");
+    l.N = integer(PyTuple_GET_ITEM(o, 2));
+    if (t->dim() != 3 || t->stride(2) != 1)
+      value_error("pool must be [num_blocks, block_size, latent + rope] with channel stride 1");
+    if (bt.scalar_type() != at::kInt || bt.dim() != 2 || (bt.stride(1) != 1 && bt.size(1) > 1))
+      value_error("block_table must be int32 [B, P] with unit column stride");
+    if (cuda_index(bt) != cuda_index(*t)) value_error("block_table must be on the pool's device");
+    c.block_size = int32_size(t->size(1));
+    if (c.block_size != 16 && c.block_size != 32 && c.block_size != 64)
+      value_error("a latent pool's blocks hold 16, 32 or 64 tokens");
+    if (l.N < 1 || bt.size(1) < (l.N + c.block_size - 1) / c.block_size)
+      value_error("block_table has fewer than ceil(seq_len / block_size) columns");
+    l.B = bt.size(0);
+    c.num_blocks = int32_size(t->size(0));
+    c.block_table = static_cast<const int32_t*>(bt.data_ptr());
+    c.block_table_stride = bt.stride(0);
+  } else {
+    raise(PyExc_TypeError, "a latent cache is a tensor or a LatentCache");
+  }
+  l.width = t->size(2);
+  l.dtype = t->scalar_type();
+  l.device = cuda_index(*t);
+  c.dtype = dtype_code(l.dtype);
+  c.rope_dim = 64;
+  c.latent_dim = int32_size(l.width - 64 < 0 ? 0 : l.width - 64);
+  c.seq_len = int32_size(l.N);
+  c.data = t->data_ptr();
+  // (the stride of a dimension of size 1 says nothing)
+  c.stride_t = t->size(1) > 1 ? t->stride(1) : l.width;
+  c.stride_b = t->size(0) > 1 ? t->stride(0) : 0;
+  return l;
+}
+
+// A tensor of an exact shape with channel stride 1, in the given dtype and on the device.
+const at::Tensor& shaped(PyObject* o, const char* name, at::IntArrayRef shape,
+                         at::ScalarType dtype, int device) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.sizes() != shape || t.scalar_type() != dtype || cuda_index(t) != device ||
+      (t.numel() > 0 && t.size(-1) > 1 && t.stride(-1) != 1)) {
+    PyErr_Format(PyExc_ValueError,
+                 "%s has another shape, dtype or device than the call's other tensors, or no "
+                 "channel stride of 1",
+                 name);
+    throw PyError{};
+  }
+  return t;
+}
+
+// The stride of dimension i, 0 where it has one element.
+int64_t stride_of(const at::Tensor& t, int i) { return t.size(i) > 1 ? t.stride(i) : 0; }
+
+// The 256 bytes where a call records what it refused on the device, or NULL.
+void* status_word(PyObject* o, int device) {
+  const at::Tensor* t = scratch(o, "workspace");
+  if (t == nullptr) return nullptr;
+  if (cuda_index(*t) != device ||
+      static_cast<size_t>(t->numel()) * t->element_size() < DKV_WORKSPACE_HEADER_BYTES)
+    value_error("workspace must hold 256 bytes on the caches' device");
+  return t->data_ptr();
+}
+
+// latent_append(c, k_rope, cache, seq_lens, new_lens, q_rope, q_out, rope, norm, eps,
+//               interleaved, workspace)
+PyObject* latent_append(PyObject* const* a) {
+  const Latent l = parse_latent(a[2]);
+  const int dev = l.device;
+  if (dev < 0) value_error("latent_append wants CUDA tensors");
+  const int64_t dc = l.c.latent_dim;
+  const at::Tensor& c0 = tensor(a[0], "c");
+  if (c0.dim() != 3) value_error("c must be [B, T, latent]");
+  const int64_t T = c0.size(1);
+  const at::Tensor& c = shaped(a[0], "c", {l.B, T, dc}, l.dtype, dev);
+  const at::Tensor& k = shaped(a[1], "k_rope", {l.B, T, 64}, l.dtype, dev);
+  dkv_latent_append_args p{};
+  p.batch = int32_size(l.B);
+  p.new_tokens = int32_size(T);
+  p.c = c.data_ptr(), p.c_stride_b = stride_of(c, 0), p.c_stride_t = stride_of(c, 1);
+  p.k = k.data_ptr(), p.k_stride_b = stride_of(k, 0), p.k_stride_t = stride_of(k, 1);
+  std::optional<at::Tensor> made;
+  if (!is_none(a[5])) {
+    const at::Tensor& q0 = tensor(a[5], "q_rope");
+    if (q0.dim() != 4) value_error("q_rope must be [B, T, H, 64]");
+    const int64_t H = q0.size(2);
+    const at::Tensor& q = shaped(a[5], "q_rope", {l.B, T, H, 64}, l.dtype, dev);
+    // (rows that no token has are left as they are)
+    if (is_none(a[6])) made = at::empty({l.B, T, H, 64}, q.options());
+    const at::Tensor& o = made ? *made : shaped(a[6], "q_out", {l.B, T, H, 64}, l.dtype, dev);
+    p.num_q_heads = int32_size(H);
+    p.q = q.data_ptr();
+    p.q_stride_b = stride_of(q, 0), p.q_stride_t = stride_of(q, 1), p.q_stride_h = stride_of(q, 2);
+    p.q_out = o.data_ptr();
+    p.o_stride_b = stride_of(o, 0), p.o_stride_t = stride_of(o, 1), p.o_stride_h = stride_of(o, 2);
+  } else if (!is_none(a[6])) {
+    value_error("q_out without q_rope");
+  }
+  if (!is_none(a[7])) {
+    if ((!PyTuple_Check(a[7]) && !PyList_Check(a[7])) || PySequence_Fast_GET_SIZE(a[7]) != 2)
+      value_error("rope must be (cos, sin)");
+    const at::Tensor& cs = tensor(PySequence_Fast_GET_ITEM(a[7], 0), "cos");
+    const at::Tensor& sn = tensor(PySequence_Fast_GET_ITEM(a[7], 1), "sin");
+    if (cs.dim() != 2 || cs.size(1) != 32 || cs.size(0) < 1 || cs.sizes() != sn.sizes() ||
+        cs.scalar_type() != at::kFloat || sn.scalar_type() != at::kFloat || cuda_index(cs) != dev ||
+        cuda_index(sn) != dev || !cs.is_contiguous() || !sn.is_contiguous())
+      value_error("rope must be two contiguous float32 [positions, 32] tables");
+    p.rope_len = int32_size(cs.size(0));
+    p.cos = static_cast<const float*>(cs.data_ptr());
+    p.sin = static_cast<const float*>(sn.data_ptr());
+  }
+  if (!is_none(a[8])) {
+    const at::Tensor& w = shaped(a[8], "norm", {dc}, l.dtype, dev);
+    p.norm = w.data_ptr();
+  }
+  p.eps = static_cast<float>(number(a[9]));
+  const int il = PyObject_IsTrue(a[10]);
+  if (il < 0) throw PyError{};
+  p.interleaved = il;
+  p.seq_lens = lengths(a[3], "seq_lens", l.B, dev);
+  p.new_lens = lengths(a[4], "new_lens", l.B, dev);
+  void* ws = status_word(a[11], dev);
+  if (T > 0)  // (an empty tensor has no address)
+    call("dkv_latent_append", dev,
+         [&](void* stream) { return dkv_latent_append(&p, &l.c, ws, stream); });
+  if (made) return THPVariable_Wrap(*made);
+  return incref(is_none(a[6]) ? Py_None : a[6]);
+}
+
+// latent_decode_attn(q_latent, q_rope, cache, scale, seq_lens, new_lens, out_dtype, out,
+//                    workspace, flags)
+PyObject* latent_decode_attn(PyObject* const* a) {
+  const Latent l = parse_latent(a[2]);
+  const int dev = l.device;
+  if (dev < 0) value_error("latent_decode_attn wants CUDA tensors");
+  const int64_t dc = l.c.latent_dim;
+  const at::Tensor& q0 = tensor(a[0], "q_latent");
+  if (q0.dim() != 4) value_error("q_latent must be [B, T, H, latent]");
+  const int64_t T = q0.size(1), H = q0.size(2);
+  const at::Tensor& ql = shaped(a[0], "q_latent", {l.B, T, H, dc}, l.dtype, dev);
+  const at::Tensor& qr = shaped(a[1], "q_rope", {l.B, T, H, 64}, l.dtype, dev);
+  at::Tensor out;
+  if (is_none(a[7])) {
+    // (rows that no token has are left as they are: here 0)
+    const auto opt = ql.options().dtype(scalar_type(a[6]));
+    out = is_none(a[5]) ? at::empty({l.B, T, H, dc}, opt) : at::zeros({l.B, T, H, dc}, opt);
+  } else {
+    out = tensor(a[7], "out");
+    shaped(a[7], "out", {l.B, T, H, dc}, out.scalar_type(), dev);
+  }
+  dkv_latent_attn p{};
+  p.batch = int32_size(l.B);
+  p.num_heads = int32_size(H);
+  p.new_tokens = int32_size(T);
+  p.flags = static_cast<uint32_t>(integer(a[9]));
+  p.scale = static_cast<float>(number(a[3]));
+  p.out_dtype = dtype_code(out.scalar_type());
+  p.q_latent = ql.data_ptr(), p.q_rope = qr.data_ptr(), p.out = out.data_ptr();
+  p.ql_stride_b = stride_of(ql, 0), p.ql_stride_t = stride_of(ql, 1), p.ql_stride_h = stride_of(ql, 2);
+  p.qr_stride_b = stride_of(qr, 0), p.qr_stride_t = stride_of(qr, 1), p.qr_stride_h = stride_of(qr, 2);
+  p.o_stride_b = stride_of(out, 0), p.o_stride_t = stride_of(out, 1), p.o_stride_h = stride_of(out, 2);
+  p.seq_lens = lengths(a[4], "seq_lens", l.B, dev);
+  p.new_lens = lengths(a[5], "new_lens", l.B, dev);
+  const size_t need = dkv_latent_workspace_bytes(&p, &l.c);
+  const at::Tensor ws = workspace_for(a[8], need, ql);
+  if (cuda_index(ws) != dev) value_error("workspace must be on the cache's device");
+  call("dkv_latent_decode_attn", dev, [&](void* stream) {
+    return dkv_latent_decode_attn(&p, &l.c, ws.data_ptr(), need, stream);
+  });
+  return is_none(a[7]) ? THPVariable_Wrap(out) : incref(a[7]);
+}
+
+// latent_prompt_attn(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, scale, causal, out_dtype,
+//                    out, workspace, flags)
+PyObject* latent_prompt_attn(PyObject* const* a) {
+  const at::Tensor &q0 = tensor(a[0], "q_nope"), &k0 = tensor(a[2], "k_nope");
+  if (q0.dim() != 3 || k0.dim() != 3) value_error("q_nope and k_nope must be [rows, H, nope]");
+  const int dev = cuda_index(q0);
+  if (dev < 0) value_error("latent_prompt_attn wants CUDA tensors");
+  const at::ScalarType dt = q0.scalar_type();
+  const int64_t Tq = q0.size(0), H = q0.size(1), dn = q0.size(2), Tk = k0.size(0);
+  const at::Tensor& qn = shaped(a[0], "q_nope", {Tq, H, dn}, dt, dev);
+  const at::Tensor& qr = shaped(a[1], "q_rope", {Tq, H, 64}, dt, dev);
+  const at::Tensor& kn = shaped(a[2], "k_nope", {Tk, H, dn}, dt, dev);
+  const at::Tensor& kr = shaped(a[3], "k_rope", {Tk, 64}, dt, dev);
+  const at::Tensor& v = shaped(a[4], "v", {Tk, H, dn}, dt, dev);
+  const at::Tensor& cu = tensor(a[5], "cu_q");
+  if (cu.dim() != 1 || cu.size(0) < 2) value_error("cu_q must be int32 [B + 1]");
+  const int64_t n = cu.size(0);
+  dkv_prompt p{};
+  p.cu_q = lengths(a[5], "cu_q", n, dev);
+  p.cu_k = is_none(a[6]) ? p.cu_q : lengths(a[6], "cu_k", n, dev);
+  at::Tensor out;
+  if (is_none(a[10])) {  // (rows outside the sequences are left as they are: here 0)
+    out = at::zeros({Tq, H, dn}, qn.options().dtype(scalar_type(a[9])));
+  } else {
+    out = tensor(a[10], "out");
+    shaped(a[10], "out", {Tq, H, dn}, out.scalar_type(), dev);
+  }
+  p.batch = int32_size(n - 1);
+  p.num_heads = int32_size(H);
+  p.nope_dim = int32_size(dn);
+  p.rope_dim = 64;
+  p.dtype = dtype_code(dt);
+  p.out_dtype = dtype_code(out.scalar_type());
+  const int causal = PyObject_IsTrue(a[8]);
+  if (causal < 0) throw PyError{};
+  p.causal = causal;
+  p.flags = static_cast<uint32_t>(integer(a[12]));
+  p.scale = static_cast<float>(number(a[7]));
+  p.total_q = int32_size(Tq);
+  p.total_k = int32_size(Tk);
+  p.q_nope = qn.data_ptr(), p.q_rope = qr.data_ptr(), p.out = out.data_ptr();
+  p.k_nope = kn.data_ptr(), p.k_rope = kr.data_ptr(), p.v = v.data_ptr();
+  p.qn_stride_t = stride_of(qn, 0), p.qn_stride_h = stride_of(qn, 1);
+  p.qr_stride_t = stride_of(qr, 0), p.qr_stride_h = stride_of(qr, 1);
+  p.kn_stride_t = stride_of(kn, 0), p.kn_stride_h = stride_of(kn, 1);
+  p.v_stride_t = stride_of(v, 0), p.v_stride_h = stride_of(v, 1);
+  p.kr_stride_t = stride_of(kr, 0);
+  p.o_stride_t = stride_of(out, 0), p.o_stride_h = stride_of(out, 1);
+  void* ws = status_word(a[11], dev);
+  if (Tq > 0 && H > 0)
+    call("dkv_latent_prompt_attn", dev,
+         [&](void* stream) { return dkv_latent_prompt_attn(&p, ws, stream); });
+  return is_none(a[10]) ? THPVariable_Wrap(out) : incref(a[10]);
+}
+
+// ------------------------------------------------------------------------- pages
+// Caches whose block table and pools a call changes.
+struct Pages {
+  dkv_pages p{};
+  const at::Tensor* table = nullptr;
+  int device = -1;
+};
+
+void add_pool(Pages* g, const at::Tensor& t) {
+  dkv_pages& p = g->p;
+  if (p.num_pools == DKV_MAX_POOLS) value_error("too many caches");
+  if (p.num_pools == 0) p.num_blocks = int32_size(t.size(0));
+  if (t.size(0) != p.num_blocks) value_error("the caches' pools have different numbers of blocks");
+  int64_t run = 1;  // the elements of a block follow one another
+  for (int64_t i = t.dim() - 1; i > 0; --i) {
+    if (t.stride(i) != run && t.size(i) != 1) value_error("a pool's blocks must be contiguous");
+    run *= t.size(i);
+  }
+  const int64_t size = t.element_size();
+  const int64_t stride = t.size(0) > 1 ? t.stride(0) : run;
+  p.pools[p.num_pools++] = {t.data_ptr(), stride * size, run * size};
+}
+
+Pages parse_pages(PyObject* o, const char* where) {
+  Pages g;
+  if ((!PyTuple_Check(o) && !PyList_Check(o)) || is(o, g_paged) || is(o, g_fp8_paged) ||
+      is(o, g_latent) || PySequence_Fast_GET_SIZE(o) < 1)
+    value_error("caches must be a list of paged caches");
+  for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(o); ++i) {
+    PyObject* c = PySequence_Fast_GET_ITEM(o, i);
+    const bool latent = is(c, g_latent), eight = is(c, g_fp8_paged);
+    const at::Tensor* table;
+    int device;
+    int32_t block = kPage;
+    if (latent) {
+      const Latent l = parse_latent(c);
+      block = l.c.block_size;
+      device = l.device;
+    } else if (eight || is(c, g_paged)) {
+      device = parse_cache(c).device;
+    } else {
+      raise(PyExc_TypeError, "caches must be PagedCache, Fp8PagedCache or LatentCache objects");
+    }
+    if (device < 0) {
+      PyErr_Format(PyExc_ValueError, "%s wants CUDA tensors", where);
+      throw PyError{};
+    }
+    table = &tensor(PyTuple_GET_ITEM(c, eight ? 2 : 1), "block_table");
+    if (i == 0) {
+      g.table = table;
+      g.device = device;
+      g.p.block_size = block;
+    } else if (table->data_ptr() != g.table->data_ptr() || table->sizes() != g.table->sizes() ||
+               table->strides() != g.table->strides() || device != g.device ||
+               block != g.p.block_size) {
+      value_error("the caches must share one block table, block size and device");
+    }
+    add_pool(&g, tensor(PyTuple_GET_ITEM(c, 0), "pool"));
+    if (eight) add_pool(&g, tensor(PyTuple_GET_ITEM(c, 1), "scale"));
+  }
+  g.p.rows = int32_size(g.table->size(0));
+  g.p.cols = int32_size(g.table->size(1));
+  g.p.block_table = static_cast<int32_t*>(g.table->data_ptr());
+  g.p.table_stride = g.table->stride(0);
+  return g;
+}
+
+int32_t* block_ints(PyObject* o, const char* name, const Pages& g) {
+  return const_cast<int32_t*>(lengths(o, name, g.p.num_blocks, g.device));
+}
+
+at::Tensor pages_workspace(PyObject* o, const Pages& g, size_t* need) {
+  *need = dkv_pages_workspace_bytes(g.p.rows, g.p.cols, g.p.num_blocks);
+  if (*need == 0) *need = DKV_WORKSPACE_HEADER_BYTES;  // (the call refuses the sizes)
+  const at::Tensor t = workspace_for(o, *need, *g.table);
+  if (cuda_index(t) != g.device) value_error("workspace must be on the caches' device");
+  return t;
+}
+
+// kv_pages_fork(caches, refs, seq_lens, parents, new_lens, workspace)
+PyObject* kv_pages_fork(PyObject* const* a) {
+  Pages g = parse_pages(a[0], "kv_pages_fork");
+  if (is_none(a[1]) || is_none(a[2])) value_error("refs and seq_lens are needed");
+  g.p.refs = block_ints(a[1], "refs", g);
+  const int32_t* lens = lengths(a[2], "seq_lens", g.p.rows, g.device);
+  const int32_t* parents = lengths(a[3], "parents", g.p.rows, g.device);
+  const int32_t* news = lengths(a[4], "new_lens", g.p.rows, g.device);
+  size_t need;
+  const at::Tensor ws = pages_workspace(a[5], g, &need);
+  call("dkv_kv_pages_fork", g.device, [&](void* stream) {
+    return dkv_kv_pages_fork(&g.p, lens, parents, news, ws.data_ptr(), need, stream);
+  });
+  Py_RETURN_NONE;
+}
+
+// kv_pages_compact(caches, refs, refs_out, block_table_out, workspace)
+PyObject* kv_pages_compact(PyObject* const* a) {
+  Pages g = parse_pages(a[0], "kv_pages_compact");
+  if (is_none(a[1])) value_error("refs are needed");
+  g.p.refs = block_ints(a[1], "refs", g);
+  int32_t* refs_out = is_none(a[2]) ? g.p.refs : block_ints(a[2], "refs_out", g);
+  int32_t* table_out = g.p.block_table;
+  int64_t stride = g.p.table_stride;
+  if (!is_none(a[3])) {
+    const at::Tensor& t = shaped(a[3], "block_table_out", g.table->sizes(), at::kInt, g.device);
+    table_out = static_cast<int32_t*>(t.data_ptr());
+    stride = t.stride(0);
+  }
+  const at::Tensor map = at::empty({g.p.num_blocks}, g.table->options());
+  size_t need;
+  const at::Tensor ws = pages_workspace(a[4], g, &need);
+  call("dkv_kv_pages_compact", g.device, [&](void* stream) {
+    return dkv_kv_pages_compact(&g.p, table_out, stride, refs_out,
+                                static_cast<int32_t*>(map.data_ptr()), ws.data_ptr(), need, stream);
+  });
+  return THPVariable_Wrap(map);
+}
+
 // A call of N positional arguments; C++ exceptions become Python ones.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -626,13 +989,18 @@ PyMethodDef method(const char* name) {
           METH_FASTCALL, nullptr};
 }
 
-PyMethodDef g_methods[] = {method<setup, 6>("setup"),
+PyMethodDef g_methods[] = {method<setup, 7>("setup"),
                            method<describe_cache, 1>("describe_cache"),
                            method<kv_meta_build, 3>("kv_meta_build"),
                            method<kv_meta_append, 6>("kv_meta_append"),
                            method<kv_append, 11>("kv_append"),
                            method<decode_attn_full, 9>("decode_attn_full"),
                            method<decode_attn_select, 16>("decode_attn_select"),
+                           method<latent_append, 12>("latent_append"),
+                           method<latent_decode_attn, 10>("latent_decode_attn"),
+                           method<latent_prompt_attn, 13>("latent_prompt_attn"),
+                           method<kv_pages_fork, 6>("kv_pages_fork"),
+                           method<kv_pages_compact, 5>("kv_pages_compact"),
                            {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods,

@@ -1,0 +1,69 @@
+// latent.h -- arguments of the kernels on latent caches.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace dkv {
+
+constexpr int kLatentRope = 64;        // channels of the rotated key
+constexpr int kMaxLatentBatch = 16384;
+
+// A cache of rows [latent | rotated key], dense or paged.
+struct LatentView {
+  uint16_t* p;
+  int64_t sb, st;     // elements
+  const int32_t* bt;  // paged: block table, row stride bts
+  int64_t bts;
+  int block, nblocks;  // tokens a block (0: dense), blocks of the pool
+  int N;
+};
+
+struct LatentAppendArgs {
+  int B, T, H, rope_len;
+  float eps;
+  const uint16_t *c, *k, *q, *norm;
+  uint16_t* q_out;
+  int64_t c_sb, c_st, k_sb, k_st, q_sb, q_st, q_sh, o_sb, o_st, o_sh;
+  const float *cos, *sin;
+  const int32_t *lens, *news;
+  LatentView cache;
+  uint32_t* status;  // nullptr: errors are not reported
+};
+
+struct LatentAttnArgs {
+  int B, T, H;
+  float scale_log2;  // softmax scale times log2(e)
+  const uint16_t *ql, *qr;
+  int64_t ql_sb, ql_st, ql_sh, qr_sb, qr_st, qr_sh;
+  void* out;
+  int out_dtype;  // 0: bf16, 1: fp16, 2: fp32
+  int64_t o_sb, o_st, o_sh;
+  const int32_t *lens, *news;
+  LatentView cache;
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+
+struct PromptArgs {
+  int B, H;
+  float scale_log2;
+  int causal;
+  const uint16_t *qn, *qr, *kn, *v, *kr;
+  int64_t qn_st, qn_sh, qr_st, qr_sh, kn_st, kn_sh, v_st, v_sh, kr_st;
+  void* out;
+  int out_dtype;
+  int64_t o_st, o_sh;
+  const int32_t *cu_q, *cu_k;
+  int total_q, total_k;
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+
+cudaError_t launch_latent_append(int dc, bool f16, bool interleaved, const LatentAppendArgs& a,
+                                 cudaStream_t s);
+cudaError_t launch_latent_attn(int dc, bool f16, const LatentAttnArgs& a, cudaStream_t s);
+cudaError_t launch_prompt_attn(int dn, bool f16, const PromptArgs& a, cudaStream_t s);
+
+}  // namespace dkv

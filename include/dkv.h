@@ -35,6 +35,17 @@
  *                           steps start from a cache that already holds the
  *                           step's token; this is the call that puts it there.
  *
+ *   dkv_latent_append /     a cache of one latent vector and one rotated key a token,
+ *   dkv_latent_decode_attn  shared by all heads: writing it, and attention of new
+ *                           tokens over it, the latent vectors being keys and
+ *                           values at once (the absorbed form).
+ *   dkv_latent_prompt_attn  attention of prompts with the keys and values expanded
+ *                           a head (the expanded form).
+ *   dkv_kv_pages_fork /     the pages of paged caches: rows of a block table that
+ *   dkv_kv_pages_compact    continue, fork, grow and end; a pool compacted.
+ *                           No page defines these four: they are what a decode
+ *                           loop needs next to the calls above.
+ *
  * Conventions shared by every entry point:
  *   - Every data pointer is a DEVICE pointer owned by the caller, 16-byte
  *     aligned.  The library allocates no device memory and keeps no per-call
@@ -412,6 +423,166 @@ dkv_status dkv_kv_quant4(int64_t rows, int32_t d, const void* x, void* codes, vo
    (always inside [mn, mx]).  Inputs are finite fp16 values. */
 dkv_status dkv_kv_dequant4(int64_t rows, int32_t d, const void* codes, const void* gmin,
                            const void* gmax, void* x, void* stream);
+
+/* ------------------------------------------------------------- latent caches */
+
+/* A cache of one row a token, [latent (dc channels) | rotated key (dr channels)],
+   bf16 or fp16, shared by all heads. */
+typedef struct dkv_latent_cache {
+  int32_t dtype;            /* DKV_BF16 | DKV_FP16 */
+  int32_t latent_dim;       /* dc in {256, 512} */
+  int32_t rope_dim;         /* dr = 64 */
+  int32_t seq_len;          /* N >= 1: tokens the cache holds per sequence */
+  int32_t block_size;       /* 0: dense [B, N, dc + dr]; 16, 32 or 64: a pool
+                               [num_blocks, block_size, dc + dr] */
+  int32_t num_blocks;       /* paged: blocks in the pool */
+  void* data;
+  int64_t stride_b;         /* elements from one sequence (dense) or block to the next */
+  int64_t stride_t;         /* elements from one token to the next, >= dc + dr; both
+                               strides multiples of 8 */
+  const int32_t* block_table;  /* paged: [B, ceil(N / block_size)], as for DKV_KV_PAGED */
+  int64_t block_table_stride;
+} dkv_latent_cache;
+
+/* New tokens for a latent cache.  Sequence b's n_b new tokens take the positions
+   N_b - n_b .. N_b - 1 (as for dkv_kv_append).  A token's row becomes
+     [ c_i rsqrt(mean(c^2) + eps) w_i | rotated k ],
+   fp32, rounded once to the cache's type; without `norm` the latent vector is stored
+   as it is.  Keys and queries are rotated as in dkv_append, over all dr channels. */
+typedef struct dkv_latent_append_args {
+  int32_t batch;            /* B in [1, 65535] */
+  int32_t num_q_heads;      /* H; 0: no queries */
+  int32_t new_tokens;       /* T >= 0 */
+  int32_t rope_len;         /* positions in cos / sin; 0: no rotation */
+  int32_t interleaved;
+  float eps;                /* >= 0 */
+  const void *c, *k, *q;    /* [B, T, dc], [B, T, dr], [B, T, H, dr], the cache's type */
+  void* q_out;              /* [B, T, H, dr]; may be q itself */
+  const void* norm;         /* [dc] weights of the cache's type, or NULL: no norm */
+  int64_t c_stride_b, c_stride_t, k_stride_b, k_stride_t;  /* elements, multiples of 8 */
+  int64_t q_stride_b, q_stride_t, q_stride_h;
+  int64_t o_stride_b, o_stride_t, o_stride_h;
+  const float *cos, *sin;   /* [rope_len, dr / 2] contiguous, 16-byte aligned */
+  const int32_t* seq_lens;  /* DEVICE [B]: N_b (NULL: all N) */
+  const int32_t* new_lens;  /* DEVICE [B]: n_b in [0, T] (NULL: all T) */
+} dkv_latent_append_args;
+
+/* Appends in one launch.  What is not touched, what is refused and what `workspace`
+   (nullable) records are as for dkv_kv_append. */
+dkv_status dkv_latent_append(const dkv_latent_append_args* p, const dkv_latent_cache* cache,
+                             void* workspace, void* stream);
+
+/* Attention of the T newest tokens over a latent cache, per token t and head h:
+     s_j = scale (q_latent . latent_j + q_rope . key_j),  out = softmax(s) latent,
+   over the tokens j < N_b - n_b + t + 1 (a new token sees those up to itself). */
+typedef struct dkv_latent_attn {
+  int32_t batch;            /* B in [1, 16384] */
+  int32_t num_heads;        /* H >= 1 */
+  int32_t new_tokens;       /* T >= 1, T * H < 2^20 */
+  uint32_t flags;           /* 0, or DKV_FLAG_FORCE_TIMEOUT */
+  float scale;
+  int32_t out_dtype;        /* DKV_FP32 | DKV_BF16 | DKV_FP16 */
+  const void *q_latent, *q_rope;  /* [B, T, H, dc], [B, T, H, dr], the cache's type */
+  void* out;                /* [B, T, H, dc] */
+  int64_t ql_stride_b, ql_stride_t, ql_stride_h;  /* elements, multiples of 8 */
+  int64_t qr_stride_b, qr_stride_t, qr_stride_h;
+  int64_t o_stride_b, o_stride_t, o_stride_h;     /* multiples of 16 bytes */
+  const int32_t* seq_lens;  /* DEVICE [B]: N_b, clamped to at most N (NULL: all N) */
+  const int32_t* new_lens;  /* DEVICE [B]: n_b, clamped into [0, T] (NULL: all T) */
+} dkv_latent_attn;
+
+/* Rows t >= n_b are not written.  A row that sees no token (N_b <= 0, or
+   N_b - n_b + t + 1 <= 0) is 0.  What the cache holds past N_b is never used,
+   whatever it is; values of the sequence's own tokens are finite, also those a row
+   does not see yet.  Softmax statistics and sums are fp32; the weights are rounded to
+   the cache's type for the product.  The same call gives the same bits; a row's last
+   bits may depend on the batch it is part of.  workspace:
+   dkv_latent_workspace_bytes(p, cache) bytes. */
+dkv_status dkv_latent_decode_attn(const dkv_latent_attn* p, const dkv_latent_cache* cache,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+size_t dkv_latent_workspace_bytes(const dkv_latent_attn* p, const dkv_latent_cache* cache);
+
+/* Attention with expanded keys and values, over ragged sequences one after another:
+   sequence b has the query rows cu_q[b] .. cu_q[b + 1] - 1 and the key rows cu_k[b] ..
+   cu_k[b + 1] - 1, the queries being its last tokens.  Per head
+     s_j = scale (q_nope . k_nope_j + q_rope . k_rope_j),  out = softmax(s) v,
+   over the sequence's keys j < n_k - n_q + i + 1 for query i (causal), or all. */
+typedef struct dkv_prompt {
+  int32_t batch;            /* B in [1, 16384] */
+  int32_t num_heads;        /* H in [1, 65535] */
+  int32_t nope_dim;         /* dn in {64, 128}: channels of q_nope, k_nope, v and out */
+  int32_t rope_dim;         /* dr = 64 */
+  int32_t dtype, out_dtype; /* of the inputs (DKV_BF16 | DKV_FP16); of out (or DKV_FP32) */
+  int32_t causal;
+  uint32_t flags;           /* 0, or DKV_FLAG_FORCE_TIMEOUT */
+  float scale;
+  int32_t total_q, total_k; /* rows that the tensors hold */
+  const void *q_nope, *q_rope;  /* [total_q, H, dn], [total_q, H, dr] */
+  const void *k_nope, *v;   /* [total_k, H, dn] */
+  const void* k_rope;       /* [total_k, dr] */
+  void* out;                /* [total_q, H, dn] */
+  int64_t qn_stride_t, qn_stride_h, qr_stride_t, qr_stride_h;  /* elements, mult. of 8 */
+  int64_t kn_stride_t, kn_stride_h, v_stride_t, v_stride_h, kr_stride_t;
+  int64_t o_stride_t, o_stride_h;  /* multiples of 16 bytes */
+  const int32_t *cu_q, *cu_k;  /* DEVICE [B + 1], ascending, from >= 0 to <= total */
+} dkv_prompt;
+
+/* Rows of out outside every sequence are not written; a query that sees no key gets 0.
+   Keys and values outside the sequences may be anything; a sequence's own are finite.
+   A sequence whose bounds descend or lie outside its tensor is left alone and recorded
+   in `workspace` (nullable, DKV_WORKSPACE_HEADER_BYTES) as DKV_ERR_DEVICE_CHECK. */
+dkv_status dkv_latent_prompt_attn(const dkv_prompt* p, void* workspace, void* stream);
+
+/* ------------------------------------------------------------------- pages */
+
+#define DKV_MAX_POOLS 16
+/* The tensors of a cache (or of several) that one block table addresses: block n of
+   pool i is the block_bytes bytes at data + n * stride.  block_bytes, stride and data
+   are multiples of 4. */
+typedef struct dkv_pool {
+  void* data;
+  int64_t stride, block_bytes;
+} dkv_pool;
+typedef struct dkv_pages {
+  int32_t rows, cols;       /* of the block table: B in [1, 16384], P >= 1 */
+  int32_t block_size;       /* tokens a block, >= 1 */
+  int32_t num_blocks;       /* of every pool */
+  int32_t num_pools;        /* 0 .. DKV_MAX_POOLS */
+  int32_t* block_table;     /* DEVICE [rows, cols]: a block, or -1 where a row has none */
+  int64_t table_stride;     /* elements from one row to the next */
+  int32_t* refs;            /* DEVICE [num_blocks]: entries that hold a block, and whoever
+                               else does; 0: the block is free */
+  dkv_pool pools[DKV_MAX_POOLS];
+} dkv_pages;
+
+/* One step of a block table, in place: row b becomes the continuation of the first
+   seq_lens[p] tokens of row p = parents[b] (NULL: b itself; -1: of nothing), with pages
+   for new_lens[b] (NULL: 0) further tokens.  All rows are read as they were.
+   - Whole pages are shared with the parent.  A last page that is not whole stays with
+     the lowest row that continues the parent, if no other entry held it before; other
+     rows copy it (every pool's block) into a page of their own.
+   - Pages needed beyond that, and those copied into, are the lowest free blocks (refs 0
+     before the call), given out in order of rows and columns.
+   - Entries past a row's pages become -1.  refs follows: +1 for every entry that a
+     block gains, -1 for each it loses; blocks left at 0 are free for the next call.
+   - An unused row: parents[b] = -1 and new_lens[b] = 0 frees it.
+   All or nothing: with a parent outside [-1, B), a length below 0, or past the table's
+   columns, an entry outside the pool within a continued row's length, or too few free
+   blocks, nothing changes and `workspace` records DKV_ERR_DEVICE_CHECK.
+   workspace: dkv_pages_workspace_bytes bytes. */
+dkv_status dkv_kv_pages_fork(const dkv_pages* p, const int32_t* seq_lens, const int32_t* parents,
+                             const int32_t* new_lens, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Moves the n blocks in use (refs > 0) to the front of their pools: those at n and past
+   it, in ascending order, to the free blocks below n.  block_map [num_blocks] receives
+   every block's new number (-1: it was free); table_out [rows, cols] the table renamed
+   (-1 where an entry is not a block in use), refs_out [num_blocks] the counts.
+   table_out and refs_out may be the table and refs themselves. */
+dkv_status dkv_kv_pages_compact(const dkv_pages* p, int32_t* table_out, int64_t table_out_stride,
+                                int32_t* refs_out, int32_t* block_map, void* workspace,
+                                size_t workspace_bytes, void* stream);
+size_t dkv_pages_workspace_bytes(int32_t rows, int32_t cols, int32_t num_blocks);
 
 /* Exact decode attention with no workspace argument and no allocation.  The
    pages have no counterpart: this serves callers that cannot allocate device
