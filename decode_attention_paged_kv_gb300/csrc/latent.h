@@ -44,7 +44,25 @@ struct LatentAttnArgs {
   LatentView cache;
   uint32_t* status;
   uint64_t wait_limit_ns;
+  bool f16;
+  int groups;     // groups of 8 heads of a new token: rows are padded to whole groups
+  int row_tiles;  // tiles of the rows (new token, head)
+  int splits;     // CTAs that share the tokens of a row tile, at most
+  int q_box;      // rows of a query copy: a tile's, or 8
+  int ctas;
+  int2* pieces;   // [B, row_tiles]: where a sequence's parts lie
+  float* part_ml;  // [splits * row_tiles, 2, rows of a tile, 2]
+  float* part_o;   // [splits * row_tiles, 2, rows of a tile, dc]
 };
+
+// How the rows and the work are cut; the workspace follows from it.
+struct LatentPlan {
+  int tile_rows;  // 16, 32 or 64
+  int groups, row_tiles, splits, ctas;
+  size_t pieces, part_ml, part_o, total;  // workspace offsets
+};
+constexpr int kLatentTile = 64;  // tokens
+constexpr int kLatentCtas = 152;
 
 struct PromptArgs {
   int B, H;
@@ -63,7 +81,12 @@ struct PromptArgs {
 
 cudaError_t launch_latent_append(int dc, bool f16, bool interleaved, const LatentAppendArgs& a,
                                  cudaStream_t s);
-cudaError_t launch_latent_attn(int dc, bool f16, const LatentAttnArgs& a, cudaStream_t s);
+// mql / mqr: maps over q_latent and q_rope {channels, H, T, B}, box {64, q_box, 1, 1}; mc: map
+// over the cache {64 channels, tokens, chunks, sequences or blocks}, box one tile of 64
+// tokens (dense, or blocks of 64), or one chunk of a block; all with a 128-byte swizzle.
+cudaError_t launch_latent_attn(int dc, int tile_rows, const LatentAttnArgs& a,
+                               const CUtensorMap& mql, const CUtensorMap& mqr,
+                               const CUtensorMap& mc, cudaStream_t s);
 cudaError_t launch_prompt_attn(int dn, bool f16, const PromptArgs& a, cudaStream_t s);
 
 }  // namespace dkv

@@ -80,6 +80,51 @@ dkv_status check_out_strides(int32_t dtype, std::initializer_list<int64_t> strid
   return DKV_OK;
 }
 
+// Rows of queries are padded to groups of 8 heads of one new token; a tile of 16, 32 or
+// 64 rows is the smallest that holds them all, else 64.  The tokens are shared by as many
+// CTAs as keep every multiprocessor busy once, for all row tiles together.
+dkv::LatentPlan latent_plan(const dkv_latent_attn* p, const dkv_latent_cache* c) {
+  dkv::LatentPlan L{};
+  L.groups = static_cast<int>(ceil_div(p->num_heads, 8));
+  const int64_t rows = 8ll * L.groups * p->new_tokens;
+  L.tile_rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+  L.row_tiles = static_cast<int>(ceil_div(rows, L.tile_rows));
+  const int64_t tiles = p->batch * ceil_div(c->seq_len, dkv::kLatentTile);
+  const int64_t fit = dkv::kLatentCtas / L.row_tiles;
+  const int64_t splits = tiles < fit ? tiles : fit;
+  L.splits = static_cast<int>(splits < 1 ? 1 : splits);
+  L.ctas = L.splits * L.row_tiles;
+  const size_t slots = L.splits > 1 ? 2 * static_cast<size_t>(L.ctas) * L.tile_rows : 0;
+  L.pieces = DKV_WORKSPACE_HEADER_BYTES;
+  L.part_ml = align_up(L.pieces + 8 * static_cast<size_t>(p->batch) * L.row_tiles);
+  L.part_o = align_up(L.part_ml + 8 * slots);
+  L.total = align_up(L.part_o + 4 * slots * c->latent_dim);
+  return L;
+}
+
+CUtensorMapDataType map_type(int32_t dtype) {
+  return dtype == DKV_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+// A 4-D map of 16-bit elements with a 128-byte swizzle; strides in elements.  (The stride
+// of a dimension of size 1 still has to be a valid, 16-byte multiple.)
+bool encode_4d(CUtensorMap* map, int32_t dtype, const void* data, const int64_t (&size)[4],
+               const int64_t (&stride)[3], const int (&box)[4]) {
+  if (!get_encode()) return false;
+  cuuint64_t dims[4], st[3];
+  cuuint32_t b[4];
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
+    dims[i] = static_cast<cuuint64_t>(size[i]);
+    b[i] = static_cast<cuuint32_t>(box[i]);
+    if (i > 0) st[i - 1] = size[i] == 1 && stride[i - 1] == 0 ? 16 : 2 * stride[i - 1];
+  }
+  return g_encode(map, map_type(dtype), 4, const_cast<void*>(data), dims, st, b, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool out_dtype_ok(int32_t t) { return t == DKV_FP32 || t == DKV_BF16 || t == DKV_FP16; }
 
 dkv_status check_attn(const dkv_latent_attn* p, const dkv_latent_cache* cache) {
@@ -170,7 +215,7 @@ size_t dkv_latent_workspace_bytes(const dkv_latent_attn* p, const dkv_latent_cac
       static_cast<int64_t>(p->new_tokens) * p->num_heads >= (1 << 20) ||
       (cache->latent_dim != 256 && cache->latent_dim != 512))
     return 0;
-  return DKV_WORKSPACE_HEADER_BYTES;
+  return latent_plan(p, cache).total;
 }
 
 dkv_status dkv_latent_decode_attn(const dkv_latent_attn* p, const dkv_latent_cache* cache,
@@ -211,7 +256,37 @@ dkv_status dkv_latent_decode_attn(const dkv_latent_attn* p, const dkv_latent_cac
   a.cache = view(cache);
   a.status = static_cast<uint32_t*>(workspace);
   a.wait_limit_ns = (p->flags & DKV_FLAG_FORCE_TIMEOUT) ? 0 : kWaitLimitNs;
-  return cuda_status(dkv::launch_latent_attn(cache->latent_dim, cache->dtype == DKV_FP16, a,
+  a.f16 = cache->dtype == DKV_FP16;
+  const dkv::LatentPlan L = latent_plan(p, cache);
+  char* ws = static_cast<char*>(workspace);
+  a.groups = L.groups;
+  a.row_tiles = L.row_tiles;
+  a.splits = L.splits;
+  a.ctas = L.ctas;
+  a.pieces = reinterpret_cast<int2*>(ws + L.pieces);
+  a.part_ml = reinterpret_cast<float*>(ws + L.part_ml);
+  a.part_o = reinterpret_cast<float*>(ws + L.part_o);
+  if (static_cast<int64_t>(p->batch) * L.row_tiles > kInt32Max) return DKV_ERR_UNSUPPORTED;
+  // a query copy takes a tile's rows where they are heads of one new token
+  a.q_box = p->new_tokens == 1 || 8 * L.groups % L.tile_rows == 0 ? L.tile_rows : 8;
+  const int dc = cache->latent_dim;
+  CUtensorMap mql, mqr, mc;
+  const int64_t H = p->num_heads, T = p->new_tokens, B = p->batch;
+  const int chunks = dc / 64 + 1;
+  const bool paged = cache->block_size > 0;
+  const int tokens = paged && cache->block_size < dkv::kLatentTile ? cache->block_size
+                                                                   : dkv::kLatentTile;
+  if (!encode_4d(&mql, cache->dtype, p->q_latent, {dc, H, T, B},
+                 {p->ql_stride_h, p->ql_stride_t, p->ql_stride_b}, {64, a.q_box, 1, 1}) ||
+      !encode_4d(&mqr, cache->dtype, p->q_rope, {dkv::kLatentRope, H, T, B},
+                 {p->qr_stride_h, p->qr_stride_t, p->qr_stride_b}, {64, a.q_box, 1, 1}) ||
+      !encode_4d(&mc, cache->dtype, cache->data,
+                 {64, paged ? cache->block_size : cache->seq_len, chunks,
+                  paged ? cache->num_blocks : B},
+                 {cache->stride_t, 64, cache->stride_b},
+                 {64, tokens, tokens == dkv::kLatentTile ? chunks : 1, 1}))
+    return DKV_ERR_CUDA;
+  return cuda_status(dkv::launch_latent_attn(dc, L.tile_rows, a, mql, mqr, mc,
                                              static_cast<cudaStream_t>(stream)));
 }
 

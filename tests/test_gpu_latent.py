@@ -283,6 +283,20 @@ def test_decode_captured_with_new_lengths(dkv):
     assert dkv.read_device_status(ws) == 0
 
 
+def test_decode_timeout(dkv):
+    # every bounded wait gives up at once: the status says so, and the next call is right
+    gen = gen_of("timeout")
+    cache, ql, qr, out = decode_case(2, 1, 16, 512, 900, 16, torch.bfloat16, gen, [900, 300], [1, 1])
+    ws = torch.zeros(dkv.latent_workspace_bytes(2, 1, 16, 512, 900), dtype=torch.uint8,
+                     device="cuda")
+    dkv.latent_decode_attn(ql, qr, cache, 0.07, seq_lens=ints([900, 300]), out=out, workspace=ws,
+                           flags=dkv.DKV_FLAG_FORCE_TIMEOUT)
+    assert dkv.read_device_status(ws) == dkv.DKV_ERR_DEVICE_TIMEOUT
+    dkv.latent_decode_attn(ql, qr, cache, 0.07, seq_lens=ints([900, 300]), out=out, workspace=ws)
+    assert dkv.read_device_status(ws) == 0
+    check_decode(cache, ql, qr, out, [900, 300], [1, 1], 0.07)
+
+
 def test_decode_two_streams(dkv):
     gen = gen_of("streams")
     cases = []
