@@ -134,7 +134,12 @@ dkv_status check_attn(const dkv_latent_attn* p, const dkv_latent_cache* cache) {
       static_cast<int64_t>(p->new_tokens) * p->num_heads >= (1 << 20))
     return DKV_ERR_UNSUPPORTED;
   if (!(fabsf(p->scale) < INFINITY)) return DKV_ERR_SHAPE;
-  return check_cache(cache, p->batch);
+  const dkv_status st = check_cache(cache, p->batch);
+  if (st != DKV_OK) return st;
+  // tiles are counted in 32 bits
+  if (p->batch * ceil_div(cache->seq_len, dkv::kLatentTile) > kInt32Max)
+    return DKV_ERR_UNSUPPORTED;
+  return DKV_OK;
 }
 
 }  // namespace

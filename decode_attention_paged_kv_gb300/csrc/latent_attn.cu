@@ -31,7 +31,10 @@
 namespace dkv {
 namespace {
 
-constexpr int kThreads = 256;  // warps: copies, products, two idle, four of softmax
+constexpr int kWarpsSoftmax = 8, kFirstSoftmax = 4;  // warps 4 .. 11
+constexpr int kThreads = 32 * (kFirstSoftmax + kWarpsSoftmax);
+constexpr int kSoftmaxThreads = 32 * kWarpsSoftmax;
+constexpr int kCopyWarps = 3;  // warps 0, 2 and 3 (1: products)
 constexpr int kTile = kLatentTile;
 constexpr int kStages = 2;
 constexpr int kChunkBytes = kTile * 128;  // 64 tokens x 64 channels
@@ -54,10 +57,12 @@ struct Shared {
       drain;
   uint32_t tmem;
   volatile int abort;
-  int seq0, off0;  // where the CTA's share begins
-  volatile uint32_t vote[2][4];
-  float factor[2][64];
-  float stat_m[64], stat_l[64];
+  volatile int failed[2];  // a softmax warp's wait expired, by turns
+  int seq0, off0;          // where the CTA's share begins
+  float top[2][2][64];     // a tile's maxima, of its two halves, by turns
+  float ref[2][64];        // the references before the tile, by turns
+  float factor[64];
+  float stat_l[2][64];
   int64_t row_at[64];  // of the output, -1: not written
 };
 
@@ -188,49 +193,71 @@ __device__ __forceinline__ Row row_of(const LatentAttnArgs& a, int rt, int r) {
   return {g / a.groups, (g % a.groups) * 8 + r % 8};
 }
 
+// Copies tiles of the cache, `part` of the copying warps; the first one queries too.
 template <int MB, int RT>
 __device__ __forceinline__ void copy_loop(const LatentAttnArgs& a, const CUtensorMap* mql,
                                           const CUtensorMap* mqr, const CUtensorMap* mc,
-                                          const Share& w, int rt, int first_t, Shared& sh,
-                                          uint32_t q_smem, uint32_t k_smem) {
+                                          const Share& w, int rt, int first_t, int part,
+                                          Shared& sh, uint32_t q_smem, uint32_t k_smem) {
   using S = Shape<MB, RT>;
-  const int lane = threadIdx.x % 32;
+  constexpr int kPer = (S::kChunks + kCopyWarps - 1) / kCopyWarps;  // chunks of a warp
   const LatentView& c = a.cache;
+  const bool pieces = c.block > 0 && c.block < kTile;  // a copy a chunk of a block
+  const int c0 = part * kPer, c1 = min(c0 + kPer, S::kChunks);
   int i = 0, segs = 0;
   bool ok = true;
   for (Walk k(a, w, first_t); ok && k.next();) {
-    for (int t = 0; ok && t < k.tiles; ++t, ++i) {
+    const int b = uniform(k.b), len = uniform(k.seq.len), tile0 = uniform(k.tile0);
+    const int tiles = uniform(k.tiles);
+    for (int t = 0; t < tiles; ++t, ++i) {
       const int s = i % kStages;
-      const int j0 = (k.tile0 + t) * kTile;
+      const int j0 = (tile0 + t) * kTile;
       if (i >= kStages &&
           !warp_wait(smem_u32(&sh.empty[s]), ((i / kStages) & 1) ^ 1, a.wait_limit_ns, &sh.abort)) {
         ok = false;
         break;
       }
       const uint32_t bar = smem_u32(&sh.full[s]), dst = k_smem + s * S::kStageBytes;
-      if (c.block == 0) {
-        if (lane == 0) {
+      if (!pieces) {
+        int blk = b, row = j0;
+        if (c.block > 0) {
+          blk = c.bt[b * c.bts + (tile0 + t)];
+          if (blk < 0 || blk >= c.nblocks) {
+            set_status(a.status, kStatusCheck);
+            blk = min(max(blk, 0), c.nblocks - 1);
+          }
+          blk = uniform(blk);
+          row = 0;
+        }
+        if (elect_one()) {
           mbar_arrive_expect_tx(bar, S::kStageBytes);
-          tma_load_4d(dst, mc, bar, 0, j0, 0, k.b);
+          tma_load_4d(dst, mc, bar, 0, row, 0, blk);
         }
       } else {
         // pages that hold tokens of the sequence
-        const int pages = min(kTile / c.block, (k.seq.len - j0 + c.block - 1) / c.block);
-        const int32_t* bt = c.bt + k.b * c.bts + j0 / c.block;
-        if (lane == 0) mbar_arrive_expect_tx(bar, pages * c.block * S::kChunks * 128);
+        const int pages = min(kTile / c.block, (len - j0 + c.block - 1) / c.block);
+        const int32_t* bt = c.bt + b * c.bts + j0 / c.block;
+        if (elect_one()) mbar_arrive_expect_tx(bar, pages * c.block * (c1 - c0) * 128);
         __syncwarp();
-        const int copies = c.block == kTile ? pages : pages * S::kChunks;
-        for (int x = lane; x < copies; x += 32) {
-          const int p = x % pages, chunk = x / pages;
+        for (int p = 0; p < pages; ++p) {
           int blk = bt[p];
           if (blk < 0 || blk >= c.nblocks) {
             set_status(a.status, kStatusCheck);
             blk = min(max(blk, 0), c.nblocks - 1);
           }
-          tma_load_4d(dst + chunk * kChunkBytes + p * c.block * 128, mc, bar, 0, 0, chunk, blk);
+          blk = uniform(blk);
+          if (elect_one()) {
+#pragma unroll
+            for (int x = 0; x < kPer; ++x)
+              if (c0 + x < c1)
+                tma_load_4d(dst + (c0 + x) * kChunkBytes + p * c.block * 128, mc, bar, 0, 0, c0 + x,
+                            blk);
+          }
+          __syncwarp();
         }
       }
-      if (t == 0) {  // the segment's queries
+      __syncwarp();
+      if (t == 0 && part == 0) {  // the segment's queries
         if (segs > 0 &&
             !warp_wait(smem_u32(&sh.q_free), (segs - 1) & 1, a.wait_limit_ns, &sh.abort)) {
           ++i;
@@ -238,18 +265,18 @@ __device__ __forceinline__ void copy_loop(const LatentAttnArgs& a, const CUtenso
           break;
         }
         const uint32_t qbar = smem_u32(&sh.q_full);
-        if (lane == 0) mbar_arrive_expect_tx(qbar, S::kQBytes);
+        if (elect_one()) mbar_arrive_expect_tx(qbar, S::kQBytes);
         __syncwarp();
-        const int per = RT / a.q_box;
-        for (int x = lane; x < per * S::kChunks; x += 32) {
-          const int chunk = x / per, r = x % per * a.q_box;
+        for (int r = 0; r < RT; r += a.q_box) {
           const Row at = row_of<RT>(a, rt, r);
-          const uint32_t qd = q_smem + chunk * (RT * 128) + r * 128;
-          // (rows past the last head or token are filled with zeros)
-          if (chunk < 2 * MB)
-            tma_load_4d(qd, mql, qbar, chunk * 64, at.h, at.t, k.b);
-          else
-            tma_load_4d(qd, mqr, qbar, 0, at.h, at.t, k.b);
+          if (elect_one()) {
+            // (rows past the last head or token are filled with zeros)
+#pragma unroll
+            for (int x = 0; x < 2 * MB; ++x)
+              tma_load_4d(q_smem + x * (RT * 128) + r * 128, mql, qbar, x * 64, at.h, at.t, b);
+            tma_load_4d(q_smem + 2 * MB * (RT * 128) + r * 128, mqr, qbar, 0, at.h, at.t, b);
+          }
+          __syncwarp();
         }
         ++segs;
       }
@@ -259,8 +286,9 @@ __device__ __forceinline__ void copy_loop(const LatentAttnArgs& a, const CUtenso
     sh.abort = 1;
     set_status(a.status, kStatusTimeout);
   }
-  // nothing is in flight when the CTA ends
-  if (lane == 0) {
+  // nothing is in flight when the CTA ends (a barrier that a part of the warps has filled
+  // only does not complete: the copies are waited for by the time they can take)
+  if (threadIdx.x % 32 == 0) {
     for (int x = max(0, i - kStages); x < i; ++x)
       mbar_wait_bounded(smem_u32(&sh.full[x % kStages]), (x / kStages) & 1, kDrainNs, nullptr);
     if (segs > 0) mbar_wait_bounded(smem_u32(&sh.q_full), (segs - 1) & 1, kDrainNs, nullptr);
@@ -275,14 +303,9 @@ struct Issuer {
   Shared& sh;
   uint32_t q_smem, k_smem, tmem;
   // O^T (+)= V^T P^T of tile i.
-  __device__ __forceinline__ bool values(int i, bool first, int seg) {
-    if (!warp_wait(smem_u32(&sh.p_ready[i & 1]), (i >> 1) & 1, a.wait_limit_ns, &sh.abort))
-      return false;
-    if (first && seg > 0 &&
-        !warp_wait(smem_u32(&sh.o_free), (seg - 1) & 1, a.wait_limit_ns, &sh.abort))
-      return false;
+  __device__ __forceinline__ void values(int i, bool first) {
     tc_fence_after();
-    if (threadIdx.x % 32 == 0) {
+    if (elect_one()) {
       const uint32_t k = k_smem + (i % kStages) * S::kStageBytes;
       const uint32_t p = k + 2 * MB * kChunkBytes;
       const uint32_t desc = mma_desc(a.f16, 128, RT, true, false);
@@ -291,17 +314,16 @@ struct Issuer {
 #pragma unroll
         for (int t = 0; t < kTile / 16; ++t)
           tc_mma(tmem + 128 + m * RT, smem_desc(k + 2 * m * kChunkBytes + t * 2048, kChunkBytes, 1024),
-                 smem_desc(p + t * 32, 16, 1024), desc, !(first && t == 0));
+                 smem_desc(p + t * 32, 16, 1024), desc, t > 0 || !first);
       tc_commit(smem_u32(&sh.o_done[i & 1]));
       tc_commit(smem_u32(&sh.empty[i % kStages]));
     }
     __syncwarp();
-    return true;
   }
   // S = Q K^T of tile i.
   __device__ __forceinline__ void scores(int i, bool last) {
     tc_fence_after();
-    if (threadIdx.x % 32 == 0) {
+    if (elect_one()) {
       const uint32_t k = k_smem + (i % kStages) * S::kStageBytes;
       const uint32_t desc = mma_desc(a.f16, 64, kTile, false, false);
 #pragma unroll
@@ -317,58 +339,88 @@ struct Issuer {
   }
 };
 
+// Issues a tile's scores when it has arrived, its values when its weights are there,
+// whichever comes first: waiting for the next tile while weights are ready would keep the
+// tile that they belong to from being replaced.
 template <int MB, int RT>
 __device__ __forceinline__ void product_loop(const LatentAttnArgs& a, const Share& w, int first_t,
                                              Shared& sh, uint32_t q_smem, uint32_t k_smem) {
   using S = Shape<MB, RT>;
   const int lane = threadIdx.x % 32;
-  Issuer<MB, RT> run{a, sh, q_smem, k_smem, sh.tmem};
-  int i = 0, prev_seg = 0;
-  bool ok = true, prev_first = false;
-  for (Walk k(a, w, first_t); ok && k.next();) {
-    if (!warp_wait(smem_u32(&sh.q_full), k.index & 1, a.wait_limit_ns, &sh.abort)) {
+  Issuer<MB, RT> run{a, sh, q_smem, k_smem, static_cast<uint32_t>(uniform(sh.tmem))};
+  const int n = uniform(static_cast<int>(w.end - w.begin));
+  int ns = 0, nv = 0;  // tiles whose scores, whose values have been issued
+  // the segment of the next scores, and what values have to know of theirs
+  Walk k(a, w, first_t);
+  int at = 0, tiles = 0, tile0 = 0, len = 0, seg = -1, value_seg = -1;
+  uint32_t begins = 0;  // bit i % 4: tile i begins a segment
+  uint64_t since = 0;
+  bool ok = true;
+  while (nv < n) {
+    bool moved = false;
+    if (nv < ns && warp_test(smem_u32(&sh.p_ready[nv & 1]), (nv >> 1) & 1)) {
+      const bool first = begins >> (nv & 3) & 1;
+      if (!first || value_seg < 0 || warp_test(smem_u32(&sh.o_free), value_seg & 1)) {
+        run.values(nv, first);
+        value_seg += first;
+        ++nv;
+        moved = true;
+      }
+    }
+    if (ns < n && ns - nv < 2) {
+      if (at == tiles) {  // a new segment
+        k.next();
+        at = 0;
+        tiles = uniform(k.tiles);
+        tile0 = uniform(k.tile0);
+        len = uniform(k.seq.len);
+        ++seg;
+      }
+      const int s = ns % kStages;
+      if (warp_test(smem_u32(&sh.full[s]), (ns / kStages) & 1) &&
+          (at > 0 || warp_test(smem_u32(&sh.q_full), seg & 1))) {
+        // rows past the sequence may hold anything: as values they must be 0 (a weight of
+        // 0 times NaN is NaN); their scores are masked
+        const int valid = len - (tile0 + at) * kTile;
+        if (valid < kTile) {
+          const uint32_t to = k_smem + s * S::kStageBytes;
+          const int words = (kTile - valid) * 8;
+          for (int x = lane; x < 2 * MB * words; x += 32)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             to + x / words * kChunkBytes + valid * 128 + x % words * 16),
+                         "r"(0)
+                         : "memory");
+          fence_async_smem();
+          __syncwarp();
+        }
+        begins = (begins & ~(1u << (ns & 3))) | static_cast<uint32_t>(at == 0) << (ns & 3);
+        ++at;
+        run.scores(ns, at == tiles);
+        ++ns;
+        moved = true;
+      }
+    }
+    if (moved) {
+      since = 0;
+      continue;
+    }
+    // nothing to do: give up after the limit
+    const uint64_t now = globaltimer_ns();
+    if (since == 0) since = now;
+    const bool over = now - since > a.wait_limit_ns || a.wait_limit_ns == 0 || sh.abort != 0;
+    if (__any_sync(0xffffffffu, over)) {
       ok = false;
       break;
     }
-    for (int t = 0; t < k.tiles; ++t, ++i) {
-      const int s = i % kStages;
-      if (!warp_wait(smem_u32(&sh.full[s]), (i / kStages) & 1, a.wait_limit_ns, &sh.abort)) {
-        ok = false;
-        break;
-      }
-      // rows past the sequence may hold anything: as values they must be 0 (a weight of
-      // 0 times NaN is NaN); their scores are masked
-      const int valid = k.seq.len - (k.tile0 + t) * kTile;
-      if (valid < kTile) {
-        const uint32_t at = k_smem + s * S::kStageBytes;
-        const int words = (kTile - valid) * 8;
-        for (int x = lane; x < 2 * MB * words; x += 32)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                           at + x / words * kChunkBytes + valid * 128 + x % words * 16),
-                       "r"(0)
-                       : "memory");
-        fence_async_smem();
-        __syncwarp();
-      }
-      run.scores(i, t == k.tiles - 1);
-      if (i > 0 && !run.values(i - 1, prev_first, prev_seg)) {
-        ok = false;
-        break;
-      }
-      prev_first = t == 0;
-      prev_seg = k.index;
-    }
   }
-  if (ok && i > 0) ok = run.values(i - 1, prev_first, prev_seg);
   if (!ok) {
     sh.abort = 1;
     set_status(a.status, kStatusTimeout);
   }
   // nothing is in flight when the tensor memory is freed
-  if (lane == 0) {
-    tc_commit(smem_u32(&sh.drain));
-    mbar_wait_bounded(smem_u32(&sh.drain), 0, kDrainNs, nullptr);
-  }
+  if (elect_one()) tc_commit(smem_u32(&sh.drain));
+  __syncwarp();
+  if (lane == 0) mbar_wait_bounded(smem_u32(&sh.drain), 0, kDrainNs, nullptr);
   __syncwarp();
 }
 
@@ -376,7 +428,8 @@ template <int MB, int RT>
 __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Share& w, int rt,
                                              int first_t, Shared& sh, uint32_t k_smem) {
   using S = Shape<MB, RT>;
-  const int lane = threadIdx.x % 32, quarter = threadIdx.x / 32 - 4;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - kFirstSoftmax;
+  const int quarter = warp % 4, half = warp / 4;  // rows, and tokens of a tile
   // a product with M = 64 leaves rows 16 q .. 16 q + 15 in lanes 32 q .. 32 q + 15
   const int r = 16 * quarter + lane;
   const bool mine = lane < 16 && r < RT;
@@ -394,77 +447,84 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
                                 &sh.abort);
       __syncwarp();
       tc_fence_after();
-      const int limit = seen - (k.tile0 + t) * kTile;
-      bool rise = false;
-      float f = 1.f;
+      const int limit = seen - (k.tile0 + t) * kTile - 32 * half;
+      float s[32];
       if (quarter_on) {
-        float s[64];
-        tmem_ld32(tq + (i & 1) * 64, reinterpret_cast<float(&)[32]>(s[0]));
-        tmem_ld32(tq + (i & 1) * 64 + 32, reinterpret_cast<float(&)[32]>(s[32]));
+        tmem_ld32(tq + (i & 1) * 64 + 32 * half, s);
         tmem_wait_ld();
-        float top = -INFINITY;
-        if (limit >= kTile) {
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (__all_sync(0xffffffffu, limit >= 32)) {
 #pragma unroll
-          for (int x = 0; x < 64; ++x) {
-            s[x] *= a.scale_log2;
-            top = fmaxf(top, s[x]);
-          }
+          for (int x = 0; x < 32; ++x) s[x] *= a.scale_log2;
         } else {
 #pragma unroll
-          for (int x = 0; x < 64; ++x) {
-            s[x] = x < limit ? s[x] * a.scale_log2 : -INFINITY;
-            top = fmaxf(top, s[x]);
-          }
+          for (int x = 0; x < 32; ++x) s[x] = x < limit ? s[x] * a.scale_log2 : -INFINITY;
         }
-        if (t == 0) {
-          m = top;
-        } else if (top > m + kRise) {
-          rise = true;
-          f = ex2(m - top);
-          l *= f;
-          m = top;
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
-        const uint32_t p = k_smem + (i % kStages) * S::kStageBytes + 2 * MB * kChunkBytes + r * 128;
 #pragma unroll
-        for (int x = 0; x < 64; x += 8) {
-          uint32_t v[4];
-#pragma unroll
-          for (int y = 0; y < 8; y += 2) {
-            const float p0 = ex2(s[x + y] - ref), p1 = ex2(s[x + y + 1] - ref);
-            l += p0 + p1;
-            v[y / 2] = a.f16 ? pack2<true>(p0, p1) : pack2<false>(p0, p1);
-          }
-          if (mine)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             p + (((x / 8) ^ (r & 7)) << 4)),
-                         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                         : "memory");
+        for (int x = 0; x < 32; ++x) top[x % 4] = fmaxf(top[x % 4], s[x]);
+        if (mine) {
+          sh.top[i & 1][half][r] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          if (half == 0) sh.ref[i & 1][r] = m;
         }
-        if (mine) sh.factor[i & 1][r] = f;
       }
-      const uint32_t vote = __any_sync(0xffffffffu, mine && rise) | __any_sync(0xffffffffu, bad) << 1;
-      if (lane == 0) sh.vote[i & 1][quarter] = vote;
-      named_barrier(1, 128);
-      const uint32_t all = sh.vote[i & 1][0] | sh.vote[i & 1][1] | sh.vote[i & 1][2] |
-                           sh.vote[i & 1][3];
-      if (all & 2) {  // (every thread of the four warps leaves here)
+      if (bad) sh.failed[i & 1] = 1;
+      named_barrier(1, kSoftmaxThreads);
+      if (sh.failed[i & 1]) {  // (every thread of these warps leaves here)
         sh.abort = 1;
         set_status(a.status, kStatusTimeout);
         return;
       }
-      if ((all & 1) && t > 0) {
+      // whether any row's maximum rises past its reference (rows lane and lane + 32)
+      bool rise = false;
+      if (t > 0) {
+        for (int x = lane; x < RT; x += 32)
+          rise |= fmaxf(sh.top[i & 1][0][x], sh.top[i & 1][1][x]) > sh.ref[i & 1][x] + kRise;
+        rise = __any_sync(0xffffffffu, rise);
+      }
+      if (quarter_on) {
+        const float top = mine ? fmaxf(sh.top[i & 1][0][r], sh.top[i & 1][1][r]) : 0.f;
+        float f = 1.f;
+        if (t == 0) {
+          m = top;
+        } else if (top > m + kRise) {
+          f = ex2(m - top);
+          l *= f;
+          m = top;
+        }
+        if (rise && mine && half == 0) sh.factor[r] = f;
+        const float ref = m == -INFINITY ? 0.f : m;
+        const uint32_t p = k_smem + (i % kStages) * S::kStageBytes + 2 * MB * kChunkBytes + r * 128;
+        float sum[4] = {};
+#pragma unroll
+        for (int x = 0; x < 32; x += 8) {
+          uint32_t v[4];
+#pragma unroll
+          for (int y = 0; y < 8; y += 2) {
+            const float p0 = ex2(s[x + y] - ref), p1 = ex2(s[x + y + 1] - ref);
+            sum[y / 2] += p0 + p1;
+            v[y / 2] = a.f16 ? pack2<true>(p0, p1) : pack2<false>(p0, p1);
+          }
+          if (mine)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             p + (((x / 8 + 4 * half) ^ (r & 7)) << 4)),
+                         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                         : "memory");
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      }
+      if (rise) {
+        named_barrier(1, kSoftmaxThreads);  // the factors are there
         bad |= !mbar_wait_bounded(smem_u32(&sh.o_done[(i - 1) & 1]), ((i - 1) >> 1) & 1,
                                   a.wait_limit_ns, &sh.abort);
         __syncwarp();
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < MB * RT; c += 16) {
+        for (int c = half * (MB * RT / 2); c < (half + 1) * (MB * RT / 2); c += 16) {
           float o[16];
           tmem_ld16(tq + 128 + c, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 16; ++x) o[x] *= sh.factor[i & 1][c % RT + x];
+          for (int x = 0; x < 16; ++x) o[x] *= sh.factor[c % RT + x];
           tmem_st16(tq + 128 + c, o);
         }
         tmem_wait_st();
@@ -475,26 +535,25 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
     }
     // the segment's output
     if (mine) {
-      sh.stat_m[r] = m;
-      sh.stat_l[r] = l;
-      sh.row_at[r] = on ? k.b * a.o_sb + at.t * a.o_st + at.h * a.o_sh : -1;
+      sh.stat_l[half][r] = l;
+      if (half == 0) sh.row_at[r] = on ? k.b * a.o_sb + at.t * a.o_st + at.h * a.o_sh : -1;
     }
     // (two barriers by turns: the products of the last two tiles may both be under way,
     // and a parity tells neighbouring phases apart only)
     bad |= !mbar_wait_bounded(smem_u32(&sh.o_done[(i - 1) & 1]), ((i - 1) >> 1) & 1,
                               a.wait_limit_ns, &sh.abort);
-    named_barrier(1, 128);
+    named_barrier(1, kSoftmaxThreads);
     tc_fence_after();
     const int channel = 32 * quarter + lane;
     const int64_t slot = 2 * static_cast<int64_t>(w.split * a.row_tiles + rt) + (k.index > 0);
     const bool whole = k.whole();
-    if (!whole && mine) {
+    if (!whole && mine && half == 0) {
       float* ml = a.part_ml + (slot * RT + r) * 2;
       ml[0] = m;
-      ml[1] = l;
+      ml[1] = l + sh.stat_l[1][r];
     }
 #pragma unroll 1
-    for (int c = 0; c < MB * RT; c += 16) {
+    for (int c = half * (MB * RT / 2); c < (half + 1) * (MB * RT / 2); c += 16) {
       float o[16];
       tmem_ld16(tq + 128 + c, o);
       tmem_wait_ld();
@@ -503,7 +562,7 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
       for (int x = 0; x < 16; ++x) {
         const int row = c % RT + x;
         if (whole) {
-          const float sum = sh.stat_l[row];
+          const float sum = sh.stat_l[0][row] + sh.stat_l[1][row];
           if (sh.row_at[row] >= 0)
             store_out(a.out, a.out_dtype, sh.row_at[row] + ch, sum > 0.f ? o[x] / sum : 0.f);
         } else {
@@ -513,7 +572,7 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
     }
     tc_fence_before();
     mbar_arrive(smem_u32(&sh.o_free));
-    if (threadIdx.x == 128 && k.tile0 + k.tiles == k.seq.tiles) {
+    if (threadIdx.x == 32 * kFirstSoftmax && k.tile0 + k.tiles == k.seq.tiles) {
       // the sequence ends here: which shares hold its parts
       const int64_t p0 = k.at - k.tile0;  // its first tile
       const int first = static_cast<int>(((p0 + 1) * w.splits + w.total - 1) / w.total) - 1;
@@ -544,20 +603,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), S::kColumns);
   if (threadIdx.x == 0) {
     prefetch_tensormap(&mql), prefetch_tensormap(&mqr), prefetch_tensormap(&mc);
+    const int copy_warps = a.cache.block > 0 && a.cache.block < kTile ? kCopyWarps : 1;
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.full[i]), copy_warps);
       mbar_init(smem_u32(&sh.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.p_ready[i]), 128);
+      mbar_init(smem_u32(&sh.p_ready[i]), kSoftmaxThreads);
       mbar_init(smem_u32(&sh.o_done[i]), 1);
     }
-    mbar_init(smem_u32(&sh.o_free), 128);
+    mbar_init(smem_u32(&sh.o_free), kSoftmaxThreads);
     mbar_init(smem_u32(&sh.q_full), 1);
     mbar_init(smem_u32(&sh.q_free), 1);
     mbar_init(smem_u32(&sh.drain), 1);
     sh.abort = 0;
+    sh.failed[0] = sh.failed[1] = 0;
     fence_barrier_init();
   }
   tc_fence_before();
@@ -568,11 +629,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first_t = row_of<RT>(a, rt, 0).t;
   const Share w = share_of(a, split, first_t, sh);
   if (w.begin < w.end) {
-    if (warp == 0)
-      copy_loop<MB, RT>(a, &mql, &mqr, &mc, w, rt, first_t, sh, q_smem, k_smem);
-    else if (warp == 1)
+    if (warp == 1)
       product_loop<MB, RT>(a, w, first_t, sh, q_smem, k_smem);
-    else if (warp >= 4)
+    else if (warp == 0 || (warp < 4 && a.cache.block > 0 && a.cache.block < kTile))
+      copy_loop<MB, RT>(a, &mql, &mqr, &mc, w, rt, first_t, warp == 0 ? 0 : warp - 1, sh, q_smem,
+                        k_smem);
+    else if (warp >= kFirstSoftmax)
       softmax_loop<MB, RT>(a, w, rt, first_t, sh, k_smem);
   }
   tc_fence_before();

@@ -92,6 +92,36 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t chunk, uin
          static_cast<uint64_t>(group >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
+// One lane of a converged warp.  (The instructions above take their operands from uniform
+// registers: issued under this predicate, from values that the compiler knows to be
+// uniform, a product takes as long as its operands do, 34 to 49 cycles for 64 x 64 to 128
+// x 64 x 16; under threadIdx.x == 0 each took 67, whatever its size.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// A value that all lanes share, as the compiler can tell.
+__device__ __forceinline__ int uniform(int x) {
+  return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x)));
+}
+// Whether the phase with `parity` has completed, without waiting; the warp's answer.
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0) != 0;
+}
+
 // kind::f16 with fp32 accumulation: both operands bf16, or both fp16.
 __device__ __forceinline__ uint32_t mma_desc(bool f16, uint32_t m, uint32_t n, bool a_mn,
                                              bool b_mn) {
