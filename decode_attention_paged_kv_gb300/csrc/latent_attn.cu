@@ -53,14 +53,14 @@ struct Shape {
 };
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages], s_full[2], p_ready[2], o_done[2], o_free, q_full, q_free,
-      drain;
+  uint64_t full[kStages], empty[kStages], s_full[2], p_ready[2], o_done[2], voted[2], o_free, q_full,
+      q_free, drain;
   uint32_t tmem;
   volatile int abort;
   volatile int failed[2];  // a softmax warp's wait expired, by turns
   int seq0, off0;          // where the CTA's share begins
   float top[2][2][64];     // a tile's maxima, of its two halves, by turns
-  float ref[2][64];        // the references before the tile, by turns
+  volatile int rose[2];    // the last tile that a score rose far in, by turns
   float factor[64];
   float stat_l[2][64];
   int64_t row_at[64];  // of the output, -1: not written
@@ -355,6 +355,7 @@ __device__ __forceinline__ void product_loop(const LatentAttnArgs& a, const Shar
   int at = 0, tiles = 0, tile0 = 0, len = 0, seg = -1, value_seg = -1;
   uint32_t begins = 0;  // bit i % 4: tile i begins a segment
   uint64_t since = 0;
+  uint32_t idle = 0;
   bool ok = true;
   while (nv < n) {
     bool moved = false;
@@ -402,9 +403,11 @@ __device__ __forceinline__ void product_loop(const LatentAttnArgs& a, const Shar
     }
     if (moved) {
       since = 0;
+      idle = 0;
       continue;
     }
-    // nothing to do: give up after the limit
+    // nothing to do: give up after the limit (the clock is slow to read: now and then)
+    if (++idle % 512 != 0 && a.wait_limit_ns != 0) continue;
     const uint64_t now = globaltimer_ns();
     if (since == 0) since = now;
     const bool over = now - since > a.wait_limit_ns || a.wait_limit_ns == 0 || sh.abort != 0;
@@ -430,113 +433,139 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
   using S = Shape<MB, RT>;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - kFirstSoftmax;
   const int quarter = warp % 4, half = warp / 4;  // rows, and tokens of a tile
-  // a product with M = 64 leaves rows 16 q .. 16 q + 15 in lanes 32 q .. 32 q + 15
-  const int r = 16 * quarter + lane;
-  const bool mine = lane < 16 && r < RT;
+  // A product with M = 64 leaves rows 16 q .. 16 q + 15 in lanes 32 q .. 32 q + 15.  A
+  // thread takes 8 tokens of each of two rows, its neighbours the rest of the half tile.
+  const int r0 = 16 * quarter + lane / 4;  // and r0 + 8
   const bool quarter_on = 16 * quarter < RT;
   const uint32_t tq = sh.tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-  const Row at = row_of<RT>(a, rt, min(r, RT - 1));
+  const Row row[2] = {row_of<RT>(a, rt, min(r0, RT - 1)), row_of<RT>(a, rt, min(r0 + 8, RT - 1))};
+  const int token = 32 * half + 2 * (lane % 4);  // the thread's first one of a tile
   int i = 0;
   bool bad = false;
   for (Walk k(a, w, first_t); k.next();) {
-    const bool on = mine && at.t < k.seq.n && at.h < a.H;
-    const int seen = on ? k.seq.len - k.seq.n + at.t + 1 : 0;
-    float m = -INFINITY, l = 0.f;
+    bool on[2];
+    int seen[2];
+    float m[2] = {-INFINITY, -INFINITY}, ref[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      on[e] = quarter_on && row[e].t < k.seq.n && row[e].h < a.H;
+      seen[e] = on[e] ? k.seq.len - k.seq.n + row[e].t + 1 : 0;
+    }
     for (int t = 0; t < k.tiles; ++t, ++i) {
       bad |= !mbar_wait_bounded(smem_u32(&sh.s_full[i & 1]), (i >> 1) & 1, a.wait_limit_ns,
                                 &sh.abort);
       __syncwarp();
       tc_fence_after();
-      const int limit = seen - (k.tile0 + t) * kTile - 32 * half;
-      float s[32];
-      if (quarter_on) {
-        tmem_ld32(tq + (i & 1) * 64 + 32 * half, s);
-        tmem_wait_ld();
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (__all_sync(0xffffffffu, limit >= 32)) {
+      const int j0 = (k.tile0 + t) * kTile;
+      const uint32_t p = k_smem + (i % kStages) * S::kStageBytes + 2 * MB * kChunkBytes;
+      float s[16], top[2] = {-INFINITY, -INFINITY}, sum[2];
+      // weights under the current references, into the tile's rotated-key columns
+      auto weights = [&]() {
+        sum[0] = sum[1] = 0.f;
 #pragma unroll
-          for (int x = 0; x < 32; ++x) s[x] *= a.scale_log2;
+        for (int x = 0; x < 16; x += 2) {
+          const int e = x >> 1 & 1, c = token + (x >> 2) * 8;  // row, token
+          const float p0 = ex2(s[x] - ref[e]), p1 = ex2(s[x + 1] - ref[e]);
+          sum[e] += p0 + p1;
+          const uint32_t v = a.f16 ? pack2<true>(p0, p1) : pack2<false>(p0, p1);
+          const int r = r0 + 8 * e;
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(p + r * 128 + (((c >> 3) ^ (r & 7)) << 4) +
+                                                      (c & 7) * 2),
+                       "r"(v)
+                       : "memory");
+        }
+      };
+      if (quarter_on) {
+        tmem_ld_16x32(tq + (i & 1) * 64 + 32 * half, s);
+        tmem_wait_ld();
+        if (__all_sync(0xffffffffu, min(seen[0], seen[1]) - j0 >= kTile)) {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) s[x] *= a.scale_log2;
         } else {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) s[x] = x < limit ? s[x] * a.scale_log2 : -INFINITY;
+          for (int x = 0; x < 16; ++x) {
+            const int c = token + (x >> 2) * 8 + (x & 1);
+            s[x] = c < seen[x >> 1 & 1] - j0 ? s[x] * a.scale_log2 : -INFINITY;
+          }
         }
 #pragma unroll
-        for (int x = 0; x < 32; ++x) top[x % 4] = fmaxf(top[x % 4], s[x]);
-        if (mine) {
-          sh.top[i & 1][half][r] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          if (half == 0) sh.ref[i & 1][r] = m;
+        for (int x = 0; x < 16; ++x) top[x >> 1 & 1] = fmaxf(top[x >> 1 & 1], s[x]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+          if (lane % 4 == 0) sh.top[i & 1][half][r0 + 8 * e] = top[e];
         }
       }
+      // the first tile sets the references; later ones keep them unless a score rises far
+      // past its row's.  (The tile's number, not a flag: nothing has to be cleared.)
+      const bool rise = t == 0 || top[0] > m[0] + kRise || top[1] > m[1] + kRise;
+      if (__any_sync(0xffffffffu, rise) && lane == 0) sh.rose[i & 1] = i + 1;
       if (bad) sh.failed[i & 1] = 1;
-      named_barrier(1, kSoftmaxThreads);
+      mbar_arrive(smem_u32(&sh.voted[i & 1]));
+      if (quarter_on && t > 0) weights();
+      // (the barrier's other threads are at the same work: this wait is short)
+      bad |= !mbar_wait_bounded(smem_u32(&sh.voted[i & 1]), (i >> 1) & 1,
+                                a.wait_limit_ns + kDrainNs, nullptr);
+      __syncwarp();
       if (sh.failed[i & 1]) {  // (every thread of these warps leaves here)
         sh.abort = 1;
         set_status(a.status, kStatusTimeout);
         return;
       }
-      // whether any row's maximum rises past its reference (rows lane and lane + 32)
-      bool rise = false;
-      if (t > 0) {
-        for (int x = lane; x < RT; x += 32)
-          rise |= fmaxf(sh.top[i & 1][0][x], sh.top[i & 1][1][x]) > sh.ref[i & 1][x] + kRise;
-        rise = __any_sync(0xffffffffu, rise);
-      }
-      if (quarter_on) {
-        const float top = mine ? fmaxf(sh.top[i & 1][0][r], sh.top[i & 1][1][r]) : 0.f;
-        float f = 1.f;
-        if (t == 0) {
-          m = top;
-        } else if (top > m + kRise) {
-          f = ex2(m - top);
-          l *= f;
-          m = top;
-        }
-        if (rise && mine && half == 0) sh.factor[r] = f;
-        const float ref = m == -INFINITY ? 0.f : m;
-        const uint32_t p = k_smem + (i % kStages) * S::kStageBytes + 2 * MB * kChunkBytes + r * 128;
-        float sum[4] = {};
+      if (sh.rose[i & 1] == i + 1) {
+        if (quarter_on) {
 #pragma unroll
-        for (int x = 0; x < 32; x += 8) {
-          uint32_t v[4];
-#pragma unroll
-          for (int y = 0; y < 8; y += 2) {
-            const float p0 = ex2(s[x + y] - ref), p1 = ex2(s[x + y + 1] - ref);
-            sum[y / 2] += p0 + p1;
-            v[y / 2] = a.f16 ? pack2<true>(p0, p1) : pack2<false>(p0, p1);
+          for (int e = 0; e < 2; ++e) {
+            const int r = r0 + 8 * e;
+            const float high = fmaxf(sh.top[i & 1][0][r], sh.top[i & 1][1][r]);
+            float f = 1.f;
+            if (t == 0) {
+              m[e] = high;
+            } else if (high > m[e] + kRise) {
+              f = ex2(m[e] - high);
+              l[e] *= f;
+              m[e] = high;
+            }
+            ref[e] = m[e] == -INFINITY ? 0.f : m[e];
+            if (half == 0 && lane % 4 == 0) sh.factor[r] = f;
           }
-          if (mine)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             p + (((x / 8 + 4 * half) ^ (r & 7)) << 4)),
-                         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                         : "memory");
+          weights();
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      }
-      if (rise) {
-        named_barrier(1, kSoftmaxThreads);  // the factors are there
-        bad |= !mbar_wait_bounded(smem_u32(&sh.o_done[(i - 1) & 1]), ((i - 1) >> 1) & 1,
-                                  a.wait_limit_ns, &sh.abort);
-        __syncwarp();
-        tc_fence_after();
+        if (t > 0) {
+          named_barrier(1, kSoftmaxThreads);  // the factors are there
+          bad |= !mbar_wait_bounded(smem_u32(&sh.o_done[(i - 1) & 1]), ((i - 1) >> 1) & 1,
+                                    a.wait_limit_ns, &sh.abort);
+          __syncwarp();
+          tc_fence_after();
 #pragma unroll 1
-        for (int c = half * (MB * RT / 2); c < (half + 1) * (MB * RT / 2); c += 16) {
-          float o[16];
-          tmem_ld16(tq + 128 + c, o);
-          tmem_wait_ld();
+          for (int c = half * (MB * RT / 2); c < (half + 1) * (MB * RT / 2); c += 16) {
+            float o[16];
+            tmem_ld16(tq + 128 + c, o);
+            tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 16; ++x) o[x] *= sh.factor[c % RT + x];
-          tmem_st16(tq + 128 + c, o);
+            for (int x = 0; x < 16; ++x) o[x] *= sh.factor[c % RT + x];
+            tmem_st16(tq + 128 + c, o);
+          }
+          tmem_wait_st();
         }
-        tmem_wait_st();
       }
+      if (quarter_on) l[0] += sum[0], l[1] += sum[1];
       fence_async_smem();
       tc_fence_before();
       mbar_arrive(smem_u32(&sh.p_ready[i & 1]));
     }
     // the segment's output
-    if (mine) {
-      sh.stat_l[half][r] = l;
-      if (half == 0) sh.row_at[r] = on ? k.b * a.o_sb + at.t * a.o_st + at.h * a.o_sh : -1;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if (quarter_on && lane % 4 == 0) {
+        const int r = r0 + 8 * e;
+        sh.stat_l[half][r] = l[e];
+        if (half == 0)
+          sh.row_at[r] = on[e] ? k.b * a.o_sb + row[e].t * a.o_st + row[e].h * a.o_sh : -1;
+      }
     }
     // (two barriers by turns: the products of the last two tiles may both be under way,
     // and a parity tells neighbouring phases apart only)
@@ -547,10 +576,13 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
     const int channel = 32 * quarter + lane;
     const int64_t slot = 2 * static_cast<int64_t>(w.split * a.row_tiles + rt) + (k.index > 0);
     const bool whole = k.whole();
-    if (!whole && mine && half == 0) {
-      float* ml = a.part_ml + (slot * RT + r) * 2;
-      ml[0] = m;
-      ml[1] = l + sh.stat_l[1][r];
+    if (!whole && quarter_on && half == 0 && lane % 4 == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float* ml = a.part_ml + (slot * RT + r0 + 8 * e) * 2;
+        ml[0] = m[e];
+        ml[1] = l[e] + sh.stat_l[1][r0 + 8 * e];
+      }
     }
 #pragma unroll 1
     for (int c = half * (MB * RT / 2); c < (half + 1) * (MB * RT / 2); c += 16) {
@@ -612,6 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sh.s_full[i]), 1);
       mbar_init(smem_u32(&sh.p_ready[i]), kSoftmaxThreads);
       mbar_init(smem_u32(&sh.o_done[i]), 1);
+      mbar_init(smem_u32(&sh.voted[i]), kSoftmaxThreads);
     }
     mbar_init(smem_u32(&sh.o_free), kSoftmaxThreads);
     mbar_init(smem_u32(&sh.q_full), 1);
@@ -619,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&sh.drain), 1);
     sh.abort = 0;
     sh.failed[0] = sh.failed[1] = 0;
+    sh.rose[0] = sh.rose[1] = 0;
     fence_barrier_init();
   }
   tc_fence_before();

@@ -68,6 +68,20 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&x)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
 }
+// 16 lanes x 32 columns: a thread holds columns 8 k + 2 (lane % 4) + {0, 1} of rows lane /
+// 4 (x[4 k], x[4 k + 1]) and lane / 4 + 8 (x[4 k + 2], x[4 k + 3]), k < 4.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t addr, float (&x)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&x)[16]) {
   uint32_t r[16];
 #pragma unroll
