@@ -82,8 +82,8 @@ struct PromptArgs {
 cudaError_t launch_latent_append(int dc, bool f16, bool interleaved, const LatentAppendArgs& a,
                                  cudaStream_t s);
 // mql / mqr: maps over q_latent and q_rope {channels, H, T, B}, box {64, q_box, 1, 1}; mc: map
-// over the cache {64 channels, tokens, chunks, sequences or blocks}, box one tile of 64
-// tokens (dense, or blocks of 64), or one chunk of a block; all with a 128-byte swizzle.
+// over the cache {64 channels, tokens, chunks, sequences or blocks}, box one chunk
+// of 64 tokens or of a block; all with a 128-byte swizzle.
 cudaError_t launch_latent_attn(int dc, int tile_rows, const LatentAttnArgs& a,
                                const CUtensorMap& mql, const CUtensorMap& mqr,
                                const CUtensorMap& mc, cudaStream_t s);

@@ -289,7 +289,7 @@ dkv_status dkv_latent_decode_attn(const dkv_latent_attn* p, const dkv_latent_cac
                  {64, paged ? cache->block_size : cache->seq_len, chunks,
                   paged ? cache->num_blocks : B},
                  {cache->stride_t, 64, cache->stride_b},
-                 {64, tokens, tokens == dkv::kLatentTile ? chunks : 1, 1}))
+                 {64, tokens, 1, 1}))
     return DKV_ERR_CUDA;
   return cuda_status(dkv::launch_latent_attn(dc, L.tile_rows, a, mql, mqr, mc,
                                              static_cast<cudaStream_t>(stream)));

@@ -34,28 +34,40 @@ namespace {
 constexpr int kWarpsSoftmax = 8, kFirstSoftmax = 4;  // warps 4 .. 11
 constexpr int kThreads = 32 * (kFirstSoftmax + kWarpsSoftmax);
 constexpr int kSoftmaxThreads = 32 * kWarpsSoftmax;
-constexpr int kCopyWarps = 3;  // warps 0, 2 and 3 (1: products)
+constexpr int kCopyWarps = 2;  // warps 0 and 2 (1 and 3: products)
 constexpr int kTile = kLatentTile;
-constexpr int kStages = 2;
 constexpr int kChunkBytes = kTile * 128;  // 64 tokens x 64 channels
+constexpr int kPairBytes = 2 * kChunkBytes;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kRise = 8.f;  // how far (log2) a score may pass the reference
 // Shortest share of a CTA, in tiles.
 constexpr int kMinShare = 2;
 
+// Shared memory: queries, then two rings that tiles pass through in pieces -- pairs of
+// latent chunks (128 channels, what one product of the values takes) and rotated keys --
+// each piece with its barriers, so that a piece is replaced as soon as its last product is
+// done.
 template <int MB, int RT>
 struct Shape {
-  static constexpr int kChunks = 2 * MB + 1;          // of 64 channels, the rotated key last
+  static constexpr int kChunks = 2 * MB + 1;  // of 64 channels, the rotated key last
   static constexpr int kQBytes = kChunks * RT * 128;
-  static constexpr int kStageBytes = kChunks * kChunkBytes;
   static constexpr int kColumns = 128 + MB * RT <= 256 ? 256 : 512;
-  static constexpr size_t kSmem = 1024 + kQBytes + kStages * kStageBytes;
+  static constexpr int kRoom = 232448 - 1024 - 4096 - kQBytes;  // (alignment, static)
+  static constexpr int kKeys = kRoom >= 3 * (MB * kPairBytes + kChunkBytes) ? 4
+                               : kRoom >= (5 * MB / 2) * kPairBytes + 3 * kChunkBytes ? 3 : 2;
+  static constexpr int kPairs0 = (kRoom - kKeys * kChunkBytes) / kPairBytes;
+  static constexpr int kPairs = kPairs0 < kKeys * MB ? kPairs0 : kKeys * MB;
+  static constexpr int kKeyAt = kPairs * kPairBytes;  // of the rings' memory
+  static constexpr size_t kSmem = 1024 + kQBytes + kKeyAt + kKeys * kChunkBytes;
+  static_assert(kPairs >= 2 * MB && kPairs <= 16 && kKeys <= 4, "");
 };
+constexpr int kMaxPairs = 16, kMaxKeys = 4;
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages], s_full[2], p_ready[2], o_done[2], voted[2], o_free, q_full,
-      q_free, drain;
+  uint64_t full[kMaxPairs], empty[kMaxPairs], key_full[kMaxKeys], key_empty[kMaxKeys];
+  uint64_t s_full[2], p_ready[2], o_done[2], voted[2], o_free, q_full, q_free, drain[2];
   uint32_t tmem;
+  uint32_t fills[kMaxPairs], key_fills[kMaxKeys], q_fills;  // copies issued, for the drain
   volatile int abort;
   volatile int failed[2];  // a softmax warp's wait expired, by turns
   int seq0, off0;          // where the CTA's share begins
@@ -64,6 +76,16 @@ struct Shared {
   float factor[64];
   float stat_l[2][64];
   int64_t row_at[64];  // of the output, -1: not written
+};
+
+// A place in a ring of N: its index and the parity of its present round.
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void step() {
+    if (++at == N) at = 0, round ^= 1;
+  }
 };
 
 // Sequence b as a row tile sees it: its length, its new tokens, its tiles.
@@ -167,11 +189,47 @@ struct Walk {
   __device__ __forceinline__ bool whole() const { return tiles == seq.tiles; }
 };
 
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit,
-                                          volatile int* abort) {
-  int ok = 0;
-  if (threadIdx.x % 32 == 0) ok = mbar_wait_bounded(bar, parity, limit, abort);
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+// The same, a tile at a time, for warps that issue products and copies: every value is one
+// that the compiler knows to be uniform, and so is the loop over `count` tiles around it
+// (in a loop that lanes might leave apart, a product took 57 cycles instead of 34).
+struct TileWalk {
+  Walk walk;
+  int count;                 // tiles of the share
+  int b, len, tile, segment;  // of the present one: sequence, its length, tile, segment
+  int left;                  // of the segment, with this one
+  bool first;                // of the segment
+  __device__ __forceinline__ TileWalk(const LatentAttnArgs& a, const Share& w, int first_t)
+      : walk(a, w, first_t), count(uniform(static_cast<int>(w.end - w.begin))), segment(-1),
+        left(0) {}
+  __device__ __forceinline__ void step() {
+    first = left <= 1;
+    if (first) {
+      walk.next();
+      b = uniform(walk.b), len = uniform(walk.seq.len), tile = uniform(walk.tile0);
+      left = uniform(walk.tiles);
+      ++segment;
+    } else {
+      ++tile;
+      --left;
+    }
+  }
+};
+
+// Waits for a barrier of each lane's own (`wanted`).  The lanes stay together -- what the
+// warp issues next takes its operands from uniform registers -- and the clock, which is
+// slow to read, is looked at now and then.
+__device__ __forceinline__ bool lanes_wait(bool wanted, uint32_t bar, uint32_t parity,
+                                           uint64_t limit, volatile int* abort) {
+  uint64_t since = 0;
+  for (uint32_t n = 1; limit > 0; ++n) {
+    if (__all_sync(0xffffffffu, !wanted || mbar_try_wait(bar, parity))) return true;
+    if (n % 64 == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (since == 0) since = now;
+      if (__any_sync(0xffffffffu, now - since > limit || *abort)) break;
+    }
+  }
+  return false;
 }
 
 __device__ __forceinline__ void store_out(void* out, int dtype, int64_t at, float y) {
@@ -193,92 +251,104 @@ __device__ __forceinline__ Row row_of(const LatentAttnArgs& a, int rt, int r) {
   return {g / a.groups, (g % a.groups) * 8 + r % 8};
 }
 
-// Copies tiles of the cache, `part` of the copying warps; the first one queries too.
+// Copies tiles of the cache, every second piece; the first of the warps queries too.
 template <int MB, int RT>
 __device__ __forceinline__ void copy_loop(const LatentAttnArgs& a, const CUtensorMap* mql,
                                           const CUtensorMap* mqr, const CUtensorMap* mc,
                                           const Share& w, int rt, int first_t, int part,
                                           Shared& sh, uint32_t q_smem, uint32_t k_smem) {
   using S = Shape<MB, RT>;
-  constexpr int kPer = (S::kChunks + kCopyWarps - 1) / kCopyWarps;  // chunks of a warp
   const LatentView& c = a.cache;
-  const bool pieces = c.block > 0 && c.block < kTile;  // a copy a chunk of a block
-  const int c0 = part * kPer, c1 = min(c0 + kPer, S::kChunks);
-  int i = 0, segs = 0;
+  Ring<S::kPairs> pair;
+  Ring<S::kKeys> key;
+  const int block = c.block == 0 ? kTile : c.block;  // tokens of a copy
+  int turn = 0;
+  uint32_t filled = 0;  // bits: the ring's first round is over (pairs, then keys)
   bool ok = true;
-  for (Walk k(a, w, first_t); ok && k.next();) {
-    const int b = uniform(k.b), len = uniform(k.seq.len), tile0 = uniform(k.tile0);
-    const int tiles = uniform(k.tiles);
-    for (int t = 0; t < tiles; ++t, ++i) {
-      const int s = i % kStages;
-      const int j0 = (tile0 + t) * kTile;
-      if (i >= kStages &&
-          !warp_wait(smem_u32(&sh.empty[s]), ((i / kStages) & 1) ^ 1, a.wait_limit_ns, &sh.abort)) {
-        ok = false;
-        break;
-      }
-      const uint32_t bar = smem_u32(&sh.full[s]), dst = k_smem + s * S::kStageBytes;
-      if (!pieces) {
-        int blk = b, row = j0;
-        if (c.block > 0) {
-          blk = c.bt[b * c.bts + (tile0 + t)];
-          if (blk < 0 || blk >= c.nblocks) {
-            set_status(a.status, kStatusCheck);
-            blk = min(max(blk, 0), c.nblocks - 1);
-          }
-          blk = uniform(blk);
-          row = 0;
-        }
-        if (elect_one()) {
-          mbar_arrive_expect_tx(bar, S::kStageBytes);
-          tma_load_4d(dst, mc, bar, 0, row, 0, blk);
-        }
-      } else {
-        // pages that hold tokens of the sequence
-        const int pages = min(kTile / c.block, (len - j0 + c.block - 1) / c.block);
-        const int32_t* bt = c.bt + b * c.bts + j0 / c.block;
-        if (elect_one()) mbar_arrive_expect_tx(bar, pages * c.block * (c1 - c0) * 128);
-        __syncwarp();
-        for (int p = 0; p < pages; ++p) {
-          int blk = bt[p];
-          if (blk < 0 || blk >= c.nblocks) {
-            set_status(a.status, kStatusCheck);
-            blk = min(max(blk, 0), c.nblocks - 1);
-          }
-          blk = uniform(blk);
-          if (elect_one()) {
+  TileWalk k(a, w, first_t);
+  for (int i = 0; ok && i < k.count; ++i) {
+    k.step();
+    const int b = k.b;
+    const int j0 = k.tile * kTile;
+    // blocks that hold tokens of the sequence
+    const int blocks = min(kTile / block, (k.len - j0 + block - 1) / block);
+    int blk[4] = {b, b, b, b};
+    if (c.block > 0) {
+      const int32_t* bt = c.bt + b * c.bts + j0 / block;
 #pragma unroll
-            for (int x = 0; x < kPer; ++x)
-              if (c0 + x < c1)
-                tma_load_4d(dst + (c0 + x) * kChunkBytes + p * c.block * 128, mc, bar, 0, 0, c0 + x,
-                            blk);
-          }
-          __syncwarp();
+      for (int p = 0; p < 4; ++p) {
+        if (p >= blocks) break;
+        int x = bt[p];
+        if (x < 0 || x >= c.nblocks) {
+          set_status(a.status, kStatusCheck);
+          x = min(max(x, 0), c.nblocks - 1);
         }
+        blk[p] = uniform(x);
       }
-      __syncwarp();
-      if (t == 0 && part == 0) {  // the segment's queries
-        if (segs > 0 &&
-            !warp_wait(smem_u32(&sh.q_free), (segs - 1) & 1, a.wait_limit_ns, &sh.abort)) {
-          ++i;
+    }
+    const int row = c.block == 0 ? j0 : 0;
+#pragma unroll
+    for (int g = 0; g <= MB; ++g) {
+      const bool is_key = g == MB;
+      const int at = is_key ? key.at : pair.at;
+      const uint32_t round = is_key ? key.round : pair.round;
+      if (turn == part) {
+        const uint32_t empty = smem_u32(is_key ? &sh.key_empty[at] : &sh.empty[at]);
+        const uint32_t full = smem_u32(is_key ? &sh.key_full[at] : &sh.full[at]);
+        if ((filled >> is_key & 1) && !lanes_wait(true, empty, round ^ 1, a.wait_limit_ns, &sh.abort)) {
           ok = false;
           break;
         }
-        const uint32_t qbar = smem_u32(&sh.q_full);
-        if (elect_one()) mbar_arrive_expect_tx(qbar, S::kQBytes);
-        __syncwarp();
-        for (int r = 0; r < RT; r += a.q_box) {
-          const Row at = row_of<RT>(a, rt, r);
-          if (elect_one()) {
-            // (rows past the last head or token are filled with zeros)
+        const uint32_t dst =
+            is_key ? k_smem + S::kKeyAt + at * kChunkBytes : k_smem + at * kPairBytes;
+        const int chunks = is_key ? 1 : 2;
+        if (elect_one()) {
+          if (is_key)
+            ++sh.key_fills[at];
+          else
+            ++sh.fills[at];
+          mbar_arrive_expect_tx(full, blocks * block * chunks * 128);
 #pragma unroll
-            for (int x = 0; x < 2 * MB; ++x)
-              tma_load_4d(q_smem + x * (RT * 128) + r * 128, mql, qbar, x * 64, at.h, at.t, b);
-            tma_load_4d(q_smem + 2 * MB * (RT * 128) + r * 128, mqr, qbar, 0, at.h, at.t, b);
+          for (int p = 0; p < 4; ++p) {
+            if (p >= blocks) break;
+            tma_load_4d(dst + p * block * 128, mc, full, 0, row, 2 * g, blk[p]);
+            if (!is_key)
+              tma_load_4d(dst + kChunkBytes + p * block * 128, mc, full, 0, row, 2 * g + 1, blk[p]);
           }
-          __syncwarp();
         }
-        ++segs;
+        __syncwarp();
+      }
+      if (++turn == kCopyWarps) turn = 0;
+      if (is_key) {
+        key.step();
+        if (key.at == 0) filled |= 2;
+      } else {
+        pair.step();
+        if (pair.at == 0) filled |= 1;
+      }
+    }
+    if (ok && k.first && part == 0) {  // the segment's queries
+      if (k.segment > 0 &&
+          !lanes_wait(true, smem_u32(&sh.q_free), (k.segment - 1) & 1, a.wait_limit_ns, &sh.abort)) {
+        ok = false;
+        break;
+      }
+      const uint32_t qbar = smem_u32(&sh.q_full);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(qbar, S::kQBytes);
+        ++sh.q_fills;
+      }
+      __syncwarp();
+      for (int r = 0; r < RT; r += a.q_box) {
+        const Row at = row_of<RT>(a, rt, r);
+        if (elect_one()) {
+          // (rows past the last head or token are filled with zeros)
+#pragma unroll
+          for (int x = 0; x < 2 * MB; ++x)
+            tma_load_4d(q_smem + x * (RT * 128) + r * 128, mql, qbar, x * 64, at.h, at.t, b);
+          tma_load_4d(q_smem + 2 * MB * (RT * 128) + r * 128, mqr, qbar, 0, at.h, at.t, b);
+        }
+        __syncwarp();
       }
     }
   }
@@ -286,145 +356,171 @@ __device__ __forceinline__ void copy_loop(const LatentAttnArgs& a, const CUtenso
     sh.abort = 1;
     set_status(a.status, kStatusTimeout);
   }
-  // nothing is in flight when the CTA ends (a barrier that a part of the warps has filled
-  // only does not complete: the copies are waited for by the time they can take)
-  if (threadIdx.x % 32 == 0) {
-    for (int x = max(0, i - kStages); x < i; ++x)
-      mbar_wait_bounded(smem_u32(&sh.full[x % kStages]), (x / kStages) & 1, kDrainNs, nullptr);
-    if (segs > 0) mbar_wait_bounded(smem_u32(&sh.q_full), (segs - 1) & 1, kDrainNs, nullptr);
+}
+
+// Rows past the sequence may hold anything: as values they must be 0 (a weight of 0 times
+// NaN is NaN); their scores are masked.  Clears rows `valid` and on of a piece (one warp).
+__device__ __forceinline__ void clear_rows(uint32_t piece, int valid) {
+  const int words = (kTile - valid) * 8;
+  for (int x = threadIdx.x % 32; x < 2 * words; x += 32)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                     piece + x / words * kChunkBytes + valid * 128 + x % words * 16),
+                 "r"(0)
+                 : "memory");
+  fence_async_smem();
+  __syncwarp();
+}
+
+// Waits (one warp) until no copy into shared memory is in flight.
+template <int MB, int RT>
+__device__ __forceinline__ void drain_copies(Shared& sh) {
+  using S = Shape<MB, RT>;
+  const int lane = threadIdx.x % 32;
+  if (lane < S::kPairs) {
+    if (sh.fills[lane] > 0)
+      mbar_wait_bounded(smem_u32(&sh.full[lane]), (sh.fills[lane] - 1) & 1, kDrainNs, nullptr);
+  } else if (lane < S::kPairs + S::kKeys) {
+    const int x = lane - S::kPairs;
+    if (sh.key_fills[x] > 0)
+      mbar_wait_bounded(smem_u32(&sh.key_full[x]), (sh.key_fills[x] - 1) & 1, kDrainNs, nullptr);
+  } else if (lane == 31 && sh.q_fills > 0) {
+    mbar_wait_bounded(smem_u32(&sh.q_full), (sh.q_fills - 1) & 1, kDrainNs, nullptr);
   }
   __syncwarp();
 }
 
-template <int MB, int RT>
-struct Issuer {
-  using S = Shape<MB, RT>;
-  const LatentAttnArgs& a;
-  Shared& sh;
-  uint32_t q_smem, k_smem, tmem;
-  // O^T (+)= V^T P^T of tile i.
-  __device__ __forceinline__ void values(int i, bool first) {
-    tc_fence_after();
-    if (elect_one()) {
-      const uint32_t k = k_smem + (i % kStages) * S::kStageBytes;
-      const uint32_t p = k + 2 * MB * kChunkBytes;
-      const uint32_t desc = mma_desc(a.f16, 128, RT, true, false);
-#pragma unroll
-      for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int t = 0; t < kTile / 16; ++t)
-          tc_mma(tmem + 128 + m * RT, smem_desc(k + 2 * m * kChunkBytes + t * 2048, kChunkBytes, 1024),
-                 smem_desc(p + t * 32, 16, 1024), desc, t > 0 || !first);
-      tc_commit(smem_u32(&sh.o_done[i & 1]));
-      tc_commit(smem_u32(&sh.empty[i % kStages]));
-    }
-    __syncwarp();
-  }
-  // S = Q K^T of tile i.
-  __device__ __forceinline__ void scores(int i, bool last) {
-    tc_fence_after();
-    if (elect_one()) {
-      const uint32_t k = k_smem + (i % kStages) * S::kStageBytes;
-      const uint32_t desc = mma_desc(a.f16, 64, kTile, false, false);
-#pragma unroll
-      for (int c = 0; c < S::kChunks; ++c)
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          tc_mma(tmem + (i & 1) * 64, smem_desc(q_smem + c * (RT * 128) + x * 32, 16, 1024),
-                 smem_desc(k + c * kChunkBytes + x * 32, 16, 1024), desc, c + x > 0);
-      tc_commit(smem_u32(&sh.s_full[i & 1]));
-      if (last) tc_commit(smem_u32(&sh.q_free));
-    }
-    __syncwarp();
-  }
-};
+// Nothing that the warp has issued is in flight when the tensor memory is freed.
+__device__ __forceinline__ void drain_products(uint64_t* bar) {
+  if (elect_one()) tc_commit(smem_u32(bar));
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) mbar_wait_bounded(smem_u32(bar), 0, kDrainNs, nullptr);
+  __syncwarp();
+}
 
-// Issues a tile's scores when it has arrived, its values when its weights are there,
-// whichever comes first: waiting for the next tile while weights are ready would keep the
-// tile that they belong to from being replaced.
+// The two products have a warp each, which waits for its operands: one warp for both has
+// to choose what is ready, and its tests took longer than a product.
+
+// S = Q K^T of each tile, when it has arrived.
 template <int MB, int RT>
-__device__ __forceinline__ void product_loop(const LatentAttnArgs& a, const Share& w, int first_t,
-                                             Shared& sh, uint32_t q_smem, uint32_t k_smem) {
+__device__ __forceinline__ void score_loop(const LatentAttnArgs& a, const Share& w, int first_t,
+                                           Shared& sh, uint32_t q_smem, uint32_t k_smem) {
   using S = Shape<MB, RT>;
   const int lane = threadIdx.x % 32;
-  Issuer<MB, RT> run{a, sh, q_smem, k_smem, static_cast<uint32_t>(uniform(sh.tmem))};
-  const int n = uniform(static_cast<int>(w.end - w.begin));
-  int ns = 0, nv = 0;  // tiles whose scores, whose values have been issued
-  // the segment of the next scores, and what values have to know of theirs
-  Walk k(a, w, first_t);
-  int at = 0, tiles = 0, tile0 = 0, len = 0, seg = -1, value_seg = -1;
-  uint32_t begins = 0;  // bit i % 4: tile i begins a segment
-  uint64_t since = 0;
-  uint32_t idle = 0;
+  const uint32_t tmem = static_cast<uint32_t>(uniform(sh.tmem));
+  const uint32_t desc = mma_desc(a.f16, 64, kTile, false, false);
+  Ring<S::kPairs> pair;
+  Ring<S::kKeys> key;
   bool ok = true;
-  while (nv < n) {
-    bool moved = false;
-    if (nv < ns && warp_test(smem_u32(&sh.p_ready[nv & 1]), (nv >> 1) & 1)) {
-      const bool first = begins >> (nv & 3) & 1;
-      if (!first || value_seg < 0 || warp_test(smem_u32(&sh.o_free), value_seg & 1)) {
-        run.values(nv, first);
-        value_seg += first;
-        ++nv;
-        moved = true;
-      }
+  TileWalk k(a, w, first_t);
+  for (int i = 0; i < k.count; ++i) {
+    k.step();
+    // the tile's pieces, a lane each; the queries; that the scores two tiles ago are read
+    uint32_t bar = smem_u32(&sh.key_full[key.at]), parity = key.round;
+    bool wanted = lane <= MB;
+    if (lane < MB) {
+      const int x = pair.at + lane, wrap = x >= S::kPairs;
+      bar = smem_u32(&sh.full[x - wrap * S::kPairs]);
+      parity = pair.round ^ wrap;
+    } else if (lane == MB + 1) {
+      bar = smem_u32(&sh.q_full), parity = k.segment & 1;
+      wanted = k.first;
+    } else if (lane == MB + 2) {
+      bar = smem_u32(&sh.p_ready[i & 1]), parity = ((i >> 1) & 1) ^ 1;
+      wanted = i >= 2;
     }
-    if (ns < n && ns - nv < 2) {
-      if (at == tiles) {  // a new segment
-        k.next();
-        at = 0;
-        tiles = uniform(k.tiles);
-        tile0 = uniform(k.tile0);
-        len = uniform(k.seq.len);
-        ++seg;
-      }
-      const int s = ns % kStages;
-      if (warp_test(smem_u32(&sh.full[s]), (ns / kStages) & 1) &&
-          (at > 0 || warp_test(smem_u32(&sh.q_full), seg & 1))) {
-        // rows past the sequence may hold anything: as values they must be 0 (a weight of
-        // 0 times NaN is NaN); their scores are masked
-        const int valid = len - (tile0 + at) * kTile;
-        if (valid < kTile) {
-          const uint32_t to = k_smem + s * S::kStageBytes;
-          const int words = (kTile - valid) * 8;
-          for (int x = lane; x < 2 * MB * words; x += 32)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             to + x / words * kChunkBytes + valid * 128 + x % words * 16),
-                         "r"(0)
-                         : "memory");
-          fence_async_smem();
-          __syncwarp();
-        }
-        begins = (begins & ~(1u << (ns & 3))) | static_cast<uint32_t>(at == 0) << (ns & 3);
-        ++at;
-        run.scores(ns, at == tiles);
-        ++ns;
-        moved = true;
-      }
+    ok = lanes_wait(wanted, bar, parity, a.wait_limit_ns, &sh.abort);
+    if (!ok) break;
+    const int places = uniform(pair.at | key.at << 8 | (i & 1) << 16);
+    uint32_t from[MB];
+#pragma unroll
+    for (int x = 0; x < MB; ++x) {
+      const int y = (places & 255) + x;
+      from[x] = k_smem + (y >= S::kPairs ? y - S::kPairs : y) * kPairBytes;
     }
-    if (moved) {
-      since = 0;
-      idle = 0;
-      continue;
+    const int valid = k.len - k.tile * kTile;
+    if (valid < kTile) {
+#pragma unroll
+      for (int x = 0; x < MB; ++x) clear_rows(from[x], valid);
     }
-    // nothing to do: give up after the limit (the clock is slow to read: now and then)
-    if (++idle % 512 != 0 && a.wait_limit_ns != 0) continue;
-    const uint64_t now = globaltimer_ns();
-    if (since == 0) since = now;
-    const bool over = now - since > a.wait_limit_ns || a.wait_limit_ns == 0 || sh.abort != 0;
-    if (__any_sync(0xffffffffu, over)) {
-      ok = false;
-      break;
+    tc_fence_after();
+    const uint32_t to = tmem + (places >> 16) * 64;
+    const uint32_t last = k_smem + S::kKeyAt + (places >> 8 & 255) * kChunkBytes;
+    if (elect_one()) {
+#pragma unroll
+      for (int x = 0; x < MB; ++x)
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          tc_mma(to, smem_desc(q_smem + (2 * x + y / 4) * (RT * 128) + y % 4 * 32, 16, 1024),
+                 smem_desc(from[x] + y / 4 * kChunkBytes + y % 4 * 32, 16, 1024), desc, x + y > 0);
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        tc_mma(to, smem_desc(q_smem + 2 * MB * (RT * 128) + y * 32, 16, 1024),
+               smem_desc(last + y * 32, 16, 1024), desc, 1);
+      tc_commit(smem_u32(&sh.s_full[i & 1]));
+      if (k.left == 1) tc_commit(smem_u32(&sh.q_free));
     }
+    __syncwarp();
+#pragma unroll
+    for (int x = 0; x < MB; ++x) pair.step();
+    key.step();
   }
   if (!ok) {
     sh.abort = 1;
     set_status(a.status, kStatusTimeout);
   }
-  // nothing is in flight when the tensor memory is freed
-  if (elect_one()) tc_commit(smem_u32(&sh.drain));
-  __syncwarp();
-  if (lane == 0) mbar_wait_bounded(smem_u32(&sh.drain), 0, kDrainNs, nullptr);
-  __syncwarp();
+  drain_products(&sh.drain[0]);
+}
+
+// O^T (+)= V^T P^T of each tile, when its weights are there.
+template <int MB, int RT>
+__device__ __forceinline__ void value_loop(const LatentAttnArgs& a, const Share& w, int first_t,
+                                           Shared& sh, uint32_t k_smem) {
+  using S = Shape<MB, RT>;
+  const int lane = threadIdx.x % 32;
+  const uint32_t tmem = static_cast<uint32_t>(uniform(sh.tmem));
+  const uint32_t desc = mma_desc(a.f16, 128, RT, true, false);
+  Ring<S::kPairs> pair;
+  Ring<S::kKeys> key;
+  bool ok = true;
+  TileWalk k(a, w, first_t);
+  for (int i = 0; i < k.count; ++i) {
+    k.step();
+    // the weights; at a segment's first tile that the last one's output is read
+    uint32_t bar = smem_u32(&sh.p_ready[i & 1]), parity = (i >> 1) & 1;
+    if (lane == 1) bar = smem_u32(&sh.o_free), parity = (k.segment - 1) & 1;
+    ok = lanes_wait(lane == 0 || (lane == 1 && k.first && k.segment > 0), bar, parity,
+                    a.wait_limit_ns, &sh.abort);
+    if (!ok) break;
+    tc_fence_after();
+    const int places = uniform(pair.at | key.at << 8 | (k.first ? 0 : 1) << 16);
+    Ring<S::kPairs> v;
+    v.at = places & 255;
+    const uint32_t p = k_smem + S::kKeyAt + (places >> 8 & 255) * kChunkBytes;
+    const uint32_t keep = places >> 16;
+    if (elect_one()) {
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        const uint32_t from = k_smem + v.at * kPairBytes;
+#pragma unroll
+        for (int x = 0; x < kTile / 16; ++x)
+          tc_mma(tmem + 128 + m * RT, smem_desc(from + x * 2048, kChunkBytes, 1024),
+                 smem_desc(p + x * 32, 16, 1024), desc, x > 0 ? 1 : keep);
+        tc_commit(smem_u32(&sh.empty[v.at]));
+        v.step();
+      }
+      tc_commit(smem_u32(&sh.key_empty[places >> 8 & 255]));
+      tc_commit(smem_u32(&sh.o_done[i & 1]));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < MB; ++m) pair.step();
+    key.step();
+  }
+  if (!ok) {
+    sh.abort = 1;
+    set_status(a.status, kStatusTimeout);
+  }
+  drain_products(&sh.drain[1]);
 }
 
 template <int MB, int RT>
@@ -441,6 +537,7 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
   const Row row[2] = {row_of<RT>(a, rt, min(r0, RT - 1)), row_of<RT>(a, rt, min(r0 + 8, RT - 1))};
   const int token = 32 * half + 2 * (lane % 4);  // the thread's first one of a tile
   int i = 0;
+  Ring<S::kKeys> key;
   bool bad = false;
   for (Walk k(a, w, first_t); k.next();) {
     bool on[2];
@@ -457,7 +554,8 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
       __syncwarp();
       tc_fence_after();
       const int j0 = (k.tile0 + t) * kTile;
-      const uint32_t p = k_smem + (i % kStages) * S::kStageBytes + 2 * MB * kChunkBytes;
+      const uint32_t p = k_smem + S::kKeyAt + key.at * kChunkBytes;
+      key.step();
       float s[16], top[2] = {-INFINITY, -INFINITY}, sum[2];
       // weights under the current references, into the tile's rotated-key columns
       auto weights = [&]() {
@@ -635,21 +733,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), S::kColumns);
   if (threadIdx.x == 0) {
     prefetch_tensormap(&mql), prefetch_tensormap(&mqr), prefetch_tensormap(&mc);
-    const int copy_warps = a.cache.block > 0 && a.cache.block < kTile ? kCopyWarps : 1;
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&sh.full[i]), copy_warps);
+    for (int i = 0; i < S::kPairs; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
       mbar_init(smem_u32(&sh.empty[i]), 1);
+      sh.fills[i] = 0;
     }
+    for (int i = 0; i < S::kKeys; ++i) {
+      mbar_init(smem_u32(&sh.key_full[i]), 1);
+      mbar_init(smem_u32(&sh.key_empty[i]), 1);
+      sh.key_fills[i] = 0;
+    }
+    sh.q_fills = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.s_full[i]), 1);
       mbar_init(smem_u32(&sh.p_ready[i]), kSoftmaxThreads);
       mbar_init(smem_u32(&sh.o_done[i]), 1);
       mbar_init(smem_u32(&sh.voted[i]), kSoftmaxThreads);
+      mbar_init(smem_u32(&sh.drain[i]), 1);
     }
     mbar_init(smem_u32(&sh.o_free), kSoftmaxThreads);
     mbar_init(smem_u32(&sh.q_full), 1);
     mbar_init(smem_u32(&sh.q_free), 1);
-    mbar_init(smem_u32(&sh.drain), 1);
     sh.abort = 0;
     sh.failed[0] = sh.failed[1] = 0;
     sh.rose[0] = sh.rose[1] = 0;
@@ -663,17 +767,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first_t = row_of<RT>(a, rt, 0).t;
   const Share w = share_of(a, split, first_t, sh);
   if (w.begin < w.end) {
-    if (warp == 1)
-      product_loop<MB, RT>(a, w, first_t, sh, q_smem, k_smem);
-    else if (warp == 0 || (warp < 4 && a.cache.block > 0 && a.cache.block < kTile))
-      copy_loop<MB, RT>(a, &mql, &mqr, &mc, w, rt, first_t, warp == 0 ? 0 : warp - 1, sh, q_smem,
-                        k_smem);
-    else if (warp >= kFirstSoftmax)
+    if (warp == 0 || warp == 2)
+      copy_loop<MB, RT>(a, &mql, &mqr, &mc, w, rt, first_t, warp / 2, sh, q_smem, k_smem);
+    else if (warp == 1)
+      score_loop<MB, RT>(a, w, first_t, sh, q_smem, k_smem);
+    else if (warp == 3)
+      value_loop<MB, RT>(a, w, first_t, sh, k_smem);
+    else
       softmax_loop<MB, RT>(a, w, rt, first_t, sh, k_smem);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (warp == 0) drain_copies<MB, RT>(sh);
   if (warp == 1) tmem_dealloc(sh.tmem, S::kColumns);
 }
 

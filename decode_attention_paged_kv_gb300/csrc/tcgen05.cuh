@@ -123,19 +123,6 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ int uniform(int x) {
   return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x)));
 }
-// Whether the phase with `parity` has completed, without waiting; the warp's answer.
-__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return __all_sync(0xffffffffu, ok != 0) != 0;
-}
-
 // kind::f16 with fp32 accumulation: both operands bf16, or both fp16.
 __device__ __forceinline__ uint32_t mma_desc(bool f16, uint32_t m, uint32_t n, bool a_mn,
                                              bool b_mn) {
