@@ -87,6 +87,11 @@ cudaError_t launch_latent_append(int dc, bool f16, bool interleaved, const Laten
 cudaError_t launch_latent_attn(int dc, int tile_rows, const LatentAttnArgs& a,
                                const CUtensorMap& mql, const CUtensorMap& mqr,
                                const CUtensorMap& mc, cudaStream_t s);
-cudaError_t launch_prompt_attn(int dn, bool f16, const PromptArgs& a, cudaStream_t s);
+// Maps over q_nope, q_rope, k_nope, v {channels, H, rows, 1}, box {64, 1, 128, 1}, and over
+// k_rope {channels, rows, 1, 1}, box {64, 128, 1, 1}; 128-byte swizzle.  blocks: CTAs, as many as
+// there can be blocks of 256 queries, times the heads.
+cudaError_t launch_prompt_attn(int dn, bool f16, const PromptArgs& a, const CUtensorMap& qn,
+                               const CUtensorMap& qr, const CUtensorMap& kn, const CUtensorMap& kr,
+                               const CUtensorMap& v, int blocks, cudaStream_t s);
 
 }  // namespace dkv

@@ -350,7 +350,29 @@ dkv_status dkv_latent_prompt_attn(const dkv_prompt* p, void* workspace, void* st
   a.total_k = p->total_k;
   a.status = static_cast<uint32_t*>(workspace);
   a.wait_limit_ns = (p->flags & DKV_FLAG_FORCE_TIMEOUT) ? 0 : kWaitLimitNs;
-  return cuda_status(dkv::launch_prompt_attn(p->nope_dim, p->dtype == DKV_FP16, a,
+  // (a scale of 0 becomes the smallest: masked scores stay at minus infinity)
+  if (a.scale_log2 == 0.f) a.scale_log2 = 1.17549435e-38f;
+  const int64_t blocks = (ceil_div(p->total_q, 256) + p->batch) * p->num_heads;
+  if (blocks > kInt32Max) return DKV_ERR_UNSUPPORTED;
+  const int64_t H = p->num_heads, dn = p->nope_dim, dr = p->rope_dim;
+  // (without keys no copy is made; a map needs an address all the same)
+  const bool keys = p->total_k > 0;
+  const int64_t Tk = keys ? p->total_k : 1;
+  const void* none = p->q_nope;
+  CUtensorMap qn, qr, kn, kr, v;
+  if (!encode_4d(&qn, p->dtype, p->q_nope, {dn, H, p->total_q, 1},
+                 {p->qn_stride_h, p->qn_stride_t, 0}, {64, 1, 128, 1}) ||
+      !encode_4d(&qr, p->dtype, p->q_rope, {dr, H, p->total_q, 1},
+                 {p->qr_stride_h, p->qr_stride_t, 0}, {64, 1, 128, 1}) ||
+      !encode_4d(&kn, p->dtype, keys ? p->k_nope : none, {dn, H, Tk, 1},
+                 {p->kn_stride_h, p->kn_stride_t, 0}, {64, 1, 128, 1}) ||
+      !encode_4d(&kr, p->dtype, keys ? p->k_rope : none, {dr, Tk, 1, 1}, {p->kr_stride_t, 0, 0},
+                 {64, 128, 1, 1}) ||
+      !encode_4d(&v, p->dtype, keys ? p->v : none, {dn, H, Tk, 1},
+                 {p->v_stride_h, p->v_stride_t, 0}, {64, 1, 128, 1}))
+    return DKV_ERR_CUDA;
+  return cuda_status(dkv::launch_prompt_attn(p->nope_dim, p->dtype == DKV_FP16, a, qn, qr, kn, kr, v,
+                                             static_cast<int>(blocks),
                                              static_cast<cudaStream_t>(stream)));
 }
 

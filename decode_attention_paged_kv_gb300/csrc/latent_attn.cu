@@ -38,7 +38,6 @@ constexpr int kCopyWarps = 2;  // warps 0 and 2 (1 and 3: products)
 constexpr int kTile = kLatentTile;
 constexpr int kChunkBytes = kTile * 128;  // 64 tokens x 64 channels
 constexpr int kPairBytes = 2 * kChunkBytes;
-constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kRise = 8.f;  // how far (log2) a score may pass the reference
 // Shortest share of a CTA, in tiles.
 constexpr int kMinShare = 2;
@@ -215,23 +214,6 @@ struct TileWalk {
   }
 };
 
-// Waits for a barrier of each lane's own (`wanted`).  The lanes stay together -- what the
-// warp issues next takes its operands from uniform registers -- and the clock, which is
-// slow to read, is looked at now and then.
-__device__ __forceinline__ bool lanes_wait(bool wanted, uint32_t bar, uint32_t parity,
-                                           uint64_t limit, volatile int* abort) {
-  uint64_t since = 0;
-  for (uint32_t n = 1; limit > 0; ++n) {
-    if (__all_sync(0xffffffffu, !wanted || mbar_try_wait(bar, parity))) return true;
-    if (n % 64 == 0) {
-      const uint64_t now = globaltimer_ns();
-      if (since == 0) since = now;
-      if (__any_sync(0xffffffffu, now - since > limit || *abort)) break;
-    }
-  }
-  return false;
-}
-
 __device__ __forceinline__ void store_out(void* out, int dtype, int64_t at, float y) {
   if (dtype == 2)
     static_cast<float*>(out)[at] = y;
@@ -386,14 +368,6 @@ __device__ __forceinline__ void drain_copies(Shared& sh) {
   } else if (lane == 31 && sh.q_fills > 0) {
     mbar_wait_bounded(smem_u32(&sh.q_full), (sh.q_fills - 1) & 1, kDrainNs, nullptr);
   }
-  __syncwarp();
-}
-
-// Nothing that the warp has issued is in flight when the tensor memory is freed.
-__device__ __forceinline__ void drain_products(uint64_t* bar) {
-  if (elect_one()) tc_commit(smem_u32(bar));
-  __syncwarp();
-  if (threadIdx.x % 32 == 0) mbar_wait_bounded(smem_u32(bar), 0, kDrainNs, nullptr);
   __syncwarp();
 }
 

@@ -1,111 +1,485 @@
-// prompt_attn.cu -- attention of prompts with expanded keys and values, the simplest
-// form: a CTA a row (query, head), a warp a key at a time, one pass with the running
-// maximum and sum.
+// prompt_attn.cu -- attention of prompts with keys and values expanded a head (the expanded
+// form): softmax(scale (q_nope . k_nope + q_rope . k_rope)) v over ragged sequences, the
+// rotated keys shared by the heads.
+//
+// 2 (2 dn + 64) flops a query and key against some bytes a key: bound by the tensor cores.
+// A CTA takes 256 queries of a head, as two tiles of 128 rows that take turns: while one
+// tile's scores pass through the softmax the tensor cores work on the other's.  Per key
+// tile of 128 and query tile
+//   S = Q K^T     M = 128, N = 128, dn + 64 channels: both operands from shared memory
+//   O += P V      M = 128, N = dn, 128 tokens: P from tensor memory, where it takes the
+//                 place of the scores it was made of; V as it was copied (MN-major)
+// A thread has a row of scores to itself (128 threads a query tile), so the softmax needs
+// no exchange; a row's output lies in the lane of its thread, so each warp scales its own
+// rows when a score passes the running reference by 2^8, which is seldom.
+//
+// Keys and values come in pieces of 128 tokens x 64 channels (16 KB) through one ring, the
+// keys of the next tile before the values of this one are done with: with 96 KB of
+// queries (dn = 128) there is room for 8 pieces, a tile and three fifths.
 
 #include "dkv_device.cuh"
 #include "dkv_kernels.h"
 #include "latent.h"
+#include "tcgen05.cuh"
 
 namespace dkv {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 384;  // warps: copies, products, two idle, 2 x 4 of softmax
+constexpr int kRows = 128;     // queries of a tile
+constexpr int kKeys = 128;     // keys of a tile
+constexpr int kPieceBytes = kKeys * 128;
+constexpr int kSlots = 8;
+constexpr float kRise = 8.f;
+
+struct Shared {
+  uint64_t full[kSlots], empty[kSlots], q_full[2], s_full[2], p_ready[2], o_done[2], drain;
+  uint32_t tmem;
+  uint32_t fills[kSlots];
+  volatile int abort;
+  int q_used;  // bits: which query tiles were copied
+  int seq, block;
+};
+
+// What the CTA computes.
+struct Work {
+  int b, h;        // sequence (-1: nothing), head
+  int q0, nq;      // its query rows
+  int k0, nk;      // its key rows
+  int row;         // the first query of the block, within the sequence
+  int tiles[2];    // key tiles of the two query tiles
+};
+
+struct Bounds {
+  int q0, nq, k0, nk;
+};
+__device__ __forceinline__ Bounds bounds(const PromptArgs& a, int b) {
+  const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+  if (q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k) {
+    set_status(a.status, kStatusCheck);
+    return {0, 0, 0, 0};
+  }
+  return {q0, q1 - q0, k0, k1 - k0};
+}
+
+// Keys that the query `row` of a sequence sees.
+__device__ __forceinline__ int seen_by(const PromptArgs& a, const Work& w, int row) {
+  return a.causal ? min(w.nk, max(0, w.nk - w.nq + row + 1)) : w.nk;
+}
+
+// The CTA's block of queries: sequences in order, heads within, blocks within from the
+// last to the first (the last sees the most keys).  Blocks of one head run side by side
+// and find its keys in the L2.
+__device__ __forceinline__ Work find_work(const PromptArgs& a, Shared& sh) {
+  __shared__ long long warp_sum[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  if (tid == 0) sh.seq = -1;
+  long long before = 0;
+  const long long me = blockIdx.x;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + tid;
+    long long n = 0;
+    if (b < a.B) n = (bounds(a, b).nq + 2ll * kRows - 1) / (2 * kRows) * a.H;
+    long long x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long up = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += up;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    long long chunk = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) x += warp_sum[i];
+      chunk += warp_sum[i];
+    }
+    x += before;
+    if (n > 0 && me < x && me >= x - n) {
+      sh.seq = b;
+      sh.block = static_cast<int>(me - (x - n));
+    }
+    before += chunk;
+    if (before > me) break;
+  }
+  __syncthreads();
+  Work w{};
+  w.b = sh.seq;
+  if (w.b < 0) return w;
+  const Bounds s = bounds(a, w.b);
+  const int blocks = (s.nq + 2 * kRows - 1) / (2 * kRows);
+  w.h = sh.block / blocks;
+  w.q0 = s.q0, w.nq = s.nq, w.k0 = s.k0, w.nk = s.nk;
+  w.row = (blocks - 1 - sh.block % blocks) * (2 * kRows);
+  for (int x = 0; x < 2; ++x) {
+    const int last = min(w.row + (x + 1) * kRows, w.nq) - 1;  // of the tile's queries
+    w.tiles[x] =
+        last < w.row + x * kRows ? 0 : (seen_by(a, w, last) + kKeys - 1) / kKeys;
+  }
+  return w;
+}
+
+template <int DN>
+struct Shape {
+  static constexpr int kQChunks = DN / 64 + 1, kVChunks = DN / 64;
+  static constexpr int kPieces = kQChunks + kVChunks;  // of a key tile
+  static constexpr int kQBytes = kQChunks * kPieceBytes;  // of a query tile
+  static constexpr size_t kSmem = 1024 + 2 * kQBytes + kSlots * kPieceBytes;
+  // tensor memory: scores and weights of the two query tiles, then their outputs
+  static constexpr uint32_t kOutput = 256;
+};
+
+struct Maps {
+  CUtensorMap qn, qr, kn, kr, v;
+};
+
+template <int DN>
+__device__ __forceinline__ void copy_loop(const PromptArgs& a, const Maps& m, const Work& w, int n,
+                                          Shared& sh, uint32_t q_smem, uint32_t ring) {
+  using S = Shape<DN>;
+  const int h = uniform(w.h), q = uniform(w.q0 + w.row), k0 = uniform(w.k0);
+  const int used = uniform((w.tiles[0] > 0 ? 1 : 0) | (w.tiles[1] > 0 ? 2 : 0));
+  if (elect_one()) {
+    sh.q_used = used;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (!(used >> x & 1)) continue;
+      const uint32_t bar = smem_u32(&sh.q_full[x]), to = q_smem + x * S::kQBytes;
+      mbar_arrive_expect_tx(bar, S::kQBytes);
+#pragma unroll
+      for (int c = 0; c < S::kQChunks - 1; ++c)
+        tma_load_4d(to + c * kPieceBytes, &m.qn, bar, 64 * c, h, q + x * kRows, 0);
+      tma_load_4d(to + (S::kQChunks - 1) * kPieceBytes, &m.qr, bar, 0, h, q + x * kRows, 0);
+    }
+  }
+  __syncwarp();
+  bool ok = true;
+  int at = 0;
+  uint32_t round = 0;
+  bool again = false;  // the ring's first round is over
+  for (int i = 0; ok && i < n; ++i) {
+    const int row = k0 + i * kKeys;
+#pragma unroll
+    for (int c = 0; c < S::kPieces; ++c) {
+      if (again && !lanes_wait(true, smem_u32(&sh.empty[at]), round ^ 1, a.wait_limit_ns, &sh.abort)) {
+        ok = false;
+        break;
+      }
+      const int slot = uniform(at);
+      const uint32_t bar = smem_u32(&sh.full[slot]), to = ring + slot * kPieceBytes;
+      if (elect_one()) {
+        ++sh.fills[slot];
+        mbar_arrive_expect_tx(bar, kPieceBytes);
+        if (c < S::kQChunks - 1)
+          tma_load_4d(to, &m.kn, bar, 64 * c, h, row, 0);
+        else if (c == S::kQChunks - 1)
+          tma_load_4d(to, &m.kr, bar, 0, row, 0, 0);
+        else
+          tma_load_4d(to, &m.v, bar, 64 * (c - S::kQChunks), h, row, 0);
+      }
+      __syncwarp();
+      if (++at == kSlots) at = 0, round ^= 1, again = true;
+    }
+  }
+  if (!ok) {
+    sh.abort = 1;
+    set_status(a.status, kStatusTimeout);
+  }
+}
+
+// Issues the products in a fixed order: a query tile's values, then its next scores (which
+// take the place of the weights just used), then the other tile's.
+template <int DN>
+__device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, const Work& w, int n,
+                                             Shared& sh, uint32_t q_smem, uint32_t ring) {
+  using S = Shape<DN>;
+  const int lane = threadIdx.x % 32;
+  const uint32_t tmem = static_cast<uint32_t>(uniform(sh.tmem));
+  const uint32_t score_desc = mma_desc(f16, kRows, kKeys, false, false);
+  const uint32_t value_desc = mma_desc(f16, kRows, 64, false, true);
+  const int tiles[2] = {uniform(w.tiles[0]), uniform(w.tiles[1])};
+  const int nk = uniform(w.nk);
+  bool ok = true;
+  // scores of key tile i, whose pieces begin at `piece` (counted from the first)
+  auto scores = [&](int x, int i) {
+    const int piece = i * S::kPieces;
+    const int p = piece + min(lane, S::kQChunks - 1);
+    uint32_t bar = smem_u32(&sh.full[p % kSlots]), parity = (p / kSlots) & 1;
+    bool wanted = lane < S::kQChunks;
+    if (lane == S::kQChunks) bar = smem_u32(&sh.q_full[x]), parity = 0, wanted = true;
+    ok = ok && lanes_wait(wanted, bar, parity, a.wait_limit_ns, &sh.abort);
+    if (!ok) return;
+    tc_fence_after();
+    const uint32_t q = q_smem + x * S::kQBytes;
+    const int base = uniform(piece);
+    if (elect_one()) {
+#pragma unroll
+      for (int c = 0; c < S::kQChunks; ++c) {
+        const uint32_t k = ring + (base + c) % kSlots * kPieceBytes;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          tc_mma(tmem + x * 128, smem_desc(q + c * kPieceBytes + y * 32, 16, 1024),
+                 smem_desc(k + y * 32, 16, 1024), score_desc, c + y > 0);
+      }
+      tc_commit(smem_u32(&sh.s_full[x]));
+      // the last to read the tile's keys
+      if (x == 1 || i >= tiles[1]) {
+#pragma unroll
+        for (int c = 0; c < S::kQChunks; ++c) tc_commit(smem_u32(&sh.empty[(base + c) % kSlots]));
+      }
+    }
+    __syncwarp();
+  };
+  auto values = [&](int x, int i) {
+    const int piece = i * S::kPieces + S::kQChunks;
+    const int p = piece + min(lane, S::kVChunks - 1);
+    uint32_t bar = smem_u32(&sh.full[p % kSlots]), parity = (p / kSlots) & 1;
+    bool wanted = lane < S::kVChunks;
+    if (lane == S::kVChunks) bar = smem_u32(&sh.p_ready[x]), parity = i & 1, wanted = true;
+    ok = ok && lanes_wait(wanted, bar, parity, a.wait_limit_ns, &sh.abort);
+    if (!ok) return;
+    const int base = uniform(piece);
+    // rows past the sequence may hold anything; a weight of 0 times NaN is NaN
+    const int valid = nk - i * kKeys;
+    if (valid < kKeys && (x == 0 || i >= tiles[0])) {
+#pragma unroll
+      for (int c = 0; c < S::kVChunks; ++c) {
+        const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
+        for (int y = lane; y < (kKeys - valid) * 8; y += 32)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + valid * 128 + y * 16),
+                       "r"(0)
+                       : "memory");
+      }
+      fence_async_smem();
+      __syncwarp();
+    }
+    tc_fence_after();
+    const uint32_t keep = uniform(i > 0);
+    if (elect_one()) {
+      // N = 128 takes two pieces, not neighbours where the ring wraps: a product each
+#pragma unroll
+      for (int c = 0; c < S::kVChunks; ++c) {
+        const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
+#pragma unroll
+        for (int y = 0; y < kKeys / 16; ++y)
+          tc_mma_ts(tmem + S::kOutput + x * 128 + c * 64, tmem + x * 128 + y * 8,
+                    smem_desc(v + y * 2048, 16, 1024), value_desc, y > 0 ? 1 : keep);
+      }
+      if (i == tiles[x] - 1) tc_commit(smem_u32(&sh.o_done[x]));
+      if (x == 1 || i >= tiles[1]) {
+#pragma unroll
+        for (int c = 0; c < S::kVChunks; ++c) tc_commit(smem_u32(&sh.empty[(base + c) % kSlots]));
+      }
+    }
+    __syncwarp();
+  };
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    if (tiles[x] > 0) scores(x, 0);
+  for (int i = 0; ok && i < n; ++i) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (i < tiles[x]) values(x, i);
+      if (i + 1 < tiles[x]) scores(x, i + 1);
+    }
+  }
+  if (!ok) {
+    sh.abort = 1;
+    set_status(a.status, kStatusTimeout);
+  }
+  drain_products(&sh.drain);
+}
 
 template <int DN, bool F16>
-__global__ void __launch_bounds__(32 * kWarps) prompt_attn_kernel(const PromptArgs a) {
-  constexpr int V = DN / 64;
-  __shared__ float part[kWarps][DN];
-  __shared__ float stat[kWarps][2];
+__device__ __forceinline__ void softmax_loop(const PromptArgs& a, const Work& w, int x, Shared& sh) {
+  using S = Shape<DN>;
+  const int lane = threadIdx.x % 32, quarter = threadIdx.x / 32 % 4;
+  const int row = w.row + x * kRows + 32 * quarter + lane;  // within the sequence
+  const bool on = row < w.nq;
+  const int seen = on ? seen_by(a, w, row) : 0;
+  const uint32_t tq = sh.tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+  const uint32_t ts = tq + x * 128, to = tq + S::kOutput + x * 128;
+  const float scale = fabsf(a.scale_log2);
+  float m = -INFINITY, l = 0.f;
+  bool ok = true;
+  const int n = w.tiles[x];
+  for (int i = 0; i < n; ++i) {
+    ok = mbar_wait_bounded(smem_u32(&sh.s_full[x]), i & 1, a.wait_limit_ns, &sh.abort);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    tc_fence_after();
+    float s[128];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, reinterpret_cast<float(&)[32]>(s[32 * c]));
+    tmem_wait_ld();
+    if (a.scale_log2 < 0.f) {
+#pragma unroll
+      for (int c = 0; c < 128; ++c) s[c] = -s[c];
+    }
+    const int limit = seen - i * kKeys;
+    if (__any_sync(0xffffffffu, limit < kKeys)) {
+#pragma unroll
+      for (int c = 0; c < 128; ++c) s[c] = c < limit ? s[c] : -INFINITY;
+    }
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int c = 0; c < 128; ++c) top[c % 4] = fmaxf(top[c % 4], s[c]);
+    const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+    if (i == 0) {
+      m = high;
+    } else {
+      const bool rise = high > m + kRise;
+      if (__any_sync(0xffffffffu, rise)) {
+        // (the products of the tile before were done when these scores were)
+        const float f = rise ? ex2(m - high) : 1.f;
+        if (rise) m = high;
+        l *= f;
+#pragma unroll 1
+        for (int c = 0; c < DN; c += 16) {
+          float o[16];
+          tmem_ld16(to + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int y = 0; y < 16; ++y) o[y] *= f;
+          tmem_st16(to + c, o);
+        }
+      }
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    float sum[4] = {};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t p[32];
+#pragma unroll
+      for (int y = 0; y < 32; ++y) {
+        const float p0 = ex2(fmaf(s[64 * c + 2 * y], scale, -ref));
+        const float p1 = ex2(fmaf(s[64 * c + 2 * y + 1], scale, -ref));
+        sum[y % 4] += p0 + p1;
+        p[y] = pack2<F16>(p0, p1);
+      }
+      tmem_st32(ts + 32 * c, p);
+    }
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(smem_u32(&sh.p_ready[x]));
+  }
+  if (ok && n > 0) {
+    ok = mbar_wait_bounded(smem_u32(&sh.o_done[x]), 0, a.wait_limit_ns, &sh.abort);
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after();
+  }
+  if (!ok) {
+    sh.abort = 1;
+    set_status(a.status, kStatusTimeout);
+    return;
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+  const int64_t at = static_cast<int64_t>(w.q0 + row) * a.o_st + w.h * a.o_sh;
+#pragma unroll 1
+  for (int c = 0; c < DN; c += 16) {
+    float o[16];
+    if (n > 0) {
+      tmem_ld16(to + c, o);
+      tmem_wait_ld();
+    }
+#pragma unroll
+    for (int y = 0; y < 16; ++y) o[y] = l > 0.f || l != l ? o[y] * inv : 0.f;
+    if (!on) continue;
+    if (a.out_dtype == 2) {
+      float4* out = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + c);
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        out[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+    } else {
+      uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + c);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = a.out_dtype == 1 ? pack2<true>(o[8 * y + 2 * e], o[8 * y + 2 * e + 1])
+                                  : pack2<false>(o[8 * y + 2 * e], o[8 * y + 2 * e + 1]);
+        out[y] = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+  }
+}
+
+template <int DN, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Maps m) {
+  using S = Shape<DN>;
+  extern __shared__ uint8_t raw[];
+  __shared__ Shared sh;
+  const uint32_t q_smem = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t ring = q_smem + 2 * S::kQBytes;
+  const int warp = threadIdx.x / 32;
   griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), 1);
+      sh.fills[i] = 0;
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(smem_u32(&sh.q_full[x]), 1);
+      mbar_init(smem_u32(&sh.s_full[x]), 1);
+      mbar_init(smem_u32(&sh.p_ready[x]), kRows);
+      mbar_init(smem_u32(&sh.o_done[x]), 1);
+    }
+    mbar_init(smem_u32(&sh.drain), 1);
+    sh.abort = 0;
+    sh.q_used = 0;
+    fence_barrier_init();
+  }
   griddep_wait();
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int i = blockIdx.x, h = blockIdx.y;
-  // the sequence that query row i belongs to
-  int b = -1;
-  for (int s = 0; s < a.B; ++s) {
-    const int q0 = a.cu_q[s], q1 = a.cu_q[s + 1], k0 = a.cu_k[s], k1 = a.cu_k[s + 1];
-    if (q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k) {
-      set_status(a.status, kStatusCheck);
-      continue;
-    }
-    if (i >= q0 && i < q1) {
-      b = s;
-      break;
-    }
-  }
-  if (b < 0) return;
-  const int nq = a.cu_q[b + 1] - a.cu_q[b], k0 = a.cu_k[b], nk = a.cu_k[b + 1] - k0;
-  const int seen = a.causal ? nk - nq + (i - a.cu_q[b]) + 1 : nk;
-  const uint32_t* qn = reinterpret_cast<const uint32_t*>(a.qn + i * a.qn_st + h * a.qn_sh);
-  const uint32_t* qr = reinterpret_cast<const uint32_t*>(a.qr + i * a.qr_st + h * a.qr_sh);
-  uint32_t q[V];
-#pragma unroll
-  for (int d = 0; d < V; ++d) q[d] = qn[lane + 32 * d];
-  const uint32_t qk = qr[lane];
-  float o[2 * V] = {}, m = -INFINITY, l = 0.f;
-  for (int j = warp; j < seen; j += kWarps) {
-    const uint32_t* kn =
-        reinterpret_cast<const uint32_t*>(a.kn + static_cast<int64_t>(k0 + j) * a.kn_st + h * a.kn_sh);
-    const uint32_t* kr =
-        reinterpret_cast<const uint32_t*>(a.kr + static_cast<int64_t>(k0 + j) * a.kr_st);
-    const uint32_t* vv =
-        reinterpret_cast<const uint32_t*>(a.v + static_cast<int64_t>(k0 + j) * a.v_st + h * a.v_sh);
-    float s = 0.f;
-#pragma unroll
-    for (int d = 0; d < V; ++d) {
-      const uint32_t k = kn[lane + 32 * d];
-      s = fmaf(lo16<F16>(q[d]), lo16<F16>(k), fmaf(hi16<F16>(q[d]), hi16<F16>(k), s));
-    }
-    const uint32_t k = kr[lane];
-    s = fmaf(lo16<F16>(qk), lo16<F16>(k), fmaf(hi16<F16>(qk), hi16<F16>(k), s));
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= a.scale_log2;
-    const float now = fmaxf(m, s), f = exp2f(m - now), p = exp2f(s - now);
-    m = now;
-    l = l * f + p;
-#pragma unroll
-    for (int d = 0; d < V; ++d) {
-      const uint32_t v = vv[lane + 32 * d];
-      o[2 * d] = o[2 * d] * f + p * lo16<F16>(v);
-      o[2 * d + 1] = o[2 * d + 1] * f + p * hi16<F16>(v);
-    }
-  }
-#pragma unroll
-  for (int d = 0; d < V; ++d) {
-    part[warp][2 * (lane + 32 * d)] = o[2 * d];
-    part[warp][2 * (lane + 32 * d) + 1] = o[2 * d + 1];
-  }
-  if (lane == 0) stat[warp][0] = m, stat[warp][1] = l;
+  const Work w = find_work(a, sh);
+  if (w.b < 0) return;  // (the grid is for the most blocks that there can be)
+  if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
+  tc_fence_before();
   __syncthreads();
-  float top = -INFINITY, sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w][0]);
-  for (int w = 0; w < kWarps; ++w)
-    if (stat[w][1] > 0.f) sum += stat[w][1] * exp2f(stat[w][0] - top);
-  for (int d = threadIdx.x; d < DN; d += 32 * kWarps) {
-    float y = 0.f;
-    for (int w = 0; w < kWarps; ++w)
-      if (stat[w][1] > 0.f) y += part[w][d] * exp2f(stat[w][0] - top);
-    y = sum > 0.f ? y / sum : 0.f;
-    const int64_t at = i * a.o_st + h * a.o_sh + d;
-    if (a.out_dtype == 2)
-      static_cast<float*>(a.out)[at] = y;
-    else if (a.out_dtype == 1)
-      static_cast<__half*>(a.out)[at] = __float2half_rn(y);
-    else
-      static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
+  tc_fence_after();
+  const int n = uniform(max(w.tiles[0], w.tiles[1]));
+  if (warp == 0)
+    copy_loop<DN>(a, m, w, n, sh, q_smem, ring);
+  else if (warp == 1)
+    product_loop<DN>(a, F16, w, n, sh, q_smem, ring);
+  else if (warp >= 4)
+    softmax_loop<DN, F16>(a, w, warp >= 8, sh);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) {  // no copy is in flight when the CTA ends
+    const int lane = threadIdx.x;
+    if (lane < kSlots && sh.fills[lane] > 0)
+      mbar_wait_bounded(smem_u32(&sh.full[lane]), (sh.fills[lane] - 1) & 1, kDrainNs, nullptr);
+    if (lane >= 30 && (sh.q_used >> (lane - 30) & 1))
+      mbar_wait_bounded(smem_u32(&sh.q_full[lane - 30]), 0, kDrainNs, nullptr);
+    __syncwarp();
   }
+  if (warp == 1) tmem_dealloc(sh.tmem, 512);
+}
+
+template <int DN, bool F16>
+cudaError_t launch_t(const PromptArgs& a, const Maps& m, int blocks, cudaStream_t s) {
+  // (an attribute of the device that is current: set on every call, it takes no time)
+  const cudaError_t e =
+      cudaFuncSetAttribute(prompt_attn_kernel<DN, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(Shape<DN>::kSmem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prompt_attn_kernel<DN, F16>, dim3(blocks), dim3(kThreads), Shape<DN>::kSmem, s, a,
+                    m);
 }
 
 }  // namespace
 
-cudaError_t launch_prompt_attn(int dn, bool f16, const PromptArgs& a, cudaStream_t s) {
-  const dim3 grid(a.total_q, a.H), block(32 * kWarps);
-  if (dn == 128)
-    return f16 ? launch_pdl(prompt_attn_kernel<128, true>, grid, block, 0, s, a)
-               : launch_pdl(prompt_attn_kernel<128, false>, grid, block, 0, s, a);
-  return f16 ? launch_pdl(prompt_attn_kernel<64, true>, grid, block, 0, s, a)
-             : launch_pdl(prompt_attn_kernel<64, false>, grid, block, 0, s, a);
+cudaError_t launch_prompt_attn(int dn, bool f16, const PromptArgs& a, const CUtensorMap& qn,
+                               const CUtensorMap& qr, const CUtensorMap& kn, const CUtensorMap& kr,
+                               const CUtensorMap& v, int blocks, cudaStream_t s) {
+  const Maps m{qn, qr, kn, kr, v};
+  if (dn == 128) return f16 ? launch_t<128, true>(a, m, blocks, s) : launch_t<128, false>(a, m, blocks, s);
+  return f16 ? launch_t<64, true>(a, m, blocks, s) : launch_t<64, false>(a, m, blocks, s);
 }
 
 }  // namespace dkv

@@ -94,6 +94,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&x)[16]) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
 // ---------------------------------------------------------------- descriptors
 // An operand in shared memory with the 128-byte swizzle, `addr` a multiple of 16 (atoms
 // of 1024 bytes are aligned to their size).
@@ -123,6 +135,23 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ int uniform(int x) {
   return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x)));
 }
+// Waits for a barrier of each lane's own (`wanted`).  The lanes stay together -- what the
+// warp issues next takes its operands from uniform registers -- and the clock, which is
+// slow to read, is looked at now and then.
+__device__ __forceinline__ bool lanes_wait(bool wanted, uint32_t bar, uint32_t parity,
+                                           uint64_t limit, volatile int* abort) {
+  uint64_t since = 0;
+  for (uint32_t n = 1; limit > 0; ++n) {
+    if (__all_sync(0xffffffffu, !wanted || mbar_try_wait(bar, parity))) return true;
+    if (n % 64 == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (since == 0) since = now;
+      if (__any_sync(0xffffffffu, now - since > limit || *abort)) break;
+    }
+  }
+  return false;
+}
+
 // kind::f16 with fp32 accumulation: both operands bf16, or both fp16.
 __device__ __forceinline__ uint32_t mma_desc(bool f16, uint32_t m, uint32_t n, bool a_mn,
                                              bool b_mn) {
@@ -156,6 +185,16 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
       : "memory");
+}
+
+constexpr uint64_t kDrainNs = 200000000ull;  // for what is in flight when a kernel gives up
+
+// Nothing that the warp has issued is in flight when the tensor memory is freed.
+__device__ __forceinline__ void drain_products(uint64_t* bar) {
+  if (elect_one()) tc_commit(smem_u32(bar));
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) mbar_wait_bounded(smem_u32(bar), 0, kDrainNs, nullptr);
+  __syncwarp();
 }
 
 __device__ __forceinline__ void fence_async_smem() {

@@ -422,6 +422,44 @@ def test_prompt_bad_bounds_are_left_alone(dkv):
         assert bool((out[110:] == 5.0).all())
 
 
+def test_prompt_timeout(dkv):
+    # every bounded wait gives up at once: the status says so, and the next call is right
+    args, out = prompt_case(2, 128, [300, 5], [700, 5], torch.bfloat16, gen_of("ptime"))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    dkv.latent_prompt_attn(*args, 0.1, out=out, workspace=ws, flags=dkv.DKV_FLAG_FORCE_TIMEOUT)
+    assert dkv.read_device_status(ws) == dkv.DKV_ERR_DEVICE_TIMEOUT
+    out.fill_(5.0)
+    dkv.latent_prompt_attn(*args, 0.1, out=out, workspace=ws)
+    assert dkv.read_device_status(ws) == 0
+    check_prompt(args, out, [300, 5], [700, 5], 0.1, True)
+
+
+def test_prompt_many_blocks(dkv):
+    # more blocks of queries than multiprocessors, so that they follow one another
+    nq, nk = [700, 1, 2049, 513], [700, 900, 2049, 1500]
+    args, out = prompt_case(40, 128, nq, nk, torch.bfloat16, gen_of("many"))
+    dkv.latent_prompt_attn(*args, 0.08, out=out)
+    check_prompt(args, out, nq, nk, 0.08, True)
+    again = torch.full_like(out, 5.0)
+    for _ in range(3):
+        dkv.latent_prompt_attn(*args, 0.08, out=again)
+        assert torch.equal(out, again)
+
+
+def test_prompt_rising_scores(dkv):
+    # every key tile raises the maximum, or lies far below it
+    n = 1000
+    for order in (1, -1):
+        args, out = prompt_case(1, 64, [300], [n], torch.bfloat16, gen_of("prise"), extra=0)
+        q, k = args[1], args[3]
+        q.zero_(), k.zero_()
+        q[..., 0] = 1.0
+        up = torch.arange(n, device="cuda")
+        k[:, 0] = (up if order > 0 else n - 1 - up) / 4
+        dkv.latent_prompt_attn(*args, 1.0, causal=False, out=out)
+        check_prompt(args, out, [300], [n], 1.0, False)
+
+
 def test_prompt_captured(dkv):
     args, out = prompt_case(3, 128, [300, 100], [400, 100], torch.bfloat16, gen_of("pg"), extra=300)
     cu_q, cu_k = args[5], args[6]
