@@ -25,7 +25,7 @@
 namespace dkv {
 namespace {
 
-constexpr int kThreads = 384;  // warps: copies, products, two idle, 2 x 4 of softmax
+constexpr int kThreads = 384;  // warps: copies, products (two), one idle, 2 x 4 of softmax
 constexpr int kRows = 128;     // queries of a tile
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kPieceBytes = kKeys * 128;
@@ -33,7 +33,7 @@ constexpr int kSlots = 8;
 constexpr float kRise = 8.f;
 
 struct Shared {
-  uint64_t full[kSlots], empty[kSlots], q_full[2], s_full[2], p_ready[2], o_done[2], drain;
+  uint64_t full[kSlots], empty[kSlots], q_full[2], s_full[2], p_ready[2], o_done[2], turn[2], drain[2];
   uint32_t tmem;
   uint32_t fills[kSlots];
   volatile int abort;
@@ -187,61 +187,48 @@ __device__ __forceinline__ void copy_loop(const PromptArgs& a, const Maps& m, co
   }
 }
 
-// Issues the products in a fixed order: a query tile's values, then its next scores (which
-// take the place of the weights just used), then the other tile's.
+// Issues query tile x's products: its values, then its next scores, which take the place of
+// the weights just used (products of one thread run in order).  A warp for each query
+// tile: between its products a warp spends some 600 cycles on barriers and descriptors,
+// which the other's fill.  They take turns all the same: left alone they fall into step,
+// both in the softmax at one time and both at the tensor cores at another.
 template <int DN>
-__device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, const Work& w, int n,
-                                             Shared& sh, uint32_t q_smem, uint32_t ring) {
+__device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, const Work& w, int x,
+                                             int n, Shared& sh, uint32_t q_smem, uint32_t ring) {
   using S = Shape<DN>;
   const int lane = threadIdx.x % 32;
   const uint32_t tmem = static_cast<uint32_t>(uniform(sh.tmem));
+  const uint32_t scores_at = tmem + x * 128, output_at = tmem + S::kOutput + x * 128;
+  const uint32_t q = q_smem + x * S::kQBytes;
   const uint32_t score_desc = mma_desc(f16, kRows, kKeys, false, false);
   const uint32_t value_desc = mma_desc(f16, kRows, 64, false, true);
-  const int tiles[2] = {uniform(w.tiles[0]), uniform(w.tiles[1])};
-  const int nk = uniform(w.nk);
+  const int tiles = uniform(w.tiles[x]), nk = uniform(w.nk);
   bool ok = true;
-  // scores of key tile i, whose pieces begin at `piece` (counted from the first)
-  auto scores = [&](int x, int i) {
-    const int piece = i * S::kPieces;
-    const int p = piece + min(lane, S::kQChunks - 1);
+  // Step i: the values of key tile i - 1 and the scores of key tile i, whose pieces follow
+  // one another.  One wait for all that they need, one go: a second wait between them
+  // left the tensor cores idle for 350 cycles.
+  for (int i = 0; i <= n; ++i) {
+    const bool values = i > 0, scores = i < n;            // steps that there are
+    const bool use_values = values && i <= tiles, use_scores = i < tiles;  // and x takes part in
+    const int piece = i * S::kPieces - S::kVChunks;  // the first: of the values
+    const int p = max(piece + lane, 0);
     uint32_t bar = smem_u32(&sh.full[p % kSlots]), parity = (p / kSlots) & 1;
-    bool wanted = lane < S::kQChunks;
-    if (lane == S::kQChunks) bar = smem_u32(&sh.q_full[x]), parity = 0, wanted = true;
-    ok = ok && lanes_wait(wanted, bar, parity, a.wait_limit_ns, &sh.abort);
-    if (!ok) return;
-    tc_fence_after();
-    const uint32_t q = q_smem + x * S::kQBytes;
-    const int base = uniform(piece);
-    if (elect_one()) {
-#pragma unroll
-      for (int c = 0; c < S::kQChunks; ++c) {
-        const uint32_t k = ring + (base + c) % kSlots * kPieceBytes;
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          tc_mma(tmem + x * 128, smem_desc(q + c * kPieceBytes + y * 32, 16, 1024),
-                 smem_desc(k + y * 32, 16, 1024), score_desc, c + y > 0);
-      }
-      tc_commit(smem_u32(&sh.s_full[x]));
-      // the last to read the tile's keys
-      if (x == 1 || i >= tiles[1]) {
-#pragma unroll
-        for (int c = 0; c < S::kQChunks; ++c) tc_commit(smem_u32(&sh.empty[(base + c) % kSlots]));
-      }
+    bool wanted = lane < S::kVChunks ? values : (scores && lane < S::kPieces);
+    if (lane == S::kPieces) {
+      bar = smem_u32(&sh.p_ready[x]), parity = (i - 1) & 1, wanted = use_values;
+    } else if (lane == S::kPieces + 1) {
+      bar = smem_u32(&sh.q_full[x]), parity = 0, wanted = use_scores;
+    } else if (lane == S::kPieces + 2) {
+      bar = smem_u32(&sh.turn[x]), parity = (i - 1 + x) & 1, wanted = i + x > 0;
     }
-    __syncwarp();
-  };
-  auto values = [&](int x, int i) {
-    const int piece = i * S::kPieces + S::kQChunks;
-    const int p = piece + min(lane, S::kVChunks - 1);
-    uint32_t bar = smem_u32(&sh.full[p % kSlots]), parity = (p / kSlots) & 1;
-    bool wanted = lane < S::kVChunks;
-    if (lane == S::kVChunks) bar = smem_u32(&sh.p_ready[x]), parity = i & 1, wanted = true;
-    ok = ok && lanes_wait(wanted, bar, parity, a.wait_limit_ns, &sh.abort);
-    if (!ok) return;
-    const int base = uniform(piece);
-    // rows past the sequence may hold anything; a weight of 0 times NaN is NaN
-    const int valid = nk - i * kKeys;
-    if (valid < kKeys && (x == 0 || i >= tiles[0])) {
+    ok = lanes_wait(wanted, bar, parity, a.wait_limit_ns, &sh.abort);
+    if (!ok) break;
+    const int base = uniform(piece + 8 * kSlots), keep = uniform(i > 1);
+    const bool do_values = uniform(use_values), do_scores = uniform(use_scores);
+    const int valid = nk - (i - 1) * kKeys;
+    if (use_values && valid < kKeys) {
+      // rows past the sequence may hold anything; a weight of 0 times NaN is NaN (both
+      // query tiles' warps clear them: with the same zeros)
 #pragma unroll
       for (int c = 0; c < S::kVChunks; ++c) {
         const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
@@ -254,40 +241,51 @@ __device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, cons
       __syncwarp();
     }
     tc_fence_after();
-    const uint32_t keep = uniform(i > 0);
     if (elect_one()) {
-      // N = 128 takes two pieces, not neighbours where the ring wraps: a product each
+      if (do_values) {
+        // (a product for each piece: two are not neighbours where the ring wraps)
 #pragma unroll
-      for (int c = 0; c < S::kVChunks; ++c) {
-        const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
+        for (int c = 0; c < S::kVChunks; ++c) {
+          const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
 #pragma unroll
-        for (int y = 0; y < kKeys / 16; ++y)
-          tc_mma_ts(tmem + S::kOutput + x * 128 + c * 64, tmem + x * 128 + y * 8,
-                    smem_desc(v + y * 2048, 16, 1024), value_desc, y > 0 ? 1 : keep);
+          for (int y = 0; y < kKeys / 16; ++y)
+            tc_mma_ts(output_at + c * 64, scores_at + y * 8, smem_desc(v + y * 2048, 16, 1024),
+                      value_desc, y > 0 ? 1 : keep);
+          tc_commit(smem_u32(&sh.empty[(base + c) % kSlots]));
+        }
+        if (i == tiles) tc_commit(smem_u32(&sh.o_done[x]));
+      } else if (values) {
+#pragma unroll
+        for (int c = 0; c < S::kVChunks; ++c) mbar_arrive(smem_u32(&sh.empty[(base + c) % kSlots]));
       }
-      if (i == tiles[x] - 1) tc_commit(smem_u32(&sh.o_done[x]));
-      if (x == 1 || i >= tiles[1]) {
+      // (the other warp takes as long to begin as the scores to issue)
+      mbar_arrive(smem_u32(&sh.turn[1 - x]));
+      if (do_scores) {
 #pragma unroll
-        for (int c = 0; c < S::kVChunks; ++c) tc_commit(smem_u32(&sh.empty[(base + c) % kSlots]));
+        for (int c = 0; c < S::kQChunks; ++c) {
+          const uint32_t k = ring + (base + S::kVChunks + c) % kSlots * kPieceBytes;
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            tc_mma(scores_at, smem_desc(q + c * kPieceBytes + y * 32, 16, 1024),
+                   smem_desc(k + y * 32, 16, 1024), score_desc, c + y > 0);
+        }
+        tc_commit(smem_u32(&sh.s_full[x]));
+#pragma unroll
+        for (int c = 0; c < S::kQChunks; ++c)
+          tc_commit(smem_u32(&sh.empty[(base + S::kVChunks + c) % kSlots]));
+      } else if (scores) {
+#pragma unroll
+        for (int c = 0; c < S::kQChunks; ++c)
+          mbar_arrive(smem_u32(&sh.empty[(base + S::kVChunks + c) % kSlots]));
       }
     }
     __syncwarp();
-  };
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-    if (tiles[x] > 0) scores(x, 0);
-  for (int i = 0; ok && i < n; ++i) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (i < tiles[x]) values(x, i);
-      if (i + 1 < tiles[x]) scores(x, i + 1);
-    }
   }
   if (!ok) {
     sh.abort = 1;
     set_status(a.status, kStatusTimeout);
   }
-  drain_products(&sh.drain);
+  drain_products(&sh.drain[x]);
 }
 
 template <int DN, bool F16>
@@ -419,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_u32(&sh.full[i]), 1);
-      mbar_init(smem_u32(&sh.empty[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), 2);
       sh.fills[i] = 0;
     }
     for (int x = 0; x < 2; ++x) {
@@ -427,8 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sh.s_full[x]), 1);
       mbar_init(smem_u32(&sh.p_ready[x]), kRows);
       mbar_init(smem_u32(&sh.o_done[x]), 1);
+      mbar_init(smem_u32(&sh.turn[x]), 1);
+      mbar_init(smem_u32(&sh.drain[x]), 1);
     }
-    mbar_init(smem_u32(&sh.drain), 1);
     sh.abort = 0;
     sh.q_used = 0;
     fence_barrier_init();
@@ -443,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n = uniform(max(w.tiles[0], w.tiles[1]));
   if (warp == 0)
     copy_loop<DN>(a, m, w, n, sh, q_smem, ring);
-  else if (warp == 1)
-    product_loop<DN>(a, F16, w, n, sh, q_smem, ring);
+  else if (warp <= 2)
+    product_loop<DN>(a, F16, w, warp - 1, n, sh, q_smem, ring);
   else if (warp >= 4)
     softmax_loop<DN, F16>(a, w, warp >= 8, sh);
   tc_fence_before();
