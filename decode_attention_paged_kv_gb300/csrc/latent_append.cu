@@ -4,10 +4,10 @@
 //   latent_i = c_i * rsqrt(mean(c^2) + eps) * w_i      (fp32, rounded once)
 //   y_a = x_a cos - x_b sin,  y_b = x_b cos + x_a sin  (as in rope.cuh)
 //
-// A warp takes a token's latent vector -- dc / 32 channels a lane, the sum of squares by
-// shuffles, so it is read once -- or eight of its rows of 64 rotary channels, four lanes
-// each.  Nothing is shared between warps, so one launch serves a decode step and a
-// prompt alike.
+// A warp takes a token: the latent vector, dc / 32 channels a lane, the sum of squares by
+// shuffles, and up to 40 rows of 64 rotary channels, four lanes each, the token's angles
+// in registers.  All loads of a warp (5 KB at 32 heads) are under way at once, which is
+// what a prompt is bound by; a decode step with more heads has further warps for them.
 
 #include "dkv_device.cuh"
 #include "dkv_kernels.h"
@@ -18,7 +18,8 @@ namespace dkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsPerWarp = 8;  // rotary rows
+constexpr int kTurns = 5;                // rotary rows of a lane
+constexpr int kRowsPerWarp = 8 * kTurns;  // rotary rows of a warp
 
 struct Fresh {
   int start, n;
@@ -56,24 +57,43 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
   griddep_wait();
   const int lane = threadIdx.x % 32;
   const int b = blockIdx.y;
-  // units of a token: its latent vector, then groups of rotary rows (the key's first)
-  const uint32_t units = 1 + (a.H + 1 + kRowsPerWarp - 1) / kRowsPerWarp;
+  // units of a token: its latent vector with its first rotary rows (the key's is row 0),
+  // then further rows
+  const uint32_t units = (a.H + 1 + kRowsPerWarp - 1) / kRowsPerWarp;
   const uint32_t w = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
   const int t = static_cast<int>(w / units), u = static_cast<int>(w % units);
   const Fresh nt = fresh_tokens(a, b);
   if (t >= nt.n) return;
   const int pos = nt.start + t;
+  const int j = lane % 4;
+  const bool rotated = a.rope_len > 0;
+  const Chunks ch = chunks_of<IL>(j, kLatentRope, rotated);
+  // everything that is read
+  uint4 raw[V], wt[V];
   if (u == 0) {
     const uint16_t* src = a.c + b * a.c_sb + t * a.c_st;
-    uint4 raw[V], wt[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      raw[i] = *reinterpret_cast<const uint4*>(src + 8 * (lane + 32 * i));
-      if (a.norm != nullptr) wt[i] = *reinterpret_cast<const uint4*>(a.norm + 8 * (lane + 32 * i));
-    }
-    uint16_t* row = row_of(a, b, pos);
-    if (row == nullptr) return;
+    for (int i = 0; i < V; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + 8 * (lane + 32 * i));
+  }
+  Raw rope[kTurns];
+  const int row0 = u * kRowsPerWarp + lane / 4;
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    const int h = row0 + 8 * i - 1;  // -1: the key
+    if (h < a.H)
+      rope[i] = load_raw(h < 0 ? a.k + b * a.k_sb + t * a.k_st
+                               : a.q + b * a.q_sb + t * a.q_st + h * a.q_sh,
+                         ch);
+  }
+  Angles ang;
+  if (rotated) ang = angles_of(a.cos, a.sin, kLatentRope, pos, j);
+  uint16_t* row = nullptr;
+  if (u == 0) {
+    row = row_of(a, b, pos);
     if (a.norm != nullptr) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        wt[i] = __ldg(reinterpret_cast<const uint4*>(a.norm + 8 * (lane + 32 * i)));
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -99,34 +119,25 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
         raw[i] = make_uint4(x[0], x[1], x[2], x[3]);
       }
     }
+    if (row != nullptr) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) *reinterpret_cast<uint4*>(row + 8 * (lane + 32 * i)) = raw[i];
-    return;
+      for (int i = 0; i < V; ++i) *reinterpret_cast<uint4*>(row + 8 * (lane + 32 * i)) = raw[i];
+    }
   }
-  const int h = (u - 1) * kRowsPerWarp + lane / 4 - 1;  // -1: the key
-  if (h >= a.H) return;
-  const int j = lane % 4;
-  const bool rotated = a.rope_len > 0;
-  const Chunks c = chunks_of<IL>(j, kLatentRope, rotated);
-  const uint16_t* src = h < 0 ? a.k + b * a.k_sb + t * a.k_st
-                              : a.q + b * a.q_sb + t * a.q_st + h * a.q_sh;
-  float x[16];
-  widen<F16>(load_raw(src, c), x);
-  if (rotated) rotate16<IL>(angles_of(a.cos, a.sin, kLatentRope, pos, j), x);
-  uint16_t* dst;
-  if (h < 0) {
-    dst = row_of(a, b, pos);
-    if (dst == nullptr) return;
-    dst += DC;
-  } else {
-    dst = a.q_out + b * a.o_sb + t * a.o_st + h * a.o_sh;
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    const int h = row0 + 8 * i - 1;
+    if (h >= a.H || (h < 0 && row == nullptr)) continue;
+    float x[16];
+    widen<F16>(rope[i], x);
+    if (rotated) rotate16<IL>(ang, x);
+    store16<F16>(h < 0 ? row + DC : a.q_out + b * a.o_sb + t * a.o_st + h * a.o_sh, ch, x);
   }
-  store16<F16>(dst, c, x);
 }
 
 template <int DC, bool F16, bool IL>
 cudaError_t launch_t(const LatentAppendArgs& a, cudaStream_t s) {
-  const int64_t units = 1 + ceil_div(a.H + 1, kRowsPerWarp);
+  const int64_t units = ceil_div(a.H + 1, kRowsPerWarp);
   const dim3 grid(static_cast<unsigned>(ceil_div(a.T * units, kThreads / 32)), a.B);
   return launch_pdl(latent_append_kernel<DC, F16, IL>, grid, dim3(kThreads), 0, s, a);
 }

@@ -668,7 +668,7 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
         if (whole) {
           const float sum = sh.stat_l[0][row] + sh.stat_l[1][row];
           if (sh.row_at[row] >= 0)
-            store_out(a.out, a.out_dtype, sh.row_at[row] + ch, sum > 0.f ? o[x] / sum : 0.f);
+            store_out(a.out, a.out_dtype, sh.row_at[row] + ch, sum > 0.f || sum != sum ? o[x] / sum : 0.f);
         } else {
           a.part_o[(slot * RT + row) * (128 * MB) + ch] = o[x];
         }
@@ -757,40 +757,75 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(sh.tmem, S::kColumns);
 }
 
-// Joins the parts of sequences that several shares cut, a CTA a row; writes the zeros of
+// Joins the parts of sequences that several shares cut, a CTA a row: up to four groups of
+// threads share a row's parts, each with four under way at once; writes the zeros of
 // sequences without tokens.
+constexpr int kJoinGroups = 4;
 template <int MB, int RT>
-__global__ void __launch_bounds__(32 * MB) latent_join_kernel(const LatentAttnArgs a) {
+__global__ void __launch_bounds__(32 * MB * kJoinGroups) latent_join_kernel(const LatentAttnArgs a) {
+  __shared__ float4 part[kJoinGroups - 1][32 * MB];
+  __shared__ float stat[kJoinGroups][2];
   griddep_launch_dependents();
   griddep_wait();
   const int b = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles, r = blockIdx.y;
+  const int tid = threadIdx.x % (32 * MB), group = threadIdx.x / (32 * MB);
+  const int groups = blockDim.x / (32 * MB);
+  const int2 p = a.pieces[static_cast<int64_t>(b) * a.row_tiles + rt];
   const Row at = row_of<RT>(a, rt, r);
   const Seq seq = sequence(a, b, row_of<RT>(a, rt, 0).t);
   if (at.t >= seq.n || at.h >= a.H) return;
-  const int64_t out = b * a.o_sb + at.t * a.o_st + at.h * a.o_sh + 4 * threadIdx.x;
+  const int64_t out = b * a.o_sb + at.t * a.o_st + at.h * a.o_sh + 4 * tid;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   if (seq.tiles > 0) {
-    const int2 p = a.pieces[static_cast<int64_t>(b) * a.row_tiles + rt];
     const int first = p.x / 2, late = p.x & 1;
     if (p.y <= 1 || p.x < 0 || first + p.y > a.splits) return;  // whole: written already
-    auto slot = [&](int i) {
-      return (2 * static_cast<int64_t>((first + i) * a.row_tiles + rt) + (i == 0 ? late : 0)) * RT + r;
-    };
     float top = -INFINITY, sum = 0.f;
-    for (int i = threadIdx.x % 32; i < p.y; i += 32) top = fmaxf(top, a.part_ml[2 * slot(i)]);
+#pragma unroll 1
+    for (int i0 = group; i0 < p.y; i0 += 4 * groups) {
+      float4 x[4];
+      float m[4], l[4];
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (top == -INFINITY) top = 0.f;  // (no token seen: every sum is 0)
-#pragma unroll 4
-    for (int i = 0; i < p.y; ++i) {
-      const int64_t s = slot(i);
-      const float f = ex2(a.part_ml[2 * s] - top);
-      const float4 x = *reinterpret_cast<const float4*>(a.part_o + s * (128 * MB) + 4 * threadIdx.x);
-      sum += f * a.part_ml[2 * s + 1];
+      for (int y = 0; y < 4; ++y) {
+        const int i = i0 + y * groups;
+        m[y] = -INFINITY, l[y] = 0.f, x[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i >= p.y) continue;
+        const int64_t s =
+            (2 * static_cast<int64_t>((first + i) * a.row_tiles + rt) + (i == 0 ? late : 0)) * RT + r;
+        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * s);
+        m[y] = ml.x, l[y] = ml.y;
+        x[y] = *reinterpret_cast<const float4*>(a.part_o + s * (128 * MB) + 4 * tid);
+      }
+      const float high = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
+      if (high == -INFINITY) continue;  // (no token seen so far)
+      const float f0 = ex2(top - high);
+      top = high;
+      sum *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float f = ex2(m[y] - high);
+        sum += f * l[y];
+        o.x += f * x[y].x, o.y += f * x[y].y, o.z += f * x[y].z, o.w += f * x[y].w;
+      }
+    }
+    if (tid == 0) stat[group][0] = top, stat[group][1] = sum;
+    if (group > 0) part[group - 1][tid] = o;
+    __syncthreads();
+    if (group > 0) return;
+    float high = top;
+    for (int g = 1; g < groups; ++g) high = fmaxf(high, stat[g][0]);
+    if (high == -INFINITY) high = 0.f;  // (no token seen: every sum is 0)
+    const float f0 = ex2(top - high);
+    sum *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+    for (int g = 1; g < groups; ++g) {
+      const float f = ex2(stat[g][0] - high);
+      const float4 x = part[g - 1][tid];
+      sum += f * stat[g][1];
       o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum > 0.f ? 1.f / sum : (sum == sum ? 0.f : sum);
     o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+  } else if (group > 0) {
+    return;
   }
   if (a.out_dtype == 2) {
     *reinterpret_cast<float4*>(static_cast<float*>(a.out) + out) = o;
@@ -812,7 +847,12 @@ cudaError_t launch_t(const LatentAttnArgs& a, const CUtensorMap& mql, const CUte
   e = launch_pdl(latent_attn_kernel<MB, RT>, dim3(a.ctas), dim3(kThreads), Shape<MB, RT>::kSmem, s,
                  a, mql, mqr, mc);
   if (e != cudaSuccess) return e;
-  return launch_pdl(latent_join_kernel<MB, RT>, dim3(a.B * a.row_tiles, RT), dim3(32 * MB), 0, s, a);
+  // about as many groups as a sequence has fours of parts (the whole call, us: 32 sequences
+  // of three parts, 128 heads: one group 152, four 171; one of 8, 16 heads: 12.4, 10.8)
+  const int parts = a.splits / a.B + 1;
+  const int groups = parts <= 4 ? 1 : (parts <= 8 ? 2 : kJoinGroups);
+  return launch_pdl(latent_join_kernel<MB, RT>, dim3(a.B * a.row_tiles, RT),
+                    dim3(32 * MB * groups), 0, s, a);
 }
 
 }  // namespace

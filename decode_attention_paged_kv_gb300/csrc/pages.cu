@@ -230,20 +230,19 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const ForkArgs a) 
 
 // ------------------------------------------------------------------- compact
 constexpr int kPer = kCompactChunk / kThreads;  // counts a thread
+static_assert(kPer == 4, "a vector a thread");
 
-// Bits of the thread's 16 counts that are in use, from index `at` on.
-__device__ __forceinline__ uint32_t live_bits(const PagesArgs& g, int64_t at) {
-  uint32_t m = 0;
-  if (at + kPer <= g.nb) {
-#pragma unroll
-    for (int k = 0; k < kPer; k += 4) {
-      const int4 u = ld4(g.refs + at + k);
-      m |= static_cast<uint32_t>((u.x > 0) | (u.y > 0) << 1 | (u.z > 0) << 2 | (u.w > 0) << 3) << k;
-    }
-  } else {
-    for (int k = 0; k < kPer && at + k < g.nb; ++k) m |= static_cast<uint32_t>(g.refs[at + k] > 0) << k;
-  }
-  return m;
+// The thread's four counts from index `at` on; past the end -1.
+__device__ __forceinline__ int4 four_refs(const PagesArgs& g, int64_t at) {
+  if (at + 4 <= g.nb) return ld4(g.refs + at);
+  int4 r = make_int4(-1, -1, -1, -1);
+  if (at < g.nb) r.x = g.refs[at];
+  if (at + 1 < g.nb) r.y = g.refs[at + 1];
+  if (at + 2 < g.nb) r.z = g.refs[at + 2];
+  return r;
+}
+__device__ __forceinline__ int live_of(const int4& r) {
+  return (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
 }
 
 __global__ void __launch_bounds__(kThreads) compact_count_kernel(const CompactArgs a) {
@@ -252,57 +251,75 @@ __global__ void __launch_bounds__(kThreads) compact_count_kernel(const CompactAr
   griddep_wait();
   const int64_t at = static_cast<int64_t>(blockIdx.x) * kCompactChunk + threadIdx.x * kPer;
   int total;
-  block_scan<kThreads>(__popc(live_bits(a.g, at)), sums, &total);
+  block_scan<kThreads>(live_of(four_refs(a.g, at)), sums, &total);
   if (threadIdx.x == 0) a.counts[blockIdx.x] = total;
+}
+
+// Sums of x and y over the CTA.
+__device__ __forceinline__ int2 block_sum2(int x, int y, int2* warp_sums) {
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
+  }
+  if (threadIdx.x % 32 == 0) warp_sums[threadIdx.x / 32] = make_int2(x, y);
+  __syncthreads();
+  int2 s = make_int2(0, 0);
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) s.x += warp_sums[i].x, s.y += warp_sums[i].y;
+  return s;
 }
 
 __global__ void __launch_bounds__(kThreads) compact_rank_kernel(const CompactArgs a) {
   __shared__ int sums[32];
+  __shared__ int2 pairs[2][kThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
   const PagesArgs& g = a.g;
   const int tid = threadIdx.x, chunk = blockIdx.x, chunks = gridDim.x;
-  int before, n, part = 0, all = 0;
+  const int64_t at = static_cast<int64_t>(chunk) * kCompactChunk + tid * kPer;
+  const int4 refs = four_refs(g, at);  // (before anything is written)
+  int part = 0, all = 0;
   for (int c = tid; c < chunks; c += kThreads) {
     const int x = a.counts[c];
     all += x;
     if (c < chunk) part += x;
   }
-  block_scan<kThreads>(part, sums, &before);
-  block_scan<kThreads>(all, sums, &n);
+  const int2 s = block_sum2(part, all, pairs[0]);
+  const int before = s.x, n = s.y;
   // blocks in use below n: whole chunks, and part of the one that n lies in
   int below = 0;
   for (int c = tid; c < n / kCompactChunk; c += kThreads) below += a.counts[c];
   const int64_t edge = static_cast<int64_t>(n / kCompactChunk) * kCompactChunk + tid * kPer;
   if (edge < n) {
-    uint32_t m = live_bits(g, edge);
-    if (n - edge < kPer) m &= (1u << (n - edge)) - 1u;
-    below += __popc(m);
+    const int4 r = four_refs(g, edge);
+    below += (r.x > 0) + (edge + 1 < n && r.y > 0) + (edge + 2 < n && r.z > 0) +
+             (edge + 3 < n && r.w > 0);
   }
-  int kept;
-  block_scan<kThreads>(below, sums, &kept);
+  const int kept = block_sum2(below, 0, pairs[1]).x;
   if (chunk == 0 && tid == 0) {
     a.totals[0] = n;
     a.totals[1] = n - kept;
   }
-  const int64_t at = static_cast<int64_t>(chunk) * kCompactChunk + tid * kPer;
-  const uint32_t live = live_bits(g, at);
   int unused;
-  int rank = before + block_scan<kThreads>(__popc(live), sums, &unused);
-  for (int k = 0; k < kPer && at + k < g.nb; ++k) {
-    const int i = static_cast<int>(at) + k;
-    const bool on = live >> k & 1;
+  int rank = before + block_scan<kThreads>(live_of(refs), sums, &unused);
+  const int count[4] = {refs.x, refs.y, refs.z, refs.w};
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int64_t i = at + k;
+    if (i >= g.nb) break;
+    const bool on = count[k] > 0;
     if (i < n) {
-      a.map[i] = on ? i : -1;
+      a.map[i] = on ? static_cast<int32_t>(i) : -1;
       if (on)
-        a.refs_out[i] = g.refs[i];
+        a.refs_out[i] = count[k];
       else
-        a.dst[i - rank] = i;  // (free blocks before i)
+        a.dst[i - rank] = static_cast<int32_t>(i);  // (free blocks before i)
     } else {
       a.rank[i] = on ? rank - kept : -1;
       if (on) {
-        a.src[rank - kept] = i;
-        a.count[rank - kept] = g.refs[i];
+        a.src[rank - kept] = static_cast<int32_t>(i);
+        a.count[rank - kept] = count[k];
       } else {
         a.map[i] = -1;
       }

@@ -56,7 +56,7 @@ struct CompactArgs {
   int items;                   // pieces of one move, over all pools
 };
 
-constexpr int kCompactChunk = 4096;   // refs a CTA counts
+constexpr int kCompactChunk = 1024;   // refs a CTA counts
 constexpr int kCompactPiece = 16384;  // bytes of a block that a CTA moves at a time
 
 cudaError_t launch_fork(const ForkArgs& a, cudaStream_t s);

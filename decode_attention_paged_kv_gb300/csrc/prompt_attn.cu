@@ -17,6 +17,11 @@
 // keys of the next tile before the values of this one are done with: with 96 KB of
 // queries (dn = 128) there is room for 8 pieces, a tile and three fifths.
 
+// A CTA stays for further blocks of queries: a warp takes over the launch of a CTA that has
+// not begun (cluster launch control) and passes its block on, so that copies run into the
+// next block while this one's softmax and output are under way, and blocks go to whichever
+// multiprocessor is free.
+
 #include "dkv_device.cuh"
 #include "dkv_kernels.h"
 #include "latent.h"
@@ -25,30 +30,34 @@
 namespace dkv {
 namespace {
 
-constexpr int kThreads = 384;  // warps: copies, products (two), one idle, 2 x 4 of softmax
+constexpr int kThreads = 384;  // warps: copies, products (two), schedule, 2 x 4 of softmax
 constexpr int kRows = 128;     // queries of a tile
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kPieceBytes = kKeys * 128;
 constexpr int kSlots = 8;
 constexpr float kRise = 8.f;
 
-struct Shared {
-  uint64_t full[kSlots], empty[kSlots], q_full[2], s_full[2], p_ready[2], o_done[2], turn[2], drain[2];
-  uint32_t tmem;
-  uint32_t fills[kSlots];
-  volatile int abort;
-  int q_used;  // bits: which query tiles were copied
-  int seq, block;
+// A block of queries of a head.
+struct Work {
+  int b, h;      // sequence (-1: no more work), head
+  int q0, nq;    // its query rows
+  int k0, nk;    // its key rows
+  int row;       // the first query of the block, within the sequence
+  int tiles[2];  // key tiles of the two query tiles
 };
 
-// What the CTA computes.
-struct Work {
-  int b, h;        // sequence (-1: nothing), head
-  int q0, nq;      // its query rows
-  int k0, nk;      // its key rows
-  int row;         // the first query of the block, within the sequence
-  int tiles[2];    // key tiles of the two query tiles
+struct Shared {
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t q_full[2], q_free[2], s_full[2], p_ready[2], o_done[2], o_free[2], turn[2], drain[2];
+  uint64_t work_full[2], work_free[2], taken, wanted;
+  alignas(16) uint4 handle;  // of the CTA taken over
+  uint32_t tmem;
+  uint32_t fills[kSlots], q_fills, takes;  // for the drain
+  volatile int abort;
+  Work work[2];  // by turns
 };
+// Warps that read a block's description: copies, two of products, eight of softmax.
+constexpr int kReaders = 11;
 
 struct Bounds {
   int q0, nq, k0, nk;
@@ -67,56 +76,149 @@ __device__ __forceinline__ int seen_by(const PromptArgs& a, const Work& w, int r
   return a.causal ? min(w.nk, max(0, w.nk - w.nq + row + 1)) : w.nk;
 }
 
-// The CTA's block of queries: sequences in order, heads within, blocks within from the
-// last to the first (the last sees the most keys).  Blocks of one head run side by side
-// and find its keys in the L2.
-__device__ __forceinline__ Work find_work(const PromptArgs& a, Shared& sh) {
-  __shared__ long long warp_sum[kThreads / 32];
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  if (tid == 0) sh.seq = -1;
-  long long before = 0;
-  const long long me = blockIdx.x;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    long long n = 0;
-    if (b < a.B) n = (bounds(a, b).nq + 2ll * kRows - 1) / (2 * kRows) * a.H;
-    long long x = n;
+// Which block a CTA number stands for: sequences in order, heads within, blocks within from
+// the last to the first (the last sees the most keys).  Blocks of one head run side by
+// side and find its keys in the L2.  One warp, 32 sequences at a time.
+struct Finder {
+  const PromptArgs& a;
+  int b0 = 0;
+  long long before = 0;  // blocks of the sequences before b0
+  Bounds mine;
+  long long blocks;  // of the lane's sequence, all heads
+  __device__ __forceinline__ explicit Finder(const PromptArgs& a_) : a(a_) { load(); }
+  __device__ __forceinline__ void load() {
+    const int b = b0 + static_cast<int>(threadIdx.x % 32);
+    mine = b < a.B ? bounds(a, b) : Bounds{0, 0, 0, 0};
+    blocks = (mine.nq + 2ll * kRows - 1) / (2 * kRows) * a.H;
+  }
+  __device__ __forceinline__ Work find(long long item) {
+    if (item < before) b0 = 0, before = 0, load();
+    const int lane = threadIdx.x % 32;
+    Work w{};
+    w.b = -1;
+    while (true) {
+      long long x = blocks;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const long long up = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += up;
+      for (int o = 1; o < 32; o *= 2) {
+        const long long up = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += up;
+      }
+      const long long end = before + x;
+      const uint32_t past = __ballot_sync(0xffffffffu, item < end);
+      if (past != 0) {
+        const int from = __ffs(past) - 1;
+        const int i = static_cast<int>(item - __shfl_sync(0xffffffffu, end - blocks, from));
+        w.b = b0 + from;
+        w.q0 = __shfl_sync(0xffffffffu, mine.q0, from);
+        w.nq = __shfl_sync(0xffffffffu, mine.nq, from);
+        w.k0 = __shfl_sync(0xffffffffu, mine.k0, from);
+        w.nk = __shfl_sync(0xffffffffu, mine.nk, from);
+        const int per = (w.nq - 1) / (2 * kRows) + 1;
+        w.h = i / per;
+        w.row = (per - 1 - i % per) * (2 * kRows);
+#pragma unroll
+        for (int x2 = 0; x2 < 2; ++x2) {
+          const int first = w.row + x2 * kRows;  // of the tile's queries
+          const int seen = seen_by(a, w, min(first + kRows, w.nq) - 1);
+          w.tiles[x2] = first >= w.nq || seen == 0 ? 0 : (seen - 1) / kKeys + 1;
+        }
+        return w;
+      }
+      if (b0 + 32 >= a.B) return w;
+      before = __shfl_sync(0xffffffffu, end, 31);
+      b0 += 32;
+      load();
     }
-    __syncthreads();
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    long long chunk = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) x += warp_sum[i];
-      chunk += warp_sum[i];
-    }
-    x += before;
-    if (n > 0 && me < x && me >= x - n) {
-      sh.seq = b;
-      sh.block = static_cast<int>(me - (x - n));
-    }
-    before += chunk;
-    if (before > me) break;
   }
-  __syncthreads();
-  Work w{};
-  w.b = sh.seq;
-  if (w.b < 0) return w;
-  const Bounds s = bounds(a, w.b);
-  const int blocks = (s.nq + 2 * kRows - 1) / (2 * kRows);
-  w.h = sh.block / blocks;
-  w.q0 = s.q0, w.nq = s.nq, w.k0 = s.k0, w.nk = s.nk;
-  w.row = (blocks - 1 - sh.block % blocks) * (2 * kRows);
-  for (int x = 0; x < 2; ++x) {
-    const int last = min(w.row + (x + 1) * kRows, w.nq) - 1;  // of the tile's queries
-    w.tiles[x] =
-        last < w.row + x * kRows ? 0 : (seen_by(a, w, last) + kKeys - 1) / kKeys;
+};
+
+// Takes over the launch of a CTA that has not begun, if there is one: asks ...
+__device__ __forceinline__ void take_cta(Shared& sh) {
+  ++sh.takes;
+  mbar_arrive_expect_tx(smem_u32(&sh.taken), 16);
+  fence_async_smem();
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(smem_u32(&sh.handle)),
+      "r"(smem_u32(&sh.taken))
+      : "memory");
+}
+// ... and, once the answer is there, which one it was.
+__device__ __forceinline__ bool taken_cta(const Shared& sh, uint32_t* cta) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t"
+      ".reg .pred p;\n\t"
+      ".reg .b128 h;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t"
+      "}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(&sh.handle))
+      : "memory");
+  *cta = x;
+  return ok != 0;
+}
+
+// Publishes the CTA's blocks, its own first, then those it takes over.
+__device__ __forceinline__ void schedule_loop(const PromptArgs& a, Shared& sh) {
+  const int lane = threadIdx.x % 32;
+  Finder find(a);
+  uint32_t cta = blockIdx.x;
+  bool ok = true, more = true;  // more: `cta` is a CTA to stand in for
+  for (int j = 0; ok; ++j) {
+    Work w{};
+    w.b = -1;
+    if (more) w = find.find(cta);
+    if (j >= 2)
+      ok = lanes_wait(true, smem_u32(&sh.work_free[j & 1]), ((j >> 1) - 1) & 1, a.wait_limit_ns,
+                      &sh.abort);
+    if (ok && lane == 0) {
+      sh.work[j & 1] = w;
+      mbar_arrive(smem_u32(&sh.work_full[j & 1]));
+    }
+    __syncwarp();
+    if (!more || !ok) break;
+    // not before this block's copies are all under way: a block that waits here for its
+    // turn is one that another multiprocessor could have begun
+    if (w.b >= 0) {
+      ok = lanes_wait(true, smem_u32(&sh.wanted), j & 1, a.wait_limit_ns, &sh.abort);
+      if (!ok) break;
+    }
+    if (lane == 0) take_cta(sh);
+    __syncwarp();
+    uint32_t turn = j;
+    while (true) {
+      ok = lanes_wait(true, smem_u32(&sh.taken), turn & 1, a.wait_limit_ns, &sh.abort);
+      more = ok && taken_cta(sh, &cta);
+      if (w.b >= 0 || !more) break;
+      // the grid is for the most blocks that there can be: the rest of it has none, and is
+      // taken out of the way sooner than launched
+      __syncwarp();
+      if (lane == 0) take_cta(sh);
+      __syncwarp();
+      ++turn;
+    }
+    if (w.b < 0) break;
   }
-  return w;
+  if (!ok) {
+    sh.abort = 1;
+    set_status(a.status, kStatusTimeout);
+  }
+}
+
+// The j-th block of the CTA, as the reading warps see it; false: there is none (or no word
+// of it: *ok).
+__device__ __forceinline__ bool next_work(const PromptArgs& a, Shared& sh, int j, Work* w, bool* ok) {
+  *ok = lanes_wait(true, smem_u32(&sh.work_full[j & 1]), (j >> 1) & 1, a.wait_limit_ns, &sh.abort);
+  if (!*ok) return false;
+  *w = sh.work[j & 1];
+  __syncwarp();
+  if (w->b >= 0 && threadIdx.x % 32 == 0) mbar_arrive(smem_u32(&sh.work_free[j & 1]));
+  return w->b >= 0;
 }
 
 template <int DN>
@@ -134,52 +236,70 @@ struct Maps {
 };
 
 template <int DN>
-__device__ __forceinline__ void copy_loop(const PromptArgs& a, const Maps& m, const Work& w, int n,
-                                          Shared& sh, uint32_t q_smem, uint32_t ring) {
+__device__ __forceinline__ void copy_loop(const PromptArgs& a, const Maps& m, Shared& sh,
+                                          uint32_t q_smem, uint32_t ring) {
   using S = Shape<DN>;
-  const int h = uniform(w.h), q = uniform(w.q0 + w.row), k0 = uniform(w.k0);
-  const int used = uniform((w.tiles[0] > 0 ? 1 : 0) | (w.tiles[1] > 0 ? 2 : 0));
-  if (elect_one()) {
-    sh.q_used = used;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (!(used >> x & 1)) continue;
-      const uint32_t bar = smem_u32(&sh.q_full[x]), to = q_smem + x * S::kQBytes;
-      mbar_arrive_expect_tx(bar, S::kQBytes);
-#pragma unroll
-      for (int c = 0; c < S::kQChunks - 1; ++c)
-        tma_load_4d(to + c * kPieceBytes, &m.qn, bar, 64 * c, h, q + x * kRows, 0);
-      tma_load_4d(to + (S::kQChunks - 1) * kPieceBytes, &m.qr, bar, 0, h, q + x * kRows, 0);
-    }
-  }
-  __syncwarp();
   bool ok = true;
   int at = 0;
   uint32_t round = 0;
   bool again = false;  // the ring's first round is over
-  for (int i = 0; ok && i < n; ++i) {
-    const int row = k0 + i * kKeys;
+  Work w;
+  for (int j = 0; next_work(a, sh, j, &w, &ok); ++j) {
+    const int h = uniform(w.h), q = uniform(w.q0 + w.row), k0 = uniform(w.k0);
+    const int used = uniform((w.tiles[0] > 0 ? 1 : 0) | (w.tiles[1] > 0 ? 2 : 0));
+    const int n = uniform(max(w.tiles[0], w.tiles[1]));
+    for (int i = 0; ok && i < max(n, 1); ++i) {
+      const int row = k0 + i * kKeys;
 #pragma unroll
-    for (int c = 0; c < S::kPieces; ++c) {
-      if (again && !lanes_wait(true, smem_u32(&sh.empty[at]), round ^ 1, a.wait_limit_ns, &sh.abort)) {
-        ok = false;
-        break;
+      for (int c = 0; c < S::kPieces; ++c) {
+        if (i == 0 && c == S::kQChunks) {  // the queries, after the first keys
+          if (j > 0)
+            ok = lanes_wait(true, smem_u32(&sh.q_free[0]), (j - 1) & 1, a.wait_limit_ns, &sh.abort) &&
+                 lanes_wait(true, smem_u32(&sh.q_free[1]), (j - 1) & 1, a.wait_limit_ns, &sh.abort);
+          if (!ok) break;
+          if (elect_one()) {
+            ++sh.q_fills;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t bar = smem_u32(&sh.q_full[x]), to = q_smem + x * S::kQBytes;
+              if (!(used >> x & 1)) {
+                mbar_arrive(bar);
+                continue;
+              }
+              mbar_arrive_expect_tx(bar, S::kQBytes);
+#pragma unroll
+              for (int d = 0; d < S::kQChunks - 1; ++d)
+                tma_load_4d(to + d * kPieceBytes, &m.qn, bar, 64 * d, h, q + x * kRows, 0);
+              tma_load_4d(to + (S::kQChunks - 1) * kPieceBytes, &m.qr, bar, 0, h, q + x * kRows, 0);
+            }
+          }
+          __syncwarp();
+        }
+        if (i >= n) continue;
+        if (again &&
+            !lanes_wait(true, smem_u32(&sh.empty[at]), round ^ 1, a.wait_limit_ns, &sh.abort)) {
+          ok = false;
+          break;
+        }
+        const int slot = uniform(at);
+        const uint32_t bar = smem_u32(&sh.full[slot]), to = ring + slot * kPieceBytes;
+        if (elect_one()) {
+          ++sh.fills[slot];
+          mbar_arrive_expect_tx(bar, kPieceBytes);
+          if (c < S::kQChunks - 1)
+            tma_load_4d(to, &m.kn, bar, 64 * c, h, row, 0);
+          else if (c == S::kQChunks - 1)
+            tma_load_4d(to, &m.kr, bar, 0, row, 0, 0);
+          else
+            tma_load_4d(to, &m.v, bar, 64 * (c - S::kQChunks), h, row, 0);
+        }
+        __syncwarp();
+        if (++at == kSlots) at = 0, round ^= 1, again = true;
       }
-      const int slot = uniform(at);
-      const uint32_t bar = smem_u32(&sh.full[slot]), to = ring + slot * kPieceBytes;
-      if (elect_one()) {
-        ++sh.fills[slot];
-        mbar_arrive_expect_tx(bar, kPieceBytes);
-        if (c < S::kQChunks - 1)
-          tma_load_4d(to, &m.kn, bar, 64 * c, h, row, 0);
-        else if (c == S::kQChunks - 1)
-          tma_load_4d(to, &m.kr, bar, 0, row, 0, 0);
-        else
-          tma_load_4d(to, &m.v, bar, 64 * (c - S::kQChunks), h, row, 0);
-      }
-      __syncwarp();
-      if (++at == kSlots) at = 0, round ^= 1, again = true;
     }
+    if (!ok) break;
+    if (elect_one()) mbar_arrive(smem_u32(&sh.wanted));
+    __syncwarp();
   }
   if (!ok) {
     sh.abort = 1;
@@ -193,8 +313,8 @@ __device__ __forceinline__ void copy_loop(const PromptArgs& a, const Maps& m, co
 // which the other's fill.  They take turns all the same: left alone they fall into step,
 // both in the softmax at one time and both at the tensor cores at another.
 template <int DN>
-__device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, const Work& w, int x,
-                                             int n, Shared& sh, uint32_t q_smem, uint32_t ring) {
+__device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, int x, Shared& sh,
+                                             uint32_t q_smem, uint32_t ring) {
   using S = Shape<DN>;
   const int lane = threadIdx.x % 32;
   const uint32_t tmem = static_cast<uint32_t>(uniform(sh.tmem));
@@ -202,84 +322,99 @@ __device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, cons
   const uint32_t q = q_smem + x * S::kQBytes;
   const uint32_t score_desc = mma_desc(f16, kRows, kKeys, false, false);
   const uint32_t value_desc = mma_desc(f16, kRows, 64, false, true);
-  const int tiles = uniform(w.tiles[x]), nk = uniform(w.nk);
   bool ok = true;
-  // Step i: the values of key tile i - 1 and the scores of key tile i, whose pieces follow
-  // one another.  One wait for all that they need, one go: a second wait between them
-  // left the tensor cores idle for 350 cycles.
-  for (int i = 0; i <= n; ++i) {
-    const bool values = i > 0, scores = i < n;            // steps that there are
-    const bool use_values = values && i <= tiles, use_scores = i < tiles;  // and x takes part in
-    const int piece = i * S::kPieces - S::kVChunks;  // the first: of the values
-    const int p = max(piece + lane, 0);
-    uint32_t bar = smem_u32(&sh.full[p % kSlots]), parity = (p / kSlots) & 1;
-    bool wanted = lane < S::kVChunks ? values : (scores && lane < S::kPieces);
-    if (lane == S::kPieces) {
-      bar = smem_u32(&sh.p_ready[x]), parity = (i - 1) & 1, wanted = use_values;
-    } else if (lane == S::kPieces + 1) {
-      bar = smem_u32(&sh.q_full[x]), parity = 0, wanted = use_scores;
-    } else if (lane == S::kPieces + 2) {
-      bar = smem_u32(&sh.turn[x]), parity = (i - 1 + x) & 1, wanted = i + x > 0;
-    }
-    ok = lanes_wait(wanted, bar, parity, a.wait_limit_ns, &sh.abort);
-    if (!ok) break;
-    const int base = uniform(piece + 8 * kSlots), keep = uniform(i > 1);
-    const bool do_values = uniform(use_values), do_scores = uniform(use_scores);
-    const int valid = nk - (i - 1) * kKeys;
-    if (use_values && valid < kKeys) {
-      // rows past the sequence may hold anything; a weight of 0 times NaN is NaN (both
-      // query tiles' warps clear them: with the same zeros)
-#pragma unroll
-      for (int c = 0; c < S::kVChunks; ++c) {
-        const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
-        for (int y = lane; y < (kKeys - valid) * 8; y += 32)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + valid * 128 + y * 16),
-                       "r"(0)
-                       : "memory");
+  // of the blocks so far: pieces (modulo two rounds of the ring), steps, key tiles of x
+  int pieces = 0, steps = 0, done = 0;
+  Work w;
+  for (int j = 0; next_work(a, sh, j, &w, &ok); ++j) {
+    const int n = uniform(max(w.tiles[0], w.tiles[1]));
+    const int tiles = uniform(w.tiles[x]), nk = uniform(w.nk);
+    // Step i: the values of key tile i - 1 and the scores of key tile i, whose pieces follow
+    // one another.  One wait for all that they need, one go: a second wait between them
+    // left the tensor cores idle for 350 cycles.
+    for (int i = 0; i <= n; ++i) {
+      const bool values = i > 0, scores = i < n;  // what the step has
+      const bool use_values = values && i <= tiles, use_scores = i < tiles;  // for x
+      const int piece = pieces + i * S::kPieces - S::kVChunks;  // the first: of the values
+      const int p = max(piece + lane, 0);
+      uint32_t bar = smem_u32(&sh.full[p % kSlots]), parity = (p / kSlots) & 1;
+      bool wanted = lane < S::kVChunks ? values : (scores && lane < S::kPieces);
+      if (lane == S::kPieces) {
+        bar = smem_u32(&sh.p_ready[x]), parity = (done + i - 1) & 1, wanted = use_values;
+      } else if (lane == S::kPieces + 1) {
+        bar = smem_u32(&sh.q_full[x]), parity = j & 1, wanted = use_scores && i == 0;
+      } else if (lane == S::kPieces + 2) {
+        bar = smem_u32(&sh.turn[x]), parity = (steps + i - 1 + x) & 1, wanted = steps + i + x > 0;
+      } else if (lane == S::kPieces + 3) {  // that the last block's output has been read
+        bar = smem_u32(&sh.o_free[x]), parity = (j - 1) & 1, wanted = j > 0 && i == 1;
       }
-      fence_async_smem();
-      __syncwarp();
-    }
-    tc_fence_after();
-    if (elect_one()) {
-      if (do_values) {
-        // (a product for each piece: two are not neighbours where the ring wraps)
+      ok = lanes_wait(wanted, bar, parity, a.wait_limit_ns, &sh.abort);
+      if (!ok) break;
+      const int base = uniform(piece + 8 * kSlots), keep = uniform(i > 1);
+      const bool do_values = uniform(use_values), do_scores = uniform(use_scores);
+      const int valid = nk - (i - 1) * kKeys;
+      if (use_values && valid < kKeys) {
+        // rows past the sequence may hold anything; a weight of 0 times NaN is NaN (both
+        // query tiles' warps clear them: with the same zeros)
 #pragma unroll
         for (int c = 0; c < S::kVChunks; ++c) {
           const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
-#pragma unroll
-          for (int y = 0; y < kKeys / 16; ++y)
-            tc_mma_ts(output_at + c * 64, scores_at + y * 8, smem_desc(v + y * 2048, 16, 1024),
-                      value_desc, y > 0 ? 1 : keep);
-          tc_commit(smem_u32(&sh.empty[(base + c) % kSlots]));
+          for (int y = lane; y < (kKeys - valid) * 8; y += 32)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + valid * 128 + y * 16),
+                         "r"(0)
+                         : "memory");
         }
-        if (i == tiles) tc_commit(smem_u32(&sh.o_done[x]));
-      } else if (values) {
-#pragma unroll
-        for (int c = 0; c < S::kVChunks; ++c) mbar_arrive(smem_u32(&sh.empty[(base + c) % kSlots]));
+        fence_async_smem();
+        __syncwarp();
       }
-      // (the other warp takes as long to begin as the scores to issue)
-      mbar_arrive(smem_u32(&sh.turn[1 - x]));
-      if (do_scores) {
+      tc_fence_after();
+      if (elect_one()) {
+        if (do_values) {
+          // (a product for each piece: two are not neighbours where the ring wraps)
 #pragma unroll
-        for (int c = 0; c < S::kQChunks; ++c) {
-          const uint32_t k = ring + (base + S::kVChunks + c) % kSlots * kPieceBytes;
+          for (int c = 0; c < S::kVChunks; ++c) {
+            const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            tc_mma(scores_at, smem_desc(q + c * kPieceBytes + y * 32, 16, 1024),
-                   smem_desc(k + y * 32, 16, 1024), score_desc, c + y > 0);
+            for (int y = 0; y < kKeys / 16; ++y)
+              tc_mma_ts(output_at + c * 64, scores_at + y * 8, smem_desc(v + y * 2048, 16, 1024),
+                        value_desc, y > 0 ? 1 : keep);
+            tc_commit(smem_u32(&sh.empty[(base + c) % kSlots]));
+          }
+        } else if (values) {
+#pragma unroll
+          for (int c = 0; c < S::kVChunks; ++c) mbar_arrive(smem_u32(&sh.empty[(base + c) % kSlots]));
         }
-        tc_commit(smem_u32(&sh.s_full[x]));
+        // (the other warp takes as long to begin as the scores to issue)
+        mbar_arrive(smem_u32(&sh.turn[1 - x]));
+        if (do_scores) {
 #pragma unroll
-        for (int c = 0; c < S::kQChunks; ++c)
-          tc_commit(smem_u32(&sh.empty[(base + S::kVChunks + c) % kSlots]));
-      } else if (scores) {
+          for (int c = 0; c < S::kQChunks; ++c) {
+            const uint32_t k = ring + (base + S::kVChunks + c) % kSlots * kPieceBytes;
 #pragma unroll
-        for (int c = 0; c < S::kQChunks; ++c)
-          mbar_arrive(smem_u32(&sh.empty[(base + S::kVChunks + c) % kSlots]));
+            for (int y = 0; y < 4; ++y)
+              tc_mma(scores_at, smem_desc(q + c * kPieceBytes + y * 32, 16, 1024),
+                     smem_desc(k + y * 32, 16, 1024), score_desc, c + y > 0);
+          }
+          tc_commit(smem_u32(&sh.s_full[x]));
+#pragma unroll
+          for (int c = 0; c < S::kQChunks; ++c)
+            tc_commit(smem_u32(&sh.empty[(base + S::kVChunks + c) % kSlots]));
+        } else if (scores) {
+#pragma unroll
+          for (int c = 0; c < S::kQChunks; ++c)
+            mbar_arrive(smem_u32(&sh.empty[(base + S::kVChunks + c) % kSlots]));
+        }
+        if (i == n) {  // the block's queries are free, its output is complete
+          tc_commit(smem_u32(&sh.q_free[x]));
+          tc_commit(smem_u32(&sh.o_done[x]));
+        }
       }
+      __syncwarp();
     }
-    __syncwarp();
+    if (!ok) break;
+    pieces = (pieces + n * S::kPieces) % (2 * kSlots);
+    steps += n + 1;
+    done += tiles;
   }
   if (!ok) {
     sh.abort = 1;
@@ -289,118 +424,120 @@ __device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, cons
 }
 
 template <int DN, bool F16>
-__device__ __forceinline__ void softmax_loop(const PromptArgs& a, const Work& w, int x, Shared& sh) {
+__device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared& sh) {
   using S = Shape<DN>;
   const int lane = threadIdx.x % 32, quarter = threadIdx.x / 32 % 4;
-  const int row = w.row + x * kRows + 32 * quarter + lane;  // within the sequence
-  const bool on = row < w.nq;
-  const int seen = on ? seen_by(a, w, row) : 0;
   const uint32_t tq = sh.tmem + (static_cast<uint32_t>(32 * quarter) << 16);
   const uint32_t ts = tq + x * 128, to = tq + S::kOutput + x * 128;
   const float scale = fabsf(a.scale_log2);
-  float m = -INFINITY, l = 0.f;
   bool ok = true;
-  const int n = w.tiles[x];
-  for (int i = 0; i < n; ++i) {
-    ok = mbar_wait_bounded(smem_u32(&sh.s_full[x]), i & 1, a.wait_limit_ns, &sh.abort);
-    ok = __all_sync(0xffffffffu, ok);
+  int done = 0;  // key tiles of the blocks so far
+  Work w;
+  for (int j = 0; next_work(a, sh, j, &w, &ok); ++j) {
+    const int row = w.row + x * kRows + 32 * quarter + lane;  // within the sequence
+    const bool on = row < w.nq;
+    const int seen = on ? seen_by(a, w, row) : 0;
+    float m = -INFINITY, l = 0.f;
+    const int n = w.tiles[x];
+    for (int i = 0; i < n; ++i, ++done) {
+      ok = lanes_wait(true, smem_u32(&sh.s_full[x]), done & 1, a.wait_limit_ns, &sh.abort);
+      if (!ok) break;
+      tc_fence_after();
+      float s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, reinterpret_cast<float(&)[32]>(s[32 * c]));
+      tmem_wait_ld();
+      if (a.scale_log2 < 0.f) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] = -s[c];
+      }
+      const int limit = seen - i * kKeys;
+      if (__any_sync(0xffffffffu, limit < kKeys)) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] = c < limit ? s[c] : -INFINITY;
+      }
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < 128; ++c) top[c % 4] = fmaxf(top[c % 4], s[c]);
+      const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+      if (i == 0) {
+        m = high;
+      } else {
+        const bool rise = high > m + kRise;
+        if (__any_sync(0xffffffffu, rise)) {
+          // (the products of the tile before were done when these scores were)
+          const float f = rise ? ex2(m - high) : 1.f;
+          if (rise) m = high;
+          l *= f;
+#pragma unroll 1
+          for (int c = 0; c < DN; c += 16) {
+            float o[16];
+            tmem_ld16(to + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] *= f;
+            tmem_st16(to + c, o);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      float sum[4] = {};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t p[32];
+#pragma unroll
+        for (int y = 0; y < 32; ++y) {
+          const float p0 = ex2(fmaf(s[64 * c + 2 * y], scale, -ref));
+          const float p1 = ex2(fmaf(s[64 * c + 2 * y + 1], scale, -ref));
+          sum[y % 4] += p0 + p1;
+          p[y] = pack2<F16>(p0, p1);
+        }
+        tmem_st32(ts + 32 * c, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sh.p_ready[x]));
+    }
+    if (ok) ok = lanes_wait(true, smem_u32(&sh.o_done[x]), j & 1, a.wait_limit_ns, &sh.abort);
     if (!ok) break;
     tc_fence_after();
-    float s[128];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, reinterpret_cast<float(&)[32]>(s[32 * c]));
-    tmem_wait_ld();
-    if (a.scale_log2 < 0.f) {
-#pragma unroll
-      for (int c = 0; c < 128; ++c) s[c] = -s[c];
-    }
-    const int limit = seen - i * kKeys;
-    if (__any_sync(0xffffffffu, limit < kKeys)) {
-#pragma unroll
-      for (int c = 0; c < 128; ++c) s[c] = c < limit ? s[c] : -INFINITY;
-    }
-    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-    for (int c = 0; c < 128; ++c) top[c % 4] = fmaxf(top[c % 4], s[c]);
-    const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-    if (i == 0) {
-      m = high;
-    } else {
-      const bool rise = high > m + kRise;
-      if (__any_sync(0xffffffffu, rise)) {
-        // (the products of the tile before were done when these scores were)
-        const float f = rise ? ex2(m - high) : 1.f;
-        if (rise) m = high;
-        l *= f;
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    const int64_t at = static_cast<int64_t>(w.q0 + row) * a.o_st + w.h * a.o_sh;
 #pragma unroll 1
-        for (int c = 0; c < DN; c += 16) {
-          float o[16];
-          tmem_ld16(to + c, o);
-          tmem_wait_ld();
+    for (int c = 0; c < DN; c += 16) {
+      float o[16];
+      if (n > 0) {
+        tmem_ld16(to + c, o);
+        tmem_wait_ld();
+      }
 #pragma unroll
-          for (int y = 0; y < 16; ++y) o[y] *= f;
-          tmem_st16(to + c, o);
+      for (int y = 0; y < 16; ++y) o[y] = l > 0.f || l != l ? o[y] * inv : 0.f;
+      if (!on) continue;
+      if (a.out_dtype == 2) {
+        float4* out = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + c);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          out[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+      } else {
+        uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + c);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          uint32_t v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = a.out_dtype == 1 ? pack2<true>(o[8 * y + 2 * e], o[8 * y + 2 * e + 1])
+                                    : pack2<false>(o[8 * y + 2 * e], o[8 * y + 2 * e + 1]);
+          out[y] = make_uint4(v[0], v[1], v[2], v[3]);
         }
       }
     }
-    const float ref = m == -INFINITY ? 0.f : m;
-    float sum[4] = {};
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t p[32];
-#pragma unroll
-      for (int y = 0; y < 32; ++y) {
-        const float p0 = ex2(fmaf(s[64 * c + 2 * y], scale, -ref));
-        const float p1 = ex2(fmaf(s[64 * c + 2 * y + 1], scale, -ref));
-        sum[y % 4] += p0 + p1;
-        p[y] = pack2<F16>(p0, p1);
-      }
-      tmem_st32(ts + 32 * c, p);
-    }
-    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    tmem_wait_st();
     tc_fence_before();
-    mbar_arrive(smem_u32(&sh.p_ready[x]));
-  }
-  if (ok && n > 0) {
-    ok = mbar_wait_bounded(smem_u32(&sh.o_done[x]), 0, a.wait_limit_ns, &sh.abort);
-    ok = __all_sync(0xffffffffu, ok);
-    tc_fence_after();
+    mbar_arrive(smem_u32(&sh.o_free[x]));
   }
   if (!ok) {
     sh.abort = 1;
     set_status(a.status, kStatusTimeout);
-    return;
-  }
-  const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-  const int64_t at = static_cast<int64_t>(w.q0 + row) * a.o_st + w.h * a.o_sh;
-#pragma unroll 1
-  for (int c = 0; c < DN; c += 16) {
-    float o[16];
-    if (n > 0) {
-      tmem_ld16(to + c, o);
-      tmem_wait_ld();
-    }
-#pragma unroll
-    for (int y = 0; y < 16; ++y) o[y] = l > 0.f || l != l ? o[y] * inv : 0.f;
-    if (!on) continue;
-    if (a.out_dtype == 2) {
-      float4* out = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + c);
-#pragma unroll
-      for (int y = 0; y < 4; ++y)
-        out[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-    } else {
-      uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + c);
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint32_t v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[e] = a.out_dtype == 1 ? pack2<true>(o[8 * y + 2 * e], o[8 * y + 2 * e + 1])
-                                  : pack2<false>(o[8 * y + 2 * e], o[8 * y + 2 * e + 1]);
-        out[y] = make_uint4(v[0], v[1], v[2], v[3]);
-      }
-    }
   }
 }
 
@@ -422,39 +559,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&sh.q_full[x]), 1);
+      mbar_init(smem_u32(&sh.q_free[x]), 1);
       mbar_init(smem_u32(&sh.s_full[x]), 1);
       mbar_init(smem_u32(&sh.p_ready[x]), kRows);
       mbar_init(smem_u32(&sh.o_done[x]), 1);
+      mbar_init(smem_u32(&sh.o_free[x]), kRows);
       mbar_init(smem_u32(&sh.turn[x]), 1);
       mbar_init(smem_u32(&sh.drain[x]), 1);
+      mbar_init(smem_u32(&sh.work_full[x]), 1);
+      mbar_init(smem_u32(&sh.work_free[x]), kReaders);
     }
+    mbar_init(smem_u32(&sh.taken), 1);
+    mbar_init(smem_u32(&sh.wanted), 1);
     sh.abort = 0;
-    sh.q_used = 0;
+    sh.q_fills = sh.takes = 0;
     fence_barrier_init();
   }
-  griddep_wait();
-  const Work w = find_work(a, sh);
-  if (w.b < 0) return;  // (the grid is for the most blocks that there can be)
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const int n = uniform(max(w.tiles[0], w.tiles[1]));
+  griddep_wait();
   if (warp == 0)
-    copy_loop<DN>(a, m, w, n, sh, q_smem, ring);
+    copy_loop<DN>(a, m, sh, q_smem, ring);
   else if (warp <= 2)
-    product_loop<DN>(a, F16, w, warp - 1, n, sh, q_smem, ring);
-  else if (warp >= 4)
-    softmax_loop<DN, F16>(a, w, warp >= 8, sh);
+    product_loop<DN>(a, F16, warp - 1, sh, q_smem, ring);
+  else if (warp == 3)
+    schedule_loop(a, sh);
+  else
+    softmax_loop<DN, F16>(a, warp >= 8, sh);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) {  // no copy is in flight when the CTA ends
+  if (warp == 0) {  // nothing that writes shared memory is in flight when the CTA ends
     const int lane = threadIdx.x;
     if (lane < kSlots && sh.fills[lane] > 0)
       mbar_wait_bounded(smem_u32(&sh.full[lane]), (sh.fills[lane] - 1) & 1, kDrainNs, nullptr);
-    if (lane >= 30 && (sh.q_used >> (lane - 30) & 1))
-      mbar_wait_bounded(smem_u32(&sh.q_full[lane - 30]), 0, kDrainNs, nullptr);
+    if (lane >= 30 && sh.q_fills > 0)
+      mbar_wait_bounded(smem_u32(&sh.q_full[lane - 30]), (sh.q_fills - 1) & 1, kDrainNs, nullptr);
+    if (lane == 29 && sh.takes > 0)
+      mbar_wait_bounded(smem_u32(&sh.taken), (sh.takes - 1) & 1, kDrainNs, nullptr);
     __syncwarp();
   }
   if (warp == 1) tmem_dealloc(sh.tmem, 512);
