@@ -39,8 +39,10 @@ constexpr int kTile = kLatentTile;
 constexpr int kChunkBytes = kTile * 128;  // 64 tokens x 64 channels
 constexpr int kPairBytes = 2 * kChunkBytes;
 constexpr float kRise = 8.f;  // how far (log2) a score may pass the reference
-// Shortest share of a CTA, in tiles.
-constexpr int kMinShare = 2;
+// Tiles up to which each has a CTA; past it a share is two at least.  (us: two sequences of
+// 1K tokens, 16 heads: one tile a share 12.8, two 14.1; one of 8K: 19.2 and 16.4, of which
+// the join of 128 parts is a third.)
+constexpr int kSingleTiles = 32;
 
 // Shared memory: queries, then two rings that tiles pass through in pieces -- pairs of
 // latent chunks (128 channels, what one product of the values takes) and rotated keys --
@@ -119,7 +121,7 @@ __device__ __forceinline__ Share share_of(const LatentAttnArgs& a, int split, in
   if (mine != 0) atomicAdd(&all, static_cast<unsigned long long>(mine));
   __syncthreads();
   w.total = static_cast<int64_t>(all);
-  const int64_t most = (w.total + kMinShare - 1) / kMinShare;
+  const int64_t most = w.total <= kSingleTiles ? w.total : (w.total + 1) / 2;
   w.splits = static_cast<int>(most < a.splits ? most : a.splits);
   w.split = split;
   if (split >= w.splits) return w;  // (no work: begin == end)
@@ -244,7 +246,8 @@ __device__ __forceinline__ void copy_loop(const LatentAttnArgs& a, const CUtenso
   Ring<S::kPairs> pair;
   Ring<S::kKeys> key;
   const int block = c.block == 0 ? kTile : c.block;  // tokens of a copy
-  int turn = 0;
+  const int lane = threadIdx.x % 32;
+  int turn = 0, ahead = 0;
   uint32_t filled = 0;  // bits: the ring's first round is over (pairs, then keys)
   bool ok = true;
   TileWalk k(a, w, first_t);
@@ -252,21 +255,24 @@ __device__ __forceinline__ void copy_loop(const LatentAttnArgs& a, const CUtenso
     k.step();
     const int b = k.b;
     const int j0 = k.tile * kTile;
-    // blocks that hold tokens of the sequence
+    // blocks that hold tokens of the sequence; their table entries are read a tile ahead
+    // (a read takes as long as a third of a tile's copies)
     const int blocks = min(kTile / block, (k.len - j0 + block - 1) / block);
     int blk[4] = {b, b, b, b};
     if (c.block > 0) {
       const int32_t* bt = c.bt + b * c.bts + j0 / block;
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        if (p >= blocks) break;
-        int x = bt[p];
-        if (x < 0 || x >= c.nblocks) {
-          set_status(a.status, kStatusCheck);
-          x = min(max(x, 0), c.nblocks - 1);
-        }
-        blk[p] = uniform(x);
+      int entry = ahead;
+      if (k.first) entry = lane < blocks ? bt[lane] : 0;
+      if (k.left > 1) {
+        const int more = min(kTile / block, (k.len - j0 - kTile + block - 1) / block);
+        ahead = lane < more ? bt[kTile / block + lane] : 0;
       }
+      if (lane < blocks && (entry < 0 || entry >= c.nblocks)) {
+        set_status(a.status, kStatusCheck);
+        entry = min(max(entry, 0), c.nblocks - 1);
+      }
+#pragma unroll
+      for (int p = 0; p < 4; ++p) blk[p] = uniform(lane == p ? entry : 0);
     }
     const int row = c.block == 0 ? j0 : 0;
 #pragma unroll
