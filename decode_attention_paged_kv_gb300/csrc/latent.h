@@ -50,6 +50,7 @@ struct LatentAttnArgs {
   int splits;     // CTAs that share the tokens of a row tile, at most
   int q_box;      // rows of a query copy: a tile's, or 8
   int ctas;
+  int weighted;   // row tiles take CTAs by their tiles (at most kMaxWeighted of them)
   int2* pieces;   // [B, row_tiles]: where a sequence's parts lie
   float* part_ml;  // [splits * row_tiles, 2, rows of a tile, 2]
   float* part_o;   // [splits * row_tiles, 2, rows of a tile, dc]
@@ -63,6 +64,7 @@ struct LatentPlan {
 };
 constexpr int kLatentTile = 64;  // tokens
 constexpr int kLatentCtas = 152;
+constexpr int kMaxWeighted = 8;
 
 struct PromptArgs {
   int B, H;

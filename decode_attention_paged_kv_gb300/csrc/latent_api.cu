@@ -94,7 +94,10 @@ dkv::LatentPlan latent_plan(const dkv_latent_attn* p, const dkv_latent_cache* c)
   const int64_t splits = tiles < fit ? tiles : fit;
   L.splits = static_cast<int>(splits < 1 ? 1 : splits);
   L.ctas = L.splits * L.row_tiles;
-  const size_t slots = L.splits > 1 ? 2 * static_cast<size_t>(L.ctas) * L.tile_rows : 0;
+  // (a bound that only rises with the sizes, so that a workspace serves smaller calls too)
+  const int64_t most = tiles * L.row_tiles;
+  const size_t slots =
+      2 * static_cast<size_t>(most < dkv::kLatentCtas ? most : dkv::kLatentCtas) * L.tile_rows;
   L.pieces = DKV_WORKSPACE_HEADER_BYTES;
   L.part_ml = align_up(L.pieces + 8 * static_cast<size_t>(p->batch) * L.row_tiles);
   L.part_o = align_up(L.part_ml + 8 * slots);
@@ -268,6 +271,8 @@ dkv_status dkv_latent_decode_attn(const dkv_latent_attn* p, const dkv_latent_cac
   a.row_tiles = L.row_tiles;
   a.splits = L.splits;
   a.ctas = L.ctas;
+  a.weighted = p->new_tokens > 1 && p->new_lens != nullptr && L.splits > 1 && L.row_tiles > 1 &&
+               L.row_tiles <= dkv::kMaxWeighted;
   a.pieces = reinterpret_cast<int2*>(ws + L.pieces);
   a.part_ml = reinterpret_cast<float*>(ws + L.part_ml);
   a.part_o = reinterpret_cast<float*>(ws + L.part_o);

@@ -43,6 +43,7 @@ constexpr float kRise = 8.f;  // how far (log2) a score may pass the reference
 // 1K tokens, 16 heads: one tile a share 12.8, two 14.1; one of 8K: 19.2 and 16.4, of which
 // the join of 128 parts is a third.)
 constexpr int kSingleTiles = 32;
+constexpr int kContiguous = 1 << 30;  // of a sequence's parts: the CTAs of a row tile follow one another
 
 // Shared memory: queries, then two rings that tiles pass through in pieces -- pairs of
 // latent chunks (128 channels, what one product of the values takes) and rotated keys --
@@ -100,30 +101,68 @@ __device__ __forceinline__ Seq sequence(const LatentAttnArgs& a, int b, int firs
   return {len, n, tiles};
 }
 
-// The CTA's share: tiles [begin, end) of the row tile's `total`, in sequence `b` from tile
+// The CTA's share: tiles [begin, end) of its row tile's `total`, in sequence `b` from tile
 // `off` on.
 struct Share {
   int64_t begin, end, total;
-  int splits, split;
+  int rt, first_t;    // the row tile, its first new token
+  int splits, split;  // CTAs of the row tile, and which this is
+  int first_cta, stride;  // their numbers
   int b, off;
 };
-__device__ __forceinline__ Share share_of(const LatentAttnArgs& a, int split, int first_t,
-                                          Shared& sh) {
+
+// Row r of a row tile: its new token and head.
+struct Row {
+  int t, h;
+};
+template <int RT>
+__device__ __forceinline__ Row row_of(const LatentAttnArgs& a, int rt, int r) {
+  const int g = rt * (RT / 8) + r / 8;
+  return {g / a.groups, (g % a.groups) * 8 + r % 8};
+}
+
+// Row tiles have as many CTAs each, side by side, so that they are at the same tokens at the
+// same time; where sequences have different numbers of new tokens, row tiles of the later
+// ones have fewer sequences, and fewer CTAs.
+template <int RT>
+__device__ __forceinline__ Share share_of(const LatentAttnArgs& a, Shared& sh) {
+  __shared__ unsigned long long tiles_of[kMaxWeighted];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   Share w{};
-  int64_t mine = 0;
-  for (int b = tid; b < a.B; b += kThreads) mine += sequence(a, b, first_t).tiles;
-  // (2^14 sequences of 2^25 tiles: counted in 64 bits)
-  __shared__ unsigned long long all;
+  w.rt = blockIdx.x % a.row_tiles, w.split = blockIdx.x / a.row_tiles;
+  w.splits = a.splits, w.first_cta = w.rt, w.stride = a.row_tiles;
+  const int counted = a.weighted ? a.row_tiles : 1;
+  if (tid < counted) tiles_of[tid] = 0;
   __syncthreads();
-  if (tid == 0) all = 0;
+  for (int r = 0; r < counted; ++r) {
+    const int first_t = row_of<RT>(a, a.weighted ? r : w.rt, 0).t;
+    int64_t mine = 0;  // (2^14 sequences of 2^25 tiles: counted in 64 bits)
+    for (int b = tid; b < a.B; b += kThreads) mine += sequence(a, b, first_t).tiles;
+    if (mine != 0) atomicAdd(&tiles_of[r], static_cast<unsigned long long>(mine));
+  }
   __syncthreads();
-  if (mine != 0) atomicAdd(&all, static_cast<unsigned long long>(mine));
-  __syncthreads();
-  w.total = static_cast<int64_t>(all);
+  w.total = static_cast<int64_t>(tiles_of[0]);
+  if (a.weighted) {
+    int64_t all = 0;
+    for (int r = 0; r < counted; ++r) all += static_cast<int64_t>(tiles_of[r]);
+    int cta = blockIdx.x, start = 0;
+    for (int r = 0; r < counted; ++r) {
+      const int64_t mine = static_cast<int64_t>(tiles_of[r]);
+      // (one each, and the rest by their tiles)
+      const int n =
+          1 + (all > 0 ? static_cast<int>((a.ctas - a.row_tiles) * mine / all) : 0);
+      if (cta < start + n || r == counted - 1) {
+        w.rt = r, w.split = cta - start, w.splits = n, w.total = mine;
+        break;
+      }
+      start += n;
+    }
+    w.first_cta = start, w.stride = 1;
+  }
+  w.first_t = row_of<RT>(a, w.rt, 0).t;
+  const int first_t = w.first_t, split = w.split;
   const int64_t most = w.total <= kSingleTiles ? w.total : (w.total + 1) / 2;
-  w.splits = static_cast<int>(most < a.splits ? most : a.splits);
-  w.split = split;
+  if (most < w.splits) w.splits = static_cast<int>(most);
   if (split >= w.splits) return w;  // (no work: begin == end)
   w.begin = split * w.total / w.splits;
   w.end = (split + 1) * w.total / w.splits;
@@ -223,16 +262,6 @@ __device__ __forceinline__ void store_out(void* out, int dtype, int64_t at, floa
     static_cast<__half*>(out)[at] = __float2half_rn(y);
   else
     static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(y);
-}
-
-// Row r of a row tile: its new token and head.
-struct Row {
-  int t, h;
-};
-template <int RT>
-__device__ __forceinline__ Row row_of(const LatentAttnArgs& a, int rt, int r) {
-  const int g = rt * (RT / 8) + r / 8;
-  return {g / a.groups, (g % a.groups) * 8 + r % 8};
 }
 
 // Copies tiles of the cache, every second piece; the first of the warps queries too.
@@ -426,16 +455,17 @@ __device__ __forceinline__ void score_loop(const LatentAttnArgs& a, const Share&
     const uint32_t to = tmem + (places >> 16) * 64;
     const uint32_t last = k_smem + S::kKeyAt + (places >> 8 & 255) * kChunkBytes;
     if (elect_one()) {
+#pragma unroll 1
+      for (int c = 0; c < S::kChunks; ++c) {
+        const int at = (places & 255) + c / 2;
+        const uint32_t pair_at = k_smem + (at >= S::kPairs ? at - S::kPairs : at) * kPairBytes;
+        const uint32_t k0 = c < 2 * MB ? pair_at + (c & 1) * kChunkBytes : last;
+        const uint32_t q0 = q_smem + c * (RT * 128);
 #pragma unroll
-      for (int x = 0; x < MB; ++x)
-#pragma unroll
-        for (int y = 0; y < 8; ++y)
-          tc_mma(to, smem_desc(q_smem + (2 * x + y / 4) * (RT * 128) + y % 4 * 32, 16, 1024),
-                 smem_desc(from[x] + y / 4 * kChunkBytes + y % 4 * 32, 16, 1024), desc, x + y > 0);
-#pragma unroll
-      for (int y = 0; y < 4; ++y)
-        tc_mma(to, smem_desc(q_smem + 2 * MB * (RT * 128) + y * 32, 16, 1024),
-               smem_desc(last + y * 32, 16, 1024), desc, 1);
+        for (int y = 0; y < 4; ++y)
+          tc_mma(to, smem_desc(q0 + y * 32, 16, 1024), smem_desc(k0 + y * 32, 16, 1024), desc,
+                 c + y > 0);
+      }
       tc_commit(smem_u32(&sh.s_full[i & 1]));
       if (k.left == 1) tc_commit(smem_u32(&sh.q_free));
     }
@@ -478,7 +508,7 @@ __device__ __forceinline__ void value_loop(const LatentAttnArgs& a, const Share&
     const uint32_t p = k_smem + S::kKeyAt + (places >> 8 & 255) * kChunkBytes;
     const uint32_t keep = places >> 16;
     if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
       for (int m = 0; m < MB; ++m) {
         const uint32_t from = k_smem + v.at * kPairBytes;
 #pragma unroll
@@ -652,7 +682,7 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
     named_barrier(1, kSoftmaxThreads);
     tc_fence_after();
     const int channel = 32 * quarter + lane;
-    const int64_t slot = 2 * static_cast<int64_t>(w.split * a.row_tiles + rt) + (k.index > 0);
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (k.index > 0);
     const bool whole = k.whole();
     if (!whole && quarter_on && half == 0 && lane % 4 == 0) {
 #pragma unroll
@@ -688,7 +718,8 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
       const int first = static_cast<int>(((p0 + 1) * w.splits + w.total - 1) / w.total) - 1;
       const int late = first * w.total / w.splits != p0;  // that share began before it
       a.pieces[static_cast<int64_t>(k.b) * a.row_tiles + rt] =
-          make_int2(2 * first + late, w.split - first + 1);
+          make_int2(2 * (w.first_cta + first * w.stride) + late,
+                    (w.split - first + 1) | (a.weighted ? kContiguous : 0));
     }
   }
   if (bad) {
@@ -743,9 +774,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   griddep_wait();
-  const int rt = blockIdx.x % a.row_tiles, split = blockIdx.x / a.row_tiles;
-  const int first_t = row_of<RT>(a, rt, 0).t;
-  const Share w = share_of(a, split, first_t, sh);
+  const Share w = share_of<RT>(a, sh);
+  const int rt = uniform(w.rt), first_t = uniform(w.first_t);
   if (w.begin < w.end) {
     if (warp == 0 || warp == 2)
       copy_loop<MB, RT>(a, &mql, &mqr, &mc, w, rt, first_t, warp / 2, sh, q_smem, k_smem);
@@ -783,20 +813,21 @@ __global__ void __launch_bounds__(32 * MB * kJoinGroups) latent_join_kernel(cons
   const int64_t out = b * a.o_sb + at.t * a.o_st + at.h * a.o_sh + 4 * tid;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   if (seq.tiles > 0) {
-    const int first = p.x / 2, late = p.x & 1;
-    if (p.y <= 1 || p.x < 0 || first + p.y > a.splits) return;  // whole: written already
+    const int first = p.x / 2, late = p.x & 1, parts = p.y & ~kContiguous;
+    const int stride = p.y & kContiguous ? 1 : a.row_tiles;
+    if (parts <= 1 || p.x < 0 || first + static_cast<int64_t>(parts - 1) * stride >= a.ctas)
+      return;  // whole: written already
     float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
-    for (int i0 = group; i0 < p.y; i0 += 4 * groups) {
+    for (int i0 = group; i0 < parts; i0 += 4 * groups) {
       float4 x[4];
       float m[4], l[4];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int i = i0 + y * groups;
         m[y] = -INFINITY, l[y] = 0.f, x[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i >= p.y) continue;
-        const int64_t s =
-            (2 * static_cast<int64_t>((first + i) * a.row_tiles + rt) + (i == 0 ? late : 0)) * RT + r;
+        if (i >= parts) continue;
+        const int64_t s = (2 * static_cast<int64_t>(first + i * stride) + (i == 0 ? late : 0)) * RT + r;
         const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * s);
         m[y] = ml.x, l[y] = ml.y;
         x[y] = *reinterpret_cast<const float4*>(a.part_o + s * (128 * MB) + 4 * tid);

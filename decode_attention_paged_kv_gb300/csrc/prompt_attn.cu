@@ -371,7 +371,7 @@ __device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, int 
       if (elect_one()) {
         if (do_values) {
           // (a product for each piece: two are not neighbours where the ring wraps)
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < S::kVChunks; ++c) {
             const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
 #pragma unroll
@@ -387,7 +387,7 @@ __device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, int 
         // (the other warp takes as long to begin as the scores to issue)
         mbar_arrive(smem_u32(&sh.turn[1 - x]));
         if (do_scores) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < S::kQChunks; ++c) {
             const uint32_t k = ring + (base + S::kVChunks + c) % kSlots * kPieceBytes;
 #pragma unroll

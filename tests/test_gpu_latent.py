@@ -169,6 +169,10 @@ DECODE = [
     (1, 1, 128, 512, 20011, [20011], [1]),
     (40, 1, 7, 256, 260, [7 * i - 8 for i in range(38)] + [260, 256], [1] * 40),
     (2, 1, 300, 512, 150, [150, 77], [1, 1]),
+    # row tiles with few sequences, with one, with none
+    (9, 5, 40, 512, 900, [900, 700, 5, 0, 64, 129, 333, 900, 1], [1, 5, 5, 5, 1, 2, 1, 0, 1]),
+    (3, 6, 70, 256, 400, [400, 399, 64], [2, 1, 2]),
+    (3, 2, 64, 512, 5000, [5000, 4999, 4000], [1, 1, 2]),
 ]
 
 
@@ -232,6 +236,31 @@ def test_decode_rising_scores(dkv):
         out = torch.zeros(1, 1, 9, 256, device="cuda")
         dkv.latent_decode_attn(ql, qr, x, 1.0, out=out)
         check_decode(x, ql, qr, out, [1024], [1], 1.0)
+
+
+def test_decode_shared_operands(dkv):
+    # one cache for all sequences, one query for all heads: dimensions of stride 0
+    gen = gen_of("expanded")
+    x = torch.randn(1, 200, 576, generator=gen, device="cuda").bfloat16().expand(3, 200, 576)
+    ql = torch.randn(3, 1, 1, 512, generator=gen, device="cuda").bfloat16().expand(3, 1, 20, 512)
+    qr = torch.randn(1, 1, 20, 64, generator=gen, device="cuda").bfloat16().expand(3, 1, 20, 64)
+    lens = [200, 7, 130]
+    out = torch.zeros(3, 1, 20, 512, device="cuda")
+    dkv.latent_decode_attn(ql, qr, x, 0.07, seq_lens=ints(lens), out=out)
+    check_decode(x, ql, qr, out, lens, [1] * 3, 0.07)
+
+
+def test_decode_workspace_of_larger_sizes(dkv):
+    # one workspace for the largest call serves those of fewer new tokens and heads, in turn
+    gen = gen_of("one workspace")
+    ws = torch.zeros(dkv.latent_workspace_bytes(4, 4, 200, 512, 700), dtype=torch.uint8,
+                     device="cuda")
+    for T, H, new in ((4, 200, [4, 1, 3, 2]), (1, 16, [1] * 4), (3, 40, [3, 3, 1, 0])):
+        lens = [700, 333, 64, 65]
+        cache, ql, qr, out = decode_case(4, T, H, 512, 700, 16, torch.bfloat16, gen, lens, new)
+        dkv.latent_decode_attn(ql, qr, cache, 0.07, seq_lens=ints(lens), new_lens=ints(new),
+                               out=out, workspace=ws)
+        check_decode(cache, ql, qr, out, lens, new, 0.07)
 
 
 def test_decode_bad_blocks_are_reported(dkv):
@@ -407,6 +436,25 @@ def test_prompt_defaults_and_ranges(dkv):
         out = dkv.latent_prompt_attn(*args[:6], None, scale)
         assert out.dtype == torch.float32
         check_prompt(args, out, [200, 77], [200, 77], scale, True)
+
+
+def test_prompt_shared_operands(dkv):
+    # keys and values that the heads share: dimensions of stride 0
+    gen = gen_of("pexpanded")
+    args, out = prompt_case(5, 64, [150, 20], [160, 20], torch.bfloat16, gen)
+    args = list(args)
+    args[2], args[4] = (args[i][:, :1].expand(-1, 5, -1) for i in (2, 4))
+    dkv.latent_prompt_attn(*args, 0.1, out=out)
+    check_prompt(args, out, [150, 20], [160, 20], 0.1, True)
+
+
+def test_prompt_many_sequences(dkv):
+    # more sequences than a warp looks at at once, most of one query
+    nq = [1 + (i % 7 == 0) * 300 for i in range(100)]
+    nk = [n + i % 5 for i, n in enumerate(nq)]
+    args, out = prompt_case(2, 64, nq, nk, torch.bfloat16, gen_of("many seqs"))
+    dkv.latent_prompt_attn(*args, 0.1, out=out)
+    check_prompt(args, out, nq, nk, 0.1, True)
 
 
 def test_prompt_bad_bounds_are_left_alone(dkv):

@@ -172,9 +172,11 @@ def test_fork_refused(dkv, lens, parents, new):
     assert run_fork(dkv, caches, tensors, table, refs, [-7, 40], [-1, 1], [1, 8], 16, ws)
 
 
-def test_fork_many_rows(dkv):
-    # more rows than the first kernel has threads, pools of more blocks than it scans at once
-    B, P, nb = 5000, 2, 40000
+@pytest.mark.parametrize("B", [5000, 16384])
+def test_fork_many_rows(dkv, B):
+    # more rows than the first kernel has threads (and than its shared memory holds without
+    # asking for more), pools of more blocks than it scans at once
+    P, nb = 2, 9000 + 5 * B
     table = torch.full((B, P), -1, dtype=torch.int32, device="cuda")
     refs = torch.zeros(nb, dtype=torch.int32, device="cuda")
     refs[:9000] = 1
@@ -272,8 +274,9 @@ def test_compact_without_tables_of_its_own_stride(dkv):
     assert wide.tolist() == [[7, 3, 11, 12], [3, -1, 13, 14]]
 
 
-def test_beams_over_an_8_bit_cache(dkv):
-    """Beams that fork, append and attend over 8-bit caches, as each of them alone over a
+@pytest.mark.parametrize("kind", ["fp8", "kv16"])
+def test_beams_over_a_cache(dkv, kind):
+    """Beams that fork, append and attend over paged caches, as each of them alone over a
     dense copy: bit for bit, whatever pages they share."""
     B, H, d, N, steps = 4, 2, 64, 160, 30
     P = N // 16
@@ -281,11 +284,14 @@ def test_beams_over_an_8_bit_cache(dkv):
     gen = torch.Generator("cuda").manual_seed(3)
     table = torch.full((B, P), -1, dtype=torch.int32, device="cuda")
     refs = torch.zeros(nb, dtype=torch.int32, device="cuda")
-    caches, _ = make_caches(dkv, "fp8", nb, table, N, H=H, d=d, seed=9)
-    dense = [dkv.Fp8Cache(torch.zeros(B, H, N, d, device="cuda").to(torch.float8_e4m3fn),
-                          torch.zeros(B, H, P, device="cuda")) for _ in "KV"]
+    eight = kind == "fp8"
+    caches, _ = make_caches(dkv, kind, nb, table, N, H=H, d=d, seed=9)
+    dense = [torch.zeros(B, H, N, d, device="cuda").bfloat16() for _ in "KV"]
+    if eight:
+        dense = [dkv.Fp8Cache(x.to(torch.float8_e4m3fn), torch.zeros(B, H, P, device="cuda"))
+                 for x in dense]
     ws = torch.zeros(max(dkv.pages_workspace_bytes(B, P, nb),
-                         dkv.workspace_bytes(B, 4, H, d, N, fp8=True)), dtype=torch.uint8,
+                         dkv.workspace_bytes(B, 4, H, d, N, fp8=eight)), dtype=torch.uint8,
                      device="cuda")
     lens = torch.zeros(B, dtype=torch.int32, device="cuda")
     rng = random.Random(2)
@@ -299,6 +305,9 @@ def test_beams_over_an_8_bit_cache(dkv):
         if step:
             lens = lens[par.long()]
             for c in dense:
+                if not eight:
+                    c.copy_(c[par.long()])
+                    continue
                 c.codes.view(torch.uint8).copy_(c.codes.view(torch.uint8)[par.long()])
                 c.scale.copy_(c.scale[par.long()])
         lens = lens + n

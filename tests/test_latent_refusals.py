@@ -83,6 +83,23 @@ def test_workspace_sizes(dkv):
             dkv.pages_workspace_bytes(*bad)
 
 
+def test_workspaces_rise_with_every_size(dkv):
+    # (a workspace for the largest call serves the smaller ones)
+    import itertools
+    sizes = ([1, 3, 64], [1, 2, 5, 9], [1, 8, 16, 17, 40, 128, 200], [256, 512],
+             [1, 64, 65, 1000, 100000])
+    need = {k: dkv.latent_workspace_bytes(*k) for k in itertools.product(*sizes)}
+    for k, n in need.items():
+        for i, options in enumerate(sizes):
+            at = options.index(k[i])
+            if at:
+                assert need[k[:i] + (options[at - 1],) + k[i + 1:]] <= n, (k, i)
+    for a, b in itertools.pairwise([1, 2, 100, 10000]):
+        assert dkv.pages_workspace_bytes(a, 7, 7) <= dkv.pages_workspace_bytes(b, 7, 7)
+        assert dkv.pages_workspace_bytes(7, a, 7) <= dkv.pages_workspace_bytes(7, b, 7)
+        assert dkv.pages_workspace_bytes(7, 7, a) <= dkv.pages_workspace_bytes(7, 7, b)
+
+
 # ---------------------------------------------------------------- the C ABI's own checks
 OK, NULL, SHAPE, ALIGN, DTYPE, UNSUPPORTED, WORKSPACE = range(7)
 ADDR = 1 << 20  # an address that nothing reads before it is refused
