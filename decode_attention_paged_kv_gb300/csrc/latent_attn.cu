@@ -72,7 +72,6 @@ struct Shared {
   uint32_t fills[kMaxPairs], key_fills[kMaxKeys], q_fills;  // copies issued, for the drain
   volatile int abort;
   volatile int failed[2];  // a softmax warp's wait expired, by turns
-  int seq0, off0;          // where the CTA's share begins
   float top[2][2][64];     // a tile's maxima, of its two halves, by turns
   volatile int rose[2];    // the last tile that a score rose far in, by turns
   float factor[64];
@@ -123,80 +122,82 @@ __device__ __forceinline__ Row row_of(const LatentAttnArgs& a, int rt, int r) {
 
 // Row tiles have as many CTAs each, side by side, so that they are at the same tokens at the
 // same time; where sequences have different numbers of new tokens, row tiles of the later
-// ones have fewer sequences, and fewer CTAs.
+// ones have fewer sequences, and fewer CTAs.  Up to 256 sequences each warp counts for
+// itself (all of it took 5000 to 6700 cycles with barriers, 64-bit sums and quotients).
+// (Tiles of all sequences together are below 2^31.)
 template <int RT>
 __device__ __forceinline__ Share share_of(const LatentAttnArgs& a, Shared& sh) {
-  __shared__ unsigned long long tiles_of[kMaxWeighted];
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  __shared__ unsigned int tiles_of[kMaxWeighted];
+  const int tid = threadIdx.x, lane = tid % 32;
+  const bool alone = a.B <= 256;
   Share w{};
   w.rt = blockIdx.x % a.row_tiles, w.split = blockIdx.x / a.row_tiles;
   w.splits = a.splits, w.first_cta = w.rt, w.stride = a.row_tiles;
   const int counted = a.weighted ? a.row_tiles : 1;
-  if (tid < counted) tiles_of[tid] = 0;
-  __syncthreads();
+  unsigned int mine_of = 0;  // lane r: tiles of row tile r
+  if (!alone) {
+    if (tid < counted) tiles_of[tid] = 0;
+    __syncthreads();
+  }
   for (int r = 0; r < counted; ++r) {
     const int first_t = row_of<RT>(a, a.weighted ? r : w.rt, 0).t;
-    int64_t mine = 0;  // (2^14 sequences of 2^25 tiles: counted in 64 bits)
-    for (int b = tid; b < a.B; b += kThreads) mine += sequence(a, b, first_t).tiles;
-    if (mine != 0) atomicAdd(&tiles_of[r], static_cast<unsigned long long>(mine));
+    unsigned int sum = 0;
+    for (int b = alone ? lane : tid; b < a.B; b += alone ? 32 : kThreads)
+      sum += sequence(a, b, first_t).tiles;
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == r) mine_of = sum;
+    if (!alone && lane == 0) atomicAdd(&tiles_of[r], sum);
   }
-  __syncthreads();
-  w.total = static_cast<int64_t>(tiles_of[0]);
+  if (!alone) {
+    __syncthreads();
+    if (lane < counted) mine_of = tiles_of[lane];
+  }
+  unsigned int total = __shfl_sync(0xffffffffu, mine_of, 0);
   if (a.weighted) {
-    int64_t all = 0;
-    for (int r = 0; r < counted; ++r) all += static_cast<int64_t>(tiles_of[r]);
-    int cta = blockIdx.x, start = 0;
+    unsigned long long all = 0;
+    for (int r = 0; r < counted; ++r) all += __shfl_sync(0xffffffffu, mine_of, r);
+    int start = 0;
     for (int r = 0; r < counted; ++r) {
-      const int64_t mine = static_cast<int64_t>(tiles_of[r]);
+      total = __shfl_sync(0xffffffffu, mine_of, r);
       // (one each, and the rest by their tiles)
-      const int n =
-          1 + (all > 0 ? static_cast<int>((a.ctas - a.row_tiles) * mine / all) : 0);
-      if (cta < start + n || r == counted - 1) {
-        w.rt = r, w.split = cta - start, w.splits = n, w.total = mine;
-        break;
-      }
+      const int n = 1 + (all > 0 ? static_cast<int>((a.ctas - a.row_tiles) *
+                                                    static_cast<unsigned long long>(total) / all)
+                                 : 0);
+      w.rt = r, w.split = blockIdx.x - start, w.splits = n;
+      if (static_cast<int>(blockIdx.x) < start + n || r == counted - 1) break;
       start += n;
     }
     w.first_cta = start, w.stride = 1;
   }
+  w.total = total;
   w.first_t = row_of<RT>(a, w.rt, 0).t;
-  const int first_t = w.first_t, split = w.split;
-  const int64_t most = w.total <= kSingleTiles ? w.total : (w.total + 1) / 2;
-  if (most < w.splits) w.splits = static_cast<int>(most);
-  if (split >= w.splits) return w;  // (no work: begin == end)
-  w.begin = split * w.total / w.splits;
-  w.end = (split + 1) * w.total / w.splits;
+  const unsigned int most = total <= kSingleTiles ? total : (total + 1) / 2;
+  if (most < static_cast<unsigned int>(w.splits)) w.splits = static_cast<int>(most);
+  if (w.split >= w.splits) return w;  // (no work: begin == end)
+  // split * total / splits, without a product past 32 bits
+  const unsigned int each = total / w.splits, rest = total % w.splits;
+  w.begin = w.split * each + w.split * rest / w.splits;
+  w.end = (w.split + 1) * each + (w.split + 1) * rest / w.splits;
   // the sequence that holds tile `begin`
   int64_t before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    const int t = b < a.B ? sequence(a, b, first_t).tiles : 0;
-    long long x = t;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int t = b < a.B ? sequence(a, b, w.first_t).tiles : 0;
+    int x = t;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const long long up = __shfl_up_sync(0xffffffffu, x, o);
+      const int up = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += up;
     }
-    __shared__ long long warp_sum[kThreads / 32];
-    __syncthreads();
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    long long chunk = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) x += warp_sum[i];
-      chunk += warp_sum[i];
+    const uint32_t past = __ballot_sync(0xffffffffu, w.begin < before + x);
+    if (past != 0) {
+      const int from = __ffs(past) - 1;
+      w.b = b0 + from;
+      w.off = static_cast<int>(w.begin - before) - __shfl_sync(0xffffffffu, x - t, from);
+      break;
     }
-    x += before;  // tiles up to and with sequence b
-    if (t > 0 && w.begin < x && w.begin >= x - t) {
-      sh.seq0 = b;
-      sh.off0 = static_cast<int>(w.begin - (x - t));
-    }
-    before += chunk;
-    if (before > w.begin) break;
+    before += __shfl_sync(0xffffffffu, x, 31);
   }
-  __syncthreads();
-  w.b = sh.seq0;
-  w.off = sh.off0;
   return w;
 }
 
@@ -742,34 +743,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / 32;
   griddep_launch_dependents();
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), S::kColumns);
-  if (threadIdx.x == 0) {
+  // (a barrier a thread or two: one thread alone takes 1000 cycles for all)
+  const int tid = threadIdx.x;
+  if (tid < S::kPairs) {
+    mbar_init(smem_u32(&sh.full[tid]), 1);
+    mbar_init(smem_u32(&sh.empty[tid]), 1);
+    sh.fills[tid] = 0;
+  } else if (tid >= 64 && tid < 64 + S::kKeys) {
+    mbar_init(smem_u32(&sh.key_full[tid - 64]), 1);
+    mbar_init(smem_u32(&sh.key_empty[tid - 64]), 1);
+    sh.key_fills[tid - 64] = 0;
+  } else if (tid >= 96 && tid < 98) {
+    const int i = tid - 96;
+    mbar_init(smem_u32(&sh.s_full[i]), 1);
+    mbar_init(smem_u32(&sh.p_ready[i]), kSoftmaxThreads);
+    mbar_init(smem_u32(&sh.o_done[i]), 1);
+    mbar_init(smem_u32(&sh.voted[i]), kSoftmaxThreads);
+    mbar_init(smem_u32(&sh.drain[i]), 1);
+    sh.failed[i] = 0;
+    sh.rose[i] = 0;
+  } else if (tid == 128) {
     prefetch_tensormap(&mql), prefetch_tensormap(&mqr), prefetch_tensormap(&mc);
-    for (int i = 0; i < S::kPairs; ++i) {
-      mbar_init(smem_u32(&sh.full[i]), 1);
-      mbar_init(smem_u32(&sh.empty[i]), 1);
-      sh.fills[i] = 0;
-    }
-    for (int i = 0; i < S::kKeys; ++i) {
-      mbar_init(smem_u32(&sh.key_full[i]), 1);
-      mbar_init(smem_u32(&sh.key_empty[i]), 1);
-      sh.key_fills[i] = 0;
-    }
-    sh.q_fills = 0;
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.p_ready[i]), kSoftmaxThreads);
-      mbar_init(smem_u32(&sh.o_done[i]), 1);
-      mbar_init(smem_u32(&sh.voted[i]), kSoftmaxThreads);
-      mbar_init(smem_u32(&sh.drain[i]), 1);
-    }
     mbar_init(smem_u32(&sh.o_free), kSoftmaxThreads);
     mbar_init(smem_u32(&sh.q_full), 1);
     mbar_init(smem_u32(&sh.q_free), 1);
+    sh.q_fills = 0;
     sh.abort = 0;
-    sh.failed[0] = sh.failed[1] = 0;
-    sh.rose[0] = sh.rose[1] = 0;
-    fence_barrier_init();
   }
+  fence_barrier_init();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
