@@ -693,22 +693,30 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
         ml[1] = l[e] + sh.stat_l[1][r0 + 8 * e];
       }
     }
+    if (whole) {
+      // (a quotient a row, not one an element)
+      const int mine = threadIdx.x - 32 * kFirstSoftmax;
+      if (mine < RT) {
+        const float sum = sh.stat_l[0][mine] + sh.stat_l[1][mine];
+        sh.factor[mine] = sum > 0.f ? 1.f / sum : (sum == sum ? 0.f : sum);
+      }
+      named_barrier(1, kSoftmaxThreads);
+    }
 #pragma unroll 1
     for (int c = half * (MB * RT / 2); c < (half + 1) * (MB * RT / 2); c += 16) {
       float o[16];
       tmem_ld16(tq + 128 + c, o);
+      const int ch = c / RT * 128 + channel, row0 = c % RT;
       tmem_wait_ld();
-      const int ch = c / RT * 128 + channel;
+      if (whole) {
 #pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        const int row = c % RT + x;
-        if (whole) {
-          const float sum = sh.stat_l[0][row] + sh.stat_l[1][row];
-          if (sh.row_at[row] >= 0)
-            store_out(a.out, a.out_dtype, sh.row_at[row] + ch, sum > 0.f || sum != sum ? o[x] / sum : 0.f);
-        } else {
-          a.part_o[(slot * RT + row) * (128 * MB) + ch] = o[x];
-        }
+        for (int x = 0; x < 16; ++x)
+          if (sh.row_at[row0 + x] >= 0)
+            store_out(a.out, a.out_dtype, sh.row_at[row0 + x] + ch, o[x] * sh.factor[row0 + x]);
+      } else {
+        float* to = a.part_o + (slot * RT + row0) * (128 * MB) + ch;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) to[x * (128 * MB)] = o[x];
       }
     }
     tc_fence_before();
