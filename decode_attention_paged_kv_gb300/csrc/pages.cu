@@ -16,6 +16,12 @@
 // compact, three kernels: counts of blocks in use per chunk; ranks of the moves' ends
 // (the k-th block in use at or past n goes to the k-th free one below n, n the number
 // in use); the copies, 16 KB an item, and the table's new names.
+//
+// Measured on a GB300: a step of 64 beams over 32K-token contexts (two pools, 8 KB a block)
+// 9.5 us, of four beams 8 us beside the caller's own work: two launches, each a chain of
+// four to six dependent loads (parents - lengths - table - counts; plan - table - blocks).
+// A gigabyte pool half in use compacted (268 MB moved) 91 us, 81 of them the copies at 6.6
+// TB/s both ways (99 with 4096 counts a CTA in the ranks' kernel), 7 MB 10 us.
 
 #include "dkv_device.cuh"
 #include "dkv_kernels.h"

@@ -21,6 +21,16 @@
 // not begun (cluster launch control) and passes its block on, so that copies run into the
 // next block while this one's softmax and output are under way, and blocks go to whichever
 // multiprocessor is free.
+//
+// Maxima, sums and outputs are fp32; a weight is rounded once to the inputs' type for its
+// product.  Measured on a GB300, bf16: the last 2K tokens of 4 prompts of 8K, 16 heads, dn =
+// 128: 483 us, 1.25 PFLOP/s of the 1.9 that a large library product reaches; one prompt of
+// 8K 307 us (1.12); 16 of 512 tokens, 32 heads, dn = 64 61 us (0.42).  What bounds it: a query tile's
+// chain scores - softmax - values, some 4000 cycles for 2560 of products for two tiles; the
+// scores' operands alone take all of the shared memory's rate while they run, and the next
+// tile's keys arrive late (8 pieces).  345 us (listed batch, now 265) with one warp for both
+// tiles' products, 296 with a warp each in turns, 266 with blocks taken over; a softmax in
+// halves and a second wait between values and scores made no difference.
 
 #include "dkv_device.cuh"
 #include "dkv_kernels.h"
