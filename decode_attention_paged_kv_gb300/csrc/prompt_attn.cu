@@ -16,7 +16,7 @@
 // Keys and values come in pieces of 128 tokens x 64 channels (16 KB) through one ring, the
 // keys of the next tile before the values of this one are done with: with 96 KB of
 // queries (dn = 128) there is room for 8 pieces, a tile and three fifths.
-
+//
 // A CTA stays for further blocks of queries: a warp takes over the launch of a CTA that has
 // not begun (cluster launch control) and passes its block on, so that copies run into the
 // next block while this one's softmax and output are under way, and blocks go to whichever
