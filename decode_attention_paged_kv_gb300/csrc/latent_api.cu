@@ -416,6 +416,19 @@ bool table_ok(int64_t rows, int64_t cols, int64_t nb) {
          rows * cols + rows <= kInt32Max;
 }
 
+// Whether two pools have bytes in common.  Blocks of two pools may alternate in memory
+// (keys and values of one tensor); then they lie at one stride.
+bool pools_meet(const dkv_pool& x, const dkv_pool& y, int64_t blocks) {
+  const uint64_t a = reinterpret_cast<uintptr_t>(x.data), b = reinterpret_cast<uintptr_t>(y.data);
+  if (a + (blocks - 1) * x.stride + x.block_bytes <= b ||
+      b + (blocks - 1) * y.stride + y.block_bytes <= a)
+    return false;
+  if (blocks == 1 || x.stride != y.stride) return true;
+  const int64_t ahead = static_cast<int64_t>(a - b) % x.stride;  // of x's blocks to y's
+  const int64_t d = ahead < 0 ? ahead + x.stride : ahead;
+  return d < y.block_bytes || d + x.block_bytes > x.stride;
+}
+
 dkv_status check_pages(const dkv_pages* p, void* workspace, size_t bytes, dkv::PagesArgs* g) {
   if (p == nullptr) return DKV_ERR_NULL;
   if (p->rows < 1 || p->cols < 1 || p->num_blocks < 1 || p->block_size < 1 || p->num_pools < 0 ||
@@ -442,8 +455,9 @@ dkv_status check_pages(const dkv_pages* p, void* workspace, size_t bytes, dkv::P
                           static_cast<uint64_t>(x.stride);
     if (bits & 3u) return DKV_ERR_ALIGN;
     if (x.block_bytes > kInt32Max) return DKV_ERR_UNSUPPORTED;
-    for (int j = 0; j < i; ++j)  // blocks that are copied twice would be moved in no order
-      if (p->pools[j].data == x.data) return DKV_ERR_SHAPE;
+    if (p->num_blocks > 1 && x.stride > INT64_MAX / 2 / p->num_blocks) return DKV_ERR_SHAPE;
+    for (int j = 0; j < i; ++j)  // bytes that are copied twice would be moved in no order
+      if (pools_meet(x, p->pools[j], p->num_blocks)) return DKV_ERR_SHAPE;
     g->pool[i] = {static_cast<char*>(x.data), x.stride, x.block_bytes, (bits & 15u) == 0};
   }
   if (workspace == nullptr ||

@@ -538,7 +538,7 @@ dkv_status dkv_latent_prompt_attn(const dkv_prompt* p, void* workspace, void* st
 #define DKV_MAX_POOLS 16
 /* The tensors of a cache (or of several) that one block table addresses: block n of
    pool i is the block_bytes bytes at data + n * stride.  block_bytes, stride and data
-   are multiples of 4. */
+   are multiples of 4; no byte belongs to two blocks, of one pool or of two. */
 typedef struct dkv_pool {
   void* data;
   int64_t stride, block_bytes;

@@ -620,3 +620,95 @@ def test_serving_loop(dkv, block):
     assert bool((refs[:used] > 0).all()) and not bool(refs[used:].any())
     decode([2, 2, 1, 2], [0, 0, 1, 2])
     decode([1, 0, 1, 1], [2, -1, 2, 3])
+
+
+@pytest.mark.parametrize("H,interleaved", [(39, False), (40, True), (128, False), (300, True)])
+def test_append_many_heads(dkv, H, interleaved):
+    # heads past a warp's: further warps of the same token, with and without room to spare
+    gen = gen_of("heads", H)
+    cache, _ = make_cache(2, 30, 512, 16, torch.bfloat16, gen)
+    c, k, q = append_inputs(2, 3, H, 512, torch.bfloat16, gen)
+    rope = dkv.rope_table(30, 64, device="cuda")
+    out = torch.full((2, 3, H + 1, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    dkv.latent_append(c, k, cache, seq_lens=ints([30, 9]), new_lens=ints([3, 2]), q_rope=q,
+                      q_out=out[:, :, :H], rope=rope, interleaved=interleaved)
+    for b, (m, n) in enumerate(((30, 3), (9, 2))):
+        cos, sin = rope[0][m - n:m, None], rope[1][m - n:m, None]
+        want = rotate64(q[b, :n], cos, sin, interleaved)
+        # one rounding to bf16, and three of fp32 (2^-24 each) of terms up to |x|
+        tol = 2.0 ** -8 * want.abs() + 2.0 ** -20 * q[b, :n].double().abs().amax()
+        assert bool(((out[b, :n, :H].double() - want).abs() <= tol).all())
+        assert bool((out[b, n:, :H] == 7).all())
+        assert torch.equal(rows_of(cache, b)[m - n:m, :512], c[b, :n])
+    assert bool((out[:, :, H] == 7).all())
+
+
+def test_step_captured_on_another_stream(dkv):
+    """A whole step -- pages, append, attention, compaction -- in one graph on a stream of its
+    own, replayed with other lengths, parents and inputs; the same calls made eagerly beside
+    it give the same bits."""
+    gen = gen_of("step graph")
+    B, T, H, dc, N, block, nb = 3, 2, 20, 256, 200, 16, 60
+    P = -(-N // block)
+    scale = 0.06
+    dt = torch.bfloat16
+
+    def state():
+        return dict(pool=torch.zeros(nb, block, dc + 64, dtype=dt, device="cuda"),
+                    table=torch.full((B, P), -1, dtype=torch.int32, device="cuda"),
+                    refs=torch.zeros(nb, dtype=torch.int32, device="cuda"),
+                    old=ints([0] * B), lens=ints([0] * B), parents=ints([-1] * B),
+                    new=ints([0] * B),
+                    c=torch.zeros(B, T, dc, dtype=dt, device="cuda"),
+                    k=torch.zeros(B, T, 64, dtype=dt, device="cuda"),
+                    q=torch.zeros(B, T, H, 64, dtype=dt, device="cuda"),
+                    ql=torch.zeros(B, T, H, dc, dtype=dt, device="cuda"),
+                    qr=torch.zeros(B, T, H, 64, dtype=dt, device="cuda"),
+                    out=torch.zeros(B, T, H, dc, device="cuda"),
+                    to=torch.zeros(nb, dtype=torch.int32, device="cuda"),
+                    ws=torch.zeros(max(dkv.pages_workspace_bytes(B, P, nb),
+                                       dkv.latent_workspace_bytes(B, T, H, dc, N)),
+                                   dtype=torch.uint8, device="cuda"))
+
+    rope = dkv.rope_table(N, 64, device="cuda")
+
+    def step(s):
+        cache = dkv.LatentCache(s["pool"], s["table"], N)
+        dkv.kv_pages_fork([cache], s["refs"], s["old"], parents=s["parents"], new_lens=s["new"],
+                          workspace=s["ws"])
+        dkv.latent_append(s["c"], s["k"], cache, seq_lens=s["lens"], new_lens=s["new"],
+                          q_rope=s["q"], q_out=s["qr"], rope=rope, workspace=s["ws"])
+        dkv.latent_decode_attn(s["ql"], s["qr"], cache, scale, seq_lens=s["lens"],
+                               new_lens=s["new"], out=s["out"], workspace=s["ws"])
+        s["to"].copy_(dkv.kv_pages_compact([cache], s["refs"], workspace=s["ws"]))
+
+    graphed, eager = state(), state()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        step(graphed)
+    lens = [0] * B
+    for i, (parents, new) in enumerate([([-1] * 3, [2, 1, 2])] + [([0, 1, 2], [2, 2, 1])] * 12 +
+                                       [([1, 1, 2], [1, 2, 0]), ([0, -1, 0], [2, 0, 1])]):
+        old, lens = lens, [(lens[p] if p >= 0 else 0) + n for p, n in zip(parents, new)]
+        fresh = {x: torch.randn(eager[x].shape, generator=gen, device="cuda").to(dt)
+                 for x in ("c", "k", "q", "ql")}
+        for s in graphed, eager:
+            for name, x in (("old", old), ("lens", lens), ("parents", parents), ("new", new)):
+                s[name].copy_(ints(x))
+            for name, x in fresh.items():
+                s[name].copy_(x)
+            s["out"].fill_(5.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            g.replay()
+        step(eager)  # at the same time
+        torch.cuda.synchronize()
+        for s in graphed, eager:
+            assert dkv.read_device_status(s["ws"]) == 0
+        for name in ("table", "refs", "out", "to"):
+            assert torch.equal(graphed[name], eager[name]), (i, name)
+        assert torch.equal(graphed["pool"], eager["pool"]), i
+        cache = dkv.LatentCache(eager["pool"], eager["table"], N)
+        check_decode(cache, eager["ql"], eager["qr"], eager["out"], lens, new, scale)

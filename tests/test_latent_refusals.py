@@ -264,3 +264,31 @@ def test_c_pages(dkv):
     assert compact(r, ADDR, 11, ADDR, other, ADDR, need, None) == SHAPE  # the table, other rows
     assert compact(r, other, 9, ADDR, other, ADDR, need, None) == SHAPE
     assert compact(r, ADDR, 10, other, other, ADDR, need, None) == SHAPE  # counts and names in one
+
+
+def test_c_pools_that_share_bytes(dkv):
+    # blocks of two pools may alternate in memory, at one stride; no byte may be in two
+    fork = dkv.lib().dkv_kv_pages_fork
+    fork.argtypes = [ctypes.c_void_p] * 5 + [ctypes.c_size_t, ctypes.c_void_p]
+
+    def call(a, b, blocks=100):
+        p = Pages(4, 10, 16, blocks, 2, ADDR, 10, ADDR)
+        p.pools[0], p.pools[1] = Pool(*a), Pool(*b)
+        # (no lengths: sound pools are refused for that, after their check)
+        return fork(ctypes.byref(p), None, None, None, ADDR, 1 << 40, None)
+
+    for a, b, want in [
+            ((ADDR, 8192, 4096), (ADDR + 4096, 8192, 4096), NULL),   # keys, values of one tensor
+            ((ADDR + 4096, 8192, 4096), (ADDR, 8192, 4096), NULL),
+            ((ADDR, 8192, 4096), (ADDR + 3 * 8192 + 4096, 8192, 4096), NULL),
+            ((ADDR, 8192, 4096), (ADDR + 4080, 8192, 4096), SHAPE),  # ends inside, begins inside
+            ((ADDR, 8192, 4096), (ADDR + 4112, 8192, 4096), SHAPE),
+            ((ADDR, 4096, 4096), (ADDR + 5 * 4096, 4096, 4096), SHAPE),
+            ((ADDR, 4096, 4096), (ADDR + 100 * 4096, 4096, 4096), NULL),
+            ((ADDR + 100 * 4096, 4096, 4096), (ADDR, 4096, 4096), NULL),
+            ((ADDR, 4096, 4096), (ADDR + 99 * 4096, 4096, 64), SHAPE),
+            ((ADDR, 8192, 64), (ADDR + 64, 4096, 64), SHAPE),         # two strides in one range
+            ((ADDR, (1 << 62), 64), (ADDR + 64, 4096, 64), SHAPE)]:
+        assert call(a, b) == want, (a, b)
+    assert call((ADDR, 0, 64), (ADDR + 64, 0, 64), blocks=1) == NULL
+    assert call((ADDR, 0, 64), (ADDR + 60, 0, 64), blocks=1) == SHAPE
