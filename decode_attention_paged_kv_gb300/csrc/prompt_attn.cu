@@ -590,14 +590,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   griddep_wait();
-  if (warp == 0)
-    copy_loop<DN>(a, m, sh, q_smem, ring);
-  else if (warp <= 2)
-    product_loop<DN>(a, F16, warp - 1, sh, q_smem, ring);
-  else if (warp == 3)
-    schedule_loop(a, sh);
-  else
+  // A row of scores and what is made of it need more registers than 168 a thread (65536 among
+  // 384), copies and products fewer: the softmax's warps take over 32 each from the others
+  // (104 + 2 x 200 = 3 x 168).  Without spilt registers 32 prompts of 256 tokens, 16 heads take
+  // 38 us, not 48, the last 2K tokens of 4 x 8K 476, not 484.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 0)
+      copy_loop<DN>(a, m, sh, q_smem, ring);
+    else if (warp <= 2)
+      product_loop<DN>(a, F16, warp - 1, sh, q_smem, ring);
+    else
+      schedule_loop(a, sh);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     softmax_loop<DN, F16>(a, warp >= 8, sh);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
