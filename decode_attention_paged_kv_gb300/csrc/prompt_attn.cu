@@ -62,7 +62,7 @@ struct Shared {
   uint64_t work_full[2], work_free[2], taken, wanted;
   alignas(16) uint4 handle;  // of the CTA taken over
   uint32_t tmem;
-  uint32_t fills[kSlots], q_fills, takes;  // for the drain
+  uint32_t fills[kSlots], q_fills[2], takes;  // for the drain
   volatile int abort;
   Work work[2];  // by turns
 };
@@ -263,27 +263,27 @@ __device__ __forceinline__ void copy_loop(const PromptArgs& a, const Maps& m, Sh
 #pragma unroll
       for (int c = 0; c < S::kPieces; ++c) {
         if (i == 0 && c == S::kQChunks) {  // the queries, after the first keys
-          if (j > 0)
-            ok = lanes_wait(true, smem_u32(&sh.q_free[0]), (j - 1) & 1, a.wait_limit_ns, &sh.abort) &&
-                 lanes_wait(true, smem_u32(&sh.q_free[1]), (j - 1) & 1, a.wait_limit_ns, &sh.abort);
-          if (!ok) break;
-          if (elect_one()) {
-            ++sh.q_fills;
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+            ok = j == 0 ||
+                 lanes_wait(true, smem_u32(&sh.q_free[x]), (j - 1) & 1, a.wait_limit_ns, &sh.abort);
+            if (!ok) break;
+            const uint32_t bar = smem_u32(&sh.q_full[x]), to = q_smem + x * S::kQBytes;
+            if (elect_one()) {
+              ++sh.q_fills[x];
+              if (used >> x & 1) {
+                mbar_arrive_expect_tx(bar, S::kQBytes);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t bar = smem_u32(&sh.q_full[x]), to = q_smem + x * S::kQBytes;
-              if (!(used >> x & 1)) {
+                for (int d = 0; d < S::kQChunks - 1; ++d)
+                  tma_load_4d(to + d * kPieceBytes, &m.qn, bar, 64 * d, h, q + x * kRows, 0);
+                tma_load_4d(to + (S::kQChunks - 1) * kPieceBytes, &m.qr, bar, 0, h, q + x * kRows, 0);
+              } else {
                 mbar_arrive(bar);
-                continue;
               }
-              mbar_arrive_expect_tx(bar, S::kQBytes);
-#pragma unroll
-              for (int d = 0; d < S::kQChunks - 1; ++d)
-                tma_load_4d(to + d * kPieceBytes, &m.qn, bar, 64 * d, h, q + x * kRows, 0);
-              tma_load_4d(to + (S::kQChunks - 1) * kPieceBytes, &m.qr, bar, 0, h, q + x * kRows, 0);
             }
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
         }
         if (i >= n) continue;
         if (again &&
@@ -414,10 +414,9 @@ __device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, int 
           for (int c = 0; c < S::kQChunks; ++c)
             mbar_arrive(smem_u32(&sh.empty[(base + S::kVChunks + c) % kSlots]));
         }
-        if (i == n) {  // the block's queries are free, its output is complete
-          tc_commit(smem_u32(&sh.q_free[x]));
-          tc_commit(smem_u32(&sh.o_done[x]));
-        }
+        // the block's queries are free; its output is complete
+        if (i == max(n - 1, 0)) tc_commit(smem_u32(&sh.q_free[x]));
+        if (i == n) tc_commit(smem_u32(&sh.o_done[x]));
       }
       __syncwarp();
     }
@@ -582,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&sh.taken), 1);
     mbar_init(smem_u32(&sh.wanted), 1);
     sh.abort = 0;
-    sh.q_fills = sh.takes = 0;
+    sh.q_fills[0] = sh.q_fills[1] = sh.takes = 0;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
@@ -613,8 +612,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x;
     if (lane < kSlots && sh.fills[lane] > 0)
       mbar_wait_bounded(smem_u32(&sh.full[lane]), (sh.fills[lane] - 1) & 1, kDrainNs, nullptr);
-    if (lane >= 30 && sh.q_fills > 0)
-      mbar_wait_bounded(smem_u32(&sh.q_full[lane - 30]), (sh.q_fills - 1) & 1, kDrainNs, nullptr);
+    if (lane >= 30 && sh.q_fills[lane - 30] > 0)
+      mbar_wait_bounded(smem_u32(&sh.q_full[lane - 30]), (sh.q_fills[lane - 30] - 1) & 1, kDrainNs,
+                        nullptr);
     if (lane == 29 && sh.takes > 0)
       mbar_wait_bounded(smem_u32(&sh.taken), (sh.takes - 1) & 1, kDrainNs, nullptr);
     __syncwarp();
