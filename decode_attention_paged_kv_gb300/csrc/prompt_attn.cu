@@ -432,6 +432,33 @@ __device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, int 
   drain_products(&sh.drain[x]);
 }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
+  return x;
+}
+__device__ __forceinline__ float2 halves_of(uint64_t x) {
+  float2 y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <int DN, bool F16>
 __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared& sh) {
   using S = Shape<DN>;
@@ -467,7 +494,7 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
       }
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 128; ++c) top[c % 4] = fmaxf(top[c % 4], s[c]);
+      for (int c = 0; c < 128; c += 2) top[c / 2 % 4] = max3(top[c / 2 % 4], s[c], s[c + 1]);
       const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
       if (i == 0) {
         m = high;
@@ -490,20 +517,23 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
         }
       }
       const float ref = m == -INFINITY ? 0.f : m;
-      float sum[4] = {};
+      const uint64_t scale2 = pair_of(scale, scale), ref2 = pair_of(-ref, -ref);
+      uint64_t sum[4] = {};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t p[32];
 #pragma unroll
         for (int y = 0; y < 32; ++y) {
-          const float p0 = ex2(fmaf(s[64 * c + 2 * y], scale, -ref));
-          const float p1 = ex2(fmaf(s[64 * c + 2 * y + 1], scale, -ref));
-          sum[y % 4] += p0 + p1;
+          const float2 e =
+              halves_of(fma2(pair_of(s[64 * c + 2 * y], s[64 * c + 2 * y + 1]), scale2, ref2));
+          const float p0 = ex2(e.x), p1 = ex2(e.y);
+          sum[y % 4] = add2(sum[y % 4], pair_of(p0, p1));
           p[y] = pack2<F16>(p0, p1);
         }
         tmem_st32(ts + 32 * c, p);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      const float2 both = halves_of(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+      l += both.x + both.y;
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(smem_u32(&sh.p_ready[x]));
