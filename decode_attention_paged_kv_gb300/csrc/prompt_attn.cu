@@ -340,8 +340,10 @@ __device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, int 
     const int n = uniform(max(w.tiles[0], w.tiles[1]));
     const int tiles = uniform(w.tiles[x]), nk = uniform(w.nk);
     // Step i: the values of key tile i - 1 and the scores of key tile i, whose pieces follow
-    // one another.  One wait for all that they need, one go: a second wait between them
-    // left the tensor cores idle for 350 cycles.
+    // one another.  One wait for all that they need, one go: a second wait between them left the
+    // tensor cores idle for 350 cycles.  Queries and output are waited for in every block,
+    // whatever it uses of them: a warp that went on without would complete a barrier twice
+    // before it is looked at.
     for (int i = 0; i <= n; ++i) {
       const bool values = i > 0, scores = i < n;  // what the step has
       const bool use_values = values && i <= tiles, use_scores = i < tiles;  // for x
@@ -352,11 +354,11 @@ __device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, int 
       if (lane == S::kPieces) {
         bar = smem_u32(&sh.p_ready[x]), parity = (done + i - 1) & 1, wanted = use_values;
       } else if (lane == S::kPieces + 1) {
-        bar = smem_u32(&sh.q_full[x]), parity = j & 1, wanted = use_scores && i == 0;
+        bar = smem_u32(&sh.q_full[x]), parity = j & 1, wanted = i == 0;
       } else if (lane == S::kPieces + 2) {
         bar = smem_u32(&sh.turn[x]), parity = (steps + i - 1 + x) & 1, wanted = steps + i + x > 0;
       } else if (lane == S::kPieces + 3) {  // that the last block's output has been read
-        bar = smem_u32(&sh.o_free[x]), parity = (j - 1) & 1, wanted = j > 0 && i == 1;
+        bar = smem_u32(&sh.o_free[x]), parity = (j - 1) & 1, wanted = j > 0 && i == min(n, 1);
       }
       ok = lanes_wait(wanted, bar, parity, a.wait_limit_ns, &sh.abort);
       if (!ok) break;

@@ -494,6 +494,28 @@ def test_prompt_many_blocks(dkv):
         assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("dn", [64, 128])
+@pytest.mark.parametrize("kind", ["one tile", "no keys", "mixed"])
+def test_prompt_blocks_that_use_one_query_tile_or_none(dkv, dn, kind):
+    # many blocks, one after another on a multiprocessor, of which only the first query tile has
+    # keys, or neither: what a block does not use must not let a warp run ahead
+    B, H = 48, 16
+    nq = [{"one tile": 100, "no keys": 300, "mixed": (100, 300, 280, 513)[b % 4]}[kind]
+          for b in range(B)]
+    nk = [{"one tile": 100, "no keys": 0, "mixed": (100, 0, 150, (1, 600)[b % 8 < 4])[b % 4]}[kind]
+          for b in range(B)]
+    args, out = prompt_case(H, dn, nq, nk, torch.bfloat16, gen_of("unused", kind, dn))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    dkv.latent_prompt_attn(*args, 0.08, out=out, workspace=ws)
+    assert dkv.read_device_status(ws) == 0
+    check_prompt(args, out, nq, nk, 0.08, True)
+    again = torch.full_like(out, 5.0)
+    for _ in range(20):
+        dkv.latent_prompt_attn(*args, 0.08, out=again, workspace=ws)
+    assert dkv.read_device_status(ws) == 0
+    assert torch.equal(out, again)
+
+
 def test_prompt_rising_scores(dkv):
     # every key tile raises the maximum, or lies far below it
     n = 1000
