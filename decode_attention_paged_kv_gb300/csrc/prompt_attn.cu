@@ -44,7 +44,7 @@ constexpr int kThreads = 384;  // warps: copies, products (two), schedule, 2 x 4
 constexpr int kRows = 128;     // queries of a tile
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kPieceBytes = kKeys * 128;
-constexpr int kSlots = 8;
+constexpr int kSlots = 8;  // pieces: of a power of two (10, where there is room: 3% slower)
 constexpr float kRise = 8.f;
 
 // A block of queries of a head.
@@ -59,6 +59,7 @@ struct Work {
 struct Shared {
   uint64_t full[kSlots], empty[kSlots];
   uint64_t q_full[2], q_free[2], s_full[2], p_ready[2], o_done[2], o_free[2], turn[2], drain[2];
+  uint64_t s_free[2], v_done[2];
   uint64_t work_full[2], work_free[2], taken, wanted;
   alignas(16) uint4 handle;  // of the CTA taken over
   uint32_t tmem;
@@ -236,9 +237,13 @@ struct Shape {
   static constexpr int kQChunks = DN / 64 + 1, kVChunks = DN / 64;
   static constexpr int kPieces = kQChunks + kVChunks;  // of a key tile
   static constexpr int kQBytes = kQChunks * kPieceBytes;  // of a query tile
+  // Tensor memory of a query tile: scores, weights, output.  With 64 channels there is room for
+  // weights beside the scores, so the next scores are made while the softmax has these.
+  static constexpr bool kApart = DN == 64;
+  static constexpr uint32_t kScores = kApart ? 256 : 128;  // from one query tile to the other
+  static constexpr uint32_t kWeights = kApart ? 128 : 0;
+  static constexpr uint32_t kOutput = kApart ? 192 : 256, kOutputs = kApart ? 256 : 128;
   static constexpr size_t kSmem = 1024 + 2 * kQBytes + kSlots * kPieceBytes;
-  // tensor memory: scores and weights of the two query tiles, then their outputs
-  static constexpr uint32_t kOutput = 256;
 };
 
 struct Maps {
@@ -317,18 +322,80 @@ __device__ __forceinline__ void copy_loop(const PromptArgs& a, const Maps& m, Sh
   }
 }
 
-// Issues query tile x's products: its values, then its next scores, which take the place of
-// the weights just used (products of one thread run in order).  A warp for each query
-// tile: between its products a warp spends some 600 cycles on barriers and descriptors,
-// which the other's fill.  They take turns all the same: left alone they fall into step,
-// both in the softmax at one time and both at the tensor cores at another.
+// O (+)= P V of a key tile, by one thread; `base`: its first piece.
+template <int DN>
+__device__ __forceinline__ void issue_values(Shared& sh, uint32_t ring, uint32_t output_at,
+                                             uint32_t weights_at, uint32_t desc, int base, int keep) {
+  using S = Shape<DN>;
+  // (a product for each piece: two are not neighbours where the ring wraps)
+#pragma unroll 1
+  for (int c = 0; c < S::kVChunks; ++c) {
+    const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
+#pragma unroll
+    for (int y = 0; y < kKeys / 16; ++y)
+      tc_mma_ts(output_at + c * 64, weights_at + y * 8, smem_desc(v + y * 2048, 16, 1024), desc,
+                y > 0 ? 1 : keep);
+    tc_commit(smem_u32(&sh.empty[(base + c) % kSlots]));
+  }
+}
+// S = Q K^T of a key tile, likewise.
+template <int DN>
+__device__ __forceinline__ void issue_scores(Shared& sh, uint32_t ring, uint32_t scores_at,
+                                             uint32_t q, uint32_t desc, int base, int x) {
+  using S = Shape<DN>;
+#pragma unroll 1
+  for (int c = 0; c < S::kQChunks; ++c) {
+    const uint32_t k = ring + (base + c) % kSlots * kPieceBytes;
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      tc_mma(scores_at, smem_desc(q + c * kPieceBytes + y * 32, 16, 1024),
+             smem_desc(k + y * 32, 16, 1024), desc, c + y > 0);
+  }
+  tc_commit(smem_u32(&sh.s_full[x]));
+#pragma unroll
+  for (int c = 0; c < S::kQChunks; ++c) tc_commit(smem_u32(&sh.empty[(base + c) % kSlots]));
+}
+// Pieces that this query tile has no use for.
+template <int DN>
+__device__ __forceinline__ void pass_pieces(Shared& sh, int base, int count) {
+  for (int c = 0; c < count; ++c)
+    mbar_arrive(smem_u32(&sh.empty[(base + c) % kSlots]));
+}
+// Rows past the sequence may hold anything; a weight of 0 times NaN is NaN (both query tiles'
+// warps clear them: with the same zeros).
+template <int DN>
+__device__ __forceinline__ void clear_values(uint32_t ring, int base, int valid) {
+  using S = Shape<DN>;
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int c = 0; c < S::kVChunks; ++c) {
+    const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
+    for (int y = lane; y < (kKeys - valid) * 8; y += 32)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + valid * 128 + y * 16),
+                   "r"(0)
+                   : "memory");
+  }
+  fence_async_smem();
+  __syncwarp();
+}
+
+// Issues query tile x's products, a warp for each query tile: between its products a warp
+// spends some 600 cycles on barriers and descriptors, which the other's fill.
+// Weights in place of the scores (128 channels): the values, then the next scores, which take
+// the place of the weights just used (products of one thread run in order), with one wait for
+// all that they need: a second one left the tensor cores idle for 350 cycles.  The query tiles
+// take turns: left alone they fall into step, both in the softmax at one time and both at the
+// tensor cores at another.
+// Weights apart (64 channels): the next scores as soon as the softmax has read these, then
+// these values; a query tile's own products run beside its softmax, and no turns are needed.
 template <int DN>
 __device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, int x, Shared& sh,
                                              uint32_t q_smem, uint32_t ring) {
   using S = Shape<DN>;
   const int lane = threadIdx.x % 32;
   const uint32_t tmem = static_cast<uint32_t>(uniform(sh.tmem));
-  const uint32_t scores_at = tmem + x * 128, output_at = tmem + S::kOutput + x * 128;
+  const uint32_t scores_at = tmem + x * S::kScores, weights_at = scores_at + S::kWeights;
+  const uint32_t output_at = tmem + S::kOutput + x * S::kOutputs;
   const uint32_t q = q_smem + x * S::kQBytes;
   const uint32_t score_desc = mma_desc(f16, kRows, kKeys, false, false);
   const uint32_t value_desc = mma_desc(f16, kRows, 64, false, true);
@@ -340,87 +407,83 @@ __device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, int 
     const int n = uniform(max(w.tiles[0], w.tiles[1]));
     const int tiles = uniform(w.tiles[x]), nk = uniform(w.nk);
     // Step i: the values of key tile i - 1 and the scores of key tile i, whose pieces follow
-    // one another.  One wait for all that they need, one go: a second wait between them left the
-    // tensor cores idle for 350 cycles.  Queries and output are waited for in every block,
-    // whatever it uses of them: a warp that went on without would complete a barrier twice
-    // before it is looked at.
+    // one another.  Queries and output are waited for in every block, whatever it uses of them:
+    // a warp that went on without would complete a barrier twice before it is looked at.
     for (int i = 0; i <= n; ++i) {
       const bool values = i > 0, scores = i < n;  // what the step has
       const bool use_values = values && i <= tiles, use_scores = i < tiles;  // for x
       const int piece = pieces + i * S::kPieces - S::kVChunks;  // the first: of the values
       const int p = max(piece + lane, 0);
       uint32_t bar = smem_u32(&sh.full[p % kSlots]), parity = (p / kSlots) & 1;
-      bool wanted = lane < S::kVChunks ? values : (scores && lane < S::kPieces);
+      const bool a_value = lane < S::kVChunks && values;
+      const bool a_score = lane >= S::kVChunks && lane < S::kPieces && scores;
+      bool value_wait = a_value, score_wait = a_score;
       if (lane == S::kPieces) {
-        bar = smem_u32(&sh.p_ready[x]), parity = (done + i - 1) & 1, wanted = use_values;
+        bar = smem_u32(&sh.p_ready[x]), parity = (done + i - 1) & 1, value_wait = use_values;
       } else if (lane == S::kPieces + 1) {
-        bar = smem_u32(&sh.q_full[x]), parity = j & 1, wanted = i == 0;
+        bar = smem_u32(&sh.q_full[x]), parity = j & 1, score_wait = i == 0;
       } else if (lane == S::kPieces + 2) {
-        bar = smem_u32(&sh.turn[x]), parity = (steps + i - 1 + x) & 1, wanted = steps + i + x > 0;
+        if (S::kApart)  // that the softmax has read the scores before
+          bar = smem_u32(&sh.s_free[x]), parity = (done + i - 1) & 1,
+          score_wait = use_scores && done + i > 0;
+        else
+          bar = smem_u32(&sh.turn[x]), parity = (steps + i - 1 + x) & 1,
+          score_wait = steps + i + x > 0;
       } else if (lane == S::kPieces + 3) {  // that the last block's output has been read
-        bar = smem_u32(&sh.o_free[x]), parity = (j - 1) & 1, wanted = j > 0 && i == min(n, 1);
+        bar = smem_u32(&sh.o_free[x]), parity = (j - 1) & 1, value_wait = j > 0 && i == min(n, 1);
       }
-      ok = lanes_wait(wanted, bar, parity, a.wait_limit_ns, &sh.abort);
-      if (!ok) break;
       const int base = uniform(piece + 8 * kSlots), keep = uniform(i > 1);
       const bool do_values = uniform(use_values), do_scores = uniform(use_scores);
       const int valid = nk - (i - 1) * kKeys;
-      if (use_values && valid < kKeys) {
-        // rows past the sequence may hold anything; a weight of 0 times NaN is NaN (both
-        // query tiles' warps clear them: with the same zeros)
-#pragma unroll
-        for (int c = 0; c < S::kVChunks; ++c) {
-          const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
-          for (int y = lane; y < (kKeys - valid) * 8; y += 32)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + valid * 128 + y * 16),
-                         "r"(0)
-                         : "memory");
+      if constexpr (S::kApart) {
+        ok = lanes_wait(score_wait, bar, parity, a.wait_limit_ns, &sh.abort);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (do_scores)
+            issue_scores<DN>(sh, ring, scores_at, q, score_desc, base + S::kVChunks, x);
+          else if (scores)
+            pass_pieces<DN>(sh, base + S::kVChunks, S::kQChunks);
+          // the block's queries are free
+          if (i == max(n - 1, 0)) tc_commit(smem_u32(&sh.q_free[x]));
         }
-        fence_async_smem();
+        __syncwarp();
+        ok = lanes_wait(value_wait, bar, parity, a.wait_limit_ns, &sh.abort);
+        if (!ok) break;
+        if (use_values && valid < kKeys) clear_values<DN>(ring, base, valid);
+        tc_fence_after();
+        if (elect_one()) {
+          if (do_values) {
+            issue_values<DN>(sh, ring, output_at, weights_at, value_desc, base, keep);
+            tc_commit(smem_u32(&sh.v_done[x]));
+          } else if (values) {
+            pass_pieces<DN>(sh, base, S::kVChunks);
+          }
+          if (i == n) tc_commit(smem_u32(&sh.o_done[x]));
+        }
+        __syncwarp();
+      } else {
+        ok = lanes_wait(value_wait || score_wait, bar, parity, a.wait_limit_ns, &sh.abort);
+        if (!ok) break;
+        if (use_values && valid < kKeys) clear_values<DN>(ring, base, valid);
+        tc_fence_after();
+        if (elect_one()) {
+          if (do_values)
+            issue_values<DN>(sh, ring, output_at, weights_at, value_desc, base, keep);
+          else if (values)
+            pass_pieces<DN>(sh, base, S::kVChunks);
+          // (the other warp takes as long to begin as the scores to issue)
+          mbar_arrive(smem_u32(&sh.turn[1 - x]));
+          if (do_scores)
+            issue_scores<DN>(sh, ring, scores_at, q, score_desc, base + S::kVChunks, x);
+          else if (scores)
+            pass_pieces<DN>(sh, base + S::kVChunks, S::kQChunks);
+          // the block's queries are free; its output is complete
+          if (i == max(n - 1, 0)) tc_commit(smem_u32(&sh.q_free[x]));
+          if (i == n) tc_commit(smem_u32(&sh.o_done[x]));
+        }
         __syncwarp();
       }
-      tc_fence_after();
-      if (elect_one()) {
-        if (do_values) {
-          // (a product for each piece: two are not neighbours where the ring wraps)
-#pragma unroll 1
-          for (int c = 0; c < S::kVChunks; ++c) {
-            const uint32_t v = ring + (base + c) % kSlots * kPieceBytes;
-#pragma unroll
-            for (int y = 0; y < kKeys / 16; ++y)
-              tc_mma_ts(output_at + c * 64, scores_at + y * 8, smem_desc(v + y * 2048, 16, 1024),
-                        value_desc, y > 0 ? 1 : keep);
-            tc_commit(smem_u32(&sh.empty[(base + c) % kSlots]));
-          }
-        } else if (values) {
-#pragma unroll
-          for (int c = 0; c < S::kVChunks; ++c) mbar_arrive(smem_u32(&sh.empty[(base + c) % kSlots]));
-        }
-        // (the other warp takes as long to begin as the scores to issue)
-        mbar_arrive(smem_u32(&sh.turn[1 - x]));
-        if (do_scores) {
-#pragma unroll 1
-          for (int c = 0; c < S::kQChunks; ++c) {
-            const uint32_t k = ring + (base + S::kVChunks + c) % kSlots * kPieceBytes;
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              tc_mma(scores_at, smem_desc(q + c * kPieceBytes + y * 32, 16, 1024),
-                     smem_desc(k + y * 32, 16, 1024), score_desc, c + y > 0);
-          }
-          tc_commit(smem_u32(&sh.s_full[x]));
-#pragma unroll
-          for (int c = 0; c < S::kQChunks; ++c)
-            tc_commit(smem_u32(&sh.empty[(base + S::kVChunks + c) % kSlots]));
-        } else if (scores) {
-#pragma unroll
-          for (int c = 0; c < S::kQChunks; ++c)
-            mbar_arrive(smem_u32(&sh.empty[(base + S::kVChunks + c) % kSlots]));
-        }
-        // the block's queries are free; its output is complete
-        if (i == max(n - 1, 0)) tc_commit(smem_u32(&sh.q_free[x]));
-        if (i == n) tc_commit(smem_u32(&sh.o_done[x]));
-      }
-      __syncwarp();
     }
     if (!ok) break;
     pieces = (pieces + n * S::kPieces) % (2 * kSlots);
@@ -466,7 +529,8 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
   using S = Shape<DN>;
   const int lane = threadIdx.x % 32, quarter = threadIdx.x / 32 % 4;
   const uint32_t tq = sh.tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-  const uint32_t ts = tq + x * 128, to = tq + S::kOutput + x * 128;
+  const uint32_t ts = tq + x * S::kScores, tp = ts + S::kWeights;
+  const uint32_t to = tq + S::kOutput + x * S::kOutputs;
   const float scale = fabsf(a.scale_log2);
   bool ok = true;
   int done = 0;  // key tiles of the blocks so far
@@ -485,6 +549,10 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, reinterpret_cast<float(&)[32]>(s[32 * c]));
       tmem_wait_ld();
+      if constexpr (S::kApart) {
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sh.s_free[x]));
+      }
       if (a.scale_log2 < 0.f) {
 #pragma unroll
         for (int c = 0; c < 128; ++c) s[c] = -s[c];
@@ -503,7 +571,14 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
       } else {
         const bool rise = high > m + kRise;
         if (__any_sync(0xffffffffu, rise)) {
-          // (the products of the tile before were done when these scores were)
+          // (the products of the tile before were done when these scores were: or, apart,
+          // are waited for)
+          if constexpr (S::kApart) {
+            ok = lanes_wait(true, smem_u32(&sh.v_done[x]), (done - 1) & 1, a.wait_limit_ns,
+                            &sh.abort);
+            if (!ok) break;
+            tc_fence_after();
+          }
           const float f = rise ? ex2(m - high) : 1.f;
           if (rise) m = high;
           l *= f;
@@ -521,6 +596,14 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
       const float ref = m == -INFINITY ? 0.f : m;
       const uint64_t scale2 = pair_of(scale, scale), ref2 = pair_of(-ref, -ref);
       uint64_t sum[4] = {};
+      if constexpr (S::kApart) {
+        // the weights before these have been used
+        if (i > 0) {
+          ok = lanes_wait(true, smem_u32(&sh.v_done[x]), (done - 1) & 1, a.wait_limit_ns, &sh.abort);
+          if (!ok) break;
+          tc_fence_after();
+        }
+      }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t p[32];
@@ -532,7 +615,7 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
           sum[y % 4] = add2(sum[y % 4], pair_of(p0, p1));
           p[y] = pack2<F16>(p0, p1);
         }
-        tmem_st32(ts + 32 * c, p);
+        tmem_st32(tp + 32 * c, p);
       }
       const float2 both = halves_of(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
       l += both.x + both.y;
@@ -606,6 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sh.o_done[x]), 1);
       mbar_init(smem_u32(&sh.o_free[x]), kRows);
       mbar_init(smem_u32(&sh.turn[x]), 1);
+      mbar_init(smem_u32(&sh.s_free[x]), kRows);
+      mbar_init(smem_u32(&sh.v_done[x]), 1);
       mbar_init(smem_u32(&sh.drain[x]), 1);
       mbar_init(smem_u32(&sh.work_full[x]), 1);
       mbar_init(smem_u32(&sh.work_free[x]), kReaders);
