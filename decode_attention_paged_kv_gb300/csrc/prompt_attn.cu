@@ -87,19 +87,35 @@ __device__ __forceinline__ int seen_by(const PromptArgs& a, const Work& w, int r
   return a.causal ? min(w.nk, max(0, w.nk - w.nq + row + 1)) : w.nk;
 }
 
-// Which block a CTA number stands for: sequences in order, heads within, blocks within from
-// the last to the first (the last sees the most keys).  Blocks of one head run side by
-// side and find its keys in the L2.  One warp, 32 sequences at a time.
+// Which block a CTA number stands for: sequences in order of their keys (of 32 at a time, the
+// most first), within from the last queries to the first (the last see the most keys), heads
+// within, so that long blocks begin early and short ones fill the end.  One warp.
 struct Finder {
   const PromptArgs& a;
   int b0 = 0;
   long long before = 0;  // blocks of the sequences before b0
+  int b;             // the lane's sequence
   Bounds mine;
-  long long blocks;  // of the lane's sequence, all heads
+  long long blocks;  // of it, all heads
   __device__ __forceinline__ explicit Finder(const PromptArgs& a_) : a(a_) { load(); }
   __device__ __forceinline__ void load() {
-    const int b = b0 + static_cast<int>(threadIdx.x % 32);
+    const int lane = threadIdx.x % 32;
+    b = b0 + lane;
     mine = b < a.B ? bounds(a, b) : Bounds{0, 0, 0, 0};
+    if (a.B > 1) {
+      int before_mine = 0, from = 0;
+#pragma unroll
+      for (int x = 0; x < 32; ++x) {
+        const int nk = __shfl_sync(0xffffffffu, mine.nk, x);
+        before_mine += nk > mine.nk || (nk == mine.nk && x < lane);
+      }
+#pragma unroll
+      for (int x = 0; x < 32; ++x)
+        if (__shfl_sync(0xffffffffu, before_mine, x) == lane) from = x;
+      b = b0 + from;
+      mine = {__shfl_sync(0xffffffffu, mine.q0, from), __shfl_sync(0xffffffffu, mine.nq, from),
+              __shfl_sync(0xffffffffu, mine.k0, from), __shfl_sync(0xffffffffu, mine.nk, from)};
+    }
     blocks = (mine.nq + 2ll * kRows - 1) / (2 * kRows) * a.H;
   }
   __device__ __forceinline__ Work find(long long item) {
@@ -119,14 +135,14 @@ struct Finder {
       if (past != 0) {
         const int from = __ffs(past) - 1;
         const int i = static_cast<int>(item - __shfl_sync(0xffffffffu, end - blocks, from));
-        w.b = b0 + from;
+        w.b = __shfl_sync(0xffffffffu, b, from);
         w.q0 = __shfl_sync(0xffffffffu, mine.q0, from);
         w.nq = __shfl_sync(0xffffffffu, mine.nq, from);
         w.k0 = __shfl_sync(0xffffffffu, mine.k0, from);
         w.nk = __shfl_sync(0xffffffffu, mine.nk, from);
         const int per = (w.nq - 1) / (2 * kRows) + 1;
-        w.h = i / per;
-        w.row = (per - 1 - i % per) * (2 * kRows);
+        w.h = i % a.H;
+        w.row = (per - 1 - i / a.H) * (2 * kRows);
 #pragma unroll
         for (int x2 = 0; x2 < 2; ++x2) {
           const int first = w.row + x2 * kRows;  // of the tile's queries
