@@ -8,7 +8,8 @@
 // tile of 128 and query tile
 //   S = Q K^T     M = 128, N = 128, dn + 64 channels: both operands from shared memory
 //   O += P V      M = 128, N = dn, 128 tokens: P from tensor memory, where it takes the
-//                 place of the scores it was made of; V as it was copied (MN-major)
+//                 place of the scores it was made of (dn = 128) or lies beside them (64: the
+//                 next scores are made meanwhile); V as it was copied (MN-major)
 // A thread has a row of scores to itself (128 threads a query tile), so the softmax needs
 // no exchange; a row's output lies in the lane of its thread, so each warp scales its own
 // rows when a score passes the running reference by 2^8, which is seldom.
@@ -24,13 +25,17 @@
 //
 // Maxima, sums and outputs are fp32; a weight is rounded once to the inputs' type for its
 // product.  Measured on a GB300, bf16: the last 2K tokens of 4 prompts of 8K, 16 heads, dn =
-// 128: 483 us, 1.25 PFLOP/s of the 1.9 that a large library product reaches; one prompt of
-// 8K 307 us (1.12); 16 of 512 tokens, 32 heads, dn = 64 61 us (0.42).  What bounds it: a query tile's
-// chain scores - softmax - values, some 4000 cycles for 2560 of products for two tiles; the
-// scores' operands alone take all of the shared memory's rate while they run, and the next
-// tile's keys arrive late (8 pieces).  345 us (listed batch, now 265) with one warp for both
-// tiles' products, 296 with a warp each in turns, 266 with blocks taken over; a softmax in
-// halves and a second wait between values and scores made no difference.
+// 128: 423 us, 1.42 PFLOP/s of the 1.9 that a large library product reaches; one prompt of
+// 8K 226 us (1.52); 2 of 2K with 128 heads 273 us (1.26); one of 16K, 8 heads, dn = 64 332 us
+// (1.24); 16 of 512 tokens, 32 heads, dn = 64 51 us (0.50).  What bounds it: with dn = 128 a
+// query tile's chain scores - softmax - values, some 3600 cycles for 2560 of products for two
+// tiles; with dn = 64 the softmax's instructions (1540 of products); of short prompts the
+// chain's beginning and end.  What carried it, listed batch of long prompts: 345 us with one
+// warp for both tiles' products, 296 with a warp each in turns, 266 with blocks taken over, 258
+// without spilt registers, 244 with weights made two at a time, 234 with products in functions
+// of their own (fewer instructions for the caches), 216 with long blocks first.  No difference
+// made a softmax in halves and a second wait between values and scores; outputs read 32
+// columns at a time were 2% slower for short prompts.
 
 #include "dkv_device.cuh"
 #include "dkv_kernels.h"
@@ -89,7 +94,8 @@ __device__ __forceinline__ int seen_by(const PromptArgs& a, const Work& w, int r
 
 // Which block a CTA number stands for: sequences in order of their keys (of 32 at a time, the
 // most first), within from the last queries to the first (the last see the most keys), heads
-// within, so that long blocks begin early and short ones fill the end.  One warp.
+// within, so that long blocks begin early and short ones fill the end; as many heads at a time
+// as leave their keys in half of the L2 (2 prompts of 2K, 128 heads: 273 us, not 281).  One warp.
 struct Finder {
   const PromptArgs& a;
   int b0 = 0;
@@ -97,7 +103,11 @@ struct Finder {
   int b;             // the lane's sequence
   Bounds mine;
   long long blocks;  // of it, all heads
-  __device__ __forceinline__ explicit Finder(const PromptArgs& a_) : a(a_) { load(); }
+  int room, all_heads;  // keys of a head that half of the L2 holds, with their values; of all
+  __device__ __forceinline__ Finder(const PromptArgs& a_, int key_bytes)
+      : a(a_), room((64 << 20) / key_bytes), all_heads(room / a.H) {
+    load();
+  }
   __device__ __forceinline__ void load() {
     const int lane = threadIdx.x % 32;
     b = b0 + lane;
@@ -141,13 +151,20 @@ struct Finder {
         w.k0 = __shfl_sync(0xffffffffu, mine.k0, from);
         w.nk = __shfl_sync(0xffffffffu, mine.nk, from);
         const int per = (w.nq - 1) / (2 * kRows) + 1;
-        w.h = i % a.H;
-        w.row = (per - 1 - i / a.H) * (2 * kRows);
+        int first = 0, heads = a.H, rest = i;
+        if (w.nk > all_heads) {  // as many heads at a time as have room
+          const int group = max(room / w.nk, 1);
+          first = i / (per * group) * group;
+          heads = min(group, a.H - first);
+          rest = i - first * per;
+        }
+        w.h = first + rest % heads;
+        w.row = (per - 1 - rest / heads) * (2 * kRows);
 #pragma unroll
         for (int x2 = 0; x2 < 2; ++x2) {
-          const int first = w.row + x2 * kRows;  // of the tile's queries
-          const int seen = seen_by(a, w, min(first + kRows, w.nq) - 1);
-          w.tiles[x2] = first >= w.nq || seen == 0 ? 0 : (seen - 1) / kKeys + 1;
+          const int row = w.row + x2 * kRows;  // of the tile's first query
+          const int seen = seen_by(a, w, min(row + kRows, w.nq) - 1);
+          w.tiles[x2] = row >= w.nq || seen == 0 ? 0 : (seen - 1) / kKeys + 1;
         }
         return w;
       }
@@ -191,9 +208,9 @@ __device__ __forceinline__ bool taken_cta(const Shared& sh, uint32_t* cta) {
 }
 
 // Publishes the CTA's blocks, its own first, then those it takes over.
-__device__ __forceinline__ void schedule_loop(const PromptArgs& a, Shared& sh) {
+__device__ __forceinline__ void schedule_loop(const PromptArgs& a, int key_bytes, Shared& sh) {
   const int lane = threadIdx.x % 32;
-  Finder find(a);
+  Finder find(a, key_bytes);
   uint32_t cta = blockIdx.x;
   bool ok = true, more = true;  // more: `cta` is a CTA to stand in for
   for (int j = 0; ok; ++j) {
@@ -733,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp <= 2)
       product_loop<DN>(a, F16, warp - 1, sh, q_smem, ring);
     else
-      schedule_loop(a, sh);
+      schedule_loop(a, 4 * DN, sh);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     softmax_loop<DN, F16>(a, warp >= 8, sh);

@@ -516,6 +516,14 @@ def test_prompt_blocks_that_use_one_query_tile_or_none(dkv, dn, kind):
     assert torch.equal(out, again)
 
 
+def test_prompt_heads_in_groups(dkv):
+    # so many keys that heads are taken some at a time, the last group smaller; not by one
+    for H, nq, nk in (64, [300, 520], [2100, 5000]), (5, [260], [30000]):
+        args, out = prompt_case(H, 128, nq, nk, torch.bfloat16, gen_of("groups", H))
+        dkv.latent_prompt_attn(*args, 0.08, out=out)
+        check_prompt(args, out, nq, nk, 0.08, True)
+
+
 def test_prompt_rising_scores(dkv):
     # every key tile raises the maximum, or lies far below it
     n = 1000
