@@ -859,7 +859,10 @@ __global__ void __launch_bounds__(32 * MB * kJoinGroups) latent_join_kernel(cons
         x[y] = *reinterpret_cast<const float4*>(a.part_o + s * (128 * MB) + 4 * tid);
       }
       const float high = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
-      if (high == -INFINITY) continue;  // (no token seen so far)
+      if (high == -INFINITY) {  // no token seen so far: sums of 0, or NaN where all scores are
+        sum += l[0] + l[1] + l[2] + l[3];
+        continue;
+      }
       const float f0 = ex2(top - high);
       top = high;
       sum *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
@@ -876,7 +879,7 @@ __global__ void __launch_bounds__(32 * MB * kJoinGroups) latent_join_kernel(cons
     if (group > 0) return;
     float high = top;
     for (int g = 1; g < groups; ++g) high = fmaxf(high, stat[g][0]);
-    if (high == -INFINITY) high = 0.f;  // (no token seen: every sum is 0)
+    if (high == -INFINITY) high = 0.f;  // (every sum is 0 or NaN, and stays so times 0)
     const float f0 = ex2(top - high);
     sum *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
     for (int g = 1; g < groups; ++g) {

@@ -238,6 +238,31 @@ def test_decode_rising_scores(dkv):
         check_decode(x, ql, qr, out, [1024], [1], 1.0)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_decode_nan_scores(dkv, dt):
+    # NaN queries, and a NaN row among those that are seen, give rows of NaN, whether one CTA
+    # holds the sequence, some share it or all do; other heads and sequences are as ever
+    dt = DT[dt]
+    for lens in ([1000], [20000], [64] * 160, [30000, 5, 64, 700, 130], [9, 9]):
+        B, N, H, dc = len(lens), max(lens), 20, 256
+        gen = gen_of("nan", B, N)
+        cache, ql, qr, out = decode_case(B, 1, H, dc, N, 16, dt, gen, lens, [1] * B)
+        ql[0, 0, 3], qr[0, 0, 17, 5] = math.nan, math.nan
+        bad = torch.zeros(B, H, dtype=torch.bool, device="cuda")
+        bad[0, 3] = bad[0, 17] = True
+        if B > 2:
+            cache.pool[int(cache.block_table[2, 0]), 1, 7] = math.nan
+            bad[2] = True
+        dkv.latent_decode_attn(ql, qr, cache, 0.07, seq_lens=ints(lens), out=out)
+        assert torch.equal(out[:, 0].isnan().all(-1), bad), lens
+        for b in range(min(B, 8)):
+            x, on = rows_of(cache, b)[:lens[b]], ~bad[b]
+            if not bool(on.any()):
+                continue
+            q = torch.cat((ql[b, 0], qr[b, 0]), -1)[on]
+            check(out[b, 0][on], *attn64(q, x, x[:, :dc], 0.07), dt, (lens, b))
+
+
 def test_decode_shared_operands(dkv):
     # one cache for all sequences, one query for all heads: dimensions of stride 0
     gen = gen_of("expanded")
