@@ -16,9 +16,9 @@
 // eight that do the softmax -- 8 tokens of each of two rows a thread, loaded so that all
 // lanes have work although 16 rows fill half of them -- and own the output.  The weights go
 // to the tile's own rotated-key columns, which nothing reads after the first product.  The
-// running maximum moves only when a score passes it by 2^8: O is scaled seldom, and
-// weights up to 2^8 lose nothing in 16 bits (each is rounded once, by half a step of the
-// type; maxima, sums and O are fp32).
+// running maximum moves only when a score passes it by 2^8: O is scaled seldom.  A weight
+// is rounded once, by half a step of the type, and relative to 2^-7 of that maximum in fp16,
+// so that the tail of a long sequence stays in its range; maxima, sums and O are fp32.
 //
 // Work: the tiles of all sequences in order are cut into equal shares, one a CTA, so
 // ragged batches balance; a sequence that shares cut leaves parts (maximum, sum, O in
@@ -55,7 +55,11 @@ constexpr int kCopyWarps = 2;  // warps 0 and 2 (1 and 3: products)
 constexpr int kTile = kLatentTile;
 constexpr int kChunkBytes = kTile * 128;  // 64 tokens x 64 channels
 constexpr int kPairBytes = 2 * kChunkBytes;
-constexpr float kRise = 8.f;  // how far (log2) a score may pass the reference
+constexpr float kRise = 8.f;  // how far (log2) a score may pass the running maximum
+// How far (log2) below that maximum fp16 weights have their reference: the largest are 2^15, and
+// those down to 2^-21 of it keep the type's 11 bits (down to 2^-14 otherwise, and none below
+// 2^-25: 1M tokens 17.4 below one lost 2.8% of the mass that their sum counts).
+constexpr float kHalfRoom = 7.f;
 // Tiles up to which each has a CTA; past it a share is two at least.  (us: two sequences of
 // 1K tokens, 16 heads: one tile a share 12.8, two 14.1; one of 8K: 19.2 and 16.4, of which
 // the join of 128 parts is a third.)
@@ -564,12 +568,14 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
   const uint32_t tq = sh.tmem + (static_cast<uint32_t>(32 * quarter) << 16);
   const Row row[2] = {row_of<RT>(a, rt, min(r0, RT - 1)), row_of<RT>(a, rt, min(r0 + 8, RT - 1))};
   const int token = 32 * half + 2 * (lane % 4);  // the thread's first one of a tile
+  const float room = a.f16 ? kHalfRoom : 0.f, far = kRise + room;
   int i = 0;
   Ring<S::kKeys> key;
   bool bad = false;
   for (Walk k(a, w, first_t); k.next();) {
     bool on[2];
     int seen[2];
+    // (m: what weights are relative to, 2^m; ref: the same, 0 where no token is seen yet)
     float m[2] = {-INFINITY, -INFINITY}, ref[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -625,7 +631,8 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
       }
       // the first tile sets the references; later ones keep them unless a score rises far
       // past its row's.  (The tile's number, not a flag: nothing has to be cleared.)
-      const bool rise = t == 0 || top[0] > m[0] + kRise || top[1] > m[1] + kRise;
+      // (Differences: a sum m + 8 would round to m or m + 16 at 2^27.)
+      const bool rise = t == 0 || top[0] - m[0] > far || top[1] - m[1] > far;
       if (__any_sync(0xffffffffu, rise) && lane == 0) sh.rose[i & 1] = i + 1;
       if (bad) sh.failed[i & 1] = 1;
       mbar_arrive(smem_u32(&sh.voted[i & 1]));
@@ -647,11 +654,11 @@ __device__ __forceinline__ void softmax_loop(const LatentAttnArgs& a, const Shar
             const float high = fmaxf(sh.top[i & 1][0][r], sh.top[i & 1][1][r]);
             float f = 1.f;
             if (t == 0) {
-              m[e] = high;
-            } else if (high > m[e] + kRise) {
-              f = ex2(m[e] - high);
+              m[e] = high - room;
+            } else if (high - m[e] > far) {
+              f = ex2(m[e] - (high - room));
               l[e] *= f;
-              m[e] = high;
+              m[e] = high - room;
             }
             ref[e] = m[e] == -INFINITY ? 0.f : m[e];
             if (half == 0 && lane % 4 == 0) sh.factor[r] = f;

@@ -263,6 +263,55 @@ def test_decode_nan_scores(dkv, dt):
             check(out[b, 0][on], *attn64(q, x, x[:, :dc], 0.07), dt, (lens, b))
 
 
+@pytest.mark.parametrize("gap", [19.7, 23.4, 25.05])
+def test_decode_fp16_long_tail(dkv, gap):
+    # one token 2^gap ahead of 32K others, every sequence whole in a CTA: the tail's weights
+    # lie far below what fp16 holds beside 1, their sum does not.  A weight is 2^7 at its row's
+    # reference and rounded by 2^-25 at most where it is an fp16 subnormal: N 2^-25 of a sum of
+    # 2^7 or more, 2^-17 of the values, beside the half step that `check` allows.
+    N, B, dc, H = 1 << 15, 152, 256, 5
+    gen = gen_of("tail", gap)
+    x = torch.zeros(1, N, dc + 64, dtype=torch.float16, device="cuda")
+    x[..., :dc] = 0.5 + torch.rand(dc, generator=gen, device="cuda")
+    x[0, 0, dc] = gap * math.log(2)
+    ql = torch.zeros(1, 1, H, dc, dtype=torch.float16, device="cuda")
+    qr = torch.zeros(1, 1, H, 64, dtype=torch.float16, device="cuda")
+    qr[..., 0] = 1.0
+    ql, qr = ql.expand(B, 1, H, dc), qr.expand(B, 1, H, 64)
+    out = dkv.latent_decode_attn(ql, qr, x.expand(B, N, dc + 64), 1.0)
+    q = torch.cat((ql[0, 0, :1], qr[0, 0, :1]), -1)
+    ref, mag, rel = attn64(q, x[0], x[0, :, :dc], 1.0)
+    check(out.flatten(0, 2), ref, mag, rel, torch.float16, gap)
+
+
+@pytest.mark.parametrize("dt,power", [("bf16", 12), ("bf16", 30), ("bf16", 60), ("bf16", 100),
+                                      ("fp16", 12), ("fp16", 21), ("fp16", 26), ("fp16", 30)])
+def test_decode_large_scores(dkv, dt, power):
+    # Scores up to 2^107: a row's largest are equal, the next ones half as large, so that the
+    # output is the mean of the largest ones' values, wherever the scores lie.  (Scores are
+    # whole numbers below 2^7 times a power of two, exact in fp32.)  Equal weights are
+    # rounded alike, by half a step of the type; the sums add 2^-12.
+    dt, H, dc, N = DT[dt], 9, 256, 700
+    gen = gen_of("large", power)
+    for scale in (0.08, -0.0721):
+        cache, ql, qr, _ = decode_case(2, 1, H, dc, N, 0, dt, gen, [N, N], [1, 1])
+        hot = torch.zeros(N, dtype=torch.bool, device="cuda")
+        hot[torch.randperm(N, generator=gen, device="cuda")[:9]] = True
+        ql.zero_()
+        qr.fill_(2.0 ** (power // 2))
+        for h in range(H):  # channels that count
+            qr[:, :, h, 61 - 5 * h:] = 0.0
+        top, low = 2.0 ** (power - power // 2), 2.0 ** (power - power // 2 - 1)
+        cache[..., dc:] = torch.where(hot, *((top, low) if scale > 0 else (low, top)))[:, None]
+        # shared by several CTAs; whole in each
+        for B in (2, 160):
+            c, q, r = (x if B == 2 else x[:1].expand(B, *x.shape[1:]) for x in (cache, ql, qr))
+            out = dkv.latent_decode_attn(q, r, c, scale)
+            x = c[:, hot, :dc].double()
+            tol = (eps(dt) / 2 * 1.01 + 2.0 ** -12) * x.abs().mean(1)
+            assert bool(((out[:, 0] - x.mean(1)[:, None]).abs() <= tol[:, None]).all()), scale
+
+
 def test_decode_shared_operands(dkv):
     # one cache for all sequences, one query for all heads: dimensions of stride 0
     gen = gen_of("expanded")
