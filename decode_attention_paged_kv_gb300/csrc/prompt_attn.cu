@@ -24,7 +24,8 @@
 // multiprocessor is free.
 //
 // Maxima, sums and outputs are fp32; a weight is rounded once to the inputs' type for its
-// product.  Measured on a GB300, bf16: the last 2K tokens of 4 prompts of 8K, 16 heads, dn =
+// product, and is 2^7 at the running maximum in fp16, so that the tail of many keys stays in
+// its range.  Measured on a GB300, bf16: the last 2K tokens of 4 prompts of 8K, 16 heads, dn =
 // 128: 423 us, 1.42 PFLOP/s of the 1.9 that a large library product reaches; one prompt of
 // 8K 226 us (1.52); 2 of 2K with 128 heads 273 us (1.26); one of 16K, 8 heads, dn = 64 332 us
 // (1.24); 16 of 512 tokens, 32 heads, dn = 64 51 us (0.50).  What bounds it: with dn = 128 a
@@ -50,7 +51,12 @@ constexpr int kRows = 128;     // queries of a tile
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kPieceBytes = kKeys * 128;
 constexpr int kSlots = 8;  // pieces: of a power of two (10, where there is room: 3% slower)
-constexpr float kRise = 8.f;
+constexpr float kRise = 8.f;  // how far (log2) a score may pass the running maximum
+// What (log2) a weight is at the running maximum: in fp16 the largest are 2^15 then, and those
+// down to 2^-21 of the maximum keep the type's 11 bits (down to 2^-14 otherwise, and none below
+// 2^-25: 1M keys 17.4 below one lost 2.8% of the mass that their sum counts).
+template <bool F16>
+constexpr float kAtTop = F16 ? 7.f : 0.f;
 
 // A block of queries of a head.
 struct Work {
@@ -626,7 +632,7 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
           }
         }
       }
-      const float ref = m == -INFINITY ? 0.f : m;
+      const float ref = m == -INFINITY ? 0.f : m - kAtTop<F16>;
       const uint64_t scale2 = pair_of(scale, scale), ref2 = pair_of(-ref, -ref);
       uint64_t sum[4] = {};
       if constexpr (S::kApart) {

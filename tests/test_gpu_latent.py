@@ -612,6 +612,24 @@ def test_prompt_rising_scores(dkv):
         check_prompt(args, out, [300], [n], 1.0, False)
 
 
+@pytest.mark.parametrize("dn", [64, 128])
+@pytest.mark.parametrize("gap", [19.7, 23.4, 25.05])
+def test_prompt_fp16_long_tail(dkv, gap, dn):
+    # one key 2^gap ahead of 32K others (see test_decode_fp16_long_tail)
+    N, H, n = 1 << 15, 2, 3
+    gen = gen_of("ptail", gap, dn)
+    z = torch.zeros(1, 1, dn, dtype=torch.float16, device="cuda")
+    qn, kn = z.expand(n, H, dn), z.expand(N, H, dn)
+    qr = torch.zeros(n, H, 64, dtype=torch.float16, device="cuda")
+    kr = torch.zeros(N, 64, dtype=torch.float16, device="cuda")
+    qr[..., 0] = 1.0
+    kr[0, 0] = gap * math.log(2)
+    v = (0.5 + torch.rand(1, H, dn, generator=gen, device="cuda")).half().expand(N, H, dn)
+    args = (qn, qr, kn, kr, v, ints([0, n]), ints([0, N]))
+    out = dkv.latent_prompt_attn(*args, 1.0)
+    check_prompt(args, out, [n], [N], 1.0, True)
+
+
 def test_prompt_captured(dkv):
     args, out = prompt_case(3, 128, [300, 100], [400, 100], torch.bfloat16, gen_of("pg"), extra=300)
     cu_q, cu_k = args[5], args[6]
