@@ -57,6 +57,10 @@ constexpr float kRise = 8.f;  // how far (log2) a score may pass the running max
 // 2^-25: 1M keys 17.4 below one lost 2.8% of the mass that their sum counts).
 template <bool F16>
 constexpr float kAtTop = F16 ? 7.f : 0.f;
+// Scaled scores (log2) past which their running maximum is taken away before they are scaled:
+// below it a scaled maximum is rounded by 2^-14 at most, which is what weights of the two ways
+// differ by; at 2^30 it would be off by 32, and weights with it.
+constexpr float kFar = 1024.f;
 
 // A block of queries of a head.
 struct Work {
@@ -578,7 +582,17 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
     const int row = w.row + x * kRows + 32 * quarter + lane;  // within the sequence
     const bool on = row < w.nq;
     const int seen = on ? seen_by(a, w, row) : 0;
-    float m = -INFINITY, l = 0.f;
+    // m: the running maximum before it is scaled; from and ref are taken from scores before and
+    // after that
+    float m = -INFINITY, from = 0.f, ref = 0.f, l = 0.f;
+    bool far = false;
+    auto refer = [&](float high) {  // (the warp's lanes together)
+      m = high;
+      const bool none = m == -INFINITY;
+      far = __any_sync(0xffffffffu, !none && fabsf(m * scale) >= kFar);
+      from = none ? 0.f : m;
+      ref = (far ? 0.f : from * scale) - kAtTop<F16>;
+    };
     const int n = w.tiles[x];
     for (int i = 0; i < n; ++i, ++done) {
       ok = lanes_wait(true, smem_u32(&sh.s_full[x]), done & 1, a.wait_limit_ns, &sh.abort);
@@ -592,9 +606,13 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
         tc_fence_before();
         mbar_arrive(smem_u32(&sh.s_free[x]));
       }
+      // (by pairs, here and where scores are far: half the code, which all tiles fetch past)
       if (a.scale_log2 < 0.f) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c) s[c] = -s[c];
+        for (int c = 0; c < 128; c += 2) {
+          const float2 y = halves_of(fma2(pair_of(s[c], s[c + 1]), pair_of(-1.f, -1.f), 0));
+          s[c] = y.x, s[c + 1] = y.y;
+        }
       }
       const int limit = seen - i * kKeys;
       if (__any_sync(0xffffffffu, limit < kKeys)) {
@@ -604,11 +622,11 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int c = 0; c < 128; c += 2) top[c / 2 % 4] = max3(top[c / 2 % 4], s[c], s[c + 1]);
-      const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+      const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
       if (i == 0) {
-        m = high;
+        refer(high);
       } else {
-        const bool rise = high > m + kRise;
+        const bool rise = (high - m) * scale > kRise;
         if (__any_sync(0xffffffffu, rise)) {
           // (the products of the tile before were done when these scores were: or, apart,
           // are waited for)
@@ -618,8 +636,8 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
             if (!ok) break;
             tc_fence_after();
           }
-          const float f = rise ? ex2(m - high) : 1.f;
-          if (rise) m = high;
+          const float f = rise ? ex2((m - high) * scale) : 1.f;
+          refer(rise ? high : m);
           l *= f;
 #pragma unroll 1
           for (int c = 0; c < DN; c += 16) {
@@ -632,7 +650,13 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
           }
         }
       }
-      const float ref = m == -INFINITY ? 0.f : m - kAtTop<F16>;
+      if (far) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 2) {
+          const float2 y = halves_of(add2(pair_of(s[c], s[c + 1]), pair_of(-from, -from)));
+          s[c] = y.x, s[c + 1] = y.y;
+        }
+      }
       const uint64_t scale2 = pair_of(scale, scale), ref2 = pair_of(-ref, -ref);
       uint64_t sum[4] = {};
       if constexpr (S::kApart) {

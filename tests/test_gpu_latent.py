@@ -630,6 +630,33 @@ def test_prompt_fp16_long_tail(dkv, gap, dn):
     check_prompt(args, out, [n], [N], 1.0, True)
 
 
+@pytest.mark.parametrize("dn", [64, 128])
+@pytest.mark.parametrize("dt,power", [("bf16", 12), ("bf16", 30), ("bf16", 60), ("bf16", 100),
+                                      ("fp16", 12), ("fp16", 21), ("fp16", 26), ("fp16", 30)])
+def test_prompt_large_scores(dkv, dt, power, dn):
+    # Scores up to 2^107: a row's largest are equal, the next ones half as large, so that the
+    # output is the mean of the largest ones' values, wherever the scores lie and however the
+    # scale rounds.  (Scores are whole numbers below 2^7 times a power of two, exact in fp32.)
+    # Equal weights are rounded alike, by half a step of the type; the sums add 2^-12.
+    dt, H, n, m = DT[dt], 4, 140, 700
+    gen = gen_of("large", power, dn)
+    for scale in (0.08, -0.0721):
+        args, _ = prompt_case(H, dn, [n], [m], dt, gen, extra=0)
+        qn, qr, kn, kr, v = args[:5]
+        hot = torch.zeros(m, dtype=torch.bool, device="cuda")
+        hot[torch.randperm(m, generator=gen, device="cuda")[:9]] = True
+        qr.zero_(), kr.zero_()
+        qn.fill_(2.0 ** (power // 2))
+        for h, count in enumerate((61, 53, 47, 31)):  # channels that count
+            qn[:, h, count:] = 0.0
+        top, low = 2.0 ** (power - power // 2), 2.0 ** (power - power // 2 - 1)
+        kn[:] = torch.where(hot, *((top, low) if scale > 0 else (low, top)))[:, None, None]
+        out = dkv.latent_prompt_attn(*args, scale, causal=False)
+        x = v[hot].double()
+        tol = (eps(dt) / 2 * 1.01 + 2.0 ** -12) * x.abs().mean(0)
+        assert bool(((out - x.mean(0)).abs() <= tol).all()), scale
+
+
 def test_prompt_captured(dkv):
     args, out = prompt_case(3, 128, [300, 100], [400, 100], torch.bfloat16, gen_of("pg"), extra=300)
     cu_q, cu_k = args[5], args[6]
