@@ -53,7 +53,7 @@ struct LatentAttnArgs {
   int weighted;   // row tiles take CTAs by their tiles (at most kMaxWeighted of them)
   int2* pieces;   // [B, row_tiles]: where a sequence's parts lie
   float* part_ml;  // [splits * row_tiles, 2, rows of a tile, 2]
-  float* part_o;   // [splits * row_tiles, 2, rows of a tile, dc]
+  float* part_o;   // [splits * row_tiles, 2, rows of a tile, dc]; also of sequences summed so far
 };
 
 // How the rows and the work are cut; the workspace follows from it.
@@ -63,6 +63,7 @@ struct LatentPlan {
   size_t pieces, part_ml, part_o, total;  // workspace offsets
 };
 constexpr int kLatentTile = 64;  // tokens
+constexpr int kLatentRun = 128;  // tiles of a sequence that are summed up at a time
 constexpr int kLatentCtas = 152;
 constexpr int kMaxWeighted = 8;
 

@@ -96,8 +96,11 @@ dkv::LatentPlan latent_plan(const dkv_latent_attn* p, const dkv_latent_cache* c)
   L.ctas = L.splits * L.row_tiles;
   // (a bound that only rises with the sizes, so that a workspace serves smaller calls too)
   const int64_t most = tiles * L.row_tiles;
-  const size_t slots =
-      2 * static_cast<size_t>(most < dkv::kLatentCtas ? most : dkv::kLatentCtas) * L.tile_rows;
+  int64_t ctas = most < dkv::kLatentCtas ? most : dkv::kLatentCtas;
+  // (more CTAs than that have whole sequences: they need room where those are long)
+  if (ceil_div(c->seq_len, dkv::kLatentTile) > dkv::kLatentRun && ctas < L.row_tiles)
+    ctas = L.row_tiles;
+  const size_t slots = 2 * static_cast<size_t>(ctas) * L.tile_rows;
   L.pieces = DKV_WORKSPACE_HEADER_BYTES;
   L.part_ml = align_up(L.pieces + 8 * static_cast<size_t>(p->batch) * L.row_tiles);
   L.part_o = align_up(L.part_ml + 8 * slots);

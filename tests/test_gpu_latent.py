@@ -312,6 +312,61 @@ def test_decode_large_scores(dkv, dt, power):
             assert bool(((out[:, 0] - x.mean(1)[:, None]).abs() <= tol[:, None]).all()), scale
 
 
+@pytest.mark.parametrize("H,dt,gap", [(5, "fp16", 20.3), (5, "fp16", 25.2), (40, "fp16", -3.0),
+                                      (16, "bf16", -3.0), (24, "bf16", 12.0)])
+def test_decode_long_sums(dkv, H, dt, gap):
+    # a million tokens with values of one sign, every sequence whole in a CTA, one token 2^gap
+    # ahead of the others: what a product's adders cut off (of a term 2^-26 of the sum so far)
+    # must not add up over the sequence.  (fp16 weights: test_decode_fp16_long_tail.)
+    N, B, dc, dt = 1 << 20, 152, 256, DT[dt]
+    gen = gen_of("sums", gap)
+    x = torch.zeros(1, N, dc + 64, dtype=dt, device="cuda")
+    x[..., :dc] = 0.5 + torch.rand(N, dc, generator=gen, device="cuda")
+    x[0, 0, dc] = gap * math.log(2)
+    ql = torch.zeros(1, 1, H, dc, dtype=dt, device="cuda")
+    qr = torch.zeros(1, 1, H, 64, dtype=dt, device="cuda")
+    qr[..., 0] = 1.0
+    ql, qr = ql.expand(B, 1, H, dc), qr.expand(B, 1, H, 64)
+    out = dkv.latent_decode_attn(ql, qr, x.expand(B, N, dc + 64), 1.0)
+    q = torch.cat((ql[0, 0, :1], qr[0, 0, :1]), -1)
+    ref, mag, rel = attn64(q, x[0], x[0, :, :dc], 1.0)
+    check(out.flatten(0, 2), ref, mag, rel, dt, gap)
+    # the weights' rounding is the same for all of the tail, or beside nothing: the sums alone
+    if gap < 0:
+        assert float(((out - ref) / ref).abs().max()) < 2.0 ** -12
+
+
+@pytest.mark.parametrize("T,H,dc", [(1, 16, 512), (3, 64, 256)])
+def test_decode_long_ragged(dkv, T, H, dc):
+    # sequences of many times the tokens that are summed up at a time, whole in a CTA and cut
+    # between CTAs, among short and empty ones; the same bits each time
+    gen, B, N = gen_of("runs", T), 40, 70000
+    lens = [(0, 7, 70000, 8192, 8193, 16384, 33000, 50)[b % 8] for b in range(B)]
+    new = [1 if T == 1 else (3, 1, 2, 0)[b % 4] for b in range(B)]
+    x = torch.randn(1, N, dc + 64, generator=gen, device="cuda").bfloat16()
+    cache = x.expand(B, N, dc + 64)
+    ql = torch.randn(B, T, H, dc, generator=gen, device="cuda").bfloat16()
+    qr = torch.randn(B, T, H, 64, generator=gen, device="cuda").bfloat16()
+    out = torch.full((B, T, H, dc), 5.0, device="cuda")
+    ws = torch.zeros(dkv.latent_workspace_bytes(B, T, H, dc, N), dtype=torch.uint8, device="cuda")
+    again = out.clone()
+    for o in (out, again):
+        dkv.latent_decode_attn(ql, qr, cache, 0.07, seq_lens=ints(lens), new_lens=ints(new), out=o,
+                               workspace=ws)
+    assert dkv.read_device_status(ws) == 0
+    assert torch.equal(out, again)
+    check_decode(cache, ql, qr, out, lens, new, 0.07)
+
+
+def test_decode_long_sequence_of_many_row_tiles(dkv):
+    # more row tiles (160) than CTAs share a sequence, and more tokens than are summed at a time
+    lens, new = [20000], [40]
+    cache, ql, qr, out = decode_case(1, 40, 256, 256, 20000, 64, torch.bfloat16, gen_of("rows+"),
+                                     lens, new)
+    dkv.latent_decode_attn(ql, qr, cache, 0.07, seq_lens=ints(lens), out=out)
+    check_decode(cache, ql, qr, out, lens, new, 0.07)
+
+
 def test_decode_shared_operands(dkv):
     # one cache for all sequences, one query for all heads: dimensions of stride 0
     gen = gen_of("expanded")
