@@ -61,6 +61,12 @@ constexpr float kAtTop = F16 ? 7.f : 0.f;
 // below it a scaled maximum is rounded by 2^-14 at most, which is what weights of the two ways
 // differ by; at 2^30 it would be off by 32, and weights with it.
 constexpr float kFar = 1024.f;
+// Key tiles whose values are summed up at a time: the products' adders cut off what lies some
+// 2^-26 below the sum so far, which adds up (of equal weights and values 0.06% over 128K keys,
+// 0.6% over 1M; of 1M keys beside a heavy one 1.6%).  Tensor memory has no room for a second
+// sum, but the row's place in the output has: its mean so far, rounded to the output's type, goes
+// there, and what that leaves of the sum stays.
+constexpr int kRun = 64;
 
 // A block of queries of a head.
 struct Work {
@@ -567,6 +573,76 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// 8 channels of the output, as they lie there.
+__device__ __forceinline__ void load8(const void* out, int dtype, int64_t at, float (&x)[8]) {
+  if (dtype == 2) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(out) + at);
+    const float4 u = p[0], w = p[1];
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
+    return;
+  }
+  const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(out) + at);
+  const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = dtype == 1 ? lo16<true>(v[i]) : lo16<false>(v[i]);
+    x[2 * i + 1] = dtype == 1 ? hi16<true>(v[i]) : hi16<false>(v[i]);
+  }
+}
+// Stores 8 channels and leaves in x what was stored: rounded, 0 where that is not finite.
+__device__ __forceinline__ void store8(void* out, int dtype, int64_t at, float (&x)[8]) {
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    if (dtype != 2) {
+      const uint32_t y = dtype == 1 ? pack2<true>(x[i], x[i + 1]) : pack2<false>(x[i], x[i + 1]);
+      x[i] = dtype == 1 ? lo16<true>(y) : lo16<false>(y);
+      x[i + 1] = dtype == 1 ? hi16<true>(y) : hi16<false>(y);
+    }
+    x[i] = fabsf(x[i]) < INFINITY ? x[i] : 0.f;
+    x[i + 1] = fabsf(x[i + 1]) < INFINITY ? x[i + 1] : 0.f;
+    v[i / 2] = dtype == 1 ? pack2<true>(x[i], x[i + 1]) : pack2<false>(x[i], x[i + 1]);
+  }
+  if (dtype == 2) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+    p[0] = make_float4(x[0], x[1], x[2], x[3]), p[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+__device__ __forceinline__ float inverse_sum(float l) {  // 0 where a row sees no key
+  return l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+}
+
+// A row's sum in tensor memory: what lies aside of it (a mean of weight `aside`) taken back and,
+// if `put`, its mean over the weights' sum l laid aside in its place.  A warp's lanes together.
+template <int DN>
+__device__ __noinline__ void sum_aside(uint32_t to, void* out, int dtype, int64_t at, bool on,
+                                       float aside, float l, bool put) {
+  const float inv = inverse_sum(l);
+#pragma unroll 1
+  for (int c = 0; c < DN; c += 8) {
+    float o[8], mean[8];
+    tmem_ld8(to + c, o);
+    tmem_wait_ld();
+    if (on && aside > 0.f) {
+      load8(out, dtype, at + c, mean);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) o[y] = fmaf(mean[y], aside, o[y]);
+    }
+    if (on && put) {
+#pragma unroll
+      for (int y = 0; y < 8; ++y) mean[y] = o[y] * inv;
+      store8(out, dtype, at + c, mean);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) o[y] = fmaf(-mean[y], l, o[y]);
+    }
+    __syncwarp();
+    tmem_st8(to + c, o);
+  }
+  tmem_wait_st();
+}
+
 template <int DN, bool F16>
 __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared& sh) {
   using S = Shape<DN>;
@@ -593,6 +669,8 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
       from = none ? 0.f : m;
       ref = (far ? 0.f : from * scale) - kAtTop<F16>;
     };
+    const int64_t at = static_cast<int64_t>(w.q0 + row) * a.o_st + w.h * a.o_sh;
+    float aside = 0.f;  // the sum of the weights whose values' mean lies in the output
     const int n = w.tiles[x];
     for (int i = 0; i < n; ++i, ++done) {
       ok = lanes_wait(true, smem_u32(&sh.s_full[x]), done & 1, a.wait_limit_ns, &sh.abort);
@@ -626,8 +704,8 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
       if (i == 0) {
         refer(high);
       } else {
-        const bool rise = (high - m) * scale > kRise;
-        if (__any_sync(0xffffffffu, rise)) {
+        const bool rise = (high - m) * scale > kRise, put = i % kRun == 0;
+        if (__any_sync(0xffffffffu, rise || put)) {
           // (the products of the tile before were done when these scores were: or, apart,
           // are waited for)
           if constexpr (S::kApart) {
@@ -638,7 +716,11 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
           }
           const float f = rise ? ex2((m - high) * scale) : 1.f;
           refer(rise ? high : m);
-          l *= f;
+          if (put) {
+            sum_aside<DN>(to, a.out, a.out_dtype, at, on, aside, l, true);
+            aside = l;
+          }
+          l *= f, aside *= f;
 #pragma unroll 1
           for (int c = 0; c < DN; c += 16) {
             float o[16];
@@ -689,11 +771,13 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
     if (ok) ok = lanes_wait(true, smem_u32(&sh.o_done[x]), j & 1, a.wait_limit_ns, &sh.abort);
     if (!ok) break;
     tc_fence_after();
-    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-    const int64_t at = static_cast<int64_t>(w.q0 + row) * a.o_st + w.h * a.o_sh;
+    if (__any_sync(0xffffffffu, aside > 0.f))
+      sum_aside<DN>(to, a.out, a.out_dtype, at, on, aside, l, false);
+    const float inv = inverse_sum(l);
 #pragma unroll 1
     for (int c = 0; c < DN; c += 16) {
       float o[16];
+      __syncwarp();
       if (n > 0) {
         tmem_ld16(to + c, o);
         tmem_wait_ld();

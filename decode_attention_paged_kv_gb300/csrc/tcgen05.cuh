@@ -68,6 +68,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&x)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, float (&x)[8]) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[i]);
+}
 // 16 lanes x 32 columns: a thread holds columns 8 k + 2 (lane % 4) + {0, 1} of rows lane /
 // 4 (x[4 k], x[4 k + 1]) and lane / 4 + 8 (x[4 k + 2], x[4 k + 3]), k < 4.
 __device__ __forceinline__ void tmem_ld_16x32(uint32_t addr, float (&x)[16]) {
@@ -94,6 +104,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&x)[16]) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const float (&x)[8]) {
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(x[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "

@@ -712,6 +712,66 @@ def test_prompt_large_scores(dkv, dt, power, dn):
         assert bool(((out - x.mean(0)).abs() <= tol).all()), scale
 
 
+@pytest.mark.parametrize("dn", [64, 128])
+@pytest.mark.parametrize("dt,gap,out_dtype", [
+    ("fp16", 20.3, "fp16"), ("fp16", 25.2, "fp32"), ("fp16", -3.0, "fp16"), ("bf16", -3.0, "fp32"),
+    ("bf16", 12.0, "bf16"), ("fp16", 20.3, "bf16"), ("bf16", -3.0, "fp16")])
+def test_prompt_long_sums(dkv, dt, gap, out_dtype, dn):
+    # a million keys with values of one sign, one key 2^gap ahead of the others: what a
+    # product's adders cut off (of a term 2^-26 of the sum so far) must not add up over the
+    # keys.  (fp16 weights: N 2^-25 of a sum of 2^7 or more, 2^-12 of the values at the most.)
+    N, H, dt = 1 << 20, 2, DT[dt]
+    nq = [1, 2, 255]
+    gen = gen_of("psums", gap, dn)
+    z = torch.zeros(1, 1, dn, dtype=dt, device="cuda")
+    n = sum(nq)
+    qn, kn = z.expand(n, H, dn), z.expand(3 * N, H, dn)
+    qr = torch.zeros(n, H, 64, dtype=dt, device="cuda")
+    kr = torch.zeros(3 * N, 64, dtype=dt, device="cuda")
+    qr[..., 0] = 1.0
+    kr[::N, 0] = gap * math.log(2)
+    v = (0.5 + torch.rand(3 * N, H, dn, generator=gen, device="cuda")).to(dt)
+    out_dtype = DT.get(out_dtype, torch.float32)
+    out = torch.full((n + 1, H, dn), 5.0, dtype=out_dtype, device="cuda")
+    dkv.latent_prompt_attn(qn, qr, kn, kr, v, ints([0, 1, 3, n]), ints([0, N, 2 * N, 3 * N]), 1.0,
+                           causal=False, out=out[:n])
+    assert bool((out[n] == 5.0).all())
+    for h in range(H):
+        i = 0
+        for b, m in enumerate(nq):
+            keys, x = kr[b * N:(b + 1) * N], v[b * N:(b + 1) * N, h]
+            ref, mag, rel = attn64(qr[:1, h], keys, x, 1.0)
+            check(out[i:i + m, h], ref, mag, rel, dt, (h, b))
+            # (the weights' rounding is the same for all of the tail: the sums alone)
+            if gap < 0 and out_dtype == torch.float32:
+                assert float(((out[i:i + m, h] - ref) / ref).abs().max()) < 2.0 ** -12
+            i += m
+
+
+@pytest.mark.parametrize("dt,out_dtype", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "fp32")])
+def test_prompt_long_rising(dkv, dt, out_dtype):
+    # sums kept aside while the running maximum rises, near 0 and far from it, among rows of a
+    # short sequence; a row of NaN queries leaves the others alone
+    dt, (nq, nk) = DT[dt], ([700, 40], [40000, 20])
+    args, out = prompt_case(2, 64, nq, nk, dt, gen_of("prise+"), out_dtype=DT.get(out_dtype,
+                                                                                 torch.float32))
+    q, k = args[1], args[3]
+    q[:740].zero_(), k[:40020].zero_()
+    q[:740, :, 0] = 1.0
+    k[:40000, 0] = torch.arange(40000, device="cuda") / 1024
+    for scale in (1.0, -1.0, 100.0):
+        out.fill_(5.0)
+        dkv.latent_prompt_attn(*args, scale, out=out)
+        check_prompt(args, out, nq, nk, scale, True)
+        q[50, 1, 3] = math.nan
+        other = torch.full_like(out, 5.0)
+        dkv.latent_prompt_attn(*args, scale, out=other)
+        q[50, 1, 3] = 0.0
+        assert bool(other[50, 1].isnan().all())
+        other[50, 1] = out[50, 1]
+        assert torch.equal(out, other)
+
+
 def test_prompt_captured(dkv):
     args, out = prompt_case(3, 128, [300, 100], [400, 100], torch.bfloat16, gen_of("pg"), extra=300)
     cu_q, cu_k = args[5], args[6]
