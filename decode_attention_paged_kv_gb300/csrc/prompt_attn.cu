@@ -616,6 +616,8 @@ __device__ __forceinline__ float inverse_sum(float l) {  // 0 where a row sees n
 
 // A row's sum in tensor memory: what lies aside of it (a mean of weight `aside`) taken back and,
 // if `put`, its mean over the weights' sum l laid aside in its place.  A warp's lanes together.
+// (Not inlined: it is seldom called, and the code around it is fetched for every tile; inlined,
+// 16 prompts of up to 777 tokens take 66.8 us, not 66.0.)
 template <int DN>
 __device__ __noinline__ void sum_aside(uint32_t to, void* out, int dtype, int64_t at, bool on,
                                        float aside, float l, bool put) {
