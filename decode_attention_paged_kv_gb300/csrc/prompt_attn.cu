@@ -84,7 +84,10 @@ struct Shared {
   uint64_t work_full[2], work_free[2], taken, wanted;
   alignas(16) uint4 handle;  // of the CTA taken over
   uint32_t tmem;
-  uint32_t fills[kSlots], q_fills[2], takes;  // for the drain
+  // copies issued and CTAs asked for: for the drain; the first slot's also show progress to warps
+  // that wait for the end of a block, which 16M keys take 200 ms to reach
+  volatile uint32_t fills[kSlots];
+  uint32_t q_fills[2], takes;
   volatile int abort;
   Work work[2];  // by turns
 };
@@ -245,7 +248,7 @@ __device__ __forceinline__ void schedule_loop(const PromptArgs& a, int key_bytes
     // not before this block's copies are all under way: a block that waits here for its
     // turn is one that another multiprocessor could have begun
     if (w.b >= 0) {
-      ok = lanes_wait(true, smem_u32(&sh.wanted), j & 1, a.wait_limit_ns, &sh.abort);
+      ok = lanes_wait(true, smem_u32(&sh.wanted), j & 1, a.wait_limit_ns, &sh.abort, &sh.fills[0]);
       if (!ok) break;
     }
     if (lane == 0) take_cta(sh);
@@ -348,7 +351,7 @@ __device__ __forceinline__ void copy_loop(const PromptArgs& a, const Maps& m, Sh
         const int slot = uniform(at);
         const uint32_t bar = smem_u32(&sh.full[slot]), to = ring + slot * kPieceBytes;
         if (elect_one()) {
-          ++sh.fills[slot];
+          sh.fills[slot] = sh.fills[slot] + 1;
           mbar_arrive_expect_tx(bar, kPieceBytes);
           if (c < S::kQChunks - 1)
             tma_load_4d(to, &m.kn, bar, 64 * c, h, row, 0);
@@ -770,7 +773,9 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
       tc_fence_before();
       mbar_arrive(smem_u32(&sh.p_ready[x]));
     }
-    if (ok) ok = lanes_wait(true, smem_u32(&sh.o_done[x]), j & 1, a.wait_limit_ns, &sh.abort);
+    // (also where the other query tile alone has keys: until it has been through them)
+    if (ok)
+      ok = lanes_wait(true, smem_u32(&sh.o_done[x]), j & 1, a.wait_limit_ns, &sh.abort, &sh.fills[0]);
     if (!ok) break;
     tc_fence_after();
     if (__any_sync(0xffffffffu, aside > 0.f))

@@ -156,15 +156,19 @@ __device__ __forceinline__ int uniform(int x) {
 }
 // Waits for a barrier of each lane's own (`wanted`).  The lanes stay together -- what the
 // warp issues next takes its operands from uniform registers -- and the clock, which is
-// slow to read, is looked at now and then.
+// slow to read, is looked at now and then.  `progress`: a count of other warps' steps; where a
+// wait is for many of them, its limit begins anew whenever the count has changed.
 __device__ __forceinline__ bool lanes_wait(bool wanted, uint32_t bar, uint32_t parity,
-                                           uint64_t limit, volatile int* abort) {
+                                           uint64_t limit, volatile int* abort,
+                                           const volatile uint32_t* progress = nullptr) {
   uint64_t since = 0;
+  uint32_t count = 0;
   for (uint32_t n = 1; limit > 0; ++n) {
     if (__all_sync(0xffffffffu, !wanted || mbar_try_wait(bar, parity))) return true;
     if (n % 64 == 0) {
       const uint64_t now = globaltimer_ns();
       if (since == 0) since = now;
+      if (progress != nullptr && *progress != count) since = now, count = *progress;
       if (__any_sync(0xffffffffu, now - since > limit || *abort)) break;
     }
   }

@@ -772,6 +772,24 @@ def test_prompt_long_rising(dkv, dt, out_dtype):
         assert torch.equal(out, other)
 
 
+@pytest.mark.parametrize("n", [200, 100])
+def test_prompt_longer_than_a_waits_limit(dkv, n):
+    # 2^25 keys: a block of queries takes longer than the 200 ms that a wait may, with both
+    # query tiles at work and with one whose warps wait for the other's block to end.
+    # (Equal keys and values, one row in memory: every sum is a whole number that fp32 holds.)
+    N = 1 << 25
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+    q, k = z(n, 1, 128), z(1, 1, 128).expand(N, 1, 128)
+    v = z(1, 1, 64)
+    v[0, 0] = torch.arange(64, device="cuda") % 8 + 1
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    out = dkv.latent_prompt_attn(q[..., :64], q[..., 64:], k[..., :64], k[:, 0, 64:],
+                                 v.expand(N, 1, 64), ints([0, n]), ints([0, N]), 0.1, causal=False,
+                                 workspace=ws)
+    assert dkv.read_device_status(ws) == 0
+    assert bool(((out - v.float()).abs() <= eps(torch.bfloat16) / 2 * v.float()).all())
+
+
 def test_prompt_captured(dkv):
     args, out = prompt_case(3, 128, [300, 100], [400, 100], torch.bfloat16, gen_of("pg"), extra=300)
     cu_q, cu_k = args[5], args[6]
