@@ -379,6 +379,41 @@ def test_decode_shared_operands(dkv):
     check_decode(x, ql, qr, out, lens, [1] * 3, 0.07)
 
 
+@pytest.mark.parametrize("B,T,H,dc", [(257, 1, 16, 256), (1000, 1, 20, 512), (300, 3, 64, 512),
+                                      (1000, 4, 40, 256)])
+def test_decode_many_sequences(dkv, B, T, H, dc):
+    # more sequences than a warp counts for itself, with one row tile and several; some empty,
+    # some without new tokens
+    gen, N = gen_of("many", B, T), 150
+    lens = [(37 * b) % 160 - 9 for b in range(B)]  # (past N: all N)
+    new = [1 if T == 1 else b % (T + 1) for b in range(B)]
+    cache, ql, qr, out = decode_case(B, T, H, dc, N, 16, torch.bfloat16, gen, lens, new)
+    ws = torch.zeros(dkv.latent_workspace_bytes(B, T, H, dc, N), dtype=torch.uint8, device="cuda")
+    again = out.clone()
+    for o in (out, again):
+        dkv.latent_decode_attn(ql, qr, cache, 0.07, seq_lens=ints(lens), new_lens=ints(new), out=o,
+                               workspace=ws)
+    assert dkv.read_device_status(ws) == 0
+    assert torch.equal(out, again)
+    check_decode(cache, ql, qr, out, [min(n, N) for n in lens], new, 0.07)
+
+
+def test_decode_many_row_tiles(dkv):
+    # more row tiles (160, of 64) than there are CTAs to share a sequence's tokens
+    lens, new = [130, 41, 7, 0], [40, 38, 9, 0]
+    cache, ql, qr, out = decode_case(4, 40, 256, 256, 130, 16, torch.bfloat16, gen_of("rows"), lens,
+                                     new)
+    ws = torch.zeros(dkv.latent_workspace_bytes(4, 40, 256, 256, 130), dtype=torch.uint8,
+                     device="cuda")
+    again = out.clone()
+    for o in (out, again):
+        dkv.latent_decode_attn(ql, qr, cache, 0.07, seq_lens=ints(lens), new_lens=ints(new), out=o,
+                               workspace=ws)
+    assert dkv.read_device_status(ws) == 0
+    assert torch.equal(out, again)
+    check_decode(cache, ql, qr, out, lens, new, 0.07)
+
+
 def test_decode_workspace_of_larger_sizes(dkv):
     # one workspace for the largest call serves those of fewer new tokens and heads, in turn
     gen = gen_of("one workspace")
