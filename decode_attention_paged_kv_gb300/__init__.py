@@ -511,6 +511,11 @@ def kv_pages_fork(caches, refs: torch.Tensor, seq_lens: torch.Tensor,
     a block, and whoever else does: pages that no row continues are released by it.
     Entries past a row's pages become -1.  Lengths are not changed: a row's new one is
     seq_lens[parents[b]] + new_lens[b].
+    Page metadata goes by row and page, not by block, and does not follow: before
+    decode_attn_select reads it, gather it by the parents (meta[parents], rows of -1
+    any), then bring it up to date with the append (kv_meta_append), or build it anew
+    (kv_meta_build).  The same goes for 8-bit metadata, and for whatever else the caller
+    keeps by row (lengths, a reuse state).
     All or nothing: a step that does not fit (too few free blocks, say) changes
     nothing and is recorded in `workspace` (read_device_status)."""
     return (_binding or _load_binding()).kv_pages_fork(caches, refs, seq_lens, parents, new_lens,
@@ -523,7 +528,8 @@ def kv_pages_compact(caches, refs: torch.Tensor, refs_out: Optional[torch.Tensor
     """Move the blocks in use (refs > 0) of the caches' pools to their front, and
     rename them in the block table and the counts (in place, or into
     block_table_out and refs_out).  Returns int32 [num_blocks]: every block's new
-    number, -1 where it was free, for whoever else knows blocks by number."""
+    number, -1 where it was free, for whoever else knows blocks by number.  Page
+    metadata, which goes by row and page, stays as it is."""
     return (_binding or _load_binding()).kv_pages_compact(caches, refs, refs_out, block_table_out,
                                                           workspace)
 

@@ -566,6 +566,8 @@ typedef struct dkv_pages {
    - Entries past a row's pages become -1.  refs follows: +1 for every entry that a
      block gains, -1 for each it loses; blocks left at 0 are free for the next call.
    - An unused row: parents[b] = -1 and new_lens[b] = 0 frees it.
+   - Page metadata and the reuse state go by row and page, not by block, and do not
+     follow: the caller gathers them by the parents before an append, or builds anew.
    All or nothing: with a parent outside [-1, B), a length below 0, or past the table's
    columns, an entry outside the pool within a continued row's length, or too few free
    blocks, nothing changes and `workspace` records DKV_ERR_DEVICE_CHECK.

@@ -321,3 +321,50 @@ def test_beams_over_a_cache(dkv, kind):
         assert torch.equal(outs[0], outs[1]), step
         if int(lens.max()) + 8 > N:
             break
+
+
+@pytest.mark.parametrize("kind", ["fp8", "kv16"])
+def test_beams_select_pages(dkv, kind):
+    """Beams that fork, append and attend page-sparsely: page metadata goes by rows of the
+    table, so the caller gathers it by the parents before it is brought up to date; then
+    selections and outputs are those of metadata built anew, bit for bit."""
+    B, H, d, N, top_k = 4, 2, 64, 320, 3
+    P = N // 16
+    nb = B * P + 1
+    gen = torch.Generator("cuda").manual_seed(4)
+    table = torch.full((B, P), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(nb, dtype=torch.int32, device="cuda")
+    caches, _ = make_caches(dkv, kind, nb, table, N, H=H, d=d, seed=10)
+    K, V = caches
+    ws = torch.zeros(max(dkv.pages_workspace_bytes(B, P, nb),
+                         dkv.workspace_bytes(B, 4, H, d, N, top_k, fp8=kind == "fp8")),
+                     dtype=torch.uint8, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    meta = tuple(torch.zeros(B, H, P, d, dtype=torch.bfloat16, device="cuda") for _ in "nx")
+    rng = random.Random(5)
+    moved = 0
+    for step in range(20):
+        parents = [rng.randrange(B) if step else -1 for _ in range(B)]
+        T = 150 if step == 0 else rng.choice([1, 1, 5])
+        n = ints([rng.randint(T // 2 + 1, T) for _ in range(B)])
+        par = ints(parents)
+        dkv.kv_pages_fork(caches, refs, lens, parents=par, new_lens=n, workspace=ws)
+        if step:
+            lens = lens[par.long()]
+            for x in meta:
+                x.copy_(x[par.long()])
+        lens = lens + n
+        k, v = (torch.randn(B, T, H, d, generator=gen, device="cuda").bfloat16() for _ in "kv")
+        q = torch.randn(B, 4, d, generator=gen, device="cuda").bfloat16()
+        dkv.kv_append(k, v, K, V, seq_lens=lens, new_lens=n, workspace=ws)
+        dkv.kv_meta_append(K, meta, seq_lens=lens, new_tokens=T, new_lens=n)
+        anew = dkv.kv_meta_build(K, seq_lens=lens)
+        got, want = (dkv.decode_attn_select(q, K, V, m, top_k, return_selected=True, seq_lens=lens,
+                                            workspace=ws) for m in (meta, anew))
+        assert dkv.read_device_status(ws) == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), step
+        for b in range(B):
+            pages = (int(lens[b]) + 15) // 16
+            assert all(torch.equal(x[b, :, :pages], y[b, :, :pages]) for x, y in zip(meta, anew))
+        moved += sum(p != b for b, p in enumerate(parents))
+    assert moved > 20
