@@ -35,8 +35,6 @@ struct LatentAppendArgs {
 struct LatentAttnArgs {
   int B, T, H;
   float scale_log2;  // softmax scale times log2(e)
-  const uint16_t *ql, *qr;
-  int64_t ql_sb, ql_st, ql_sh, qr_sb, qr_st, qr_sh;
   void* out;
   int out_dtype;  // 0: bf16, 1: fp16, 2: fp32
   int64_t o_sb, o_st, o_sh;
@@ -71,8 +69,6 @@ struct PromptArgs {
   int B, H;
   float scale_log2;
   int causal;
-  const uint16_t *qn, *qr, *kn, *v, *kr;
-  int64_t qn_st, qn_sh, qr_st, qr_sh, kn_st, kn_sh, v_st, v_sh, kr_st;
   void* out;
   int out_dtype;
   int64_t o_st, o_sh;

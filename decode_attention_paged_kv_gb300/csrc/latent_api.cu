@@ -255,10 +255,6 @@ dkv_status dkv_latent_decode_attn(const dkv_latent_attn* p, const dkv_latent_cac
   a.T = p->new_tokens;
   a.H = p->num_heads;
   a.scale_log2 = p->scale * 1.4426950408889634f;
-  a.ql = static_cast<const uint16_t*>(p->q_latent);
-  a.qr = static_cast<const uint16_t*>(p->q_rope);
-  a.ql_sb = p->ql_stride_b, a.ql_st = p->ql_stride_t, a.ql_sh = p->ql_stride_h;
-  a.qr_sb = p->qr_stride_b, a.qr_st = p->qr_stride_t, a.qr_sh = p->qr_stride_h;
   a.out = p->out;
   a.out_dtype = out_code(p->out_dtype);
   a.o_sb = p->o_stride_b, a.o_st = p->o_stride_t, a.o_sh = p->o_stride_h;
@@ -339,16 +335,6 @@ dkv_status dkv_latent_prompt_attn(const dkv_prompt* p, void* workspace, void* st
   a.H = p->num_heads;
   a.scale_log2 = p->scale * 1.4426950408889634f;
   a.causal = p->causal;
-  a.qn = static_cast<const uint16_t*>(p->q_nope);
-  a.qr = static_cast<const uint16_t*>(p->q_rope);
-  a.kn = static_cast<const uint16_t*>(p->k_nope);
-  a.v = static_cast<const uint16_t*>(p->v);
-  a.kr = static_cast<const uint16_t*>(p->k_rope);
-  a.qn_st = p->qn_stride_t, a.qn_sh = p->qn_stride_h;
-  a.qr_st = p->qr_stride_t, a.qr_sh = p->qr_stride_h;
-  a.kn_st = p->kn_stride_t, a.kn_sh = p->kn_stride_h;
-  a.v_st = p->v_stride_t, a.v_sh = p->v_stride_h;
-  a.kr_st = p->kr_stride_t;
   a.out = p->out;
   a.out_dtype = out_code(p->out_dtype);
   a.o_st = p->o_stride_t, a.o_sh = p->o_stride_h;
