@@ -43,7 +43,7 @@
  *                           a head (the expanded form).
  *   dkv_kv_pages_fork /     the pages of paged caches: rows of a block table that
  *   dkv_kv_pages_compact    continue, fork, grow and end; a pool compacted.
- *                           No page defines these four: they are what a decode
+ *                           No page defines these five: they are what a decode
  *                           loop needs next to the calls above.
  *
  * Conventions shared by every entry point:
