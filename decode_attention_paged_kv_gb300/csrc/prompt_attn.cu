@@ -449,7 +449,9 @@ __device__ __forceinline__ void product_loop(const PromptArgs& a, bool f16, int 
   const uint32_t scores_at = tmem + x * S::kScores, weights_at = scores_at + S::kWeights;
   const uint32_t output_at = tmem + S::kOutput + x * S::kOutputs;
   const uint32_t q = q_smem + x * S::kQBytes;
-  const uint32_t score_desc = mma_desc(f16, kRows, kKeys, false, false);
+  // (a scale below 0: products of negated queries, so that the softmax takes its size alone)
+  const uint32_t score_desc =
+      mma_desc(f16, kRows, kKeys, false, false) | (a.scale_log2 < 0.f ? kNegateA : 0u);
   const uint32_t value_desc = mma_desc(f16, kRows, 64, false, true);
   bool ok = true;
   // of the blocks so far: pieces (modulo two rounds of the ring), steps, key tiles of x
@@ -670,9 +672,10 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
     auto refer = [&](float high) {  // (the warp's lanes together)
       m = high;
       const bool none = m == -INFINITY;
-      far = __any_sync(0xffffffffu, !none && fabsf(m * scale) >= kFar);
       from = none ? 0.f : m;
-      ref = (far ? 0.f : from * scale) - kAtTop<F16>;
+      ref = from * scale - kAtTop<F16>;
+      far = __any_sync(0xffffffffu, fabsf(ref) >= kFar);
+      if (far) ref = -kAtTop<F16>;
     };
     const int64_t at = static_cast<int64_t>(w.q0 + row) * a.o_st + w.h * a.o_sh;
     float aside = 0.f;  // the sum of the weights whose values' mean lies in the output
@@ -688,14 +691,6 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
       if constexpr (S::kApart) {
         tc_fence_before();
         mbar_arrive(smem_u32(&sh.s_free[x]));
-      }
-      // (by pairs, here and where scores are far: half the code, which all tiles fetch past)
-      if (a.scale_log2 < 0.f) {
-#pragma unroll
-        for (int c = 0; c < 128; c += 2) {
-          const float2 y = halves_of(fma2(pair_of(s[c], s[c + 1]), pair_of(-1.f, -1.f), 0));
-          s[c] = y.x, s[c + 1] = y.y;
-        }
       }
       const int limit = seen - i * kKeys;
       if (__any_sync(0xffffffffu, limit < kKeys)) {
@@ -737,6 +732,7 @@ __device__ __forceinline__ void softmax_loop(const PromptArgs& a, int x, Shared&
           }
         }
       }
+      // (by pairs: half the code, which all tiles fetch past)
       if (far) {
 #pragma unroll
         for (int c = 0; c < 128; c += 2) {

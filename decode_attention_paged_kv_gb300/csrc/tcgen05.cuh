@@ -183,6 +183,8 @@ __device__ __forceinline__ uint32_t mma_desc(bool f16, uint32_t m, uint32_t n, b
          (n >> 3) << 17 | (m >> 4) << 24;
 }
 
+constexpr uint32_t kNegateA = 1u << 13;  // of an instruction descriptor: -a
+
 // d (+)= a b, issued by one thread; `accumulate` 0 overwrites d.
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
                                        uint32_t accumulate) {
