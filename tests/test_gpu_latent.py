@@ -367,6 +367,27 @@ def test_decode_long_sequence_of_many_row_tiles(dkv):
     check_decode(cache, ql, qr, out, lens, new, 0.07)
 
 
+def test_decode_long_nan_scores(dkv):
+    # NaN queries and a NaN row in sequences that are summed up in segments, whole and cut
+    B, N, H, dc = 40, 33000, 20, 256
+    gen = gen_of("long nan")
+    x = torch.randn(1, N, dc + 64, generator=gen, device="cuda").bfloat16()
+    ql = torch.randn(B, 1, H, dc, generator=gen, device="cuda").bfloat16()
+    qr = torch.randn(B, 1, H, 64, generator=gen, device="cuda").bfloat16()
+    ql[::3, 0, 3], qr[1, 0, 17, 5] = math.nan, math.nan
+    x[0, 30000, 2] = math.nan
+    lens = [33000 if b % 4 == 0 else 30000 for b in range(B)]
+    out = dkv.latent_decode_attn(ql, qr, x.expand(B, N, dc + 64), 0.07, seq_lens=ints(lens))
+    bad = torch.zeros(B, H, dtype=torch.bool, device="cuda")
+    bad[::3, 3] = bad[1, 17] = True
+    bad[::4] = True
+    assert torch.equal(out[:, 0].isnan().all(-1), bad)
+    x = x[0, :30000]
+    for b in (1, 2, 3, 39):
+        q = torch.cat((ql[b, 0], qr[b, 0]), -1)[~bad[b]]
+        check(out[b, 0][~bad[b]], *attn64(q, x, x[:, :dc], 0.07), torch.bfloat16, b)
+
+
 def test_decode_shared_operands(dkv):
     # one cache for all sequences, one query for all heads: dimensions of stride 0
     gen = gen_of("expanded")
