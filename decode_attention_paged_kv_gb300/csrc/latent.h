@@ -61,7 +61,7 @@ struct LatentPlan {
   size_t pieces, part_ml, part_o, total;  // workspace offsets
 };
 constexpr int kLatentTile = 64;  // tokens
-constexpr int kLatentRun = 128;  // tiles of a sequence that are summed up at a time
+constexpr int kLatentRun = 256;  // tiles of a sequence that are summed up at a time
 constexpr int kLatentCtas = 152;
 constexpr int kMaxWeighted = 8;
 

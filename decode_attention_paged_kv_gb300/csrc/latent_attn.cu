@@ -224,8 +224,9 @@ __device__ __forceinline__ Share share_of(const LatentAttnArgs& a, Shared& sh) {
 
 // Walks a share segment by segment: consecutive tiles of a sequence, kLatentRun at most.  The
 // products' adders cut off what lies some 2^-26 below the sum so far, which adds up: of equal
-// weights and values 0.06% over 128K tokens, 0.6% over 1M, of 1M tokens beside a heavy one
-// 1.6%.  So a long sequence is summed up in segments, joined by additions that round.
+// weights and values 0.05% over 128K tokens, 0.6% over 1M, of 1M tokens beside a heavy one
+// 1.6%.  So a long sequence is summed up in segments of 16K tokens, which stay below 2^-12,
+// joined by additions that round.
 struct Walk {
   const LatentAttnArgs& a;
   int first_t;

@@ -341,7 +341,7 @@ def test_decode_long_ragged(dkv, T, H, dc):
     # sequences of many times the tokens that are summed up at a time, whole in a CTA and cut
     # between CTAs, among short and empty ones; the same bits each time
     gen, B, N = gen_of("runs", T), 40, 70000
-    lens = [(0, 7, 70000, 8192, 8193, 16384, 33000, 50)[b % 8] for b in range(B)]
+    lens = [(0, 7, 70000, 16385, 8193, 16384, 33000, 50)[b % 8] for b in range(B)]
     new = [1 if T == 1 else (3, 1, 2, 0)[b % 4] for b in range(B)]
     x = torch.randn(1, N, dc + 64, generator=gen, device="cuda").bfloat16()
     cache = x.expand(B, N, dc + 64)
