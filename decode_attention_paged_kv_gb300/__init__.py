@@ -457,7 +457,9 @@ def latent_decode_attn(q_latent: torch.Tensor, q_rope: torch.Tensor, cache, scal
     sees the sequence's first seq_lens - new_lens + t + 1 tokens.  Rows past
     new_lens are not written.
     scale has no default: it goes by the width of the unabsorbed heads, which the
-    cache does not know (1 / sqrt(128 + 64), say)."""
+    cache does not know (1 / sqrt(128 + 64), say).
+    Softmax weights are rounded once to the cache's 16-bit type, whatever out_dtype
+    is; maxima and sums are fp32."""
     return (_binding or _load_binding()).latent_decode_attn(
         q_latent, q_rope, cache, scale, seq_lens, new_lens, out_dtype, out, workspace, flags)
 
@@ -489,6 +491,8 @@ def latent_prompt_attn(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch
     causal means that query i of n_q sees the first n_k - n_q + i + 1 keys: whole
     prompts, and the last chunk of prompts whose first tokens are cached already.
     dn = 64 or 128.  Rows past the last sequence may be there and are left alone.
+    Softmax weights are rounded once to the inputs' type, whatever out_dtype is; maxima
+    and sums are fp32.  out shares no memory with the keys and values.
     workspace: where bounds that do not fit the tensors are recorded
     (read_device_status); such a sequence is left alone."""
     return (_binding or _load_binding()).latent_prompt_attn(

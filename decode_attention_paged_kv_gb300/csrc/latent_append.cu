@@ -9,8 +9,10 @@
 // in registers.  All loads of a warp (5 KB at 32 heads) are under way at once, which is
 // what a prompt is bound by; a decode step with more heads has further warps for them.
 //
-// Measured on a GB300, 32 heads, dc = 512: 8 ragged prompts of up to 8K tokens 55 us (4.5
-// TB/s; 88 us with six warps a token, each one load deep), one token of 64 sequences 2.9 us,
+// Measured on a GB300, 32 heads, dc = 512: 8 ragged prompts of up to 8K tokens 55 to 87 us over
+// six draws of lengths, 5.0 to 5.8 TB/s by their tokens (the first, 55 us: 88 with six warps a
+// token, each one load deep): 100 registers leave two CTAs a multiprocessor, and a warp has
+// nothing of a next token under way while it computes and stores one; one token of 64 sequences 2.9 us,
 // the latency of the launch and of the loads lengths - rows, table - stores.
 
 #include "dkv_device.cuh"

@@ -26,9 +26,9 @@
 // the second of them finds in the L2.
 //
 // Measured on a GB300 (copy rate 6.78 TB/s), bf16, dc = 512: 16 sequences of 20K tokens with
-// 16 heads 72 us dense and on blocks of any size (378 MB: 5.2 TB/s), one of 1M tokens 201 us
-// (6.0 TB/s), 32 of 8K with 128 heads 114 us (311 MB; 640 TFLOP/s), 8 of 8K with four new
-// tokens and 32 heads 45 us (404 TFLOP/s); one of 1K, 16
+// 16 heads 71 us dense and on blocks of any size (378 MB: 5.3 TB/s), one of 1M tokens 198 us
+// (6.1 TB/s), 32 of 8K with 128 heads 115 us (311 MB; 635 TFLOP/s), 8 of 8K with four new
+// tokens and 32 heads 46 us (398 TFLOP/s); one of 1K, 16
 // heads, dc = 256: 10 us, most of it the two launches' latencies.  What bounds it: a tile
 // passes through copies, scores, softmax and values one after the other, 6000 to 7000
 // cycles, and shared memory holds 2 tiles beside 64 queries (2.75 beside 16); the products'

@@ -26,15 +26,17 @@
 // Maxima, sums and outputs are fp32; a weight is rounded once to the inputs' type for its
 // product, and is 2^7 at the running maximum in fp16, so that the tail of many keys stays in
 // its range.  Measured on a GB300, bf16: the last 2K tokens of 4 prompts of 8K, 16 heads, dn =
-// 128: 423 us, 1.42 PFLOP/s of the 1.9 that a large library product reaches; one prompt of
-// 8K 226 us (1.52); 2 of 2K with 128 heads 273 us (1.26); one of 16K, 8 heads, dn = 64 332 us
-// (1.24); 16 of 512 tokens, 32 heads, dn = 64 51 us (0.50).  What bounds it: with dn = 128 a
+// 128: 425 us, 1.42 PFLOP/s of the 1.9 that a large library product reaches; one prompt of
+// 8K 230 us (1.50); 2 of 2K with 128 heads 274 us (1.25); one of 16K, 8 heads, dn = 64 336 us
+// (1.23); 16 of 512 tokens, 32 heads, dn = 64 51 us (0.50).  What bounds it: with dn = 128 a
 // query tile's chain scores - softmax - values, some 3600 cycles for 2560 of products for two
 // tiles; with dn = 64 the softmax's instructions (1540 of products); of short prompts the
-// chain's beginning and end.  What carried it, listed batch of long prompts: 345 us with one
+// chain's beginning and end.  What carried it, the last 2K of up to 8K tokens of 4 prompts, one
+// draw of lengths (others take up to 325 us as it is, 1.12 to 1.41 PFLOP/s): 345 us with one
 // warp for both tiles' products, 296 with a warp each in turns, 266 with blocks taken over, 258
 // without spilt registers, 244 with weights made two at a time, 234 with products in functions
-// of their own (fewer instructions for the caches), 216 with long blocks first.  No difference
+// of their own (fewer instructions for the caches), 216 with long blocks first; 218 since scores
+// far from 0 and sums of many keys are right.  No difference
 // made a softmax in halves and a second wait between values and scores; outputs read 32
 // columns at a time were 2% slower for short prompts.
 

@@ -494,8 +494,9 @@ typedef struct dkv_latent_attn {
 /* Rows t >= n_b are not written.  A row that sees no token (N_b <= 0, or
    N_b - n_b + t + 1 <= 0) is 0.  What the cache holds past N_b is never used,
    whatever it is; values of the sequence's own tokens are finite, also those a row
-   does not see yet.  Softmax statistics and sums are fp32; the weights are rounded to
-   the cache's type for the product.  The same call gives the same bits; a row's last
+   does not see yet.  NaN scores give a row of NaN.  Softmax statistics and sums are fp32;
+   the weights are rounded once to the cache's type for the product, half a step each
+   (in fp16 those below 2^-21 of the largest by 2^-32 of it).  The same call gives the same bits; a row's last
    bits may depend on the batch it is part of.  workspace:
    dkv_latent_workspace_bytes(p, cache) bytes. */
 dkv_status dkv_latent_decode_attn(const dkv_latent_attn* p, const dkv_latent_cache* cache,
@@ -529,6 +530,8 @@ typedef struct dkv_prompt {
 
 /* Rows of out outside every sequence are not written; a query that sees no key gets 0.
    Keys and values outside the sequences may be anything; a sequence's own are finite.
+   Weights are rounded as in dkv_latent_decode_attn.  out shares no memory with k_nope, k_rope
+   or v: rows of more than 16K keys hold sums in it meanwhile.
    A sequence whose bounds descend or lie outside its tensor is left alone and recorded
    in `workspace` (nullable, DKV_WORKSPACE_HEADER_BYTES) as DKV_ERR_DEVICE_CHECK. */
 dkv_status dkv_latent_prompt_attn(const dkv_prompt* p, void* workspace, void* stream);
